@@ -167,6 +167,61 @@ mlp_status mlp_op_wait_timeout_check(uint64_t limit_ns, uint32_t* err_dev, void*
 /* Row argmax of z [B, C] (ldz) into int32 out [B]; lowest index on ties. */
 mlp_status mlp_op_argmax(int dtype, int64_t B, int64_t C, const void* z, int64_t ldz, int32_t* out, void* stream);
 
+/* Layer norm over the rows of X [M, D] (ldx; MLP_F32 or MLP_BF16), the norm
+ * in front of a feed-forward block:
+ *   mean_i = sum_j X_ij / D,  rstd_i = 1 / sqrt(sum_j (X_ij - mean_i)^2 / D
+ *   + eps),  Y_ij = (X_ij - mean_i) rstd_i gamma_j + beta_j.
+ *   gamma, beta fp32 [D] (nullable: 1 and 0); Y [M, D] (ldy, dtype; may be
+ *   X); mean, rstd fp32 [M] (nullable: not kept).  eps >= 0 and finite.
+ * Any D up to 65535 * 256 and any alignment of the elements; rows whose base
+ * and pitch are 16-byte aligned move by 16-byte accesses.  Statistics are
+ * fp32, from the elements as stored. */
+mlp_status mlp_op_layernorm(int dtype, int64_t M, int64_t D, const void* X, int64_t ldx, const float* gamma,
+                            const float* beta, float eps, void* Y, int64_t ldy, float* mean, float* rstd,
+                            void* stream);
+
+/* Its vector-Jacobian product: with xh = (X - mean) rstd and w = gamma dY,
+ *   dX = rstd (w - mean_j(w) - xh mean_j(w xh))   (dtype, lddx; may be dY),
+ *   dgamma_j = sum_i dY_ij xh_ij,  dbeta_j = sum_i dY_ij  (fp32 [D], nullable).
+ * X, mean and rstd are what the forward read and kept.  workspace (device, at
+ * least the bytes below for this shape) holds per-block partial sums of
+ * dgamma and dbeta, added in a fixed order; it is not needed where both are
+ * null.  Workspaces of calls that may overlap must not. */
+size_t mlp_op_layernorm_backward_workspace_bytes(int dtype, int64_t M, int64_t D);
+mlp_status mlp_op_layernorm_backward(int dtype, int64_t M, int64_t D, const void* dY, int64_t lddy, const void* X,
+                                     int64_t ldx, const float* gamma, const float* mean, const float* rstd, void* dX,
+                                     int64_t lddx, float* dgamma, float* dbeta, void* workspace, size_t ws_bytes,
+                                     void* stream);
+
+/* Activation checkpoints in 8 bits: a matrix kept between the forward and the
+ * backward pass as e4m3 codes with one scale per row and 32 columns (about
+ * half the bytes of bf16).  For a block of 32 columns with amax its largest
+ * finite magnitude, k is the smallest exponent >= -120 with amax <= 448 2^k;
+ * E holds k + 127, Q the values X 2^-k rounded to e4m3 (to nearest, ties to
+ * even).  A code stands for e4m3 * 2^k, exact in fp32 and in bf16, off by at
+ * most 2^-4 of the value (2^-17.8 of the block's amax where that is more).
+ * Infinities and NaN are kept as NaN; a magnitude of 2^128 (1 - 2^-5) or more
+ * reads back as infinite.
+ *   X, Y [rows, cols] (ldx, ldy; MLP_F32 or MLP_BF16), Q uint8 [rows, cols]
+ *   (ldq), E uint8 [rows, ceil(cols / 32)] (lde).
+ * Any alignment; 16-byte aligned rows of X / Y with 8-byte aligned rows of Q
+ * move by wide accesses. */
+mlp_status mlp_op_quant8(int dtype, int64_t rows, int64_t cols, const void* X, int64_t ldx, uint8_t* Q, int64_t ldq,
+                         uint8_t* E, int64_t lde, void* stream);
+mlp_status mlp_op_dequant8(int dtype, int64_t rows, int64_t cols, const uint8_t* Q, int64_t ldq, const uint8_t* E,
+                           int64_t lde, void* Y, int64_t ldy, void* stream);
+
+/* mlp_op_wgrad with the layer's input kept as an 8-bit checkpoint:
+ *   dW = dY^T X (fp32 [N, K], lddw), db = sum over rows of dY (nullable),
+ *   dY [B, N] (ldy; MLP_F32 or MLP_BF16), X [B, K] the values of Q (ldq), E
+ *   (lde).  The values are read back into the workspace (16-byte aligned, at
+ *   least the bytes below; the dtype holds them exactly), so the result is
+ *   that of mlp_op_wgrad on them. */
+size_t mlp_op_wgrad8_workspace_bytes(int dtype, int64_t N, int64_t K, int64_t B);
+mlp_status mlp_op_wgrad8(int dtype, int64_t N, int64_t K, int64_t B, const void* dY, int64_t ldy, const uint8_t* Q,
+                         int64_t ldq, const uint8_t* E, int64_t lde, float* dW, int64_t lddw, float* db,
+                         void* workspace, size_t ws_bytes, uint32_t* err_dev, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -82,6 +82,14 @@ _SIGS = {
     "mlp_op_adamw": (_I32, [_I64, _P, _P, _P, _P, _P, _I64, _F, _F, _F, _F, _F, _P]),
     "mlp_op_optim": (_I32, [_I32, _I64, _P, _P, _P, _P, _P, _I64, _F, _F, _F, _F, _F, _F, _P, _P, _P]),
     "mlp_op_argmax": (_I32, [_I32, _I64, _I64, _P, _I64, _P, _P]),
+    "mlp_op_layernorm": (_I32, [_I32, _I64, _I64, _P, _I64, _P, _P, _F, _P, _I64, _P, _P, _P]),
+    "mlp_op_layernorm_backward_workspace_bytes": (_SZ, [_I32, _I64, _I64]),
+    "mlp_op_layernorm_backward": (_I32, [_I32, _I64, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _I64, _P, _P, _P, _SZ,
+                                         _P]),
+    "mlp_op_quant8": (_I32, [_I32, _I64, _I64, _P, _I64, _P, _I64, _P, _I64, _P]),
+    "mlp_op_dequant8": (_I32, [_I32, _I64, _I64, _P, _I64, _P, _I64, _P, _I64, _P]),
+    "mlp_op_wgrad8_workspace_bytes": (_SZ, [_I32, _I64, _I64, _I64]),
+    "mlp_op_wgrad8": (_I32, [_I32, _I64, _I64, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _SZ, _P, _P]),
     "mlp_op_wait_timeout_check": (_I32, [_c.c_uint64, _P, _P]),
 }
 
@@ -328,6 +336,36 @@ def mlp_op_wait_timeout_check(limit_ns, err, stream) -> None:
 
 def mlp_op_argmax(dtype, B, C, z, ldz, out, stream) -> None:
     _check(lib().mlp_op_argmax(dtype, B, C, z, ldz, out, stream))
+
+
+def mlp_op_layernorm(dtype, M, D, X, ldx, gamma, beta, eps, Y, ldy, mean, rstd, stream) -> None:
+    _check(lib().mlp_op_layernorm(dtype, M, D, X, ldx, gamma, beta, eps, Y, ldy, mean, rstd, stream))
+
+
+def mlp_op_layernorm_backward_workspace_bytes(dtype, M, D) -> int:
+    return lib().mlp_op_layernorm_backward_workspace_bytes(dtype, M, D)
+
+
+def mlp_op_layernorm_backward(dtype, M, D, dY, lddy, X, ldx, gamma, mean, rstd, dX, lddx, dgamma, dbeta, ws, ws_bytes,
+                              stream) -> None:
+    _check(lib().mlp_op_layernorm_backward(dtype, M, D, dY, lddy, X, ldx, gamma, mean, rstd, dX, lddx, dgamma, dbeta,
+                                           ws, ws_bytes, stream))
+
+
+def mlp_op_quant8(dtype, rows, cols, X, ldx, Q, ldq, E, lde, stream) -> None:
+    _check(lib().mlp_op_quant8(dtype, rows, cols, X, ldx, Q, ldq, E, lde, stream))
+
+
+def mlp_op_dequant8(dtype, rows, cols, Q, ldq, E, lde, Y, ldy, stream) -> None:
+    _check(lib().mlp_op_dequant8(dtype, rows, cols, Q, ldq, E, lde, Y, ldy, stream))
+
+
+def mlp_op_wgrad8_workspace_bytes(dtype, N, K, B) -> int:
+    return lib().mlp_op_wgrad8_workspace_bytes(dtype, N, K, B)
+
+
+def mlp_op_wgrad8(dtype, N, K, B, dY, ldy, Q, ldq, E, lde, dW, lddw, db, ws, ws_bytes, err, stream) -> None:
+    _check(lib().mlp_op_wgrad8(dtype, N, K, B, dY, ldy, Q, ldq, E, lde, dW, lddw, db, ws, ws_bytes, err, stream))
 
 
 # ---- convenience wrapper ---------------------------------------------------

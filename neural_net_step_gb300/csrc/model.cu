@@ -1589,4 +1589,105 @@ mlp_status mlp_op_argmax(int dtype, int64_t B, int64_t C, const void* z, int64_t
   return run_ops(&r, 1, stream);
 }
 
+mlp_status mlp_op_layernorm(int dtype, int64_t M, int64_t D, const void* X, int64_t ldx, const float* gamma,
+                            const float* beta, float eps, void* Y, int64_t ldy, float* mean, float* rstd,
+                            void* stream) {
+  if (!dtype_ok(dtype)) return fail(MLP_ERR_DTYPE, "bad dtype");
+  if (!X || !Y) return fail(MLP_ERR_ARG, "null pointer");
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(MLP_ERR_ARG, "eps must be finite and not negative");
+  LayerNormOp op;
+  op.dtype = dtype; op.M = M; op.D = D; op.x = X; op.ldx = ldx; op.gamma = gamma; op.beta = beta; op.eps = eps;
+  op.y = Y; op.ldy = ldy; op.mean = mean; op.rstd = rstd;
+  LaunchRec r;
+  char e_[512] = "";
+  if (layernorm_plan(op, &r, e_, sizeof(e_)) < 0) return fail(MLP_ERR_SHAPE, "%s", e_);
+  return run_ops(&r, 1, stream);
+}
+
+size_t mlp_op_layernorm_backward_workspace_bytes(int dtype, int64_t M, int64_t D) {
+  if (!dtype_ok(dtype) || M < 1 || D < 1) return 0;
+  return layernorm_bwd_workspace_bytes(M, D);
+}
+
+mlp_status mlp_op_layernorm_backward(int dtype, int64_t M, int64_t D, const void* dY, int64_t lddy, const void* X,
+                                     int64_t ldx, const float* gamma, const float* mean, const float* rstd, void* dX,
+                                     int64_t lddx, float* dgamma, float* dbeta, void* workspace, size_t ws_bytes,
+                                     void* stream) {
+  if (!dtype_ok(dtype)) return fail(MLP_ERR_DTYPE, "bad dtype");
+  if (!dY || !X || !mean || !rstd || !dX) return fail(MLP_ERR_ARG, "null pointer");
+  LayerNormBwdOp op;
+  op.dtype = dtype; op.M = M; op.D = D; op.dy = dY; op.lddy = lddy; op.x = X; op.ldx = ldx; op.gamma = gamma;
+  op.mean = mean; op.rstd = rstd; op.dx = dX; op.lddx = lddx; op.dgamma = dgamma; op.dbeta = dbeta;
+  op.ws = (float*)workspace; op.ws_bytes = ws_bytes;
+  LaunchRec r[3];
+  char e_[512] = "";
+  const int n = layernorm_bwd_plan(op, r, e_, sizeof(e_));
+  if (n < 0) return fail(MLP_ERR_SHAPE, "%s", e_);
+  return run_ops(r, n, stream);
+}
+
+mlp_status mlp_op_quant8(int dtype, int64_t rows, int64_t cols, const void* X, int64_t ldx, uint8_t* Q, int64_t ldq,
+                         uint8_t* E, int64_t lde, void* stream) {
+  if (!dtype_ok(dtype)) return fail(MLP_ERR_DTYPE, "bad dtype");
+  if (!X || !Q || !E) return fail(MLP_ERR_ARG, "null pointer");
+  LaunchRec r;
+  char e_[512] = "";
+  if (quant8_plan(dtype, rows, cols, X, ldx, Q, ldq, E, lde, &r, e_, sizeof(e_)) < 0)
+    return fail(MLP_ERR_SHAPE, "%s", e_);
+  return run_ops(&r, 1, stream);
+}
+
+mlp_status mlp_op_dequant8(int dtype, int64_t rows, int64_t cols, const uint8_t* Q, int64_t ldq, const uint8_t* E,
+                           int64_t lde, void* Y, int64_t ldy, void* stream) {
+  if (!dtype_ok(dtype)) return fail(MLP_ERR_DTYPE, "bad dtype");
+  if (!Q || !E || !Y) return fail(MLP_ERR_ARG, "null pointer");
+  LaunchRec r;
+  char e_[512] = "";
+  if (dequant8_plan(dtype, rows, cols, Q, ldq, E, lde, Y, ldy, &r, e_, sizeof(e_)) < 0)
+    return fail(MLP_ERR_SHAPE, "%s", e_);
+  return run_ops(&r, 1, stream);
+}
+
+// The values of the checkpoint at the workspace's start (row pitch a multiple
+// of 8 elements, for TMA), the weight gradient's own workspace after them.
+static size_t wgrad8_values_bytes(int dtype, int64_t K, int64_t B) {
+  return (size_t)round_up(B * round_up(K, 8) * (dtype == MLP_F32 ? 4 : 2), 256);
+}
+
+size_t mlp_op_wgrad8_workspace_bytes(int dtype, int64_t N, int64_t K, int64_t B) {
+  if (!dtype_ok(dtype) || N < 1 || K < 1 || B < 1 || N > INT32_MAX || K > INT32_MAX || B > INT32_MAX) return 0;
+  if ((double)B * (double)K > 1e15 || (double)N * (double)K > 1e15) return 0;   // (more than any device holds)
+  return wgrad8_values_bytes(dtype, K, B) + wgrad_workspace_bytes(dtype, N, K, B, wgrad_splits(dtype, N, K, B));
+}
+
+mlp_status mlp_op_wgrad8(int dtype, int64_t N, int64_t K, int64_t B, const void* dY, int64_t ldy, const uint8_t* Q,
+                         int64_t ldq, const uint8_t* E, int64_t lde, float* dW, int64_t lddw, float* db,
+                         void* workspace, size_t ws_bytes, uint32_t* err_dev, void* stream) {
+  if (!dtype_ok(dtype)) return fail(MLP_ERR_DTYPE, "bad dtype");
+  if (!dY || !Q || !E || !dW || !workspace) return fail(MLP_ERR_ARG, "null pointer");
+  const size_t need = mlp_op_wgrad8_workspace_bytes(dtype, N, K, B);
+  if (need == 0 || ldy < N || lddw < K) return fail(MLP_ERR_SHAPE, "bad shape or leading dimension");
+  // the tensor cores' dW leaves by TMA in units of 16 bytes: a row's last unit must be whole
+  if (dtype == MLP_BF16 && (K % 4 || lddw % 4 || (uintptr_t)dW % 16))
+    return fail(MLP_ERR_SHAPE, "bf16: K and lddw multiples of 4, dW 16-byte aligned");
+  if (ws_bytes < need || (uintptr_t)workspace % 16) return fail(MLP_ERR_ARG, "workspace too small or misaligned");
+  const size_t vbytes = wgrad8_values_bytes(dtype, K, B);
+  const int64_t ldx = round_up(K, 8);
+  LaunchRec r[3];
+  char e_[512] = "";
+  if (dequant8_plan(dtype, B, K, Q, ldq, E, lde, workspace, ldx, r, e_, sizeof(e_)) < 0)
+    return fail(MLP_ERR_SHAPE, "%s", e_);
+  GemmOp op;
+  op.dtype = dtype; op.kind = GEMM_WGRAD;
+  op.M = N; op.N = K; op.K = B;
+  op.A = dY; op.lda = ldy; op.a_kmajor = false;
+  op.B = workspace; op.ldb = ldx; op.b_kmajor = false;
+  op.dW = dW; op.ld_dw = lddw; op.db = db;
+  op.ws = (float*)((uint8_t*)workspace + vbytes); op.ws_bytes = ws_bytes - vbytes;
+  op.err = err_dev;
+  const int n = gemm_plan(op, r + 1, e_, sizeof(e_));
+  if (n < 0) return fail(MLP_ERR_SHAPE, "%s", e_);
+  return run_ops(r, n + 1, stream);
+}
+
 }  // extern "C"

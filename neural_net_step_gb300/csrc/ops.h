@@ -269,6 +269,39 @@ bool tc_fused_head_ok(int64_t M, int64_t N, int64_t K, int64_t C);
 HeadPartials tc_fused_head_partials(int64_t M);
 int head_plan(const HeadOp& op, LaunchRec* rec, char* err, size_t errlen);
 
+// Layer norm over the rows of x [M, D] (norm.cu).
+struct LayerNormOp {
+  int dtype = 0;
+  int64_t M = 0, D = 0;
+  const void* x = nullptr; int64_t ldx = 0;
+  const float* gamma = nullptr; const float* beta = nullptr;   // nullable: 1, 0
+  float eps = 0.f;
+  void* y = nullptr; int64_t ldy = 0;
+  float* mean = nullptr; float* rstd = nullptr;                // nullable
+};
+int layernorm_plan(const LayerNormOp& op, LaunchRec* rec, char* err, size_t errlen);
+struct LayerNormBwdOp {
+  int dtype = 0;
+  int64_t M = 0, D = 0;
+  const void* dy = nullptr; int64_t lddy = 0;
+  const void* x = nullptr; int64_t ldx = 0;
+  const float* gamma = nullptr;                                // nullable: 1
+  const float* mean = nullptr; const float* rstd = nullptr;
+  void* dx = nullptr; int64_t lddx = 0;
+  float* dgamma = nullptr; float* dbeta = nullptr;             // nullable
+  float* ws = nullptr; size_t ws_bytes = 0;
+};
+size_t layernorm_bwd_workspace_bytes(int64_t M, int64_t D);
+// Up to three records.
+int layernorm_bwd_plan(const LayerNormBwdOp& op, LaunchRec* recs, char* err, size_t errlen);
+
+// Activations in 8 bits (e4m3.cuh): codes q [rows, cols] (ldq), scale bytes e
+// [rows, ceil(cols / 32)] (lde) of x (ckpt8.cu), and the values they stand for.
+int quant8_plan(int dtype, int64_t rows, int64_t cols, const void* x, int64_t ldx, uint8_t* q, int64_t ldq,
+                uint8_t* e, int64_t lde, LaunchRec* rec, char* err, size_t errlen);
+int dequant8_plan(int dtype, int64_t rows, int64_t cols, const uint8_t* q, int64_t ldq, const uint8_t* e, int64_t lde,
+                  void* y, int64_t ldy, LaunchRec* rec, char* err, size_t errlen);
+
 // One thread waits, through the bounded wait every tcgen05 kernel uses, for
 // an mbarrier phase that nothing completes: after limit_ns it marks
 // ERRBIT_TIMEOUT in err_dev and returns (the error path, exercised).

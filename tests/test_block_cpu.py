@@ -1,0 +1,80 @@
+"""Refusals of the feed-forward block's operations: every bad argument is
+turned down before anything is enqueued (no GPU needed), and workspace sizes."""
+import pytest
+
+import neural_net_step_gb300 as nn
+
+P = 1 << 20   # a well-aligned stand-in for a device address (never read)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    from neural_net_step_gb300 import build
+    build.build()
+    return nn.lib()
+
+
+def _refused(f, good, **bad):
+    args = dict(good)
+    args.update(bad)
+    with pytest.raises(nn.MlpError) as e:
+        f(*args.values())
+    assert e.value.status in (1, 2, 3), e.value   # argument, shape or dtype; not a CUDA error
+    return e.value.status
+
+
+LN = dict(dtype=nn.BF16, M=4, D=64, X=P, ldx=64, gamma=P, beta=P, eps=1e-5, Y=P, ldy=64, mean=P, rstd=P, stream=None)
+LNB = dict(dtype=nn.BF16, M=4, D=64, dY=P, lddy=64, X=P, ldx=64, gamma=P, mean=P, rstd=P, dX=P, lddx=64, dgamma=P,
+           dbeta=P, ws=P, ws_bytes=1 << 30, stream=None)
+Q8 = dict(dtype=nn.BF16, rows=4, cols=64, X=P, ldx=64, Q=P, ldq=64, E=P, lde=2, stream=None)
+D8 = dict(dtype=nn.BF16, rows=4, cols=64, Q=P, ldq=64, E=P, lde=2, Y=P, ldy=64, stream=None)
+W8 = dict(dtype=nn.BF16, N=64, K=64, B=16, dY=P, ldy=64, Q=P, ldq=64, E=P, lde=2, dW=P, lddw=64, db=P, ws=P,
+          ws_bytes=1 << 30, err=None, stream=None)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(dtype=nn.F32X3), dict(dtype=9), dict(X=None), dict(Y=None), dict(M=0), dict(M=-1), dict(D=0), dict(D=1 << 30),
+    dict(M=1 << 40), dict(ldx=63), dict(ldy=63), dict(eps=-1e-5), dict(eps=float("nan")), dict(eps=float("inf"))])
+def test_layernorm_refuses(bad):
+    _refused(nn.mlp_op_layernorm, LN, **bad)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(dtype=nn.F32X3), dict(dY=None), dict(X=None), dict(mean=None), dict(rstd=None), dict(dX=None), dict(M=0),
+    dict(D=0), dict(D=1 << 30), dict(lddy=63), dict(ldx=63), dict(lddx=63), dict(ws=None), dict(ws_bytes=0),
+    dict(ws_bytes=4 * 2 * 64 - 1), dict(ws=P + 2)])
+def test_layernorm_backward_refuses(bad):
+    _refused(nn.mlp_op_layernorm_backward, LNB, **bad)
+
+
+@pytest.mark.parametrize("bad", [dict(dtype=2), dict(X=None), dict(Q=None), dict(E=None), dict(rows=0), dict(cols=0),
+                                 dict(cols=1 << 40), dict(ldx=63), dict(ldq=63), dict(lde=1), dict(rows=-3)])
+def test_quant8_refuses(bad):
+    _refused(nn.mlp_op_quant8, Q8, **bad)
+
+
+@pytest.mark.parametrize("bad", [dict(dtype=2), dict(Y=None), dict(Q=None), dict(E=None), dict(rows=0), dict(cols=0),
+                                 dict(ldy=63), dict(ldq=63), dict(lde=1)])
+def test_dequant8_refuses(bad):
+    _refused(nn.mlp_op_dequant8, D8, **bad)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(dtype=nn.F32X3), dict(dY=None), dict(Q=None), dict(E=None), dict(dW=None), dict(ws=None), dict(N=0),
+    dict(K=0), dict(B=0), dict(B=1 << 40), dict(ldy=63), dict(ldy=65), dict(dY=P + 2), dict(ldq=63), dict(lde=1),
+    dict(lddw=63), dict(K=33, lddw=36), dict(lddw=66), dict(dW=P + 8), dict(ws_bytes=64 * 16 * 2 - 1), dict(ws=P + 8)])
+def test_wgrad8_refuses(bad):
+    _refused(nn.mlp_op_wgrad8, W8, **bad)
+
+
+def test_workspace_sizes():
+    for dt in (nn.F32, nn.BF16):
+        n = nn.mlp_op_layernorm_backward_workspace_bytes(dt, 65536, 1024)
+        assert n % (2 * 1024 * 4) == 0 and 1 <= n // (2 * 1024 * 4) <= 1216
+        assert nn.mlp_op_layernorm_backward_workspace_bytes(dt, 1, 8) == 2 * 8 * 4
+        # the values, 256-byte rounded, then the weight gradient's own
+        assert nn.mlp_op_wgrad8_workspace_bytes(dt, 64, 100, 10) >= 10 * 104 * (4 if dt == nn.F32 else 2)
+    for bad in ((2, 4, 4), (nn.BF16, 0, 4), (nn.BF16, 4, 0)):
+        assert nn.mlp_op_layernorm_backward_workspace_bytes(*bad) == 0
+        assert nn.mlp_op_wgrad8_workspace_bytes(*bad, 4) == 0
+    assert nn.mlp_op_wgrad8_workspace_bytes(nn.BF16, 1 << 30, 1 << 30, 1 << 30) == 0
