@@ -211,6 +211,37 @@ mlp_status mlp_op_quant8(int dtype, int64_t rows, int64_t cols, const void* X, i
 mlp_status mlp_op_dequant8(int dtype, int64_t rows, int64_t cols, const uint8_t* Q, int64_t ldq, const uint8_t* E,
                            int64_t lde, void* Y, int64_t ldy, void* stream);
 
+/* The gated feed-forward projection of a language-model block: both
+ * projections, the activation and the product in one kernel,
+ *   s = X W^T + b,  g = s[:, :F],  u = s[:, F:],  H = act(g) * u.
+ *   X [M, K] (ldx); W [2F, K] (ldw), the gate's F rows and then the up
+ *   projection's; b fp32 [2F], nullable; H [M, F] (ldh).
+ *   act: MLP_ACT_NONE, _RELU, _GELU_TANH or MLP_ACT_SILU (g / (1 + e^-g)).
+ * s is kept for the backward when S is set: in the dtype, S [M, 2F] (lds); or
+ * with SE set as an 8-bit checkpoint (mlp_op_quant8), S uint8 [M, 2F] the
+ * codes and SE uint8 [M, 2 ceil(F / 32)] (ldse) the scales, the gate's blocks
+ * first (gate and up half each as one matrix of F columns).  H comes from the
+ * fp32 sums, before s is rounded.  MLP_F32 or MLP_BF16; MLP_BF16 takes K, F
+ * and the leading dimensions (but ldse) in multiples of 8 and 16-byte aligned
+ * matrices (S codes: 8-byte).  M from one token on. */
+enum { MLP_ACT_SILU = 3 };   /* the gated operations only */
+mlp_status mlp_op_gated_linear(int dtype, int act, int64_t M, int64_t F, int64_t K, const void* X, int64_t ldx,
+                               const void* W, int64_t ldw, const float* b, void* H, int64_t ldh, void* S, int64_t lds,
+                               uint8_t* SE, int64_t ldse, uint32_t* err_dev, void* stream);
+
+/* Its vector-Jacobian product, through the down projection Y = H Wd^T that
+ * follows it (mlp_op_dgrad with the gate in the epilogue):
+ *   dH = dY Wd,  dS = [dH * u * act'(g) | dH * act(g)],  H = act(g) * u.
+ *   dY [M, N] (lddy); Wd [N, F] (ldw); S (lds), SE (ldse) what the forward
+ *   kept; dS [M, 2F] (ldds); H [M, F] (ldh), nullable: formed again from s,
+ *   so that it need not be kept for dWd = dY^T H.
+ * dX and the projections' gradients are mlp_op_dgrad(MLP_ACT_NONE) and
+ * mlp_op_wgrad (or _wgrad8) of dS and W with 2F output columns.  ReLU's
+ * derivative at 0 is 0.  Types and alignment as above, N a multiple of 8. */
+mlp_status mlp_op_gated_dgrad(int dtype, int act, int64_t M, int64_t N, int64_t F, const void* dY, int64_t lddy,
+                              const void* Wd, int64_t ldw, const void* S, int64_t lds, const uint8_t* SE, int64_t ldse,
+                              void* dS, int64_t ldds, void* H, int64_t ldh, uint32_t* err_dev, void* stream);
+
 /* mlp_op_wgrad with the layer's input kept as an 8-bit checkpoint:
  *   dW = dY^T X (fp32 [N, K], lddw), db = sum over rows of dY (nullable),
  *   dY [B, N] (ldy; MLP_F32 or MLP_BF16), X [B, K] the values of Q (ldq), E

@@ -19,6 +19,7 @@ MLP_OK = 0
 STATUS_NAMES = {0: "MLP_OK", 1: "MLP_ERR_ARG", 2: "MLP_ERR_SHAPE", 3: "MLP_ERR_DTYPE", 4: "MLP_ERR_CUDA",
                 5: "MLP_ERR_LABEL_RANGE", 6: "MLP_ERR_NONFINITE", 7: "MLP_ERR_STATE", 8: "MLP_ERR_TIMEOUT"}
 ACT_NONE, ACT_RELU, ACT_GELU_TANH = 0, 1, 2
+ACT_SILU = 3   # the gated operations only
 F32, BF16 = 0, 1
 F32X3 = 2   # op-level GEMM operands: fp32 as three bf16 planes [3][rows][ld]
 PLANE_P, PLANE_G, PLANE_M, PLANE_V = 0, 1, 2, 3
@@ -88,6 +89,10 @@ _SIGS = {
                                          _P]),
     "mlp_op_quant8": (_I32, [_I32, _I64, _I64, _P, _I64, _P, _I64, _P, _I64, _P]),
     "mlp_op_dequant8": (_I32, [_I32, _I64, _I64, _P, _I64, _P, _I64, _P, _I64, _P]),
+    "mlp_op_gated_linear": (_I32, [_I32, _I32, _I64, _I64, _I64, _P, _I64, _P, _I64, _P, _P, _I64, _P, _I64, _P, _I64,
+                                   _P, _P]),
+    "mlp_op_gated_dgrad": (_I32, [_I32, _I32, _I64, _I64, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P,
+                                  _I64, _P, _P]),
     "mlp_op_wgrad8_workspace_bytes": (_SZ, [_I32, _I64, _I64, _I64]),
     "mlp_op_wgrad8": (_I32, [_I32, _I64, _I64, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _SZ, _P, _P]),
     "mlp_op_wait_timeout_check": (_I32, [_c.c_uint64, _P, _P]),
@@ -358,6 +363,16 @@ def mlp_op_quant8(dtype, rows, cols, X, ldx, Q, ldq, E, lde, stream) -> None:
 
 def mlp_op_dequant8(dtype, rows, cols, Q, ldq, E, lde, Y, ldy, stream) -> None:
     _check(lib().mlp_op_dequant8(dtype, rows, cols, Q, ldq, E, lde, Y, ldy, stream))
+
+
+def mlp_op_gated_linear(dtype, act, M, F, K, X, ldx, W, ldw, b, H, ldh, S, lds, SE, ldse, err, stream) -> None:
+    _check(lib().mlp_op_gated_linear(dtype, act, M, F, K, X, ldx, W, ldw, b, H, ldh, S, lds, SE, ldse, err, stream))
+
+
+def mlp_op_gated_dgrad(dtype, act, M, N, F, dY, lddy, Wd, ldw, S, lds, SE, ldse, dS, ldds, H, ldh, err,
+                       stream) -> None:
+    _check(lib().mlp_op_gated_dgrad(dtype, act, M, N, F, dY, lddy, Wd, ldw, S, lds, SE, ldse, dS, ldds, H, ldh, err,
+                                    stream))
 
 
 def mlp_op_wgrad8_workspace_bytes(dtype, N, K, B) -> int:

@@ -120,11 +120,6 @@ struct Dequant8Params {
   int units;
 };
 
-// 2^(byte - 127); every byte stands for a scale (0 for fp32's subnormal 2^-127).
-__device__ __forceinline__ float scale_of(uint32_t byte) {
-  return byte ? __uint_as_float(byte << 23) : __uint_as_float(0x00400000u);
-}
-
 template <typename T>
 __global__ void __launch_bounds__(256) dequant8_vec_kernel(const __grid_constant__ Dequant8Params p) {
   pdl_enter();
@@ -134,7 +129,7 @@ __global__ void __launch_bounds__(256) dequant8_vec_kernel(const __grid_constant
     const int c = (int)(i - row * p.units) * 8;
     const uint8_t* qr = p.q + row * p.ldq + c;
     T* yr = reinterpret_cast<T*>(p.y) + row * p.ldy + c;
-    const float s = scale_of(p.e[row * p.lde + (c >> 5)]);
+    const float s = q8_scale(p.e[row * p.lde + (c >> 5)]);
     float v[8];
     if (c + 8 <= p.cols) {
       const uint2 w = *reinterpret_cast<const uint2*>(qr);
@@ -142,11 +137,7 @@ __global__ void __launch_bounds__(256) dequant8_vec_kernel(const __grid_constant
       q8_unpack(w.y, s, v + 4);
       store8(yr, v);
     } else {
-      for (int j = 0; j < p.cols - c; ++j) {
-        float u[4];
-        q8_unpack(qr[j], s, u);
-        yr[j] = from_f32<T>(u[0]);
-      }
+      for (int j = 0; j < p.cols - c; ++j) yr[j] = from_f32<T>(q8_value(qr[j], p.e[row * p.lde + (c >> 5)]));
     }
   }
 }
@@ -160,9 +151,7 @@ __global__ void __launch_bounds__(256) dequant8_kernel(const __grid_constant__ D
     const int64_t row = i / p.units;
     const int b = (int)(i - row * p.units), c = b * 32 + lane;
     if (c >= p.cols) continue;
-    float u[4];
-    q8_unpack(p.q[row * p.ldq + c], scale_of(p.e[row * p.lde + b]), u);
-    reinterpret_cast<T*>(p.y)[row * p.ldy + c] = from_f32<T>(u[0]);
+    reinterpret_cast<T*>(p.y)[row * p.ldy + c] = from_f32<T>(q8_value(p.q[row * p.ldq + c], p.e[row * p.lde + b]));
   }
 }
 

@@ -51,5 +51,15 @@ __device__ __forceinline__ void q8_unpack(uint32_t w, float scale, float* v) {
   const float2 a = __half22float2(lo), b = __half22float2(hi);
   v[0] = a.x * scale; v[1] = a.y * scale; v[2] = b.x * scale; v[3] = b.y * scale;
 }
+// 2^(byte - 127) of a scale byte (0 stands for fp32's subnormal 2^-127; a
+// program may hand in scales below the encoder's).
+__device__ __forceinline__ float q8_scale(uint32_t byte) {
+  return byte ? __uint_as_float(byte << 23) : __uint_as_float(0x00400000u);
+}
+__device__ __forceinline__ float q8_value(uint32_t code, uint32_t byte) {
+  float v[4];
+  q8_unpack(code, q8_scale(byte), v);
+  return v[0];
+}
 
 }  // namespace mlpk

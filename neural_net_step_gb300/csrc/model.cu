@@ -1648,6 +1648,60 @@ mlp_status mlp_op_dequant8(int dtype, int64_t rows, int64_t cols, const uint8_t*
   return run_ops(&r, 1, stream);
 }
 
+// Layout rules of the gated operations' matrices beyond their sizes.
+static const char* gated_layout(const GatedOp& op) {
+  if (op.lda < op.K || op.ldb < (op.fwd ? op.K : op.F) || (op.h && op.ldh < op.F) || (op.s && op.lds < 2 * op.F) ||
+      (op.se && op.ldse < 2 * ceil_div(op.F, 32)) || (op.ds && op.ldds < 2 * op.F))
+    return "leading dimension too small";
+  if (op.dtype == MLP_F32) return nullptr;
+  auto off16 = [](const void* p, int64_t ld) { return (uintptr_t)p % 16 != 0 || ld % 8 != 0; };
+  if (op.F % 8 || op.K % 8) return "bf16: widths in multiples of 8";
+  if (off16(op.A, op.lda) || off16(op.B, op.ldb) || (op.h && off16(op.h, op.ldh)) || (op.ds && off16(op.ds, op.ldds)) ||
+      (op.s && !op.se && off16(op.s, op.lds)) || (op.se && ((uintptr_t)op.s % 8 || op.lds % 8)))
+    return "bf16: 16-byte aligned matrices and rows (codes: 8-byte)";
+  return nullptr;
+}
+static mlp_status run_gated(const GatedOp& op, void* stream) {
+  const int64_t top = INT32_MAX;
+  if (op.M < 1 || op.F < 1 || op.K < 1 || op.M > top || op.F > top / 2 || op.K > top)
+    return fail(MLP_ERR_SHAPE, "bad gated shape %lld x %lld x %lld", (long long)op.M, (long long)op.F, (long long)op.K);
+  if (const char* why = gated_layout(op)) return fail(MLP_ERR_SHAPE, "%s", why);
+  LaunchRec r;
+  char e_[512] = "";
+  if (gated_plan(op, &r, e_, sizeof(e_)) < 0) return fail(MLP_ERR_SHAPE, "%s", e_);
+  return run_ops(&r, 1, stream);
+}
+static bool gate_act_ok(int a) { return act_ok(a) || a == MLP_ACT_SILU; }
+
+mlp_status mlp_op_gated_linear(int dtype, int act, int64_t M, int64_t F, int64_t K, const void* X, int64_t ldx,
+                               const void* W, int64_t ldw, const float* b, void* H, int64_t ldh, void* S, int64_t lds,
+                               uint8_t* SE, int64_t ldse, uint32_t* err_dev, void* stream) {
+  if (!dtype_ok(dtype)) return fail(MLP_ERR_DTYPE, "bad dtype");
+  if (!gate_act_ok(act)) return fail(MLP_ERR_ARG, "bad activation");
+  if (!X || !W || !H || (SE && !S)) return fail(MLP_ERR_ARG, "null pointer");
+  GatedOp op;
+  op.dtype = dtype; op.act = act; op.fwd = true;
+  op.M = M; op.F = F; op.K = K;
+  op.A = X; op.lda = ldx; op.B = W; op.ldb = ldw; op.bias = b; op.h = H; op.ldh = ldh;
+  op.s = S; op.lds = lds; op.se = SE; op.ldse = ldse; op.err = err_dev;
+  return run_gated(op, stream);
+}
+
+mlp_status mlp_op_gated_dgrad(int dtype, int act, int64_t M, int64_t N, int64_t F, const void* dY, int64_t lddy,
+                              const void* Wd, int64_t ldw, const void* S, int64_t lds, const uint8_t* SE, int64_t ldse,
+                              void* dS, int64_t ldds, void* H, int64_t ldh, uint32_t* err_dev, void* stream) {
+  if (!dtype_ok(dtype)) return fail(MLP_ERR_DTYPE, "bad dtype");
+  if (!gate_act_ok(act)) return fail(MLP_ERR_ARG, "bad activation");
+  if (!dY || !Wd || !S || !dS) return fail(MLP_ERR_ARG, "null pointer");
+  GatedOp op;
+  op.dtype = dtype; op.act = act; op.fwd = false;
+  op.M = M; op.F = F; op.K = N;
+  op.A = dY; op.lda = lddy; op.B = Wd; op.ldb = ldw; op.h = H; op.ldh = ldh;
+  op.s = const_cast<void*>(S); op.lds = lds; op.se = const_cast<uint8_t*>(SE); op.ldse = ldse;
+  op.ds = dS; op.ldds = ldds; op.err = err_dev;
+  return run_gated(op, stream);
+}
+
 // The values of the checkpoint at the workspace's start (row pitch a multiple
 // of 8 elements, for TMA), the weight gradient's own workspace after them.
 static size_t wgrad8_values_bytes(int dtype, int64_t K, int64_t B) {

@@ -302,6 +302,25 @@ int quant8_plan(int dtype, int64_t rows, int64_t cols, const void* x, int64_t ld
 int dequant8_plan(int dtype, int64_t rows, int64_t cols, const uint8_t* q, int64_t ldq, const uint8_t* e, int64_t lde,
                   void* y, int64_t ldy, LaunchRec* rec, char* err, size_t errlen);
 
+// The gated feed-forward projection (gated.cu).  fwd: A = X [M, K], B = W
+// [2F, K], writes h [M, F] and, when set, s; else A = dY [M, K], B = Wd [K, F],
+// reads s, writes ds [M, 2F] and, when set, h.  s is [M, 2F] in the dtype, or
+// e4m3 codes with the scale bytes se [M, 2 ceil(F / 32)] (gate blocks first).
+struct GatedOp {
+  int dtype = 0, act = 0;
+  bool fwd = true;
+  int64_t M = 0, F = 0, K = 0;
+  const void* A = nullptr; int64_t lda = 0;
+  const void* B = nullptr; int64_t ldb = 0;
+  const float* bias = nullptr;
+  void* h = nullptr; int64_t ldh = 0;
+  void* s = nullptr; int64_t lds = 0;
+  uint8_t* se = nullptr; int64_t ldse = 0;
+  void* ds = nullptr; int64_t ldds = 0;
+  uint32_t* err = nullptr;
+};
+int gated_plan(const GatedOp& op, LaunchRec* rec, char* err, size_t errlen);
+
 // One thread waits, through the bounded wait every tcgen05 kernel uses, for
 // an mbarrier phase that nothing completes: after limit_ns it marks
 // ERRBIT_TIMEOUT in err_dev and returns (the error path, exercised).

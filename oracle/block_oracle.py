@@ -34,14 +34,20 @@ def layer_norm_vjp(dy, x, mean, rstd, gamma=None):
 
 
 # ---- the gated projection -------------------------------------------------
+def _sigmoid(t):
+    e = np.exp(-np.abs(t))
+    return np.where(t >= 0, 1.0, e) / (1.0 + e)
+
+
 def act(g, kind):
     if kind == ACT_NONE:
         return g
     if kind == ACT_RELU:
         return np.maximum(g, 0.0)
     if kind == ACT_SILU:
-        return g / (1.0 + np.exp(-g))
-    return 0.5 * g * (1.0 + np.tanh(np.sqrt(2.0 / np.pi) * (g + 0.044715 * g ** 3)))
+        return g * _sigmoid(g)
+    # 0.5 g (1 + tanh(c)) = g / (1 + e^{-2c}); 1 + tanh(c) itself would cancel far down the left tail
+    return g * _sigmoid(2.0 * np.sqrt(2.0 / np.pi) * (g + 0.044715 * g ** 3))
 
 
 def act_grad(g, kind):
@@ -50,11 +56,10 @@ def act_grad(g, kind):
     if kind == ACT_RELU:
         return (g > 0).astype(np.float64)
     if kind == ACT_SILU:
-        s = 1.0 / (1.0 + np.exp(-g))
-        return s + g * s * (1.0 - s)
-    c = np.sqrt(2.0 / np.pi)
-    t = np.tanh(c * (g + 0.044715 * g ** 3))
-    return 0.5 * (1.0 + t) + 0.5 * g * (1.0 - t * t) * c * (1.0 + 3 * 0.044715 * g * g)
+        return _sigmoid(g) + g * _sigmoid(g) * _sigmoid(-g)
+    c = 2.0 * np.sqrt(2.0 / np.pi)
+    t = c * (g + 0.044715 * g ** 3)
+    return _sigmoid(t) + g * _sigmoid(t) * _sigmoid(-t) * c * (1.0 + 3 * 0.044715 * g * g)
 
 
 def gated_linear(x, w, b, kind):
@@ -92,9 +97,8 @@ def q8_encode(x):
         fin = np.isfinite(v)
         top = np.where(fin, np.abs(v), 0.0).max(axis=1)
         k = np.full(rows, -120)
-        for r in range(rows):
-            while top[r] > 448.0 * 2.0 ** k[r]:
-                k[r] += 1
+        while np.any(top > 448.0 * 2.0 ** k.astype(np.float64)):
+            k += top > 448.0 * 2.0 ** k.astype(np.float64)
         e[:, b] = k + 127
         s = np.where(fin, np.abs(v), 0.0) * 2.0 ** -k.astype(np.float64)[:, None]
         hi = np.searchsorted(table, s)                     # first code whose value >= s

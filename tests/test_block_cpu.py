@@ -78,3 +78,35 @@ def test_workspace_sizes():
         assert nn.mlp_op_layernorm_backward_workspace_bytes(*bad) == 0
         assert nn.mlp_op_wgrad8_workspace_bytes(*bad, 4) == 0
     assert nn.mlp_op_wgrad8_workspace_bytes(nn.BF16, 1 << 30, 1 << 30, 1 << 30) == 0
+
+
+GF = dict(dtype=nn.BF16, act=nn.ACT_SILU, M=4, F=64, K=32, X=P, ldx=32, W=P, ldw=32, b=P, H=P, ldh=64, S=P, lds=128,
+          SE=None, ldse=4, err=None, stream=None)
+GB = dict(dtype=nn.BF16, act=nn.ACT_SILU, M=4, N=32, F=64, dY=P, lddy=32, Wd=P, ldw=64, S=P, lds=128, SE=None, ldse=4,
+          dS=P, ldds=128, H=P, ldh=64, err=None, stream=None)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(dtype=nn.F32X3), dict(act=4), dict(act=-1), dict(X=None), dict(W=None), dict(H=None), dict(S=None, SE=P),
+    dict(M=0), dict(F=0), dict(K=0), dict(M=1 << 33), dict(F=1 << 31), dict(K=1 << 33), dict(ldx=24), dict(ldw=24),
+    dict(ldh=56), dict(lds=120), dict(SE=P, ldse=3), dict(F=60), dict(K=28), dict(X=P + 2), dict(W=P + 8),
+    dict(H=P + 4), dict(S=P + 8), dict(SE=P, S=P + 4), dict(ldx=33), dict(ldw=36), dict(ldh=68), dict(lds=132),
+    dict(SE=P, lds=132)])
+def test_gated_linear_refuses(bad):
+    _refused(nn.mlp_op_gated_linear, GF, **bad)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(dtype=nn.F32X3), dict(act=4), dict(dY=None), dict(Wd=None), dict(S=None), dict(dS=None), dict(M=0), dict(N=0),
+    dict(F=0), dict(M=1 << 33), dict(F=1 << 31), dict(lddy=24), dict(ldw=56), dict(lds=120), dict(ldds=120),
+    dict(ldh=56), dict(SE=P, ldse=3), dict(F=60), dict(N=28), dict(dY=P + 2), dict(Wd=P + 8), dict(dS=P + 4),
+    dict(H=P + 8), dict(S=P + 2), dict(SE=P, S=P + 4), dict(ldds=132), dict(lddy=36)])
+def test_gated_dgrad_refuses(bad):
+    _refused(nn.mlp_op_gated_dgrad, GB, **bad)
+
+
+def test_silu_belongs_to_the_gated_operations():
+    with pytest.raises(nn.MlpError):
+        nn.mlp_op_linear_act(nn.BF16, nn.ACT_SILU, 4, 64, 64, P, 64, P, 64, P, P, 64, None, 0, None, None)
+    with pytest.raises(nn.MlpError):
+        nn.mlp_arena_bytes([8, 8, 4], None, nn.ACT_SILU, nn.F32, 4)

@@ -41,6 +41,16 @@ def test_gated_gradients_against_differences(kind):
     assert np.array_equal(h, bo.act(s[:, :11], kind) * s[:, 11:])
 
 
+def test_activations_are_the_textbook_ones():
+    g = np.linspace(-5, 5, 101)
+    gelu = 0.5 * g * (1 + np.tanh(np.sqrt(2 / np.pi) * (g + 0.044715 * g ** 3)))
+    assert np.abs(bo.act(g, bo.ACT_GELU_TANH) - gelu).max() < 1e-14
+    assert np.abs(bo.act(g, bo.ACT_SILU) - g / (1 + np.exp(-g))).max() < 1e-14
+    # far down the left tail: g e^{2c}, to first order in e^{2c} = 1e-17
+    c = np.sqrt(2 / np.pi) * (-6.5 - 0.044715 * 6.5 ** 3)
+    assert abs(bo.act(np.float64(-6.5), bo.ACT_GELU_TANH) / (-6.5 * np.exp(2 * c)) - 1) < 1e-13
+
+
 def test_gated_linear_is_two_projections():
     rng = np.random.default_rng(9)
     x, w, b = rng.normal(size=(3, 5)), rng.normal(size=(8, 5)), rng.normal(size=8)
