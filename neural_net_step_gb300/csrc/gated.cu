@@ -5,7 +5,7 @@
 //             dS = [dH * u * act'(g) | dH * act(g)], H = act(g) * u again.
 // s is kept for the backward in the dtype or in 8 bits (e4m3.cuh).
 //
-// On the FFMA pipes: 128 x 128 tiles, 8 x 8 results per thread, 16-deep
+// bf16 runs on the tensor cores (gated_tc.cu).  fp32 on the FFMA pipes: 128 x 128 tiles, 8 x 8 results per thread, 16-deep
 // slices through shared memory.  The forward's tile is 64 gate and the 64 up
 // columns that belong to them, so a thread holds both factors of its results.
 #include <stdio.h>
@@ -22,20 +22,20 @@ namespace mlpk {
 namespace {
 
 struct GatedParams {
-  const void* A; int64_t lda;      // X, or dY
-  const void* B; int64_t ldb;      // W [2F, K], or Wd [K, F]
+  const float* A; int64_t lda;      // X, or dY
+  const float* B; int64_t ldb;      // W [2F, K], or Wd [K, F]
   const float* bias;               // [2F] or null
-  void* h; int64_t ldh;            // (the backward's may be null)
+  float* h; int64_t ldh;           // (the backward's may be null)
   void* s; int64_t lds;            // kept pre-activations, or codes when se is set
   uint8_t* se; int64_t ldse;
-  void* ds; int64_t ldds;          // the backward's result
+  float* ds; int64_t ldds;         // the backward's result
   int M, F, K;
   int act;
 };
 
 constexpr int GT = 128, GK = 16;
 
-template <typename T, bool FWD>
+template <bool FWD>
 __global__ void __launch_bounds__(256) gated_simt_kernel(const __grid_constant__ GatedParams p) {
   pdl_enter();
   __shared__ __align__(16) float As[2][GK][GT + 4];
@@ -44,24 +44,24 @@ __global__ void __launch_bounds__(256) gated_simt_kernel(const __grid_constant__
   constexpr int TF = FWD ? GT / 2 : GT;   // F columns per tile
   const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
   const int m0 = blockIdx.y * GT, f0 = blockIdx.x * TF;
-  const T* A = reinterpret_cast<const T*>(p.A);
-  const T* B = reinterpret_cast<const T*>(p.B);
+  const float* A = p.A;
+  const float* B = p.B;
   float ra[PER], rb[PER];
   auto load = [&](int k0) {
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int idx = tid + i * 256, m = idx / GK, k = k0 + idx % GK;
-      ra[i] = (m0 + m < p.M && k < p.K) ? to_f32(A[(int64_t)(m0 + m) * p.lda + k]) : 0.f;
+      ra[i] = (m0 + m < p.M && k < p.K) ? A[(int64_t)(m0 + m) * p.lda + k] : 0.f;
     }
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int idx = tid + i * 256;
       if (FWD) {   // tile column n: gate row f0 + n, or up row F + f0 + n - 64
         const int n = idx / GK, k = k0 + idx % GK, f = f0 + (n & (TF - 1));
-        rb[i] = (f < p.F && k < p.K) ? to_f32(B[((int64_t)f + (n < TF ? 0 : p.F)) * p.ldb + k]) : 0.f;
+        rb[i] = (f < p.F && k < p.K) ? B[((int64_t)f + (n < TF ? 0 : p.F)) * p.ldb + k] : 0.f;
       } else {
         const int n = idx % GT, k = k0 + idx / GT;
-        rb[i] = (f0 + n < p.F && k < p.K) ? to_f32(B[(int64_t)k * p.ldb + f0 + n]) : 0.f;
+        rb[i] = (f0 + n < p.F && k < p.K) ? B[(int64_t)k * p.ldb + f0 + n] : 0.f;
       }
     }
   };
@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(256) gated_simt_kernel(const __grid_constant__
   // thread (ty, tx): rows ty*4 + 0..3 and 64 + ty*4 + 0..3; tile columns
   // tx*4 + 0..3 and 64 + tx*4 + 0..3 (the forward's second four are the up
   // columns of its first four)
-  T* h = reinterpret_cast<T*>(p.h);
+  float* h = p.h;
   const int64_t nb = q8_blocks(p.F);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -146,17 +146,17 @@ __global__ void __launch_bounds__(256) gated_simt_kernel(const __grid_constant__
           p.se[(int64_t)m * p.ldse + nb + (f >> 5)] = (uint8_t)(ku + 127);
         }
       } else if (p.s && row_ok) {
-        T* s = reinterpret_cast<T*>(p.s) + (int64_t)m * p.lds;
+        float* s = reinterpret_cast<float*>(p.s) + (int64_t)m * p.lds;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           if (f + j < p.F) {
-            s[f + j] = from_f32<T>(g[j]);
-            s[p.F + f + j] = from_f32<T>(u[j]);
+            s[f + j] = g[j];
+            s[p.F + f + j] = u[j];
           }
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if (row_ok && f + j < p.F) h[(int64_t)m * p.ldh + f + j] = from_f32<T>(gate_act(g[j], p.act) * u[j]);
+        if (row_ok && f + j < p.F) h[(int64_t)m * p.ldh + f + j] = gate_act(g[j], p.act) * u[j];
     } else if (row_ok) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -169,17 +169,17 @@ __global__ void __launch_bounds__(256) gated_simt_kernel(const __grid_constant__
           g = q8_value(q[f], e[0]);
           u = q8_value(q[p.F + f], e[nb]);
         } else {
-          const T* s = reinterpret_cast<const T*>(p.s) + (int64_t)m * p.lds;
-          g = to_f32(s[f]);
-          u = to_f32(s[p.F + f]);
+          const float* s = reinterpret_cast<const float*>(p.s) + (int64_t)m * p.lds;
+          g = s[f];
+          u = s[p.F + f];
         }
         float a, da;
         gate_act_grad(g, p.act, a, da);
         const float d = acc[i][j];
-        T* o = reinterpret_cast<T*>(p.ds) + (int64_t)m * p.ldds + f;
-        o[0] = from_f32<T>(d * u * da);
-        o[p.F] = from_f32<T>(d * a);
-        if (h) h[(int64_t)m * p.ldh + f] = from_f32<T>(a * u);
+        float* o = p.ds + (int64_t)m * p.ldds + f;
+        o[0] = d * u * da;
+        o[p.F] = d * a;
+        if (h) h[(int64_t)m * p.ldh + f] = a * u;
       }
     }
   }
@@ -192,13 +192,10 @@ int gated_plan(const GatedOp& op, LaunchRec* rec, char* err, size_t errlen) {
     snprintf(err, errlen, "bad gated shape M=%lld F=%lld K=%lld", (long long)op.M, (long long)op.F, (long long)op.K);
     return -1;
   }
-  GatedParams p{op.A, op.lda, op.B, op.ldb, op.bias, op.h, op.ldh, op.s, op.lds, op.se, op.ldse, op.ds, op.ldds,
-                (int)op.M, (int)op.F, (int)op.K, op.act};
-  const bool f32 = op.dtype == DT_F32;
-  rec->func = op.fwd ? (f32 ? (const void*)gated_simt_kernel<float, true>
-                            : (const void*)gated_simt_kernel<__nv_bfloat16, true>)
-                     : (f32 ? (const void*)gated_simt_kernel<float, false>
-                            : (const void*)gated_simt_kernel<__nv_bfloat16, false>);
+  if (op.dtype == DT_BF16) return gated_tc_plan(op, rec, err, errlen);
+  const GatedParams p{(const float*)op.A, op.lda, (const float*)op.B, op.ldb, op.bias, (float*)op.h, op.ldh,
+                      op.s, op.lds, op.se, op.ldse, (float*)op.ds, op.ldds, (int)op.M, (int)op.F, (int)op.K, op.act};
+  rec->func = op.fwd ? (const void*)gated_simt_kernel<true> : (const void*)gated_simt_kernel<false>;
   rec->grid = dim3((unsigned)ceil_div(op.F, op.fwd ? GT / 2 : GT), (unsigned)ceil_div(op.M, GT));
   if (rec->grid.y > 65535) {
     snprintf(err, errlen, "gated: %lld rows are too many", (long long)op.M);

@@ -320,6 +320,7 @@ struct GatedOp {
   uint32_t* err = nullptr;
 };
 int gated_plan(const GatedOp& op, LaunchRec* rec, char* err, size_t errlen);
+int gated_tc_plan(const GatedOp& op, LaunchRec* rec, char* err, size_t errlen);   // bf16 (gated_tc.cu)
 
 // One thread waits, through the bounded wait every tcgen05 kernel uses, for
 // an mbarrier phase that nothing completes: after limit_ns it marks
