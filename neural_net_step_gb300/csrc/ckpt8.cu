@@ -78,7 +78,10 @@ __global__ void __launch_bounds__(256) quant8_vec_kernel(const __grid_constant__
     }
     uint32_t m = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, q8_mag(v[j]));
+    for (int j = 0; j < 8; ++j) {
+      m = max(m, q8_mag(v[j]));
+      v[j] = q8_no_inf(v[j]);
+    }
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
     const int k = q8_exponent(m);
@@ -107,7 +110,7 @@ __global__ void __launch_bounds__(256) quant8_kernel(const __grid_constant__ Qua
     const int b = (int)(i - row * p.units), c = b * 32 + lane;
     const float v = c < p.cols ? to_f32(reinterpret_cast<const T*>(p.x)[row * p.ldx + c]) : 0.f;
     const int k = q8_exponent(__reduce_max_sync(0xffffffffu, q8_mag(v)));
-    if (c < p.cols) p.q[row * p.ldq + c] = (uint8_t)q8_pack(v * q8_pow2(-k), 0.f, 0.f, 0.f);
+    if (c < p.cols) p.q[row * p.ldq + c] = (uint8_t)q8_pack(q8_no_inf(v) * q8_pow2(-k), 0.f, 0.f, 0.f);
     if (lane == 0) p.e[row * p.lde + b] = (uint8_t)(k + 127);
   }
 }

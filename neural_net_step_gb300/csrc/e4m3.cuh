@@ -33,16 +33,15 @@ __device__ __forceinline__ int q8_exponent(uint32_t amax_bits) {
 }
 __device__ __forceinline__ float q8_pow2(int k) { return __uint_as_float((uint32_t)(k + 127) << 23); }
 
-// Four codes from four scaled values (x * 2^-k; non-finite ones to NaN).
+// Four codes from four scaled values (x * 2^-k); NaN becomes NaN, but an
+// infinity 448: values that may hold one go through q8_no_inf first.
 __device__ __forceinline__ uint32_t q8_pack(float a, float b, float c, float d) {
-  const float inf = __uint_as_float(0x7f800000u), nan = __uint_as_float(0x7fffffffu);
-  a = fabsf(a) == inf ? nan : a;
-  b = fabsf(b) == inf ? nan : b;
-  c = fabsf(c) == inf ? nan : c;
-  d = fabsf(d) == inf ? nan : d;
   const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
   const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
   return lo | (hi << 16);
+}
+__device__ __forceinline__ float q8_no_inf(float x) {
+  return (__float_as_uint(x) & 0x7fffffffu) == 0x7f800000u ? __uint_as_float(0x7fffffffu) : x;
 }
 // The values of four codes, times `scale` = 2^k.
 __device__ __forceinline__ void q8_unpack(uint32_t w, float scale, float* v) {

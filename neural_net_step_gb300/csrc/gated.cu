@@ -124,7 +124,10 @@ __global__ void __launch_bounds__(256) gated_simt_kernel(const __grid_constant__
         // the eight threads of a 32-column block are neighbours
         uint32_t mg = 0, mu = 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) { mg = max(mg, q8_mag(g[j])); mu = max(mu, q8_mag(u[j])); }
+        for (int j = 0; j < 4; ++j) {
+          mg = max(mg, q8_mag(g[j]));
+          mu = max(mu, q8_mag(u[j]));
+        }
 #pragma unroll
         for (int o = 1; o < 8; o <<= 1) {
           mg = max(mg, __shfl_xor_sync(0xffffffffu, mg, o));
@@ -132,8 +135,10 @@ __global__ void __launch_bounds__(256) gated_simt_kernel(const __grid_constant__
         }
         const int kg = q8_exponent(mg), ku = q8_exponent(mu);
         const float sg = q8_pow2(-kg), su = q8_pow2(-ku);
-        const uint32_t cg = q8_pack(g[0] * sg, g[1] * sg, g[2] * sg, g[3] * sg);
-        const uint32_t cu = q8_pack(u[0] * su, u[1] * su, u[2] * su, u[3] * su);
+        const uint32_t cg = q8_pack(q8_no_inf(g[0]) * sg, q8_no_inf(g[1]) * sg, q8_no_inf(g[2]) * sg,
+                                    q8_no_inf(g[3]) * sg);
+        const uint32_t cu = q8_pack(q8_no_inf(u[0]) * su, q8_no_inf(u[1]) * su, q8_no_inf(u[2]) * su,
+                                    q8_no_inf(u[3]) * su);
         uint8_t* q = reinterpret_cast<uint8_t*>(p.s) + (int64_t)m * p.lds;
 #pragma unroll
         for (int j = 0; j < 4; ++j)

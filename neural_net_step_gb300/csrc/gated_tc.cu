@@ -32,20 +32,27 @@
 namespace mlpk {
 namespace tc {
 
-constexpr int GT_EPI_WARPS = 8;
-constexpr int GT_THREADS = 64 + 32 * GT_EPI_WARPS;   // producer warp, MMA warp, 8 epilogue warps
+// Producer warp, MMA warp, 16 epilogue warps.  The epilogues do 20 to 30
+// instructions per element with little to overlap inside a warp: with 8 warps
+// (2 per scheduler) the backward issued in a third of the cycles.
+constexpr int GT_EPI_WARPS = 16;
+constexpr int GT_THREADS = 64 + 32 * GT_EPI_WARPS;
 
-// Stages of 32 KB and the epilogue's staging per warp.  Forward: two 32 x 64
-// boxes (4 KB) that the stores of g, u and h take in turn.  Backward: two
-// sets of three 32 x 32 boxes (2 KB) for dg, du and h.
+// Stages of 32 KB, and per epilogue warp three boxes of 32 rows x 32 bf16
+// (2 KB).  A lane computes along its own row (that is how TMEM is read), but
+// a warp's global accesses go row by row, four lanes to the 64 bytes of a row:
+// the boxes turn one into the other.  (Lanes reading or writing their own rows
+// cost 32 cache lines per instruction; bulk-tensor stores of 64-byte rows,
+// tried before, kept the TMA unit busy that the main loop needs: 218 us for
+// the GELU backward at 16384 x 4096 x 1024.)
 template <bool FWD> struct GtCfg {
   static constexpr int TBM = 2 * BM;
   static constexpr int TF = FWD ? 128 : 256;             // F columns per tile
   static constexpr int A_BYTES = BM * BK * 2;
   static constexpr int B_BYTES = 128 * BK * 2;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int STAGES = FWD ? 5 : 4;
-  static constexpr int EPI_WARP_BYTES = FWD ? 2 * 4096 : 6 * 2048;
+  static constexpr int STAGES = 4;
+  static constexpr int EPI_WARP_BYTES = 3 * 2048;
   static constexpr int EPI_BYTES = GT_EPI_WARPS * EPI_WARP_BYTES;
   static constexpr int ACC_COLS = 256;
   static constexpr int TMEM_COLS = 2 * ACC_COLS;
@@ -56,27 +63,39 @@ template <bool FWD> struct GtCfg {
 struct GtParams {
   CUtensorMap tmA;       // X or dY, box {64, 128}
   CUtensorMap tmB;       // W, box {64, 128}; Wd (MN-major), box {64, 64}
-  CUtensorMap tmG, tmU;  // forward: the halves of S (bf16); backward: of dS
-  CUtensorMap tmH;
   int M, F, K;
   int num_kb, tiles_m, tiles_f, num_tiles, m_fast;
-  int act;
-  int keep;              // forward: S in bf16 is wanted
-  int want_h;            // backward: H is wanted
   uint32_t idesc;
   const float* bias;
-  const __nv_bfloat16* s; int64_t lds;   // backward: kept in bf16
+  __nv_bfloat16* h; int64_t ldh;         // (the backward's may be null)
+  __nv_bfloat16* s; int64_t lds;         // kept in bf16 (null: in 8 bits, or not at all)
+  __nv_bfloat16* ds; int64_t ldds;       // backward
   uint8_t* q; int64_t ldq;               // codes (forward writes, backward reads)
   uint8_t* e; int64_t lde;
   int nb;                                // scale bytes of half a row
   uint32_t* err;
 };
 
-// 32 values (one row's block) as an 8-bit checkpoint: 8 words of codes; the scale byte is returned.
+// 32 values (one row's block) as an 8-bit checkpoint: 8 words of codes; the
+// scale byte is returned.  The maximum of the magnitudes skips NaN by itself;
+// a block that holds an infinity takes the long way.
 __device__ __forceinline__ uint32_t q8_block(const float* v, uint32_t (&w)[8]) {
-  uint32_t m = 0;
+  float a[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int j = 0; j < 32; ++j) m = max(m, q8_mag(v[j]));
+  for (int j = 0; j < 32; ++j) a[j & 3] = fmaxf(a[j & 3], fabsf(v[j]));
+  uint32_t m = __float_as_uint(fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])));
+  if (m >= 0x7f800000u) {
+    m = 0;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) m = max(m, q8_mag(v[j]));
+    const int k = q8_exponent(m);
+    const float s = q8_pow2(-k);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      w[j] = q8_pack(q8_no_inf(v[4 * j]) * s, q8_no_inf(v[4 * j + 1]) * s, q8_no_inf(v[4 * j + 2]) * s,
+                     q8_no_inf(v[4 * j + 3]) * s);
+    return (uint32_t)(k + 127);
+  }
   const int k = q8_exponent(m);
   const float s = q8_pow2(-k);
 #pragma unroll
@@ -84,7 +103,40 @@ __device__ __forceinline__ uint32_t q8_block(const float* v, uint32_t (&w)[8]) {
   return (uint32_t)(k + 127);
 }
 
-template <bool FWD, bool Q8>
+// Byte offset of 16-byte unit j of row r in a box (64-byte rows; units
+// exchanged so that neither 8 rows' units j nor 2 whole rows share banks), and
+// of 8-byte unit j of row r in a box of codes (32-byte rows).
+__device__ __forceinline__ int box_at(int r, int j) { return r * 64 + ((j ^ ((r >> 1) & 3)) << 4); }
+__device__ __forceinline__ int code_at(int r, int j) { return r * 32 + ((j ^ ((r >> 2) & 3)) << 3); }
+
+// A lane's 32 values in bf16 into its row of a box.
+__device__ __forceinline__ void stage_row32(uint8_t* box, int lane, const float* v) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint32_t w[4];
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      const __nv_bfloat162 b2 = __floats2bfloat162_rn(v[8 * j + 2 * h], v[8 * j + 2 * h + 1]);
+      w[h] = *reinterpret_cast<const uint32_t*>(&b2);
+    }
+    *reinterpret_cast<uint4*>(box + box_at(lane, j)) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+// A box to rows m, m + 1, .. of a matrix at column f, clipped at M and F (F a
+// multiple of 8): lane l moves units l % 4 of rows l / 4, l / 4 + 8, ..
+__device__ __forceinline__ void store_box(const uint8_t* box, int lane, __nv_bfloat16* out, int64_t ld, int m, int M,
+                                          int f, int F) {
+  const int j = lane & 3;
+  if (f + 8 * j >= F) return;
+  __nv_bfloat16* o = out + f + 8 * j;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 8 * i + (lane >> 2);
+    if (m + r < M) *reinterpret_cast<uint4*>(o + (int64_t)(m + r) * ld) = *reinterpret_cast<const uint4*>(box + box_at(r, j));
+  }
+}
+
+template <bool FWD, bool Q8, int ACT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT_THREADS, 1)
 gated_cg2_kernel(const __grid_constant__ GtParams p) {
   using C = GtCfg<FWD>;
@@ -140,7 +192,6 @@ gated_cg2_kernel(const __grid_constant__ GtParams p) {
     if (lane == 0) {
       prefetch_tmap(&p.tmA);
       prefetch_tmap(&p.tmB);
-      if (FWD || p.want_h) prefetch_tmap(&p.tmH);
       int it = 0;
       bool ok = true;
       for (int t = t0; t < p.num_tiles && ok; t += tstep) {
@@ -199,34 +250,65 @@ gated_cg2_kernel(const __grid_constant__ GtParams p) {
       }
     }
   } else {
-    // ---------------- epilogue warps 2..9: this CTA's 128 rows ----------------
+    // ---------------- epilogue warps 2..17: this CTA's 128 rows ----------------
     // warp w reads TMEM lanes 32 (w % 4) .. +31: lane l owns tile row
-    // 32 (w % 4) + l, in the columns of its half of the tile
+    // 32 (w % 4) + l, in the columns of its quarter of the tile
     const int q = warp & 3;
-    const int half = (warp - 2) >> 2;
+    const int quarter = (warp - 2) >> 2;
     const uint32_t stage0 = epi_base + (uint32_t)((warp - 2) * C::EPI_WARP_BYTES);
-    uint8_t* stage_ptr = base_ptr + (stage0 - base);
+    uint8_t* box0 = base_ptr + (stage0 - base);
+    uint8_t* box1 = box0 + 2048;
+    uint8_t* box2 = box0 + 4096;
+    const int lr = lane >> 2, lj = lane & 3;   // a lane's row and unit in row-by-row accesses
     int tc = 0;
     bool ok = true;
-    if (FWD) {
-      for (int t = t0; t < p.num_tiles && ok; t += tstep, ++tc) {
-        int m0, f0;
-        origin(t, m0, f0);
-        const int buf = tc & 1;
-        const int f = f0 + half * 64, gm = m0 + q * 32 + lane;
-        const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * C::ACC_COLS + half * 64);
-        // the chunk's bias (lane j: columns j and 32 + j), before the accumulator wait
-        float bg0 = 0.f, bg1 = 0.f, bu0 = 0.f, bu1 = 0.f;
-        if (p.bias) {
-          if (f + lane < p.F) { bg0 = __ldg(p.bias + f + lane); bu0 = __ldg(p.bias + p.F + f + lane); }
-          if (f + 32 + lane < p.F) { bg1 = __ldg(p.bias + f + 32 + lane); bu1 = __ldg(p.bias + p.F + f + 32 + lane); }
+    // backward: the kept g and u of a 32-column chunk, fetched a chunk ahead
+    // row by row: lane l holds units l % 4 (8 columns) of rows l / 4 + 8 i, and
+    // the scale bytes of its own row
+    constexpr int NW = FWD ? 1 : Q8 ? 8 : 16;
+    uint32_t ng[NW], nu[NW];
+    uint32_t ne = 0x7f7fu;
+    auto fetch = [&](int m, int f) {   // rows m .., columns f ..
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = m + 8 * i + lr, c = f + 8 * lj;
+        const bool in = r < p.M && c < p.F;   // (F is a multiple of 8)
+        if constexpr (Q8 && !FWD) {
+          const uint8_t* qr = p.q + (int64_t)r * p.ldq + c;
+          const uint2 a = in ? __ldg(reinterpret_cast<const uint2*>(qr)) : make_uint2(0u, 0u);
+          const uint2 b = in ? __ldg(reinterpret_cast<const uint2*>(qr + p.F)) : make_uint2(0u, 0u);
+          ng[2 * i] = a.x; ng[2 * i + 1] = a.y;
+          nu[2 * i] = b.x; nu[2 * i + 1] = b.y;
+        } else if constexpr (!FWD) {
+          const __nv_bfloat16* sr = p.s + (int64_t)r * p.lds + c;
+          const uint4 a = in ? __ldg(reinterpret_cast<const uint4*>(sr)) : make_uint4(0u, 0u, 0u, 0u);
+          const uint4 b = in ? __ldg(reinterpret_cast<const uint4*>(sr + p.F)) : make_uint4(0u, 0u, 0u, 0u);
+          ng[4 * i] = a.x; ng[4 * i + 1] = a.y; ng[4 * i + 2] = a.z; ng[4 * i + 3] = a.w;
+          nu[4 * i] = b.x; nu[4 * i + 1] = b.y; nu[4 * i + 2] = b.z; nu[4 * i + 3] = b.w;
         }
+      }
+      if (Q8 && m + lane < p.M && f < p.F) {
+        const uint8_t* er = p.e + (int64_t)(m + lane) * p.lde + (f >> 5);
+        ne = (uint32_t)__ldg(er) | ((uint32_t)__ldg(er + p.nb) << 8);
+      }
+    };
+    for (int t = t0; t < p.num_tiles && ok; t += tstep, ++tc) {
+      int m0, f0;
+      origin(t, m0, f0);
+      m0 += q * 32;   // this warp's rows
+      const int buf = tc & 1;
+      const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * C::ACC_COLS);
+      if constexpr (FWD) {
+        // 32 columns: gate and up
+        const int f = f0 + quarter * 32;
+        float bg = 0.f, bu = 0.f;   // lane j: the bias of column j, before the accumulator wait
+        if (p.bias && f + lane < p.F) { bg = __ldg(p.bias + f + lane); bu = __ldg(p.bias + p.F + f + lane); }
         ok = __all_sync(0xffffffffu, mbar_wait_cluster(tfull_bar(buf), ((uint32_t)tc >> 1) & 1u, p.err));
         if (!ok) break;
         tc_fence_after();
-        float g[64], u[64];
-        tmem_ld64(trow, g);
-        tmem_ld64(trow + 128u, u);
+        float g[32], u[32];
+        tmem_ld32(trow, g, quarter * 32);
+        tmem_ld32(trow, u, 128 + quarter * 32);
         // this warp's part of the accumulator is in registers: hand it back to CTA 0
         tc_fence_before();
         __syncwarp();
@@ -235,164 +317,127 @@ gated_cg2_kernel(const __grid_constant__ GtParams p) {
         if (p.bias) {
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
-            g[j] += __shfl_sync(0xffffffffu, bg0, j);
-            g[32 + j] += __shfl_sync(0xffffffffu, bg1, j);
-            u[j] += __shfl_sync(0xffffffffu, bu0, j);
-            u[32 + j] += __shfl_sync(0xffffffffu, bu1, j);
+            g[j] += __shfl_sync(0xffffffffu, bg, j);
+            u[j] += __shfl_sync(0xffffffffu, bu, j);
           }
         }
-        uint8_t* srow = stage_ptr + lane * 128;
-        if (Q8) {
-          // a lane's 64 columns are two whole blocks (columns beyond F hold
-          // the next rows of W: they count as 0)
+        if constexpr (Q8) {
+          // a lane's 32 columns are one block (columns beyond F hold the
+          // next rows of W: they count as 0)
+          if (f + 32 > p.F) {
 #pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            const int fb = f + 32 * b;
-            if (fb + 32 > p.F) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (fb + j >= p.F) g[32 * b + j] = u[32 * b + j] = 0.f;
-            }
-#pragma unroll
-            for (int part = 0; part < 2; ++part) {
-              uint32_t w[8];
-              const uint32_t byte = q8_block((part ? u : g) + 32 * b, w);
-              if (gm < p.M && fb < p.F) {
-                uint8_t* qr = p.q + (int64_t)gm * p.ldq + (int64_t)part * p.F + fb;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)   // (F is a multiple of 8)
-                  if (fb + 8 * j < p.F) *reinterpret_cast<uint2*>(qr + 8 * j) = make_uint2(w[2 * j], w[2 * j + 1]);
-                p.e[(int64_t)gm * p.lde + part * p.nb + (fb >> 5)] = (uint8_t)byte;
-              }
-            }
+            for (int j = 0; j < 32; ++j)
+              if (f + j >= p.F) g[j] = u[j] = 0.f;
           }
-        } else if (p.keep) {
-          // g and u through the two staging boxes and TMA stores (which clip the ragged edges)
-          if (lane == 0) bulk_wait_read0();
-          __syncwarp();
-          stage_plane(srow, lane, g, false);
-          stage_plane(srow + 4096, lane, u, false);
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            tma_store_2d(&p.tmG, stage0, f, m0 + q * 32);
-            bulk_commit();
-            tma_store_2d(&p.tmU, stage0 + 4096u, f, m0 + q * 32);
-            bulk_commit();
+#pragma unroll
+          for (int part = 0; part < 2; ++part) {
+            uint32_t w[8];
+            const uint32_t byte = q8_block(part ? u : g, w);
+            uint8_t* box = part ? box2 : box1;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              *reinterpret_cast<uint2*>(box + code_at(lane, j)) = make_uint2(w[2 * j], w[2 * j + 1]);
+            if (m0 + lane < p.M) p.e[(int64_t)(m0 + lane) * p.lde + part * p.nb + (f >> 5)] = (uint8_t)byte;
           }
+        } else if (p.s) {
+          stage_row32(box1, lane, g);
+          stage_row32(box2, lane, u);
         }
-        if (p.act == ACT_SILU) {
 #pragma unroll
-          for (int j = 0; j < 64; ++j) g[j] = gate_act(g[j], ACT_SILU) * u[j];
-        } else if (p.act == ACT_GELU_TANH) {
-#pragma unroll
-          for (int j = 0; j < 64; ++j) g[j] = gelu_tanh(g[j]) * u[j];
-        } else if (p.act == ACT_RELU) {
-#pragma unroll
-          for (int j = 0; j < 64; ++j) g[j] = fmaxf(g[j], 0.f) * u[j];
-        } else {
-#pragma unroll
-          for (int j = 0; j < 64; ++j) g[j] *= u[j];
-        }
-        // h through the first box, free once g's store (or the last tile's) has read it
-        if (lane == 0) {
-          if (!Q8 && p.keep) bulk_wait_read1();
-          else bulk_wait_read0();
-        }
+        for (int j = 0; j < 32; ++j) g[j] = gate_act(g[j], ACT) * u[j];
+        stage_row32(box0, lane, g);
         __syncwarp();
-        stage_plane(srow, lane, g, false);
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          tma_store_2d(&p.tmH, stage0, f, m0 + q * 32);
-          bulk_commit();
-        }
-      }
-    } else {
-      int set = 0;
-      for (int t = t0; t < p.num_tiles && ok; t += tstep, ++tc) {
-        int m0, f0;
-        origin(t, m0, f0);
-        const int buf = tc & 1;
-        const int gm = m0 + q * 32 + lane;
-        const bool row_ok = gm < p.M;
-        const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * C::ACC_COLS + half * 128);
-        // the kept g and u of 32 columns: bf16 pairs (16 words each) or codes (8 words each) and scales
-        constexpr int NW = Q8 ? 8 : 16;
-        uint32_t ng[NW], nu[NW];
-        uint32_t ne = 0;
-        auto fetch = [&](int c) {
-          const int f = f0 + half * 128 + c;
-          ne = 0x7f7fu;
+        store_box(box0, lane, p.h, p.ldh, m0, p.M, f, p.F);
+        if constexpr (Q8) {
+          if (f + 8 * lj < p.F) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {   // eight columns at a time (F is a multiple of 8)
-            const bool in = row_ok && f + 8 * j < p.F;
-            if (Q8) {
-              const uint8_t* qr = p.q + (int64_t)gm * p.ldq + f + 8 * j;
-              const uint2 a = in ? __ldg(reinterpret_cast<const uint2*>(qr)) : make_uint2(0u, 0u);
-              const uint2 b = in ? __ldg(reinterpret_cast<const uint2*>(qr + p.F)) : make_uint2(0u, 0u);
-              ng[2 * j] = a.x; ng[2 * j + 1] = a.y;
-              nu[2 * j] = b.x; nu[2 * j + 1] = b.y;
-            } else {
-              const __nv_bfloat16* sr = p.s + (int64_t)gm * p.lds + f + 8 * j;
-              const uint4 a = in ? __ldg(reinterpret_cast<const uint4*>(sr)) : make_uint4(0u, 0u, 0u, 0u);
-              const uint4 b = in ? __ldg(reinterpret_cast<const uint4*>(sr + p.F)) : make_uint4(0u, 0u, 0u, 0u);
-              ng[(4 * j) % NW] = a.x; ng[(4 * j + 1) % NW] = a.y; ng[(4 * j + 2) % NW] = a.z; ng[(4 * j + 3) % NW] = a.w;
-              nu[(4 * j) % NW] = b.x; nu[(4 * j + 1) % NW] = b.y; nu[(4 * j + 2) % NW] = b.z; nu[(4 * j + 3) % NW] = b.w;
+            for (int i = 0; i < 4; ++i) {
+              const int r = 8 * i + lr;
+              if (m0 + r >= p.M) continue;
+              uint8_t* o = p.q + (int64_t)(m0 + r) * p.ldq + f + 8 * lj;
+              *reinterpret_cast<uint2*>(o) = *reinterpret_cast<const uint2*>(box1 + code_at(r, lj));
+              *reinterpret_cast<uint2*>(o + p.F) = *reinterpret_cast<const uint2*>(box2 + code_at(r, lj));
             }
           }
-          if (Q8 && row_ok && f < p.F) {
-            const uint8_t* er = p.e + (int64_t)gm * p.lde + (f >> 5);
-            ne = (uint32_t)__ldg(er) | ((uint32_t)__ldg(er + p.nb) << 8);
-          }
-        };
-        fetch(0);
+        } else if (p.s) {
+          store_box(box1, lane, p.s, p.lds, m0, p.M, f, p.F);
+          store_box(box2, lane, p.s + p.F, p.lds, m0, p.M, f, p.F);
+        }
+        __syncwarp();   // the boxes are read before the next tile fills them
+      } else {
+        if (tc == 0) fetch(m0, f0 + quarter * 64);
         ok = __all_sync(0xffffffffu, mbar_wait_cluster(tfull_bar(buf), ((uint32_t)tc >> 1) & 1u, p.err));
         if (!ok) break;
         tc_fence_after();
 #pragma unroll 1
-        for (int c = 0; c < 128; c += 32) {
-          const int f = f0 + half * 128 + c;
+        for (int c = 0; c < 64; c += 32) {   // 64 columns, 32 at a time
+          const int f = f0 + quarter * 64 + c;
+          // the fetched units into the boxes, their own rows out of them below
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if constexpr (Q8) {
+              *reinterpret_cast<uint2*>(box0 + code_at(8 * i + lr, lj)) = make_uint2(ng[2 * i], ng[2 * i + 1]);
+              *reinterpret_cast<uint2*>(box1 + code_at(8 * i + lr, lj)) = make_uint2(nu[2 * i], nu[2 * i + 1]);
+            } else {
+              *reinterpret_cast<uint4*>(box0 + box_at(8 * i + lr, lj)) =
+                  make_uint4(ng[4 * i], ng[4 * i + 1], ng[4 * i + 2], ng[4 * i + 3]);
+              *reinterpret_cast<uint4*>(box1 + box_at(8 * i + lr, lj)) =
+                  make_uint4(nu[4 * i], nu[4 * i + 1], nu[4 * i + 2], nu[4 * i + 3]);
+            }
+          }
+          const float eg = q8_scale(ne & 0xffu), eu = q8_scale(ne >> 8);
+          __syncwarp();
           float d[32];
-          tmem_ld32(trow, d, c);
-          if (c == 96) {
+          tmem_ld32(trow, d, quarter * 64 + c);
+          if (c == 0) {
+            fetch(m0, f + 32);
+          } else {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(lead_tempty0 + 8u * (uint32_t)buf);
+            if (t + tstep < p.num_tiles) {
+              int m1, f1;
+              origin(t + tstep, m1, f1);
+              fetch(m1 + q * 32, f1 + quarter * 64);
+            }
           }
-          if (f >= p.F) continue;   // wholly beyond F
-          uint32_t cg[NW], cu[NW];
+          uint32_t cg[Q8 ? 8 : 1], cu[Q8 ? 8 : 1];
+          if constexpr (Q8) {   // all of the row's codes, before results take their place
 #pragma unroll
-          for (int j = 0; j < NW; ++j) { cg[j] = ng[j]; cu[j] = nu[j]; }
-          const float eg = q8_scale(ne & 0xffu), eu = q8_scale(ne >> 8);
-          if (c < 96) fetch(c + 32);
-          // the staging set of two chunks ago is free
-          if (lane == 0) bulk_wait_read1();
-          __syncwarp();
-          uint8_t* srow = stage_ptr + set * 6144 + lane * 64;
+            for (int j = 0; j < 4; ++j) {
+              const uint2 a = *reinterpret_cast<const uint2*>(box0 + code_at(lane, j));
+              const uint2 b = *reinterpret_cast<const uint2*>(box1 + code_at(lane, j));
+              cg[2 * j] = a.x; cg[2 * j + 1] = a.y;
+              cu[2 * j] = b.x; cu[2 * j + 1] = b.y;
+            }
+            __syncwarp();
+          }
 #pragma unroll
           for (int j = 0; j < 4; ++j) {   // eight columns: one 16-byte unit of each box
             float g[8], u[8];
-            if (Q8) {
+            if constexpr (Q8) {
               q8_unpack(cg[2 * j], eg, g);
               q8_unpack(cg[2 * j + 1], eg, g + 4);
               q8_unpack(cu[2 * j], eu, u);
               q8_unpack(cu[2 * j + 1], eu, u + 4);
             } else {
+              const uint4 a = *reinterpret_cast<const uint4*>(box0 + box_at(lane, j));
+              const uint4 b = *reinterpret_cast<const uint4*>(box1 + box_at(lane, j));
+              const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
               for (int h = 0; h < 4; ++h) {
-                g[2 * h] = __uint_as_float(cg[(4 * j + h) % NW] << 16);
-                g[2 * h + 1] = __uint_as_float(cg[(4 * j + h) % NW] & 0xFFFF0000u);
-                u[2 * h] = __uint_as_float(cu[(4 * j + h) % NW] << 16);
-                u[2 * h + 1] = __uint_as_float(cu[(4 * j + h) % NW] & 0xFFFF0000u);
+                g[2 * h] = __uint_as_float(wa[h] << 16);
+                g[2 * h + 1] = __uint_as_float(wa[h] & 0xFFFF0000u);
+                u[2 * h] = __uint_as_float(wb[h] << 16);
+                u[2 * h + 1] = __uint_as_float(wb[h] & 0xFFFF0000u);
               }
             }
             uint32_t wg[4], wu[4], wh[4];
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
               float a0, a1, d0, d1;
-              gate_act_grad(g[2 * h], p.act, a0, d0);
-              gate_act_grad(g[2 * h + 1], p.act, a1, d1);
+              gate_act_grad(g[2 * h], ACT, a0, d0);
+              gate_act_grad(g[2 * h + 1], ACT, a1, d1);
               const float e0 = d[8 * j + 2 * h], e1 = d[8 * j + 2 * h + 1];
               const __nv_bfloat162 x = __floats2bfloat162_rn(e0 * u[2 * h] * d0, e1 * u[2 * h + 1] * d1);
               const __nv_bfloat162 y = __floats2bfloat162_rn(e0 * a0, e1 * a1);
@@ -401,27 +446,18 @@ gated_cg2_kernel(const __grid_constant__ GtParams p) {
               wu[h] = *reinterpret_cast<const uint32_t*>(&y);
               wh[h] = *reinterpret_cast<const uint32_t*>(&z);
             }
-            // 64-byte rows, 64B swizzle: unit j of row r at j ^ ((r >> 1) & 3)
-            const int at = (j ^ ((lane >> 1) & 3)) << 4;
-            *reinterpret_cast<uint4*>(srow + at) = make_uint4(wg[0], wg[1], wg[2], wg[3]);
-            *reinterpret_cast<uint4*>(srow + 2048 + at) = make_uint4(wu[0], wu[1], wu[2], wu[3]);
-            if (p.want_h) *reinterpret_cast<uint4*>(srow + 4096 + at) = make_uint4(wh[0], wh[1], wh[2], wh[3]);
+            *reinterpret_cast<uint4*>(box0 + box_at(lane, j)) = make_uint4(wg[0], wg[1], wg[2], wg[3]);
+            *reinterpret_cast<uint4*>(box1 + box_at(lane, j)) = make_uint4(wu[0], wu[1], wu[2], wu[3]);
+            *reinterpret_cast<uint4*>(box2 + box_at(lane, j)) = make_uint4(wh[0], wh[1], wh[2], wh[3]);
           }
-          fence_async_smem();
           __syncwarp();
-          if (lane == 0) {
-            const uint32_t st = stage0 + (uint32_t)(set * 6144);
-            tma_store_2d(&p.tmG, st, f, m0 + q * 32);
-            tma_store_2d(&p.tmU, st + 2048u, f, m0 + q * 32);
-            if (p.want_h) tma_store_2d(&p.tmH, st + 4096u, f, m0 + q * 32);
-            bulk_commit();
-          }
-          set ^= 1;
+          store_box(box0, lane, p.ds, p.ldds, m0, p.M, f, p.F);
+          store_box(box1, lane, p.ds + p.F, p.ldds, m0, p.M, f, p.F);
+          if (p.h) store_box(box2, lane, p.h, p.ldh, m0, p.M, f, p.F);
+          __syncwarp();   // the boxes are read before the next chunk fills them
         }
       }
     }
-    if (lane == 0) bulk_wait_all();
-    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
@@ -437,14 +473,23 @@ gated_cg2_kernel(const __grid_constant__ GtParams p) {
 }  // namespace tc
 
 namespace {
-template <bool FWD, bool Q8>
+template <bool FWD, bool Q8, int ACT>
 const void* gated_kernel_ptr() {
   static std::once_flag once;
   std::call_once(once, [] {
-    cudaFuncSetAttribute((const void*)tc::gated_cg2_kernel<FWD, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaFuncSetAttribute((const void*)tc::gated_cg2_kernel<FWD, Q8, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                          tc::GtCfg<FWD>::SMEM_BYTES);
   });
-  return (const void*)tc::gated_cg2_kernel<FWD, Q8>;
+  return (const void*)tc::gated_cg2_kernel<FWD, Q8, ACT>;
+}
+template <bool FWD, bool Q8>
+const void* gated_pick(int act) {
+  switch (act) {
+    case ACT_RELU: return gated_kernel_ptr<FWD, Q8, ACT_RELU>();
+    case ACT_GELU_TANH: return gated_kernel_ptr<FWD, Q8, ACT_GELU_TANH>();
+    case ACT_SILU: return gated_kernel_ptr<FWD, Q8, ACT_SILU>();
+    default: return gated_kernel_ptr<FWD, Q8, ACT_NONE>();
+  }
 }
 }  // namespace
 
@@ -456,15 +501,6 @@ int gated_tc_plan(const GatedOp& op, LaunchRec* rec, char* err, size_t errlen) {
   if (op.fwd ? !make_tmap(&p.tmB, op.B, op.K, 2 * op.F, op.ldb, 64, 128, err, errlen)
              : !make_tmap(&p.tmB, op.B, op.F, op.K, op.ldb, 64, 64, err, errlen))
     return -1;
-  // the halves of S / dS as matrices of F columns each, so that stores clip at F
-  __nv_bfloat16* two = (__nv_bfloat16*)(op.fwd ? (op.se ? nullptr : op.s) : op.ds);
-  const int64_t ld2 = op.fwd ? op.lds : op.ldds;
-  auto out_map = [&](CUtensorMap* tm, const void* ptr, int64_t ld) {
-    return op.fwd ? make_tmap(tm, ptr, op.F, op.M, ld, 64, 32, err, errlen)
-                  : make_tmap_sw64(tm, ptr, op.F, op.M, ld, 32, 32, err, errlen);
-  };
-  if (two && (!out_map(&p.tmG, two, ld2) || !out_map(&p.tmU, two + op.F, ld2))) return -1;
-  if (op.h && !out_map(&p.tmH, op.h, op.ldh)) return -1;
   p.M = (int)op.M; p.F = (int)op.F; p.K = (int)op.K;
   p.num_kb = (int)ceil_div(op.K, tc::BK);
   p.tiles_m = (int)ceil_div(op.M, tc::GtCfg<true>::TBM);
@@ -476,20 +512,19 @@ int gated_tc_plan(const GatedOp& op, LaunchRec* rec, char* err, size_t errlen) {
   p.num_tiles = p.tiles_m * p.tiles_f;
   // rows first where A is the smaller operand, so that B is read from DRAM about once
   p.m_fast = op.M < (op.fwd ? 2 * op.F : op.F) ? 1 : 0;
-  p.act = op.act;
-  p.keep = two != nullptr;
-  p.want_h = op.h != nullptr;
   p.idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((op.fwd ? 0u : 1u) << 16) | ((256u >> 3) << 17) | ((256u >> 4) << 24);
   p.bias = op.bias;
+  p.h = (__nv_bfloat16*)op.h; p.ldh = op.ldh;
+  p.ds = (__nv_bfloat16*)op.ds; p.ldds = op.ldds;
   if (op.se) {
     p.q = (uint8_t*)op.s; p.ldq = op.lds; p.e = op.se; p.lde = op.ldse;
-  } else if (!op.fwd) {
-    p.s = (const __nv_bfloat16*)op.s; p.lds = op.lds;
+  } else {
+    p.s = (__nv_bfloat16*)op.s; p.lds = op.lds;
   }
   p.nb = (int)q8_blocks(op.F);
   p.err = op.err;
-  rec->func = op.fwd ? (op.se ? gated_kernel_ptr<true, true>() : gated_kernel_ptr<true, false>())
-                     : (op.se ? gated_kernel_ptr<false, true>() : gated_kernel_ptr<false, false>());
+  rec->func = op.fwd ? (op.se ? gated_pick<true, true>(op.act) : gated_pick<true, false>(op.act))
+                     : (op.se ? gated_pick<false, true>(op.act) : gated_pick<false, false>(op.act));
   rec->smem = op.fwd ? tc::GtCfg<true>::SMEM_BYTES : tc::GtCfg<false>::SMEM_BYTES;
   rec->grid = dim3((unsigned)(2 * std::min(p.num_tiles, cg2_max_clusters())));
   rec->block = dim3(tc::GT_THREADS);

@@ -296,9 +296,6 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
 // err where the layout allows no map.
 bool make_tmap(CUtensorMap* tm, const void* ptr, int64_t inner, int64_t outer, int64_t ld, int box_inner,
                int box_outer, char* err, size_t errlen);
-// The same with the 64B swizzle (64-byte box rows).
-bool make_tmap_sw64(CUtensorMap* tm, const void* ptr, int64_t inner, int64_t outer, int64_t ld, int box_inner,
-                    int box_outer, char* err, size_t errlen);
 // Multiprocessors of the device, and the CTA pairs of a 2-SM kernel that fit
 // on it at once.
 int device_sms();

@@ -2150,8 +2150,8 @@ EncodeTiledFn encode_fn() {
 // 2-D bf16 tensor map: inner extent `inner` (contiguous), outer extent
 // `outer` with row pitch `ld` elements; box {box_inner, box_outer}; 128B
 // swizzle; out-of-range elements read as zero.
-static bool encode_bf16(CUtensorMap* tm, const void* ptr, int64_t inner, int64_t outer, int64_t ld, int box_inner,
-                        int box_outer, CUtensorMapSwizzle swizzle, char* err, size_t errlen) {
+bool make_tmap(CUtensorMap* tm, const void* ptr, int64_t inner, int64_t outer, int64_t ld, int box_inner,
+               int box_outer, char* err, size_t errlen) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) { snprintf(err, errlen, "cuTensorMapEncodeTiled unavailable"); return false; }
   if (((uintptr_t)ptr & 15) || ((ld * 2) & 15)) {
@@ -2163,7 +2163,7 @@ static bool encode_bf16(CUtensorMap* tm, const void* ptr, int64_t inner, int64_t
   cuuint32_t box[2] = {(cuuint32_t)box_inner, (cuuint32_t)box_outer};
   cuuint32_t estr[2] = {1, 1};
   CUresult r = fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
     snprintf(err, errlen, "cuTensorMapEncodeTiled failed (%d) inner=%lld outer=%lld ld=%lld box=%dx%d", (int)r,
@@ -2171,14 +2171,6 @@ static bool encode_bf16(CUtensorMap* tm, const void* ptr, int64_t inner, int64_t
     return false;
   }
   return true;
-}
-bool make_tmap(CUtensorMap* tm, const void* ptr, int64_t inner, int64_t outer, int64_t ld, int box_inner,
-               int box_outer, char* err, size_t errlen) {
-  return encode_bf16(tm, ptr, inner, outer, ld, box_inner, box_outer, CU_TENSOR_MAP_SWIZZLE_128B, err, errlen);
-}
-bool make_tmap_sw64(CUtensorMap* tm, const void* ptr, int64_t inner, int64_t outer, int64_t ld, int box_inner,
-                    int box_outer, char* err, size_t errlen) {
-  return encode_bf16(tm, ptr, inner, outer, ld, box_inner, box_outer, CU_TENSOR_MAP_SWIZZLE_64B, err, errlen);
 }
 
 namespace {
