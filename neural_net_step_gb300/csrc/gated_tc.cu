@@ -38,22 +38,25 @@ namespace tc {
 constexpr int GT_EPI_WARPS = 16;
 constexpr int GT_THREADS = 64 + 32 * GT_EPI_WARPS;
 
-// Stages of 32 KB, and per epilogue warp three boxes of 32 rows x 32 bf16
-// (2 KB).  A lane computes along its own row (that is how TMEM is read), but
-// a warp's global accesses go row by row, four lanes to the 64 bytes of a row:
-// the boxes turn one into the other.  (Lanes reading or writing their own rows
-// cost 32 cache lines per instruction; bulk-tensor stores of 64-byte rows,
-// tried before, kept the TMA unit busy that the main loop needs: 218 us for
-// the GELU backward at 16384 x 4096 x 1024.)
+// TMEM is read a row per lane, but global memory wants whole rows: 64-byte
+// pieces of rows (a warp's 32 columns) ran the backward's reads and writes at
+// 3.9 TB/s together, 128-byte pieces at 5.0, 512-byte ones at 5.3.  So the
+// four warps that read the same 32 TMEM lanes hand their columns to one
+// another through shared memory, as one box of 32 whole tile rows, and each
+// then moves 8 of the rows:
+//   forward: g, u and h in bf16 (or codes), three boxes of 32 x 256 bytes;
+//   backward: dH in fp32, 32 x 1024 bytes; the gate's arithmetic is then done
+//   row by row, eight columns per lane, on g and u straight from global
+//   memory (fetched four rows ahead) and its results go straight back.
 template <bool FWD> struct GtCfg {
   static constexpr int TBM = 2 * BM;
   static constexpr int TF = FWD ? 128 : 256;             // F columns per tile
   static constexpr int A_BYTES = BM * BK * 2;
   static constexpr int B_BYTES = 128 * BK * 2;
-  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int STAGES = 4;
-  static constexpr int EPI_WARP_BYTES = 3 * 2048;
-  static constexpr int EPI_BYTES = GT_EPI_WARPS * EPI_WARP_BYTES;
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;  // 32 KB
+  static constexpr int STAGES = FWD ? 4 : 3;
+  static constexpr int EPI_GROUP_BYTES = FWD ? 3 * 8192 : 32768;
+  static constexpr int EPI_BYTES = 4 * EPI_GROUP_BYTES;
   static constexpr int ACC_COLS = 256;
   static constexpr int TMEM_COLS = 2 * ACC_COLS;
   static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + EPI_BYTES + 1024 + 256;
@@ -78,8 +81,8 @@ struct GtParams {
 
 // 32 values (one row's block) as an 8-bit checkpoint: 8 words of codes; the
 // scale byte is returned.  The maximum of the magnitudes skips NaN by itself;
-// a block that holds an infinity takes the long way.
-__device__ __forceinline__ uint32_t q8_block(const float* v, uint32_t (&w)[8]) {
+// a block that holds an infinity takes the long way (and v loses it).
+__device__ __forceinline__ uint32_t q8_block(float (&v)[32], uint32_t (&w)[8]) {
   float a[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int j = 0; j < 32; ++j) a[j & 3] = fmaxf(a[j & 3], fabsf(v[j]));
@@ -87,14 +90,10 @@ __device__ __forceinline__ uint32_t q8_block(const float* v, uint32_t (&w)[8]) {
   if (m >= 0x7f800000u) {
     m = 0;
 #pragma unroll
-    for (int j = 0; j < 32; ++j) m = max(m, q8_mag(v[j]));
-    const int k = q8_exponent(m);
-    const float s = q8_pow2(-k);
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      w[j] = q8_pack(q8_no_inf(v[4 * j]) * s, q8_no_inf(v[4 * j + 1]) * s, q8_no_inf(v[4 * j + 2]) * s,
-                     q8_no_inf(v[4 * j + 3]) * s);
-    return (uint32_t)(k + 127);
+    for (int j = 0; j < 32; ++j) {
+      m = max(m, q8_mag(v[j]));
+      v[j] = q8_no_inf(v[j]);
+    }
   }
   const int k = q8_exponent(m);
   const float s = q8_pow2(-k);
@@ -103,14 +102,39 @@ __device__ __forceinline__ uint32_t q8_block(const float* v, uint32_t (&w)[8]) {
   return (uint32_t)(k + 127);
 }
 
-// Byte offset of 16-byte unit j of row r in a box (64-byte rows; units
-// exchanged so that neither 8 rows' units j nor 2 whole rows share banks), and
-// of 8-byte unit j of row r in a box of codes (32-byte rows).
-__device__ __forceinline__ int box_at(int r, int j) { return r * 64 + ((j ^ ((r >> 1) & 3)) << 4); }
-__device__ __forceinline__ int code_at(int r, int j) { return r * 32 + ((j ^ ((r >> 2) & 3)) << 3); }
+// Barrier `id` over the 128 threads of four warps; true where every one of
+// them arrives with `ok` (so that they give up together).
+__device__ __forceinline__ bool group_sync(uint32_t id, bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred q, %2, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)ok), "r"(id)
+      : "memory");
+  return r != 0;
+}
 
-// A lane's 32 values in bf16 into its row of a box.
-__device__ __forceinline__ void stage_row32(uint8_t* box, int lane, const float* v) {
+// Hand a drained accumulator back.  Relaxed: the MMAs that follow overwrite
+// only what this thread's TMEM loads have already returned; a release would
+// wait for the epilogue's outstanding global stores (3% of the backward).
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar_cluster) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+}
+
+// Byte offsets in the boxes: 16-byte unit j (0..15) of row r with 256-byte
+// rows, 8-byte unit j (0..15) of a row of codes (128 bytes), 16-byte unit j
+// (0..63) of a row of fp32 (1024 bytes).  Units are exchanged so that neither
+// the same unit of a quarter-warp's rows nor a quarter-warp's units of one row
+// share banks (fp32: units 2 l and 2 l + 1 of lane l).
+__device__ __forceinline__ int box_at(int r, int j) { return r * 256 + ((j ^ (r & 7)) << 4); }
+__device__ __forceinline__ int code_at(int r, int j) { return r * 128 + ((j ^ (r & 15)) << 3); }
+__device__ __forceinline__ int fbox_at(int r, int j) { return r * 1024 + ((j ^ ((j >> 3) & 1) ^ (r & 7)) << 4); }
+
+// A lane's 32 values in bf16 into its row of a box, from unit j0 on.
+__device__ __forceinline__ void stage_row32(uint8_t* box, int lane, int j0, const float* v) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     uint32_t w[4];
@@ -119,20 +143,7 @@ __device__ __forceinline__ void stage_row32(uint8_t* box, int lane, const float*
       const __nv_bfloat162 b2 = __floats2bfloat162_rn(v[8 * j + 2 * h], v[8 * j + 2 * h + 1]);
       w[h] = *reinterpret_cast<const uint32_t*>(&b2);
     }
-    *reinterpret_cast<uint4*>(box + box_at(lane, j)) = make_uint4(w[0], w[1], w[2], w[3]);
-  }
-}
-// A box to rows m, m + 1, .. of a matrix at column f, clipped at M and F (F a
-// multiple of 8): lane l moves units l % 4 of rows l / 4, l / 4 + 8, ..
-__device__ __forceinline__ void store_box(const uint8_t* box, int lane, __nv_bfloat16* out, int64_t ld, int m, int M,
-                                          int f, int F) {
-  const int j = lane & 3;
-  if (f + 8 * j >= F) return;
-  __nv_bfloat16* o = out + f + 8 * j;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = 8 * i + (lane >> 2);
-    if (m + r < M) *reinterpret_cast<uint4*>(o + (int64_t)(m + r) * ld) = *reinterpret_cast<const uint4*>(box + box_at(r, j));
+    *reinterpret_cast<uint4*>(box + box_at(lane, j0 + j)) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
@@ -252,59 +263,50 @@ gated_cg2_kernel(const __grid_constant__ GtParams p) {
   } else {
     // ---------------- epilogue warps 2..17: this CTA's 128 rows ----------------
     // warp w reads TMEM lanes 32 (w % 4) .. +31: lane l owns tile row
-    // 32 (w % 4) + l, in the columns of its quarter of the tile
+    // 32 (w % 4) + l, in the columns of its quarter of the tile; afterwards
+    // it moves rows 8 quarter .. +7 of the same 32
     const int q = warp & 3;
     const int quarter = (warp - 2) >> 2;
-    const uint32_t stage0 = epi_base + (uint32_t)((warp - 2) * C::EPI_WARP_BYTES);
-    uint8_t* box0 = base_ptr + (stage0 - base);
-    uint8_t* box1 = box0 + 2048;
-    uint8_t* box2 = box0 + 4096;
-    const int lr = lane >> 2, lj = lane & 3;   // a lane's row and unit in row-by-row accesses
+    uint8_t* box = base_ptr + (epi_base - base) + q * C::EPI_GROUP_BYTES;
     int tc = 0;
     bool ok = true;
-    // backward: the kept g and u of a 32-column chunk, fetched a chunk ahead
-    // row by row: lane l holds units l % 4 (8 columns) of rows l / 4 + 8 i, and
-    // the scale bytes of its own row
-    constexpr int NW = FWD ? 1 : Q8 ? 8 : 16;
-    uint32_t ng[NW], nu[NW];
-    uint32_t ne = 0x7f7fu;
-    auto fetch = [&](int m, int f) {   // rows m .., columns f ..
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = m + 8 * i + lr, c = f + 8 * lj;
-        const bool in = r < p.M && c < p.F;   // (F is a multiple of 8)
-        if constexpr (Q8 && !FWD) {
-          const uint8_t* qr = p.q + (int64_t)r * p.ldq + c;
-          const uint2 a = in ? __ldg(reinterpret_cast<const uint2*>(qr)) : make_uint2(0u, 0u);
-          const uint2 b = in ? __ldg(reinterpret_cast<const uint2*>(qr + p.F)) : make_uint2(0u, 0u);
-          ng[2 * i] = a.x; ng[2 * i + 1] = a.y;
-          nu[2 * i] = b.x; nu[2 * i + 1] = b.y;
-        } else if constexpr (!FWD) {
-          const __nv_bfloat16* sr = p.s + (int64_t)r * p.lds + c;
-          const uint4 a = in ? __ldg(reinterpret_cast<const uint4*>(sr)) : make_uint4(0u, 0u, 0u, 0u);
-          const uint4 b = in ? __ldg(reinterpret_cast<const uint4*>(sr + p.F)) : make_uint4(0u, 0u, 0u, 0u);
-          ng[4 * i] = a.x; ng[4 * i + 1] = a.y; ng[4 * i + 2] = a.z; ng[4 * i + 3] = a.w;
-          nu[4 * i] = b.x; nu[4 * i + 1] = b.y; nu[4 * i + 2] = b.z; nu[4 * i + 3] = b.w;
-        }
-      }
-      if (Q8 && m + lane < p.M && f < p.F) {
-        const uint8_t* er = p.e + (int64_t)(m + lane) * p.lde + (f >> 5);
-        ne = (uint32_t)__ldg(er) | ((uint32_t)__ldg(er + p.nb) << 8);
+    // backward: the kept g and u of eight columns (8 lane ..) of the rows to
+    // come, as bf16 pairs or codes and their scale bytes, four rows ahead;
+    // row i of a tile in slot i % 4
+    constexpr int AHEAD = 4, NW = FWD ? 1 : Q8 ? 2 : 4;
+    uint32_t ng[AHEAD][NW], nu[AHEAD][NW], ne[AHEAD];
+    auto fetch = [&](int slot, int r, int f) {   // row r, tile columns f ..
+      const int c = f + 8 * lane;
+      const bool in = r < p.M && c < p.F;   // (F is a multiple of 8)
+      if constexpr (Q8 && !FWD) {
+        const uint8_t* qr = p.q + (int64_t)r * p.ldq + c;
+        const uint8_t* er = p.e + (int64_t)r * p.lde + (c >> 5);
+        const uint2 a = in ? __ldg(reinterpret_cast<const uint2*>(qr)) : make_uint2(0u, 0u);
+        const uint2 b = in ? __ldg(reinterpret_cast<const uint2*>(qr + p.F)) : make_uint2(0u, 0u);
+        ng[slot][0] = a.x; ng[slot][1] = a.y;
+        nu[slot][0] = b.x; nu[slot][1] = b.y;
+        ne[slot] = in ? (uint32_t)__ldg(er) | ((uint32_t)__ldg(er + p.nb) << 8) : 0u;
+      } else if constexpr (!FWD) {
+        const __nv_bfloat16* sr = p.s + (int64_t)r * p.lds + c;
+        const uint4 a = in ? __ldg(reinterpret_cast<const uint4*>(sr)) : make_uint4(0u, 0u, 0u, 0u);
+        const uint4 b = in ? __ldg(reinterpret_cast<const uint4*>(sr + p.F)) : make_uint4(0u, 0u, 0u, 0u);
+        ng[slot][0] = a.x; ng[slot][1] = a.y; ng[slot][2] = a.z; ng[slot][3] = a.w;
+        nu[slot][0] = b.x; nu[slot][1] = b.y; nu[slot][2] = b.z; nu[slot][3] = b.w;
       }
     };
     for (int t = t0; t < p.num_tiles && ok; t += tstep, ++tc) {
       int m0, f0;
       origin(t, m0, f0);
-      m0 += q * 32;   // this warp's rows
+      m0 += q * 32;   // these four warps' rows
       const int buf = tc & 1;
       const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * C::ACC_COLS);
+      const int mr = m0 + 8 * quarter;   // the rows this warp moves
       if constexpr (FWD) {
         // 32 columns: gate and up
         const int f = f0 + quarter * 32;
         float bg = 0.f, bu = 0.f;   // lane j: the bias of column j, before the accumulator wait
         if (p.bias && f + lane < p.F) { bg = __ldg(p.bias + f + lane); bu = __ldg(p.bias + p.F + f + lane); }
         ok = __all_sync(0xffffffffu, mbar_wait_cluster(tfull_bar(buf), ((uint32_t)tc >> 1) & 1u, p.err));
-        if (!ok) break;
         tc_fence_after();
         float g[32], u[32];
         tmem_ld32(trow, g, quarter * 32);
@@ -312,14 +314,30 @@ gated_cg2_kernel(const __grid_constant__ GtParams p) {
         // this warp's part of the accumulator is in registers: hand it back to CTA 0
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(lead_tempty0 + 8u * (uint32_t)buf);
-        if (f >= p.F) continue;   // wholly beyond F
+        if (lane == 0) mbar_arrive_cluster_relaxed(lead_tempty0 + 8u * (uint32_t)buf);
         if (p.bias) {
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
             g[j] += __shfl_sync(0xffffffffu, bg, j);
             u[j] += __shfl_sync(0xffffffffu, bu, j);
           }
+        }
+        if (!Q8 && p.s) {
+          stage_row32(box + 8192, lane, 4 * quarter, g);
+          stage_row32(box + 16384, lane, 4 * quarter, u);
+        }
+        {
+          uint32_t w[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const __nv_bfloat162 b2 =
+                __floats2bfloat162_rn(gate_act(g[2 * j], ACT) * u[2 * j], gate_act(g[2 * j + 1], ACT) * u[2 * j + 1]);
+            w[j] = *reinterpret_cast<const uint32_t*>(&b2);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4*>(box + box_at(lane, 4 * quarter + j)) =
+                make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
         }
         if constexpr (Q8) {
           // a lane's 32 columns are one block (columns beyond F hold the
@@ -333,129 +351,114 @@ gated_cg2_kernel(const __grid_constant__ GtParams p) {
           for (int part = 0; part < 2; ++part) {
             uint32_t w[8];
             const uint32_t byte = q8_block(part ? u : g, w);
-            uint8_t* box = part ? box2 : box1;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              *reinterpret_cast<uint2*>(box + code_at(lane, j)) = make_uint2(w[2 * j], w[2 * j + 1]);
-            if (m0 + lane < p.M) p.e[(int64_t)(m0 + lane) * p.lde + part * p.nb + (f >> 5)] = (uint8_t)byte;
+              *reinterpret_cast<uint2*>(box + 8192 + 4096 * part + code_at(lane, 4 * quarter + j)) =
+                  make_uint2(w[2 * j], w[2 * j + 1]);
+            if (ok && m0 + lane < p.M && f < p.F)
+              p.e[(int64_t)(m0 + lane) * p.lde + part * p.nb + (f >> 5)] = (uint8_t)byte;
           }
-        } else if (p.s) {
-          stage_row32(box1, lane, g);
-          stage_row32(box2, lane, u);
         }
-#pragma unroll
-        for (int j = 0; j < 32; ++j) g[j] = gate_act(g[j], ACT) * u[j];
-        stage_row32(box0, lane, g);
-        __syncwarp();
-        store_box(box0, lane, p.h, p.ldh, m0, p.M, f, p.F);
-        if constexpr (Q8) {
-          if (f + 8 * lj < p.F) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int r = 8 * i + lr;
-              if (m0 + r >= p.M) continue;
-              uint8_t* o = p.q + (int64_t)(m0 + r) * p.ldq + f + 8 * lj;
-              *reinterpret_cast<uint2*>(o) = *reinterpret_cast<const uint2*>(box1 + code_at(r, lj));
-              *reinterpret_cast<uint2*>(o + p.F) = *reinterpret_cast<const uint2*>(box2 + code_at(r, lj));
-            }
-          }
-        } else if (p.s) {
-          store_box(box1, lane, p.s, p.lds, m0, p.M, f, p.F);
-          store_box(box2, lane, p.s + p.F, p.lds, m0, p.M, f, p.F);
-        }
-        __syncwarp();   // the boxes are read before the next tile fills them
-      } else {
-        if (tc == 0) fetch(m0, f0 + quarter * 64);
-        ok = __all_sync(0xffffffffu, mbar_wait_cluster(tfull_bar(buf), ((uint32_t)tc >> 1) & 1u, p.err));
+        ok = group_sync(1 + q, ok);
         if (!ok) break;
-        tc_fence_after();
-#pragma unroll 1
-        for (int c = 0; c < 64; c += 32) {   // 64 columns, 32 at a time
-          const int f = f0 + quarter * 64 + c;
-          // the fetched units into the boxes, their own rows out of them below
+        // 16 lanes to a row: 16 bytes of bf16 or 8 codes each
+        const int j = lane & 15, c = f0 + 8 * j;
+        if (c < p.F) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
+            const int r = 2 * i + (lane >> 4), br = 8 * quarter + r, m = mr + r;
+            if (m >= p.M) continue;
+            *reinterpret_cast<uint4*>(p.h + (int64_t)m * p.ldh + c) =
+                *reinterpret_cast<const uint4*>(box + box_at(br, j));
             if constexpr (Q8) {
-              *reinterpret_cast<uint2*>(box0 + code_at(8 * i + lr, lj)) = make_uint2(ng[2 * i], ng[2 * i + 1]);
-              *reinterpret_cast<uint2*>(box1 + code_at(8 * i + lr, lj)) = make_uint2(nu[2 * i], nu[2 * i + 1]);
-            } else {
-              *reinterpret_cast<uint4*>(box0 + box_at(8 * i + lr, lj)) =
-                  make_uint4(ng[4 * i], ng[4 * i + 1], ng[4 * i + 2], ng[4 * i + 3]);
-              *reinterpret_cast<uint4*>(box1 + box_at(8 * i + lr, lj)) =
-                  make_uint4(nu[4 * i], nu[4 * i + 1], nu[4 * i + 2], nu[4 * i + 3]);
+              uint8_t* o = p.q + (int64_t)m * p.ldq + c;
+              *reinterpret_cast<uint2*>(o) = *reinterpret_cast<const uint2*>(box + 8192 + code_at(br, j));
+              *reinterpret_cast<uint2*>(o + p.F) = *reinterpret_cast<const uint2*>(box + 12288 + code_at(br, j));
+            } else if (p.s) {
+              __nv_bfloat16* o = p.s + (int64_t)m * p.lds + c;
+              *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(box + 8192 + box_at(br, j));
+              *reinterpret_cast<uint4*>(o + p.F) = *reinterpret_cast<const uint4*>(box + 16384 + box_at(br, j));
             }
           }
-          const float eg = q8_scale(ne & 0xffu), eu = q8_scale(ne >> 8);
-          __syncwarp();
-          float d[32];
-          tmem_ld32(trow, d, quarter * 64 + c);
-          if (c == 0) {
-            fetch(m0, f + 32);
+        }
+        named_bar_sync(1 + q, 128);   // the boxes are read before the next tile fills them
+      } else {
+        if (tc == 0) {
+#pragma unroll
+          for (int i = 0; i < AHEAD; ++i) fetch(i, mr + i, f0);
+        }
+        ok = __all_sync(0xffffffffu, mbar_wait_cluster(tfull_bar(buf), ((uint32_t)tc >> 1) & 1u, p.err));
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float d[16];
+          tmem_ld16(trow + (uint32_t)(quarter * 64 + 16 * c), d);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<float4*>(box + fbox_at(lane, 16 * quarter + 4 * c + j)) =
+                make_float4(d[4 * j], d[4 * j + 1], d[4 * j + 2], d[4 * j + 3]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_relaxed(lead_tempty0 + 8u * (uint32_t)buf);
+        ok = group_sync(1 + q, ok);
+        if (!ok) break;
+        // the next tile's rows, to fetch while this one's last rows are worked on
+        int next_m = p.M, next_f = 0;   // (none: nothing is read)
+        if (t + tstep < p.num_tiles) {
+          origin(t + tstep, next_m, next_f);
+          next_m += q * 32 + 8 * quarter;
+        }
+        const int c = f0 + 8 * lane;
+#pragma unroll 1
+        for (int i0 = 0; i0 < 8; i0 += AHEAD) {
+        const int fm = i0 + AHEAD < 8 ? mr + i0 + AHEAD : next_m, ff = i0 + AHEAD < 8 ? f0 : next_f;
+#pragma unroll
+        for (int slot = 0; slot < AHEAD; ++slot) {
+          const int i = i0 + slot, m = mr + i;
+          float g[8], u[8], d[8];
+          if constexpr (Q8) {
+            const float eg = q8_scale(ne[slot] & 0xffu), eu = q8_scale(ne[slot] >> 8);
+            q8_unpack(ng[slot][0], eg, g);
+            q8_unpack(ng[slot][1], eg, g + 4);
+            q8_unpack(nu[slot][0], eu, u);
+            q8_unpack(nu[slot][1], eu, u + 4);
           } else {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(lead_tempty0 + 8u * (uint32_t)buf);
-            if (t + tstep < p.num_tiles) {
-              int m1, f1;
-              origin(t + tstep, m1, f1);
-              fetch(m1 + q * 32, f1 + quarter * 64);
-            }
-          }
-          uint32_t cg[Q8 ? 8 : 1], cu[Q8 ? 8 : 1];
-          if constexpr (Q8) {   // all of the row's codes, before results take their place
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint2 a = *reinterpret_cast<const uint2*>(box0 + code_at(lane, j));
-              const uint2 b = *reinterpret_cast<const uint2*>(box1 + code_at(lane, j));
-              cg[2 * j] = a.x; cg[2 * j + 1] = a.y;
-              cu[2 * j] = b.x; cu[2 * j + 1] = b.y;
-            }
-            __syncwarp();
-          }
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {   // eight columns: one 16-byte unit of each box
-            float g[8], u[8];
-            if constexpr (Q8) {
-              q8_unpack(cg[2 * j], eg, g);
-              q8_unpack(cg[2 * j + 1], eg, g + 4);
-              q8_unpack(cu[2 * j], eu, u);
-              q8_unpack(cu[2 * j + 1], eu, u + 4);
-            } else {
-              const uint4 a = *reinterpret_cast<const uint4*>(box0 + box_at(lane, j));
-              const uint4 b = *reinterpret_cast<const uint4*>(box1 + box_at(lane, j));
-              const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-              for (int h = 0; h < 4; ++h) {
-                g[2 * h] = __uint_as_float(wa[h] << 16);
-                g[2 * h + 1] = __uint_as_float(wa[h] & 0xFFFF0000u);
-                u[2 * h] = __uint_as_float(wb[h] << 16);
-                u[2 * h + 1] = __uint_as_float(wb[h] & 0xFFFF0000u);
-              }
-            }
-            uint32_t wg[4], wu[4], wh[4];
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
-              float a0, a1, d0, d1;
-              gate_act_grad(g[2 * h], ACT, a0, d0);
-              gate_act_grad(g[2 * h + 1], ACT, a1, d1);
-              const float e0 = d[8 * j + 2 * h], e1 = d[8 * j + 2 * h + 1];
-              const __nv_bfloat162 x = __floats2bfloat162_rn(e0 * u[2 * h] * d0, e1 * u[2 * h + 1] * d1);
-              const __nv_bfloat162 y = __floats2bfloat162_rn(e0 * a0, e1 * a1);
-              const __nv_bfloat162 z = __floats2bfloat162_rn(a0 * u[2 * h], a1 * u[2 * h + 1]);
-              wg[h] = *reinterpret_cast<const uint32_t*>(&x);
-              wu[h] = *reinterpret_cast<const uint32_t*>(&y);
-              wh[h] = *reinterpret_cast<const uint32_t*>(&z);
+              g[2 * h] = __uint_as_float(ng[slot][h % NW] << 16);
+              g[2 * h + 1] = __uint_as_float(ng[slot][h % NW] & 0xFFFF0000u);
+              u[2 * h] = __uint_as_float(nu[slot][h % NW] << 16);
+              u[2 * h + 1] = __uint_as_float(nu[slot][h % NW] & 0xFFFF0000u);
             }
-            *reinterpret_cast<uint4*>(box0 + box_at(lane, j)) = make_uint4(wg[0], wg[1], wg[2], wg[3]);
-            *reinterpret_cast<uint4*>(box1 + box_at(lane, j)) = make_uint4(wu[0], wu[1], wu[2], wu[3]);
-            *reinterpret_cast<uint4*>(box2 + box_at(lane, j)) = make_uint4(wh[0], wh[1], wh[2], wh[3]);
           }
-          __syncwarp();
-          store_box(box0, lane, p.ds, p.ldds, m0, p.M, f, p.F);
-          store_box(box1, lane, p.ds + p.F, p.ldds, m0, p.M, f, p.F);
-          if (p.h) store_box(box2, lane, p.h, p.ldh, m0, p.M, f, p.F);
-          __syncwarp();   // the boxes are read before the next chunk fills them
+          fetch(slot, fm + slot, ff);
+          *reinterpret_cast<float4*>(d) = *reinterpret_cast<const float4*>(box + fbox_at(8 * quarter + i, 2 * lane));
+          *reinterpret_cast<float4*>(d + 4) =
+              *reinterpret_cast<const float4*>(box + fbox_at(8 * quarter + i, 2 * lane + 1));
+          uint32_t wg[4], wu[4], wh[4];
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            float a0, a1, d0, d1;
+            gate_act_grad(g[2 * h], ACT, a0, d0);
+            gate_act_grad(g[2 * h + 1], ACT, a1, d1);
+            const float e0 = d[2 * h], e1 = d[2 * h + 1];
+            const __nv_bfloat162 x = __floats2bfloat162_rn(e0 * u[2 * h] * d0, e1 * u[2 * h + 1] * d1);
+            const __nv_bfloat162 y = __floats2bfloat162_rn(e0 * a0, e1 * a1);
+            const __nv_bfloat162 z = __floats2bfloat162_rn(a0 * u[2 * h], a1 * u[2 * h + 1]);
+            wg[h] = *reinterpret_cast<const uint32_t*>(&x);
+            wu[h] = *reinterpret_cast<const uint32_t*>(&y);
+            wh[h] = *reinterpret_cast<const uint32_t*>(&z);
+          }
+          if (m < p.M && c < p.F) {
+            __nv_bfloat16* o = p.ds + (int64_t)m * p.ldds + c;
+            *reinterpret_cast<uint4*>(o) = make_uint4(wg[0], wg[1], wg[2], wg[3]);
+            *reinterpret_cast<uint4*>(o + p.F) = make_uint4(wu[0], wu[1], wu[2], wu[3]);
+            if (p.h) *reinterpret_cast<uint4*>(p.h + (int64_t)m * p.ldh + c) = make_uint4(wh[0], wh[1], wh[2], wh[3]);
+          }
         }
+        }
+        named_bar_sync(1 + q, 128);   // the box is read before the next tile fills it
       }
     }
   }
