@@ -17,6 +17,7 @@
 #include <stdio.h>
 
 #include <algorithm>
+#include <mutex>
 
 #include "common.cuh"
 #include "ops.h"
@@ -71,6 +72,7 @@ struct LnFwdParams {
   float* mean; float* rstd;
   int64_t M; int D;
   float eps;
+  int tpr;              // threads per row (a multiple of 32 that divides the block)
 };
 
 // Sums of NS values over the WARPS warps that share a row, the same in every
@@ -96,79 +98,283 @@ __device__ __forceinline__ void row_sums(float (&v)[NS], float (&sh)[NS][WARPS])
 // mean and 1 / sqrt(variance + eps).
 __device__ __forceinline__ void finish_stats(const float (&s)[2], float inv_d, float eps, float& rest, float& rstd) {
   rest = s[0] * inv_d;
-  rstd = 1.0f / sqrtf(fmaxf(fmaf(-rest, rest, s[1] * inv_d), 0.f) + eps);
+  rstd = rsqrtf(fmaxf(fmaf(-rest, rest, s[1] * inv_d), 0.f) + eps);   // (2 ulp)
 }
 
-// WARPS = 1: a warp per row, eight rows per block; else a block per row.
-// Thread t of a row's threads holds vectors t, t + threads, ... (NV of them,
-// VEC elements each).
-template <typename T, int VEC, int NV, int WARPS>
-__global__ void __launch_bounds__(256) ln_fwd_kernel(const __grid_constant__ LnFwdParams p) {
-  pdl_enter();
-  __shared__ float sh1[1][WARPS], sh2[2][WARPS];
-  constexpr int TPR = 32 * WARPS;
-  const int64_t row = WARPS == 1 ? blockIdx.x * (int64_t)8 + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
-  if (row >= p.M) return;   // (a warp, or the whole block)
-  const int t = WARPS == 1 ? threadIdx.x & 31 : threadIdx.x;
-  const T* xr = reinterpret_cast<const T*>(p.x) + row * p.ldx;
-  float v[NV][VEC];
-  float s[1] = {0.f};
+// Two fp32 values in a register pair: one instruction does both (the kernels
+// below are bound by instruction issue before they are by DRAM otherwise).
+struct F2 { uint64_t v; };
+__device__ __forceinline__ F2 pack2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(F2 x, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x.v)); }
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ float sum2(F2 x) {
+  float a, b;
+  unpack2(x, a, b);
+  return a + b;
+}
+
+// How rows of at most kMaxRow elements are walked, forward and backward: tpr
+// threads (whole warps) share a row, EPT elements each, and a block's groups of
+// tpr threads take rows in turn, so that the gradients' columns stay with
+// their threads.  Aligned rows are prefetched into a ring in shared memory
+// (cp.async), each thread only its own elements, so a thread waits for no
+// other; the rest are loaded when their turn comes.  The scale and the shift
+// lie in shared memory.
+//   EPT: with 8 elements a thread the kernels were bound by instruction issue
+// (about 250 instructions a row and warp besides the elements: 94 us for
+// 65536 x 1024 bf16 forward); with 32 the sums cost a tenth of that.  bf16
+// takes 32, fp32 and unaligned rows 16 (their registers), short rows fewer.
+template <bool FWD> struct RowCfg {   // one block to an SM
+  static constexpr int THREADS = FWD ? 1024 : 512;   // at most (64 and 128 registers)
+  static constexpr int RING = FWD ? 192 : 384;       // bytes of the ring per thread
+};
+
+template <typename T, int VEC, int EPT, int NT>   // NT tensors a row: x, or x and dy
+struct RowFetch {
+  static constexpr int NV = EPT / VEC;
+  static constexpr bool RING = VEC > 1;
+  static constexpr int FIT = RowCfg<NT == 1>::RING / (EPT * (int)sizeof(T) * NT);
+  static constexpr int STAGES = FIT > 6 ? 6 : FIT;
+  static_assert(!RING || STAGES >= 2, "a row ahead at least");
+  const T* src[NT];      // the tensors, at this thread's first element
+  int64_t ld[NT];
+  int64_t M, step;       // rows, rows from one to the next
+  int cols;              // this thread's elements start below D from (cols) on: unit i is there while i * tpr * VEC < cols
+  int hop;               // elements from unit to unit
+  uint32_t ring;         // this thread's 16 bytes of unit 0 of stage 0
+  uint32_t pitch;        // bytes from unit to unit
+  uint4 raw[NT][RING ? NV : 1];
+  T one[NT][RING ? 1 : NV];
+
+  __device__ __forceinline__ void setup(int t, int tpr, int D, uint32_t ring0) {
+    cols = D - t * VEC;
+    hop = tpr * VEC;
+    ring = ring0 + threadIdx.x * 16;
+    pitch = blockDim.x * 16;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (t + i * TPR) * VEC;
-    if (c < p.D) {
-      load_vec<T, VEC>(xr + c, v[i]);
-    } else {
+    for (int k = 0; k < NT; ++k) src[k] += t * VEC;
+  }
+  __device__ __forceinline__ bool in(int i) const { return i * hop < cols; }
+  __device__ __forceinline__ void issue(int64_t row, int stage) {
+    if constexpr (RING) {
+      if (row < M) {
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) v[i][j] = 0.f;
+        for (int k = 0; k < NT; ++k) {
+          const T* r = src[k] + row * ld[k];
+          const uint32_t to = ring + (uint32_t)(stage * NT + k) * NV * pitch;
+#pragma unroll
+          for (int i = 0; i < NV; ++i)
+            if (in(i))
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + (uint32_t)i * pitch), "l"(r + i * hop)
+                           : "memory");
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
     }
   }
+  __device__ __forceinline__ void start(int64_t row) {
+    if constexpr (RING) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
+      for (int s = 0; s < STAGES - 1; ++s) issue(row + s * step, s);
+    }
+  }
+  // Row `row`'s elements into raw (stage by stage), the next fetch under way.
+  __device__ __forceinline__ void take(int64_t row, int& stage) {
+    if constexpr (RING) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) s[0] += v[i][j];
-  const float inv_d = 1.0f / (float)p.D;
-  row_sums<WARPS, 1>(s, sh1);
-  const float mean = s[0] * inv_d;
-  float sd[2] = {0.f, 0.f};
+      for (int k = 0; k < NT; ++k)
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const bool in = (t + i * TPR) * VEC < p.D;
+        for (int i = 0; i < NV; ++i)
+          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(raw[k][i].x), "=r"(raw[k][i].y), "=r"(raw[k][i].z), "=r"(raw[k][i].w)
+                       : "r"(ring + (uint32_t)((stage * NT + k) * NV + i) * pitch)
+                       : "memory");
+      issue(row + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);   // the row before's, read by now
+      stage = stage + 1 == STAGES ? 0 : stage + 1;
+    } else {
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      v[i][j] -= mean;
-      if (in) {
-        sd[0] += v[i][j];
-        sd[1] = fmaf(v[i][j], v[i][j], sd[1]);
+      for (int k = 0; k < NT; ++k)
+#pragma unroll
+        for (int i = 0; i < NV; ++i) one[k][i] = in(i) ? src[k][row * ld[k] + i * hop] : from_f32<T>(0.f);
+    }
+  }
+  // Elements 2 q and 2 q + 1 of this thread (of the order c(q) below); single
+  // elements beyond D are `fill`.
+  __device__ __forceinline__ F2 get(int k, int q, float fill) const {
+    if constexpr (!RING) {
+      return pack2(to_f32(one[k][2 * q]), in(2 * q + 1) ? to_f32(one[k][2 * q + 1]) : fill);
+    } else {
+      const uint4& r = raw[k][2 * q / VEC];
+      if constexpr (sizeof(T) == 4) {
+        return (q & 1) ? pack2(__uint_as_float(r.z), __uint_as_float(r.w)) : pack2(__uint_as_float(r.x), __uint_as_float(r.y));
+      } else {
+        const uint32_t w = (q & 3) == 0 ? r.x : (q & 3) == 1 ? r.y : (q & 3) == 2 ? r.z : r.w;
+        return pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
       }
     }
   }
-  row_sums<WARPS, 2>(sd, sh2);
-  float rest, rstd;
-  finish_stats(sd, inv_d, p.eps, rest, rstd);
-  if (t == 0) {
-    if (p.mean) p.mean[row] = mean + rest;
-    if (p.rstd) p.rstd[row] = rstd;
+  // Whether pair q is there at all, and the row's elements it holds: offsets
+  // from this thread's first one.
+  __device__ __forceinline__ bool has(int q) const { return in(2 * q / VEC); }
+  __device__ __forceinline__ int at(int q) const { return 2 * q / VEC * hop + (VEC == 1 ? 0 : 2 * q % VEC); }
+  // A vector of D floats in shared memory, in the order the threads use it:
+  // four consecutive elements of thread t at 16 t, so that a warp's 16-byte
+  // loads run through it (in memory order, lanes 32 bytes apart conflicted
+  // four ways: 52 us for the forward of 65536 x 1024).
+  __device__ __forceinline__ static int place(int c, int tpr) {   // of element c
+    if constexpr (VEC == 8) {
+      const int unit = c >> 3, i = unit / tpr, t = unit - i * tpr;
+      return ((2 * i + ((c >> 2) & 1)) * tpr + t) * 4 + (c & 3);
+    } else {
+      return c;
+    }
   }
-  T* yr = reinterpret_cast<T*>(p.y) + row * p.ldy;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (t + i * TPR) * VEC;
-    if (c >= p.D) continue;
-    float g[VEC], b[VEC];
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) { g[j] = 1.f; b[j] = 0.f; }
-    if (p.gamma) {
-#pragma unroll
-      for (int j = 0; j < VEC; j += (VEC == 1 ? 1 : 4)) load_vec<float, VEC == 1 ? 1 : 4>(p.gamma + c + j, g + j);
+  // Pairs q and q + 1 (q even) of such a vector, v at this thread's first element.
+  __device__ __forceinline__ void vec4(const float* v, int q, F2& a, F2& b) const {
+    if constexpr (RING) {
+      const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(v + (2 * q / 4) * (hop / VEC) * 4);
+      a.v = w.x;
+      b.v = w.y;
+    } else {
+      a = pack2(v[at(q)], in(2 * q + 1) ? v[at(q) + hop] : 0.f);
+      b = has(q + 1) ? pack2(v[at(q + 1)], in(2 * q + 3) ? v[at(q + 1) + hop] : 0.f) : pack2(0.f, 0.f);
     }
-    if (p.beta) {
+  }
+};
+// A thread's results to its elements of a row, a unit (unaligned: two pairs)
+// at a time: f(q, a, b) gives pairs q and q + 1.
+template <typename T, int VEC, int EPT, class F, class Get>
+__device__ __forceinline__ void put_row(const F& f, T* row, Get get) {
+  constexpr int PAIRS = VEC == 1 ? 2 : VEC / 2;
 #pragma unroll
-      for (int j = 0; j < VEC; j += (VEC == 1 ? 1 : 4)) load_vec<float, VEC == 1 ? 1 : 4>(p.beta + c + j, b + j);
+  for (int q = 0; q < EPT / 2; q += PAIRS) {
+    if (!f.has(q)) continue;
+    float v[2 * PAIRS];
+#pragma unroll
+    for (int h = 0; h < PAIRS; h += 2) {
+      F2 a, b;
+      get(q + h, a, b);
+      unpack2(a, v[2 * h], v[2 * h + 1]);
+      unpack2(b, v[2 * h + 2], v[2 * h + 3]);
     }
+    if constexpr (VEC == 1) {
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) v[i][j] = fmaf((v[i][j] - rest) * rstd, g[j], b[j]);
-    store_vec<T, VEC>(yr + c, v[i]);
+      for (int j = 0; j < 4; ++j)
+        if (f.in(2 * q + j)) row[(2 * q + j) * f.hop] = from_f32<T>(v[j]);
+    } else {
+      store_vec<T, VEC>(row + f.at(q), v);
+    }
+  }
+}
+
+// Sums of NS values over the warps of a row's group, the same in every thread
+// of it.  w: the block's [32 * NS] floats of one of two buffers used in turn
+// (a group's next use of the same buffer lies two barriers later).
+template <int NS>
+__device__ __forceinline__ void group_sums(float (&v)[NS], float* w, int group, int wpr) {
+#pragma unroll
+  for (int k = 0; k < NS; ++k) v[k] = warp_sum(v[k]);
+  if (wpr == 1) return;
+  if ((threadIdx.x & 31) == 0)
+#pragma unroll
+    for (int k = 0; k < NS; ++k) w[NS * (threadIdx.x >> 5) + k] = v[k];
+  asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(wpr * 32) : "memory");
+#pragma unroll
+  for (int k = 0; k < NS; ++k) v[k] = 0.f;
+  for (int i = 0; i < wpr; ++i)
+#pragma unroll
+    for (int k = 0; k < NS; ++k) v[k] += w[NS * (group * wpr + i) + k];
+}
+
+constexpr int kSumBytes = 2 * 32 * 2 * 4;   // group_sums' two buffers
+
+template <typename T, int VEC, int EPT>
+__global__ void __launch_bounds__(RowCfg<true>::THREADS, 1) ln_fwd_kernel(const __grid_constant__ LnFwdParams p) {
+  pdl_enter();
+  using F = RowFetch<T, VEC, EPT, 1>;
+  constexpr int NP = EPT / 2;
+  extern __shared__ __align__(16) float ln_smem[];
+  const int tpr = p.tpr, groups = (int)blockDim.x / tpr, wpr = tpr >> 5;
+  float* scale = ln_smem + kSumBytes / 4;          // [tpr EPT]
+  float* shift = scale + tpr * EPT;
+  const int group = (int)threadIdx.x / tpr, t = (int)threadIdx.x % tpr;
+  F f;
+  f.src[0] = reinterpret_cast<const T*>(p.x);
+  f.ld[0] = p.ldx;
+  f.M = p.M; f.step = (int64_t)gridDim.x * groups;
+  f.setup(t, tpr, p.D, (uint32_t)__cvta_generic_to_shared(shift + tpr * EPT));
+  int64_t row = blockIdx.x * (int64_t)groups + group;
+  f.start(row);
+  for (int c = threadIdx.x; c < p.D; c += blockDim.x) {
+    scale[F::place(c, tpr)] = p.gamma ? p.gamma[c] : 1.f;
+    shift[F::place(c, tpr)] = p.beta ? p.beta[c] : 0.f;
+  }
+  __syncthreads();
+  const float inv_d = 1.0f / (float)p.D;
+  const int my = VEC == 1 ? t : t * 4;   // this thread's first place in them
+  int stage = 0;
+  for (; row < p.M; row += f.step) {
+    f.take(row, stage);
+    F2 v[NP], a = pack2(0.f, 0.f), b = a;
+#pragma unroll
+    for (int q = 0; q < NP; ++q) {
+      v[q] = f.get(0, q, 0.f);
+      if (f.has(q)) a = add2(a, v[q]);
+    }
+    float s[1] = {sum2(a)}, sd[2];
+    group_sums<1>(s, ln_smem, group, wpr);
+    const float mean = s[0] * inv_d;
+    const F2 minus = pack2(-mean, -mean);
+    a = b;
+#pragma unroll
+    for (int q = 0; q < NP; ++q) {
+      v[q] = add2(v[q], minus);
+      if (VEC == 1 && !f.in(2 * q + 1)) {   // (a single last element)
+        float x, y;
+        unpack2(v[q], x, y);
+        v[q] = pack2(x, 0.f);
+      }
+      if (f.has(q)) {
+        a = add2(a, v[q]);
+        b = fma2(v[q], v[q], b);
+      }
+    }
+    sd[0] = sum2(a);
+    sd[1] = sum2(b);
+    group_sums<2>(sd, ln_smem + 64, group, wpr);
+    float rest, rstd;
+    finish_stats(sd, inv_d, p.eps, rest, rstd);
+    if (t == 0) {
+      if (p.mean) p.mean[row] = mean + rest;
+      if (p.rstd) p.rstd[row] = rstd;
+    }
+    const F2 less = pack2(-rest, -rest), times = pack2(rstd, rstd);
+    put_row<T, VEC, EPT>(f, reinterpret_cast<T*>(p.y) + row * p.ldy + t * VEC, [&](int q, F2& y0, F2& y1) {
+      F2 g0, g1, b0, b1;
+      f.vec4(scale + my, q, g0, g1);
+      f.vec4(shift + my, q, b0, b1);
+      y0 = fma2(mul2(add2(v[q], less), times), g0, b0);
+      y1 = fma2(mul2(add2(v[q + 1], less), times), g1, b1);
+    });
   }
 }
 
@@ -215,114 +421,97 @@ struct LnBwdParams {
   int tpr;              // threads per row (a multiple of 32 that divides the block)
 };
 
-constexpr int kBwdEpt = 8;   // elements of a row per thread
-
-// `tpr` threads share a row, 8 elements each; the block's groups walk the
-// rows and keep their columns' dgamma / dbeta sums in registers, adding them
-// over the groups at the end: one partial row pair per block.
-template <typename T, int VEC>
-__global__ void __launch_bounds__(1024) ln_bwd_kernel(const __grid_constant__ LnBwdParams p) {
+// The groups keep their columns' dgamma / dbeta sums in registers and add them
+// over the block at the end: one partial row pair per block.  x and dy stay
+// packed between the two uses of a row.
+template <typename T, int VEC, int EPT>
+__global__ void __launch_bounds__(RowCfg<false>::THREADS, 1) ln_bwd_kernel(const __grid_constant__ LnBwdParams p) {
   pdl_enter();
-  constexpr int NV = kBwdEpt / VEC;
-  extern __shared__ float ln_smem[];          // [2][32][2] warp sums, then the groups' column sums
-  float* wsum = ln_smem;
-  float* colsum = ln_smem + 128;
-  const int tpr = p.tpr, groups = (int)blockDim.x / tpr;
+  using F = RowFetch<T, VEC, EPT, 2>;
+  constexpr int NP = EPT / 2;
+  extern __shared__ __align__(16) float ln_smem[];
+  const int tpr = p.tpr, groups = (int)blockDim.x / tpr, wpr = tpr >> 5;
+  float* scale = ln_smem + kSumBytes / 4;                 // [tpr EPT]
+  float* colsum = scale + tpr * EPT;                      // the ring's place, once the rows are done
   const int group = (int)threadIdx.x / tpr, t = (int)threadIdx.x % tpr;
-  const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31;
-  const int wpr = tpr >> 5, w0 = group * wpr;   // this row's warps
+  F f;
+  f.src[0] = reinterpret_cast<const T*>(p.x);
+  f.src[1] = reinterpret_cast<const T*>(p.dy);
+  f.ld[0] = p.ldx; f.ld[1] = p.lddy;
+  f.M = p.M; f.step = (int64_t)gridDim.x * groups;
+  f.setup(t, tpr, p.D, (uint32_t)__cvta_generic_to_shared(colsum));
+  int64_t row = blockIdx.x * (int64_t)groups + group;
+  f.start(row);
+  for (int c = threadIdx.x; c < p.D; c += blockDim.x) scale[F::place(c, tpr)] = p.gamma ? p.gamma[c] : 1.f;
   const float inv_d = 1.0f / (float)p.D;
-  float g[NV][VEC], dg[NV][VEC], db[NV][VEC];
+  const F2 zero = pack2(0.f, 0.f);
+  F2 dg[NP], db[NP];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (t + i * tpr) * VEC;
+  for (int q = 0; q < NP; ++q) dg[q] = db[q] = zero;
+  float mean = 0.f, rstd = 0.f;
+  if (row < p.M) { mean = p.mean[row]; rstd = p.rstd[row]; }
+  __syncthreads();
+  const float* sc = scale + (VEC == 1 ? t : t * 4);
+  int stage = 0, buf = 0;
+  for (; row < p.M; row += f.step) {
+    float next_mean = 0.f, next_rstd = 0.f;
+    if (row + f.step < p.M) { next_mean = p.mean[row + f.step]; next_rstd = p.rstd[row + f.step]; }
+    f.take(row, stage);
+    const F2 minus = pack2(-mean, -mean), times = pack2(rstd, rstd);
+    F2 a = zero, b = zero;
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      g[i][j] = c + j < p.D ? (p.gamma ? p.gamma[c + j] : 1.f) : 0.f;
-      dg[i][j] = db[i][j] = 0.f;
-    }
-  }
-  int buf = 0;
-  for (int64_t row = blockIdx.x * (int64_t)groups + group; row < p.M; row += (int64_t)gridDim.x * groups) {
-    const T* xr = reinterpret_cast<const T*>(p.x) + row * p.ldx;
-    const T* dr = reinterpret_cast<const T*>(p.dy) + row * p.lddy;
-    const float mean = p.mean[row], rstd = p.rstd[row];
-    float x[NV][VEC], d[NV][VEC];
+    for (int q0 = 0; q0 < NP; q0 += 2) {
+      if (!f.has(q0)) continue;
+      F2 g[2];
+      f.vec4(sc, q0, g[0], g[1]);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (t + i * tpr) * VEC;
-      if (c < p.D) {
-        load_vec<T, VEC>(xr + c, x[i]);
-        load_vec<T, VEC>(dr + c, d[i]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) { x[i][j] = mean; d[i][j] = 0.f; }
+      for (int q = q0; q < q0 + 2; ++q) {
+        if (VEC == 1 && !f.has(q)) continue;
+        const F2 d = f.get(1, q, 0.f), xh = mul2(add2(f.get(0, q, mean), minus), times), w = mul2(d, g[q - q0]);
+        dg[q] = fma2(d, xh, dg[q]);
+        db[q] = add2(db[q], d);
+        a = add2(a, w);
+        b = fma2(w, xh, b);
       }
     }
-    float s1 = 0.f, s2 = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        const float xh = (x[i][j] - mean) * rstd;
-        dg[i][j] = fmaf(d[i][j], xh, dg[i][j]);
-        db[i][j] += d[i][j];
-        x[i][j] = xh;
-        d[i][j] *= g[i][j];
-        s1 += d[i][j];
-        s2 = fmaf(d[i][j], xh, s2);
-      }
-    s1 = warp_sum(s1);
-    s2 = warp_sum(s2);
-    if (wpr > 1) {
-      float* w = wsum + buf * 64;
-      if (lane == 0) { w[2 * warp] = s1; w[2 * warp + 1] = s2; }
-      asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(tpr) : "memory");
-      s1 = s2 = 0.f;
-      for (int k = 0; k < wpr; ++k) {
-        s1 += w[2 * (w0 + k)];
-        s2 += w[2 * (w0 + k) + 1];
-      }
-      buf ^= 1;
-    }
-    const float c1 = s1 * inv_d, c2 = s2 * inv_d;
-    T* or_ = reinterpret_cast<T*>(p.dx) + row * p.lddx;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (t + i * tpr) * VEC;
-      if (c >= p.D) continue;
-      float o[VEC];
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) o[j] = rstd * (d[i][j] - c1 - x[i][j] * c2);
-      store_vec<T, VEC>(or_ + c, o);
-    }
+    float s[2] = {sum2(a), sum2(b)};
+    group_sums<2>(s, ln_smem + 64 * buf, group, wpr);
+    buf ^= 1;
+    // rstd (w - c1 - xh c2) = w rstd - c1 rstd - (x - mean) rstd^2 c2
+    const float c1 = -s[0] * inv_d * rstd, c2 = -s[1] * inv_d * rstd * rstd;
+    const F2 p1 = pack2(c1, c1), p2 = pack2(c2, c2);
+    put_row<T, VEC, EPT>(f, reinterpret_cast<T*>(p.dx) + row * p.lddx + t * VEC, [&](int q, F2& o0, F2& o1) {
+      F2 g0, g1;
+      f.vec4(sc, q, g0, g1);
+      o0 = fma2(add2(f.get(0, q, mean), minus), p2, fma2(mul2(f.get(1, q, 0.f), g0), times, p1));
+      o1 = fma2(add2(f.get(0, q + 1, mean), minus), p2, fma2(mul2(f.get(1, q + 1, 0.f), g1), times, p1));
+    });
+    mean = next_mean;
+    rstd = next_rstd;
   }
   if (!p.part) return;
-  // the groups' column sums, group by group
+  // every group's column sums, added in the groups' order
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();
+  float* mine = colsum + (int64_t)group * 2 * p.D + t * VEC;
+#pragma unroll
+  for (int q = 0; q < NP; ++q) {
+    if (!f.has(q)) continue;
+    const int c = f.at(q), second = VEC == 1 ? f.hop : 1;
+    float x, y;
+    unpack2(dg[q], x, y);
+    mine[c] = x;
+    if (VEC > 1 || f.in(2 * q + 1)) mine[c + second] = y;
+    unpack2(db[q], x, y);
+    mine[p.D + c] = x;
+    if (VEC > 1 || f.in(2 * q + 1)) mine[p.D + c + second] = y;
+  }
+  __syncthreads();
   float* out = p.part + (int64_t)blockIdx.x * 2 * p.D;
-  for (int k = 0; k < groups; ++k) {
-    if (group == k) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (t + i * tpr) * VEC;
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          if (c + j >= p.D) continue;
-          if (k > 0) {
-            dg[i][j] += colsum[c + j];
-            db[i][j] += colsum[p.D + c + j];
-          }
-          if (k + 1 < groups) {
-            colsum[c + j] = dg[i][j];
-            colsum[p.D + c + j] = db[i][j];
-          } else {
-            out[c + j] = dg[i][j];
-            out[p.D + c + j] = db[i][j];
-          }
-        }
-      }
-    }
-    __syncthreads();
+  for (int c = threadIdx.x; c < 2 * p.D; c += blockDim.x) {
+    float sum = 0.f;
+    for (int k = 0; k < groups; ++k) sum += colsum[(int64_t)k * 2 * p.D + c];
+    out[c] = sum;
   }
 }
 
@@ -369,28 +558,28 @@ __global__ void __launch_bounds__(256) ln_bwd_wide_cols_kernel(const __grid_cons
   out[p.D + c] = db;
 }
 
-// dgamma and dbeta from the blocks' partial rows: 32 columns per block, eight
-// warps that each add every eighth partial, then the eight sums in order.
+// dgamma and dbeta from the blocks' partial rows: 32 columns per block, 32
+// warps that each add every 32nd partial, then the 32 sums in order.
 struct LnReduceParams {
   const float* part; int parts; int D;
   float* dgamma; float* dbeta;
 };
-__global__ void __launch_bounds__(256) ln_param_reduce_kernel(const __grid_constant__ LnReduceParams p) {
+__global__ void __launch_bounds__(1024) ln_param_reduce_kernel(const __grid_constant__ LnReduceParams p) {
   pdl_enter();
-  __shared__ float sh[8][32];
+  __shared__ float sh[32][32];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int64_t c = blockIdx.x * (int64_t)32 + lane, n = 2 * (int64_t)p.D;
   float s = 0.f;
   if (c < n) {
 #pragma unroll 4
-    for (int k = w; k < p.parts; k += 8) s += p.part[k * n + c];
+    for (int k = w; k < p.parts; k += 32) s += p.part[k * n + c];
   }
   sh[w][lane] = s;
   __syncthreads();
   if (w == 0 && c < n) {
     s = 0.f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) s += sh[k][lane];
+    for (int k = 0; k < 32; ++k) s += sh[k][lane];
     if (c < p.D) {
       if (p.dgamma) p.dgamma[c] = s;
     } else if (p.dbeta) {
@@ -399,32 +588,55 @@ __global__ void __launch_bounds__(256) ln_param_reduce_kernel(const __grid_const
   }
 }
 
-template <typename T, int VEC, int WARPS>
-const void* fwd_pick(int64_t D) {
-  constexpr int unit = 32 * WARPS;
-  if (D <= unit * 8) return (const void*)ln_fwd_kernel<T, VEC, 8 / VEC, WARPS>;
-  if (D <= unit * 16) return (const void*)ln_fwd_kernel<T, VEC, 16 / VEC, WARPS>;
-  return (const void*)ln_fwd_kernel<T, VEC, 32 / VEC, WARPS>;
-}
-
 bool aligned16(const void* p, int64_t ld, size_t es) {
   return ((uintptr_t)p & 15) == 0 && (ld * (int64_t)es) % 16 == 0;
 }
 
-// Blocks (and partial rows) of the backward, and its threads per row.
-struct BwdShape { int tpr, threads; int64_t blocks; };
-BwdShape bwd_shape(int64_t M, int64_t D) {
-  BwdShape s;
-  if (D > kMaxRow) {
-    s.tpr = s.threads = 0;
-    s.blocks = std::min<int64_t>(M, 32);
-    return s;
-  }
-  s.tpr = (int)(32 * ceil_div(D, 32 * kBwdEpt));
-  const int groups = std::min(std::max(1, 512 / s.tpr), 15);   // (named barriers 1..15)
+// How a block walks rows of D elements: elements per thread, threads per row,
+// block and grid.
+struct RowShape { int ept, tpr, threads; int64_t blocks; };
+template <bool FWD>
+RowShape row_shape(bool f32, bool vec, int64_t M, int64_t D) {
+  RowShape s;
+  s.ept = D <= 256 ? 8 : D <= 512 || f32 || !vec ? 16 : 32;
+  s.tpr = (int)(32 * ceil_div(D, 32 * s.ept));
+  // (rows of two warps and more: 15 named barriers.  The forward's scale and
+  // shift leave 768 threads' rings beside them from 4096 elements on.)
+  int groups = (FWD && D > 4096 ? 768 : RowCfg<FWD>::THREADS) / s.tpr;
+  if (s.tpr > 32) groups = std::min(groups, 15);
   s.threads = s.tpr * groups;
-  s.blocks = std::min<int64_t>(ceil_div(M, groups), kSMs * std::max(1, 1024 / s.threads));
+  s.blocks = std::min<int64_t>(ceil_div(M, groups), kSMs);
   return s;
+}
+template <bool FWD>
+unsigned row_smem(const RowShape& s, bool ring, int64_t D) {
+  const int64_t fixed = kSumBytes + (FWD ? 2 : 1) * (int64_t)s.tpr * s.ept * 4, cols = (int64_t)(s.threads / s.tpr) * 2 * D * 4;
+  return (unsigned)(fixed + std::max<int64_t>(ring ? s.threads * RowCfg<FWD>::RING : 0, FWD ? 0 : cols));
+}
+// Blocks of the backward, each with its partial rows of dgamma and dbeta (the
+// most that any alignment of this shape takes).
+int64_t bwd_blocks(bool f32, bool vec, int64_t M, int64_t D) {
+  return D > kMaxRow ? std::min<int64_t>(M, 32) : row_shape<false>(f32, vec, M, D).blocks;
+}
+
+template <typename T, int VEC, int EPT, bool FWD>
+const void* row_kernel() {
+  static std::once_flag once;
+  const void* k = FWD ? (const void*)ln_fwd_kernel<T, VEC, EPT> : (const void*)ln_bwd_kernel<T, VEC, EPT>;
+  std::call_once(once, [k] {
+    cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
+  });
+  return k;
+}
+template <bool FWD>
+const void* row_pick(bool f32, bool vec, int ept) {
+  if (f32) {
+    if (vec) return ept == 8 ? row_kernel<float, 4, 8, FWD>() : row_kernel<float, 4, 16, FWD>();
+    return ept == 8 ? row_kernel<float, 1, 8, FWD>() : row_kernel<float, 1, 16, FWD>();
+  }
+  using B = __nv_bfloat16;
+  if (vec) return ept == 8 ? row_kernel<B, 8, 8, FWD>() : ept == 16 ? row_kernel<B, 8, 16, FWD>() : row_kernel<B, 8, 32, FWD>();
+  return ept == 8 ? row_kernel<B, 1, 8, FWD>() : row_kernel<B, 1, 16, FWD>();
 }
 
 }  // namespace
@@ -434,33 +646,31 @@ int layernorm_plan(const LayerNormOp& op, LaunchRec* rec, char* err, size_t errl
     snprintf(err, errlen, "bad layer-norm shape %lld x %lld", (long long)op.M, (long long)op.D);
     return -1;
   }
-  const LnFwdParams q{op.x, op.ldx, op.gamma, op.beta, op.y, op.ldy, op.mean, op.rstd, op.M, (int)op.D, op.eps};
   const bool f32 = op.dtype == DT_F32;
   const size_t es = f32 ? 4 : 2;
-  const int vec = f32 ? 4 : 8;
-  const bool v = op.D % vec == 0 && aligned16(op.x, op.ldx, es) && aligned16(op.y, op.ldy, es) &&
-                 aligned16(op.gamma, 0, 4) && aligned16(op.beta, 0, 4);
-  rec->block = dim3(256);
-  rec->grid = dim3((unsigned)op.M);
+  const bool v = op.D % (f32 ? 4 : 8) == 0 && aligned16(op.x, op.ldx, es) && aligned16(op.y, op.ldy, es);
+  LnFwdParams q{op.x, op.ldx, op.gamma, op.beta, op.y, op.ldy, op.mean, op.rstd, op.M, (int)op.D, op.eps, 0};
   if (op.D > kMaxRow) {
     rec->func = f32 ? (const void*)ln_fwd_wide_kernel<float> : (const void*)ln_fwd_wide_kernel<__nv_bfloat16>;
+    rec->grid = dim3((unsigned)op.M);
     rec->block = dim3(1024);
-  } else if (op.D <= 1024) {
-    rec->grid = dim3((unsigned)ceil_div(op.M, 8));
-    rec->func = f32 ? (v ? fwd_pick<float, 4, 1>(op.D) : fwd_pick<float, 1, 1>(op.D))
-                    : (v ? fwd_pick<__nv_bfloat16, 8, 1>(op.D) : fwd_pick<__nv_bfloat16, 1, 1>(op.D));
+    rec->smem = 0;
   } else {
-    rec->func = f32 ? (v ? fwd_pick<float, 4, 8>(op.D) : fwd_pick<float, 1, 8>(op.D))
-                    : (v ? fwd_pick<__nv_bfloat16, 8, 8>(op.D) : fwd_pick<__nv_bfloat16, 1, 8>(op.D));
+    const RowShape s = row_shape<true>(f32, v, op.M, op.D);
+    q.tpr = s.tpr;
+    rec->func = row_pick<true>(f32, v, s.ept);
+    rec->grid = dim3((unsigned)s.blocks);
+    rec->block = dim3((unsigned)s.threads);
+    rec->smem = row_smem<true>(s, v, op.D);
   }
-  rec->smem = 0;
   rec->name = "layernorm_fwd";
   rec->set_args(q);
   return 1;
 }
 
-size_t layernorm_bwd_workspace_bytes(int64_t M, int64_t D) {
-  return (size_t)bwd_shape(M, D).blocks * 2 * (size_t)D * sizeof(float);
+size_t layernorm_bwd_workspace_bytes(int dtype, int64_t M, int64_t D) {
+  const bool f32 = dtype == DT_F32;
+  return (size_t)std::max(bwd_blocks(f32, true, M, D), bwd_blocks(f32, false, M, D)) * 2 * (size_t)D * sizeof(float);
 }
 
 int layernorm_bwd_plan(const LayerNormBwdOp& op, LaunchRec* recs, char* err, size_t errlen) {
@@ -470,25 +680,24 @@ int layernorm_bwd_plan(const LayerNormBwdOp& op, LaunchRec* recs, char* err, siz
     return -1;
   }
   const bool params = op.dgamma || op.dbeta;
-  if (params && (!op.ws || op.ws_bytes < layernorm_bwd_workspace_bytes(op.M, op.D) || (uintptr_t)op.ws % 4)) {
+  if (params && (!op.ws || op.ws_bytes < layernorm_bwd_workspace_bytes(op.dtype, op.M, op.D) || (uintptr_t)op.ws % 4)) {
     snprintf(err, errlen, "layer-norm backward workspace too small (%zu < %zu) or misaligned", op.ws_bytes,
-             layernorm_bwd_workspace_bytes(op.M, op.D));
+             layernorm_bwd_workspace_bytes(op.dtype, op.M, op.D));
     return -1;
   }
-  const BwdShape s = bwd_shape(op.M, op.D);
   const bool f32 = op.dtype == DT_F32;
   const size_t es = f32 ? 4 : 2;
-  const int vec = f32 ? 4 : 8;
-  const bool v = op.D % vec == 0 && aligned16(op.x, op.ldx, es) && aligned16(op.dy, op.lddy, es) &&
+  const bool v = op.D % (f32 ? 4 : 8) == 0 && aligned16(op.x, op.ldx, es) && aligned16(op.dy, op.lddy, es) &&
                  aligned16(op.dx, op.lddx, es);
-  const LnBwdParams q{op.dy, op.lddy, op.x, op.ldx, op.gamma, op.mean, op.rstd, op.dx, op.lddx,
-                      params ? op.ws : nullptr, op.M, (int)op.D, s.tpr};
+  const int64_t blocks = bwd_blocks(f32, v, op.M, op.D);
+  LnBwdParams q{op.dy, op.lddy, op.x, op.ldx, op.gamma, op.mean, op.rstd, op.dx, op.lddx,
+                params ? op.ws : nullptr, op.M, (int)op.D, 0};
   int n = 0;
   if (op.D > kMaxRow) {
     if (params) {
       recs[n].func = f32 ? (const void*)ln_bwd_wide_cols_kernel<float>
                          : (const void*)ln_bwd_wide_cols_kernel<__nv_bfloat16>;
-      recs[n].grid = dim3((unsigned)s.blocks, (unsigned)ceil_div(op.D, 256));
+      recs[n].grid = dim3((unsigned)blocks, (unsigned)ceil_div(op.D, 256));
       recs[n].block = dim3(256);
       recs[n].name = "layernorm_bwd_cols";
       recs[n++].set_args(q);
@@ -497,21 +706,20 @@ int layernorm_bwd_plan(const LayerNormBwdOp& op, LaunchRec* recs, char* err, siz
     recs[n].grid = dim3((unsigned)op.M);
     recs[n].block = dim3(1024);
   } else {
-    recs[n].func = f32 ? (v ? (const void*)ln_bwd_kernel<float, 4> : (const void*)ln_bwd_kernel<float, 1>)
-                       : (v ? (const void*)ln_bwd_kernel<__nv_bfloat16, 8>
-                            : (const void*)ln_bwd_kernel<__nv_bfloat16, 1>);
+    const RowShape s = row_shape<false>(f32, v, op.M, op.D);
+    q.tpr = s.tpr;
+    recs[n].func = row_pick<false>(f32, v, s.ept);
     recs[n].grid = dim3((unsigned)s.blocks);
     recs[n].block = dim3((unsigned)s.threads);
-    // warp sums, and the column sums handed from group to group
-    recs[n].smem = (unsigned)(128 * 4 + (s.threads > s.tpr ? 2 * op.D * 4 : 0));
+    recs[n].smem = row_smem<false>(s, v, op.D);
   }
   recs[n].name = "layernorm_bwd";
   recs[n++].set_args(q);
   if (params) {
-    const LnReduceParams r{op.ws, (int)s.blocks, (int)op.D, op.dgamma, op.dbeta};
+    const LnReduceParams r{op.ws, (int)blocks, (int)op.D, op.dgamma, op.dbeta};
     recs[n].func = (const void*)ln_param_reduce_kernel;
     recs[n].grid = dim3((unsigned)ceil_div(2 * op.D, 32));
-    recs[n].block = dim3(256);
+    recs[n].block = dim3(1024);
     recs[n].name = "layernorm_param_reduce";
     recs[n++].set_args(r);
   }
