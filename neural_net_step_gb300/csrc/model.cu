@@ -1332,6 +1332,30 @@ static mlp_status run_ops(LaunchRec* r, int n, void* stream) {
   return ok();
 }
 
+// The kernels of one operation in order: those after the first are launched
+// as soon as their predecessor's blocks have started (a programmatic edge) and
+// wait for its results themselves (pdl_enter), so that their launch latency
+// runs beside it.
+static mlp_status run_chain(LaunchRec* r, int n, void* stream) {
+  for (int i = 0; i < n; ++i) {
+    cudaLaunchConfig_t cfg;
+    memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = r[i].grid;
+    cfg.blockDim = r[i].block;
+    cfg.dynamicSmemBytes = r[i].smem;
+    cfg.stream = (cudaStream_t)stream;
+    cudaLaunchAttribute a;
+    a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    a.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &a;
+    cfg.numAttrs = i > 0 ? 1 : 0;
+    void* argp[1] = {r[i].args};
+    cudaError_t e = cudaLaunchKernelExC(&cfg, r[i].func, argp);
+    if (e != cudaSuccess) return fail(MLP_ERR_CUDA, "launch of %s failed: %s", r[i].name, cudaGetErrorString(e));
+  }
+  return ok();
+}
+
 static bool dtype_ok(int d) { return d == MLP_F32 || d == MLP_BF16; }
 static bool gemm_dtype_ok(int d) { return d == MLP_F32 || d == MLP_BF16 || d == MLP_F32X3; }
 static bool act_ok(int a) { return a >= MLP_ACT_NONE && a <= MLP_ACT_GELU_TANH; }
@@ -1623,7 +1647,7 @@ mlp_status mlp_op_layernorm_backward(int dtype, int64_t M, int64_t D, const void
   char e_[512] = "";
   const int n = layernorm_bwd_plan(op, r, e_, sizeof(e_));
   if (n < 0) return fail(MLP_ERR_SHAPE, "%s", e_);
-  return run_ops(r, n, stream);
+  return run_chain(r, n, stream);
 }
 
 mlp_status mlp_op_quant8(int dtype, int64_t rows, int64_t cols, const void* X, int64_t ldx, uint8_t* Q, int64_t ldq,
@@ -1741,7 +1765,7 @@ mlp_status mlp_op_wgrad8(int dtype, int64_t N, int64_t K, int64_t B, const void*
   op.err = err_dev;
   const int n = gemm_plan(op, r + 1, e_, sizeof(e_));
   if (n < 0) return fail(MLP_ERR_SHAPE, "%s", e_);
-  return run_ops(r, n + 1, stream);
+  return run_chain(r, n + 1, stream);
 }
 
 }  // extern "C"

@@ -139,15 +139,17 @@ __device__ __forceinline__ float sum2(F2 x) {
 // other; the rest are loaded when their turn comes.  The scale and the shift
 // lie in shared memory.
 //   EPT: with 8 elements a thread the kernels were bound by instruction issue
-// (about 250 instructions a row and warp besides the elements: 94 us for
-// 65536 x 1024 bf16 forward); with 32 the sums cost a tenth of that.  bf16
-// takes 32, fp32 and unaligned rows 16 (their registers), short rows fewer.
+// (about 250 instructions a row and warp besides the elements: 94 us for the
+// forward of 65536 x 1024 bf16); more elements share that.  The forward takes
+// 32 of bf16 (47 us); the backward, whose 2 EPT column sums stay in registers,
+// and fp32 and unaligned rows take 16 (backward of the same: 75 us; with 32
+// the sums spill, 142 us); short rows 8.
 template <bool FWD> struct RowCfg {   // one block to an SM
   static constexpr int THREADS = FWD ? 1024 : 512;   // at most (64 and 128 registers)
   static constexpr int RING = FWD ? 192 : 384;       // bytes of the ring per thread
 };
 
-template <typename T, int VEC, int EPT, int NT>   // NT tensors a row: x, or x and dy
+template <typename T, int VEC, int EPT, int NT, bool FULL>   // NT tensors a row: x, or x and dy; FULL: no thread's elements end early
 struct RowFetch {
   static constexpr int NV = EPT / VEC;
   static constexpr bool RING = VEC > 1;
@@ -172,7 +174,7 @@ struct RowFetch {
 #pragma unroll
     for (int k = 0; k < NT; ++k) src[k] += t * VEC;
   }
-  __device__ __forceinline__ bool in(int i) const { return i * hop < cols; }
+  __device__ __forceinline__ bool in(int i) const { return FULL || i * hop < cols; }
   __device__ __forceinline__ void issue(int64_t row, int stage) {
     if constexpr (RING) {
       if (row < M) {
@@ -307,10 +309,10 @@ __device__ __forceinline__ void group_sums(float (&v)[NS], float* w, int group, 
 
 constexpr int kSumBytes = 2 * 32 * 2 * 4;   // group_sums' two buffers
 
-template <typename T, int VEC, int EPT>
+template <typename T, int VEC, int EPT, bool FULL>
 __global__ void __launch_bounds__(RowCfg<true>::THREADS, 1) ln_fwd_kernel(const __grid_constant__ LnFwdParams p) {
   pdl_enter();
-  using F = RowFetch<T, VEC, EPT, 1>;
+  using F = RowFetch<T, VEC, EPT, 1, FULL>;
   constexpr int NP = EPT / 2;
   extern __shared__ __align__(16) float ln_smem[];
   const int tpr = p.tpr, groups = (int)blockDim.x / tpr, wpr = tpr >> 5;
@@ -424,10 +426,10 @@ struct LnBwdParams {
 // The groups keep their columns' dgamma / dbeta sums in registers and add them
 // over the block at the end: one partial row pair per block.  x and dy stay
 // packed between the two uses of a row.
-template <typename T, int VEC, int EPT>
+template <typename T, int VEC, int EPT, bool FULL>
 __global__ void __launch_bounds__(RowCfg<false>::THREADS, 1) ln_bwd_kernel(const __grid_constant__ LnBwdParams p) {
   pdl_enter();
-  using F = RowFetch<T, VEC, EPT, 2>;
+  using F = RowFetch<T, VEC, EPT, 2, FULL>;
   constexpr int NP = EPT / 2;
   extern __shared__ __align__(16) float ln_smem[];
   const int tpr = p.tpr, groups = (int)blockDim.x / tpr, wpr = tpr >> 5;
@@ -598,7 +600,7 @@ struct RowShape { int ept, tpr, threads; int64_t blocks; };
 template <bool FWD>
 RowShape row_shape(bool f32, bool vec, int64_t M, int64_t D) {
   RowShape s;
-  s.ept = D <= 256 ? 8 : D <= 512 || f32 || !vec ? 16 : 32;
+  s.ept = D <= 256 ? 8 : D <= 512 || f32 || !vec || !FWD ? 16 : 32;
   s.tpr = (int)(32 * ceil_div(D, 32 * s.ept));
   // (rows of two warps and more: 15 named barriers.  The forward's scale and
   // shift leave 768 threads' rings beside them from 4096 elements on.)
@@ -619,24 +621,29 @@ int64_t bwd_blocks(bool f32, bool vec, int64_t M, int64_t D) {
   return D > kMaxRow ? std::min<int64_t>(M, 32) : row_shape<false>(f32, vec, M, D).blocks;
 }
 
-template <typename T, int VEC, int EPT, bool FWD>
+template <typename T, int VEC, int EPT, bool FULL, bool FWD>
 const void* row_kernel() {
   static std::once_flag once;
-  const void* k = FWD ? (const void*)ln_fwd_kernel<T, VEC, EPT> : (const void*)ln_bwd_kernel<T, VEC, EPT>;
-  std::call_once(once, [k] {
-    cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
-  });
+  const void* k = FWD ? (const void*)ln_fwd_kernel<T, VEC, EPT, FULL> : (const void*)ln_bwd_kernel<T, VEC, EPT, FULL>;
+  std::call_once(once, [k] { cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448); });
   return k;
 }
+// FULL where every thread's elements are all there (a row length that is a
+// multiple of 32 EPT): no tests of the columns, half the instructions.
+template <typename T, int VEC, int EPT, bool FWD>
+const void* row_full(bool full) {
+  return full ? row_kernel<T, VEC, EPT, true, FWD>() : row_kernel<T, VEC, EPT, false, FWD>();
+}
 template <bool FWD>
-const void* row_pick(bool f32, bool vec, int ept) {
-  if (f32) {
-    if (vec) return ept == 8 ? row_kernel<float, 4, 8, FWD>() : row_kernel<float, 4, 16, FWD>();
-    return ept == 8 ? row_kernel<float, 1, 8, FWD>() : row_kernel<float, 1, 16, FWD>();
-  }
+const void* row_pick(bool f32, bool vec, const RowShape& s, int64_t D) {
   using B = __nv_bfloat16;
-  if (vec) return ept == 8 ? row_kernel<B, 8, 8, FWD>() : ept == 16 ? row_kernel<B, 8, 16, FWD>() : row_kernel<B, 8, 32, FWD>();
-  return ept == 8 ? row_kernel<B, 1, 8, FWD>() : row_kernel<B, 1, 16, FWD>();
+  const bool e8 = s.ept == 8, full = D == (int64_t)s.tpr * s.ept;
+  if (!vec) {
+    if (f32) return e8 ? row_kernel<float, 1, 8, false, FWD>() : row_kernel<float, 1, 16, false, FWD>();
+    return e8 ? row_kernel<B, 1, 8, false, FWD>() : row_kernel<B, 1, 16, false, FWD>();
+  }
+  if (f32) return e8 ? row_full<float, 4, 8, FWD>(full) : row_full<float, 4, 16, FWD>(full);
+  return e8 ? row_full<B, 8, 8, FWD>(full) : s.ept == 16 ? row_full<B, 8, 16, FWD>(full) : row_full<B, 8, 32, FWD>(full);
 }
 
 }  // namespace
@@ -658,7 +665,7 @@ int layernorm_plan(const LayerNormOp& op, LaunchRec* rec, char* err, size_t errl
   } else {
     const RowShape s = row_shape<true>(f32, v, op.M, op.D);
     q.tpr = s.tpr;
-    rec->func = row_pick<true>(f32, v, s.ept);
+    rec->func = row_pick<true>(f32, v, s, op.D);
     rec->grid = dim3((unsigned)s.blocks);
     rec->block = dim3((unsigned)s.threads);
     rec->smem = row_smem<true>(s, v, op.D);
@@ -708,7 +715,7 @@ int layernorm_bwd_plan(const LayerNormBwdOp& op, LaunchRec* recs, char* err, siz
   } else {
     const RowShape s = row_shape<false>(f32, v, op.M, op.D);
     q.tpr = s.tpr;
-    recs[n].func = row_pick<false>(f32, v, s.ept);
+    recs[n].func = row_pick<false>(f32, v, s, op.D);
     recs[n].grid = dim3((unsigned)s.blocks);
     recs[n].block = dim3((unsigned)s.threads);
     recs[n].smem = row_smem<false>(s, v, op.D);
