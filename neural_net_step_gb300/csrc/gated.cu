@@ -5,12 +5,13 @@
 //             dS = [dH * u * act'(g) | dH * act(g)], H = act(g) * u again.
 // s is kept for the backward in the dtype or in 8 bits (e4m3.cuh).
 //
-// bf16 runs on the tensor cores (gated_tc.cu).  fp32 on the FFMA pipes: 128 x 128 tiles, 8 x 8 results per thread, 16-deep
-// slices through shared memory.  The forward's tile is 64 gate and the 64 up
-// columns that belong to them, so a thread holds both factors of its results.
+// bf16 runs on the tensor cores (gated_tc.cu; a few rows: gated_small.cu).  fp32
+// on the FFMA pipes: tiles of 16 RM rows by 128 columns, RM x 8 results per
+// thread.  The forward's tile is 64 gate and the 64 up columns that belong to
+// them, so a thread holds both factors of its results.
 #include <stdio.h>
 
-#include <algorithm>
+#include <mutex>
 
 #include "common.cuh"
 #include "e4m3.cuh"
@@ -33,83 +34,110 @@ struct GatedParams {
   int act;
 };
 
-constexpr int GT = 128, GK = 16;
+// Tile of 16 RM rows by GT columns, GK deep, in a ring of GSTAGES slices that
+// cp.async fills an element at a time (any alignment; elements outside the
+// matrices as zeros) and transposes on the way.
+constexpr int GT = 128, GK = 16, GSTAGES = 4;
 
-template <bool FWD>
+__device__ __forceinline__ void copy4(uint32_t dst, const float* src, bool in) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
+}
+// d += a b on two fp32 values at once.
+__device__ __forceinline__ void fma2(uint64_t& d, uint64_t a, uint64_t b) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
+}
+
+template <bool FWD, int RM>   // RM rows and 8 columns per thread
 __global__ void __launch_bounds__(256) gated_simt_kernel(const __grid_constant__ GatedParams p) {
   pdl_enter();
-  __shared__ __align__(16) float As[2][GK][GT + 4];
-  __shared__ __align__(16) float Bs[2][GK][GT + 4];
-  constexpr int PER = GT * GK / 256;
+  constexpr int BM = 16 * RM, PA = BM + 4, PB = GT + 4;   // rows, pitches of the two slices
+  constexpr int SLICE = GK * (PA + PB);
+  extern __shared__ __align__(16) float gated_smem[];     // [GSTAGES][GK][PA], [GK][PB]
   constexpr int TF = FWD ? GT / 2 : GT;   // F columns per tile
   const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
-  const int m0 = blockIdx.y * GT, f0 = blockIdx.x * TF;
+  const int m0 = blockIdx.y * BM, f0 = blockIdx.x * TF;
   const float* A = p.A;
   const float* B = p.B;
-  float ra[PER], rb[PER];
-  auto load = [&](int k0) {
+  const uint32_t base = (uint32_t)__cvta_generic_to_shared(gated_smem);
+  auto load = [&](int slice) {
+    const int k0 = slice * GK;
+    const uint32_t as = base + (uint32_t)((slice % GSTAGES) * SLICE) * 4u, bs = as + GK * PA * 4u;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int idx = tid + i * 256, m = idx / GK, k = k0 + idx % GK;
-      ra[i] = (m0 + m < p.M && k < p.K) ? A[(int64_t)(m0 + m) * p.lda + k] : 0.f;
+    for (int i = 0; i < RM; ++i) {
+      const int idx = tid + i * 256, m = idx / GK, kk = idx % GK, k = k0 + kk;
+      const bool in = m0 + m < p.M && k < p.K;
+      copy4(as + (uint32_t)(kk * PA + m) * 4u, in ? A + (int64_t)(m0 + m) * p.lda + k : A, in);
     }
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
+    for (int i = 0; i < GT * GK / 256; ++i) {
       const int idx = tid + i * 256;
       if (FWD) {   // tile column n: gate row f0 + n, or up row F + f0 + n - 64
-        const int n = idx / GK, k = k0 + idx % GK, f = f0 + (n & (TF - 1));
-        rb[i] = (f < p.F && k < p.K) ? B[((int64_t)f + (n < TF ? 0 : p.F)) * p.ldb + k] : 0.f;
+        const int n = idx / GK, kk = idx % GK, k = k0 + kk, f = f0 + (n & (TF - 1));
+        const bool in = f < p.F && k < p.K;
+        copy4(bs + (uint32_t)(kk * PB + n) * 4u, in ? B + ((int64_t)f + (n < TF ? 0 : p.F)) * p.ldb + k : B, in);
       } else {
-        const int n = idx % GT, k = k0 + idx / GT;
-        rb[i] = (f0 + n < p.F && k < p.K) ? B[(int64_t)k * p.ldb + f0 + n] : 0.f;
+        const int n = idx % GT, kk = idx / GT, k = k0 + kk;
+        const bool in = f0 + n < p.F && k < p.K;
+        copy4(bs + (uint32_t)(kk * PB + n) * 4u, in ? B + (int64_t)k * p.ldb + f0 + n : B, in);
       }
     }
   };
-  auto store = [&](int buf) {
+  // two columns to an accumulator: one instruction forms both products
+  uint64_t acc2[RM][4];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int idx = tid + i * 256;
-      As[buf][idx % GK][idx / GK] = ra[i];
-      if (FWD) Bs[buf][idx % GK][idx / GK] = rb[i];
-      else Bs[buf][idx / GT][idx % GT] = rb[i];
-    }
-  };
-  float acc[8][8];
+  for (int i = 0; i < RM; ++i)
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
-  load(0);
-  store(0);
-  __syncthreads();
+    for (int j = 0; j < 4; ++j) acc2[i][j] = 0ull;
   const int nt = (p.K + GK - 1) / GK;
+#pragma unroll
+  for (int s = 0; s < GSTAGES - 1; ++s) {
+    if (s < nt) load(s);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
   for (int t = 0; t < nt; ++t) {
-    const int cur = t & 1;
-    if (t + 1 < nt) load((t + 1) * GK);
+    asm volatile("cp.async.wait_group %0;" ::"n"(GSTAGES - 2) : "memory");
+    __syncthreads();   // slice t has landed for every thread, and slice t - 1 is read
+    if (t + GSTAGES - 1 < nt) load(t + GSTAGES - 1);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    const float* As = gated_smem + (t % GSTAGES) * SLICE;
+    const float* Bs = As + GK * PA;
 #pragma unroll
     for (int kk = 0; kk < GK; ++kk) {
-      float a[8], b[8];
-      *reinterpret_cast<float4*>(a) = *reinterpret_cast<const float4*>(&As[cur][kk][ty * 4]);
-      *reinterpret_cast<float4*>(a + 4) = *reinterpret_cast<const float4*>(&As[cur][kk][64 + ty * 4]);
-      *reinterpret_cast<float4*>(b) = *reinterpret_cast<const float4*>(&Bs[cur][kk][tx * 4]);
-      *reinterpret_cast<float4*>(b + 4) = *reinterpret_cast<const float4*>(&Bs[cur][kk][64 + tx * 4]);
+      // rows ty * 4 + 0..3 and 64 + the same (RM = 8), ty * 4 .. (4), ty * 2 .. (2)
+      float a[RM];
+      if constexpr (RM == 2) {
+        *reinterpret_cast<float2*>(a) = *reinterpret_cast<const float2*>(As + kk * PA + ty * 2);
+      } else {
+        *reinterpret_cast<float4*>(a) = *reinterpret_cast<const float4*>(As + kk * PA + ty * 4);
+        if constexpr (RM == 8) *reinterpret_cast<float4*>(a + 4) = *reinterpret_cast<const float4*>(As + kk * PA + 64 + ty * 4);
+      }
+      ulonglong2 b[2];
+      b[0] = *reinterpret_cast<const ulonglong2*>(Bs + kk * PB + tx * 4);
+      b[1] = *reinterpret_cast<const ulonglong2*>(Bs + kk * PB + 64 + tx * 4);
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
+      for (int i = 0; i < RM; ++i) {
+        uint64_t aa;
+        asm("mov.b64 %0, {%1, %1};" : "=l"(aa) : "f"(a[i]));
+        fma2(acc2[i][0], aa, b[0].x);
+        fma2(acc2[i][1], aa, b[0].y);
+        fma2(acc2[i][2], aa, b[1].x);
+        fma2(acc2[i][3], aa, b[1].y);
+      }
     }
-    if (t + 1 < nt) store(cur ^ 1);
-    __syncthreads();
   }
 
-  // thread (ty, tx): rows ty*4 + 0..3 and 64 + ty*4 + 0..3; tile columns
-  // tx*4 + 0..3 and 64 + tx*4 + 0..3 (the forward's second four are the up
+  float acc[RM][8];
+#pragma unroll
+  for (int i = 0; i < RM; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) asm("mov.b64 {%0, %1}, %2;" : "=f"(acc[i][2 * j]), "=f"(acc[i][2 * j + 1]) : "l"(acc2[i][j]));
+  // thread (ty, tx): its rows; tile columns tx*4 + 0..3 and 64 + tx*4 + 0..3 (the forward's second four are the up
   // columns of its first four)
   float* h = p.h;
   const int64_t nb = q8_blocks(p.F);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int m = m0 + (i < 4 ? ty * 4 + i : 60 + ty * 4 + i);
+  for (int i = 0; i < RM; ++i) {
+    const int m = m0 + (RM == 2 ? ty * 2 + i : i < 4 ? ty * 4 + i : 60 + ty * 4 + i);
     const bool row_ok = m < p.M;
     if (FWD) {
       const int f = f0 + tx * 4;
@@ -190,6 +218,21 @@ __global__ void __launch_bounds__(256) gated_simt_kernel(const __grid_constant__
   }
 }
 
+unsigned simt_smem(int rm) { return (unsigned)(GSTAGES * GK * (16 * rm + 4 + GT + 4) * 4); }
+template <bool FWD, int RM>
+const void* simt_kernel() {
+  static std::once_flag once;
+  std::call_once(once, [] {
+    cudaFuncSetAttribute((const void*)gated_simt_kernel<FWD, RM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                         simt_smem(RM));
+  });
+  return (const void*)gated_simt_kernel<FWD, RM>;
+}
+template <bool FWD>
+const void* simt_pick(int rm) {
+  return rm == 8 ? simt_kernel<FWD, 8>() : rm == 4 ? simt_kernel<FWD, 4>() : simt_kernel<FWD, 2>();
+}
+
 }  // namespace
 
 int gated_plan(const GatedOp& op, LaunchRec* rec, char* err, size_t errlen) {
@@ -197,17 +240,24 @@ int gated_plan(const GatedOp& op, LaunchRec* rec, char* err, size_t errlen) {
     snprintf(err, errlen, "bad gated shape M=%lld F=%lld K=%lld", (long long)op.M, (long long)op.F, (long long)op.K);
     return -1;
   }
+  if (gated_small_takes(op)) return gated_small_plan(op, rec);
   if (op.dtype == DT_BF16) return gated_tc_plan(op, rec, err, errlen);
   const GatedParams p{(const float*)op.A, op.lda, (const float*)op.B, op.ldb, op.bias, (float*)op.h, op.ldh,
                       op.s, op.lds, op.se, op.ldse, (float*)op.ds, op.ldds, (int)op.M, (int)op.F, (int)op.K, op.act};
-  rec->func = op.fwd ? (const void*)gated_simt_kernel<true> : (const void*)gated_simt_kernel<false>;
-  rec->grid = dim3((unsigned)ceil_div(op.F, op.fwd ? GT / 2 : GT), (unsigned)ceil_div(op.M, GT));
+  const int64_t cols = ceil_div(op.F, op.fwd ? GT / 2 : GT);
+  // the tallest tile that still gives most SMs one (fp32, forward / backward of
+  // 1000 x 1000 x 784 with rm = 8, 4, 2: 90, 107, 152 us from 128, 256, 512
+  // tiles; 97, 66, 87 us from 64, 128, 256; one row: 82, 58, 48 us)
+  int rm = 8;
+  while (rm > 2 && cols * ceil_div(op.M, 16 * rm) < 100) rm /= 2;
+  rec->func = op.fwd ? simt_pick<true>(rm) : simt_pick<false>(rm);
+  rec->grid = dim3((unsigned)cols, (unsigned)ceil_div(op.M, 16 * rm));
   if (rec->grid.y > 65535) {
     snprintf(err, errlen, "gated: %lld rows are too many", (long long)op.M);
     return -1;
   }
   rec->block = dim3(256);
-  rec->smem = 0;
+  rec->smem = simt_smem(rm);
   rec->name = op.fwd ? "gated_fwd" : "gated_dgrad";
   rec->set_args(p);
   return 1;

@@ -322,6 +322,9 @@ struct GatedOp {
 int gated_plan(const GatedOp& op, LaunchRec* rec, char* err, size_t errlen);
 int gated_tc_plan(const GatedOp& op, LaunchRec* rec, char* err, size_t errlen);   // bf16 (gated_tc.cu)
 
+bool gated_small_takes(const GatedOp& op);   // a few bf16 rows, forward (gated_small.cu)
+int gated_small_plan(const GatedOp& op, LaunchRec* rec);
+
 // One thread waits, through the bounded wait every tcgen05 kernel uses, for
 // an mbarrier phase that nothing completes: after limit_ns it marks
 // ERRBIT_TIMEOUT in err_dev and returns (the error path, exercised).
