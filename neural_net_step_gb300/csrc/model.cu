@@ -1761,6 +1761,7 @@ mlp_status mlp_op_wgrad8(int dtype, int64_t N, int64_t K, int64_t B, const void*
   op.A = dY; op.lda = ldy; op.a_kmajor = false;
   op.B = workspace; op.ldb = ldx; op.b_kmajor = false;
   op.dW = dW; op.ld_dw = lddw; op.db = db;
+  op.promote = true;
   op.ws = (float*)((uint8_t*)workspace + vbytes); op.ws_bytes = ws_bytes - vbytes;
   op.err = err_dev;
   const int n = gemm_plan(op, r + 1, e_, sizeof(e_));

@@ -69,6 +69,10 @@ struct GemmOp {
   // -1 where there is at least one full wave of pair tiles, 0 never, 1
   // wherever the form allows (N and M of at least 256, no softmax-CE)
   int cg2 = -1;
+  // weight gradient on CTA pairs: the reduction in chunks whose sums are added
+  // in fp32 registers (the tensor cores' accumulation loses more over a long
+  // one); elsewhere it has no effect
+  bool promote = false;
   float2* ce_stats = nullptr; float* ce_zy = nullptr;
   const float2* ce_rowstat = nullptr;
   const int32_t* ce_labels = nullptr;

@@ -1914,13 +1914,24 @@ struct W2Cfg {
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;         // 32 KB
   static constexpr int STAGES = 6;
   static constexpr int EPI_BYTES = P_EPI_WARPS * 4096;          // one 32 x 32 fp32 box per epilogue warp
-  static constexpr int TMEM_COLS = 256;                         // the dW accumulator, one buffer
+  static constexpr int ACC_COLS = 256;                          // the dW accumulator
   static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + EPI_BYTES + 1024 + 256;
   static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
-  static_assert(8 * (3 * STAGES + 3) <= 256, "barrier slots");
+  static_assert(8 * (3 * STAGES + 5) <= 256, "barrier slots");
 };
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
+// PROMOTE: the tensor cores' accumulation loses low bits with every MMA (it
+// does not round to nearest), so a long reduction is cut into chunks of
+// kPromoteStages stages, in two accumulator buffers in turn, and the epilogue
+// warps add each chunk to fp32 registers: 8192 x 1024 over 8192 rows of e4m3
+// values is 3.6e-6 off (2-norm) in one chain.  Their registers then hold the
+// sums throughout, so two warps of their own sum the bias gradient (12 warps
+// have as many registers each as 10).
+constexpr int kPromoteStages = 32;   // 2048 rows
+constexpr int kPromoteThreads = P_THREADS + 64;
+
+template <bool PROMOTE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PROMOTE ? kPromoteThreads : P_THREADS, 1)
 tc_wgrad_cg2_kernel(const __grid_constant__ WParams p) {
   using C = W2Cfg;
   extern __shared__ uint8_t smem_raw[];
@@ -1934,9 +1945,10 @@ tc_wgrad_cg2_kernel(const __grid_constant__ WParams p) {
   auto full_bar = [&](int s) { return bar_base + 8u * s; };
   auto empty_bar = [&](int s) { return bar_base + 8u * (C::STAGES + s); };
   auto dbdone_bar = [&](int s) { return bar_base + 8u * (2 * C::STAGES + s); };
-  const uint32_t tfull = bar_base + 8u * (3 * C::STAGES);
-  const uint32_t tempty = bar_base + 8u * (3 * C::STAGES + 1);
-  const uint32_t tmem_slot = bar_base + 8u * (3 * C::STAGES + 2);
+  constexpr int BUFS = PROMOTE ? 2 : 1;   // accumulator buffers
+  const uint32_t tfull = bar_base + 8u * (3 * C::STAGES);          // [BUFS]
+  const uint32_t tempty = tfull + 8u * BUFS;                       // [BUFS]
+  const uint32_t tmem_slot = tempty + 8u * BUFS;
   volatile uint32_t* tmem_slot_ptr = reinterpret_cast<volatile uint32_t*>(base_ptr + (tmem_slot - base));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();   // 0: the CTA whose thread issues the MMAs
@@ -1944,13 +1956,15 @@ tc_wgrad_cg2_kernel(const __grid_constant__ WParams p) {
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(full_bar(s), 1);
       mbar_init(empty_bar(s), 1);
-      mbar_init(dbdone_bar(s), P_EPI_WARPS);
+      mbar_init(dbdone_bar(s), PROMOTE ? 2 : P_EPI_WARPS);
     }
-    mbar_init(tfull, 1);
-    mbar_init(tempty, 2 * P_EPI_WARPS);   // the epilogue warps of both CTAs
+    for (int b = 0; b < BUFS; ++b) {
+      mbar_init(tfull + 8u * b, 1);
+      mbar_init(tempty + 8u * b, 2 * (P_EPI_WARPS + (PROMOTE ? 2 : 0)));   // the warps below of both CTAs
+    }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 1) tmem_alloc_cg2(tmem_slot, C::TMEM_COLS);
+  if (warp == 1) tmem_alloc_cg2(tmem_slot, BUFS * C::ACC_COLS);
   tc_fence_before();
   cluster_sync_all();   // both CTAs' barriers exist before either's use
   tc_fence_after();
@@ -2017,15 +2031,24 @@ tc_wgrad_cg2_kernel(const __grid_constant__ WParams p) {
   } else if (warp == 1) {
     // ---------------- MMA issuer (CTA 0) ----------------
     if (rank == 0 && lane == 0) {
-      int it = 0, tc = 0;
+      int it = 0, tc = 0, cc = 0;
       bool ok = true;
       for (int u = u0; u < p.num_units && ok; u += ustep, ++tc) {
         int m0, n0, split, kb0, kb1;
         unit_coords(u, m0, n0, split, kb0, kb1);
-        if (!mbar_wait_cluster(tempty, ((uint32_t)tc & 1u) ^ 1u, p.err)) break;
-        tc_fence_after();
-        const uint32_t d = tmem;
+        if (!PROMOTE) {
+          if (!mbar_wait_cluster(tempty, ((uint32_t)tc & 1u) ^ 1u, p.err)) break;
+          tc_fence_after();
+        }
+        uint32_t d = tmem;
         for (int kb = kb0; kb < kb1; ++kb, ++it) {
+          const bool first = PROMOTE ? (kb - kb0) % kPromoteStages == 0 : kb == kb0;   // of its accumulator
+          if (PROMOTE && first) {
+            // chunk cc goes to buffer cc % 2, once its last chunk is drained
+            if (!mbar_wait_cluster(tempty + 8u * (cc & 1), (((uint32_t)cc >> 1) & 1u) ^ 1u, p.err)) { ok = false; break; }
+            tc_fence_after();
+            d = tmem + (uint32_t)((cc & 1) * C::ACC_COLS);
+          }
           const int s = it % C::STAGES;
           if (!mbar_wait(full_bar(s), (uint32_t)(it / C::STAGES) & 1u, p.err)) { ok = false; break; }
           tc_fence_after();
@@ -2035,12 +2058,59 @@ tc_wgrad_cg2_kernel(const __grid_constant__ WParams p) {
           for (int kk = 0; kk < BK / 16; ++kk) {
             const uint64_t ad = sdesc(sa + kk * 2048u, (uint32_t)C::CHUNK_BYTES, 1024u);
             const uint64_t bd = sdesc(sb + kk * 2048u, (uint32_t)C::CHUNK_BYTES, 1024u);
-            mma_bf16_cg2(d, ad, bd, p.idesc, (kb > kb0 || kk > 0) ? 1u : 0u);
+            mma_bf16_cg2(d, ad, bd, p.idesc, (!first || kk > 0) ? 1u : 0u);
           }
           mma_commit_cg2(empty_bar(s));
+          if (PROMOTE && (kb + 1 == kb1 || (kb + 1 - kb0) % kPromoteStages == 0)) {
+            mma_commit_cg2(tfull + 8u * (cc & 1));
+            ++cc;
+          }
         }
-        mma_commit_cg2(tfull);
+        if (!PROMOTE) mma_commit_cg2(tfull);
       }
+    }
+  } else if (PROMOTE && warp >= 2 + P_EPI_WARPS) {
+    // ---------------- bias-gradient warps 10, 11 ----------------
+    // each sums what every second epilogue warp would (db_stage_add), stage by
+    // stage as the MMAs finish with them.  They keep step chunk by chunk, in units
+    // without a sum too: a wait for a stage's barrier tells its phases apart
+    // only while this warp is neither a phase ahead nor behind.
+    const int first = warp - 2 - P_EPI_WARPS;   // epilogue warps first, first + 2, ..
+    int it = 0, cc = 0;
+    bool ok = true;
+    for (int u = u0; u < p.num_units && ok; u += ustep) {
+      int m0, n0, split, kb0, kb1;
+      unit_coords(u, m0, n0, split, kb0, kb1);
+      const int part = unit_part(m0, n0);
+      float a0[4] = {0.f, 0.f, 0.f, 0.f}, a1[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int ks = kb0; ks < kb1 && ok; ks += kPromoteStages, ++cc) {
+        const int ke = min(kb1, ks + kPromoteStages);
+        if (part >= 0) {
+          for (int kb = ks; kb < ke && ok; ++kb, ++it) {
+            const int s = it % C::STAGES;
+            ok = __all_sync(0xffffffffu, mbar_wait(empty_bar(s), (uint32_t)(it / C::STAGES) & 1u, p.err));
+            if (!ok) break;
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+              if (db_warp_in_part(first + 2 * w, part, p.tiles_n, p.db_share))
+                db_stage_add(base_ptr + (a_base - base) + s * C::A_BYTES, first + 2 * w, lane, a0[w], a1[w]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(dbdone_bar(s));
+          }
+          if (!ok) break;
+        } else {
+          it += ke - ks;
+        }
+        const uint32_t buf = (uint32_t)cc & 1u;
+        ok = __all_sync(0xffffffffu, mbar_wait_cluster(tfull + 8u * buf, ((uint32_t)cc >> 1) & 1u, p.err));
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_cluster(lead_tempty + 8u * buf);
+      }
+      if (!ok || part < 0) continue;
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+        if (db_warp_in_part(first + 2 * w, part, p.tiles_n, p.db_share))
+          db_finish_store(a0[w], a1[w], first + 2 * w, lane, m0 + (int)rank * BM, p.M, split, p.db_out);
     }
   } else {
     // ---------------- epilogue warps 2..9: this CTA's 128 rows ----------------
@@ -2048,45 +2118,67 @@ tc_wgrad_cg2_kernel(const __grid_constant__ WParams p) {
     const int half = (warp - 2) >> 2;
     const uint32_t stage0 = epi_base + (uint32_t)((warp - 2) * 4096);
     uint8_t* srow = base_ptr + (stage0 - base) + lane * 128;
-    int tc = 0, it = 0;
+    int tc = 0, it = 0, cc = 0;
     bool ok = true;
     for (int u = u0; u < p.num_units && ok; u += ustep, ++tc) {
       int m0, n0, split, kb0, kb1;
       unit_coords(u, m0, n0, split, kb0, kb1);
       const int mr = m0 + (int)rank * BM;   // this CTA's rows
       const int part = unit_part(m0, n0);
-      if (part >= 0) {
-        // this unit's part of the bias gradient of this CTA's rows, stage by
-        // stage as the MMAs finish with them (the stage's bytes have landed
-        // by then); every warp waits and arrives, the part's warps sum
-        const bool mine = db_warp_in_part(warp - 2, part, p.tiles_n, p.db_share);
-        float a0 = 0.f, a1 = 0.f;
-        for (int kb = kb0; kb < kb1 && ok; ++kb, ++it) {
-          const int s = it % C::STAGES;
-          ok = __all_sync(0xffffffffu, mbar_wait(empty_bar(s), (uint32_t)(it / C::STAGES) & 1u, p.err));
-          if (!ok) break;
-          if (mine) db_stage_add(base_ptr + (a_base - base) + s * C::A_BYTES, warp - 2, lane, a0, a1);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(dbdone_bar(s));
-        }
-        if (!ok) break;
-        if (mine) db_finish_store(a0, a1, warp - 2, lane, mr, p.M, split, p.db_out);
-      } else {
-        it += kb1 - kb0;
-      }
-      ok = __all_sync(0xffffffffu, mbar_wait_cluster(tfull, (uint32_t)tc & 1u, p.err));
-      if (!ok) break;
-      tc_fence_after();
       // this warp's 128 columns into registers, the accumulator handed back
       // to CTA 0, then four 32 x 32 fp32 stores
       const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16);
       const int c0 = half * (C::TBN / 2);
       float v[128];
+      // PROMOTE: chunk by chunk, else the unit is one
+      const int chunk = PROMOTE ? kPromoteStages : kb1 - kb0;
+      const bool mine = part >= 0 && db_warp_in_part(warp - 2, part, p.tiles_n, p.db_share);
+      float a0 = 0.f, a1 = 0.f;
+      if (PROMOTE) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(trow, v + 32 * c, c0 + 32 * c);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(lead_tempty);
+        for (int j = 0; j < 128; ++j) v[j] = 0.f;
+      }
+#pragma unroll 1
+      for (int ks = kb0; ks < kb1 && ok; ks += chunk) {
+        const int ke = min(kb1, ks + chunk);
+        if (!PROMOTE && part >= 0) {
+          // this unit's part of the bias gradient of this CTA's rows, stage by
+          // stage as the MMAs finish with them (the stage's bytes have landed
+          // by then); every warp waits and arrives, the part's warps sum
+          for (int kb = ks; kb < ke && ok; ++kb, ++it) {
+            const int s = it % C::STAGES;
+            ok = __all_sync(0xffffffffu, mbar_wait(empty_bar(s), (uint32_t)(it / C::STAGES) & 1u, p.err));
+            if (!ok) break;
+            if (mine) db_stage_add(base_ptr + (a_base - base) + s * C::A_BYTES, warp - 2, lane, a0, a1);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(dbdone_bar(s));
+          }
+          if (!ok) break;
+          if (mine && ke == kb1) db_finish_store(a0, a1, warp - 2, lane, mr, p.M, split, p.db_out);
+        } else if (!PROMOTE) {
+          it += ke - ks;
+        }
+        const uint32_t n = (uint32_t)(PROMOTE ? cc++ : tc), buf = PROMOTE ? n & 1u : 0u;
+        ok = __all_sync(0xffffffffu, mbar_wait_cluster(tfull + 8u * buf, (PROMOTE ? n >> 1 : n) & 1u, p.err));
+        if (!ok) break;
+        tc_fence_after();
+        if (!PROMOTE) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(trow + buf * C::ACC_COLS, v + 32 * c, c0 + 32 * c);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            float w[16];
+            tmem_ld16(trow + buf * C::ACC_COLS + (uint32_t)(c0 + 16 * c), w);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[16 * c + j] += w[j];
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(lead_tempty + 8u * buf);
+      }
+      if (!ok) break;
 #pragma unroll
       for (int sub = 0; sub < 4; ++sub) {
         const int gn = n0 + c0 + sub * 32;
@@ -2117,7 +2209,7 @@ tc_wgrad_cg2_kernel(const __grid_constant__ WParams p) {
   cluster_sync_all();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc_cg2(tmem, C::TMEM_COLS);
+    tmem_dealloc_cg2(tmem, BUFS * C::ACC_COLS);
   }
 }
 
@@ -2409,13 +2501,14 @@ const void* tcw_kernel_ptr() {
   return (const void*)tc::tc_wgrad_persistent_kernel<X3, WBN>;
 }
 
+template <bool PROMOTE>
 const void* tcw2_kernel_ptr() {
   static std::once_flag once;
   std::call_once(once, [] {
-    cudaFuncSetAttribute((const void*)tc::tc_wgrad_cg2_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaFuncSetAttribute((const void*)tc::tc_wgrad_cg2_kernel<PROMOTE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                          tc::W2Cfg::SMEM_BYTES);
   });
-  return (const void*)tc::tc_wgrad_cg2_kernel;
+  return (const void*)tc::tc_wgrad_cg2_kernel<PROMOTE>;
 }
 
 // Weight gradient on CTA pairs (2-SM MMAs, 256 x 256 tiles, split K).
@@ -2454,12 +2547,14 @@ int tc_wgrad_cg2_plan(const GemmOp& op, LaunchRec* recs, char* err, size_t errle
     p.db_out = op.db;
   }
   const int clusters = std::min(p.num_units, cg2_max_clusters());
-  p.db_share = p.num_units <= clusters ? 1 : 0;   // one wave
+  // one wave; and where two warps sum beside the others, whom a whole row
+  // tile's sums would hold up (8192 x 1024 over 8192 rows: 125 us)
+  p.db_share = op.promote || p.num_units <= clusters ? 1 : 0;
   LaunchRec& r = recs[0];
-  r.func = tcw2_kernel_ptr();
+  r.func = op.promote ? tcw2_kernel_ptr<true>() : tcw2_kernel_ptr<false>();
   r.smem = G::SMEM_BYTES;
   r.grid = dim3((unsigned)(2 * clusters));
-  r.block = dim3(tc::P_THREADS);
+  r.block = dim3(op.promote ? tc::kPromoteThreads : tc::P_THREADS);
   r.early = true;
   r.name = "tc2_gemm_wgrad";
   r.set_args(p);
