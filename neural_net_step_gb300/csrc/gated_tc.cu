@@ -44,7 +44,8 @@ constexpr int GT_THREADS = 64 + 32 * GT_EPI_WARPS;
 // four warps that read the same 32 TMEM lanes hand their columns to one
 // another through shared memory, as one box of 32 whole tile rows, and each
 // then moves 8 of the rows:
-//   forward: g, u and h in bf16 (or codes), three boxes of 32 x 256 bytes;
+//   forward: g and u in bf16, two boxes of 32 x 256 bytes, then h in the first
+//   of them (or h and the codes together);
 //   backward: dH in fp32, 32 x 1024 bytes; the gate's arithmetic is then done
 //   row by row, eight columns per lane, on g and u straight from global
 //   memory (fetched four rows ahead) and its results go straight back.
@@ -54,8 +55,8 @@ template <bool FWD> struct GtCfg {
   static constexpr int A_BYTES = BM * BK * 2;
   static constexpr int B_BYTES = 128 * BK * 2;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;  // 32 KB
-  static constexpr int STAGES = FWD ? 4 : 3;
-  static constexpr int EPI_GROUP_BYTES = FWD ? 3 * 8192 : 32768;
+  static constexpr int STAGES = FWD ? 5 : 3;
+  static constexpr int EPI_GROUP_BYTES = FWD ? 2 * 8192 : 32768;
   static constexpr int EPI_BYTES = 4 * EPI_GROUP_BYTES;
   static constexpr int ACC_COLS = 256;
   static constexpr int TMEM_COLS = 2 * ACC_COLS;
@@ -322,47 +323,60 @@ gated_cg2_kernel(const __grid_constant__ GtParams p) {
             u[j] += __shfl_sync(0xffffffffu, bu, j);
           }
         }
+        // 16 lanes to a row: 16 bytes of bf16 or 8 codes each
+        const int j = lane & 15, c = f0 + 8 * j;
         if (!Q8 && p.s) {
-          stage_row32(box + 8192, lane, 4 * quarter, g);
-          stage_row32(box + 16384, lane, 4 * quarter, u);
+          stage_row32(box, lane, 4 * quarter, g);
+          stage_row32(box + 8192, lane, 4 * quarter, u);
+          ok = group_sync(1 + q, ok);
+          if (!ok) break;
+          if (c < p.F) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int r = 2 * i + (lane >> 4), br = 8 * quarter + r, m = mr + r;
+              if (m >= p.M) continue;
+              __nv_bfloat16* o = p.s + (int64_t)m * p.lds + c;
+              *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(box + box_at(br, j));
+              *reinterpret_cast<uint4*>(o + p.F) = *reinterpret_cast<const uint4*>(box + 8192 + box_at(br, j));
+            }
+          }
+          named_bar_sync(1 + q, 128);
         }
         {
           uint32_t w[16];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
+          for (int i = 0; i < 16; ++i) {
             const __nv_bfloat162 b2 =
-                __floats2bfloat162_rn(gate_act(g[2 * j], ACT) * u[2 * j], gate_act(g[2 * j + 1], ACT) * u[2 * j + 1]);
-            w[j] = *reinterpret_cast<const uint32_t*>(&b2);
+                __floats2bfloat162_rn(gate_act(g[2 * i], ACT) * u[2 * i], gate_act(g[2 * i + 1], ACT) * u[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&b2);
           }
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<uint4*>(box + box_at(lane, 4 * quarter + j)) =
-                make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<uint4*>(box + box_at(lane, 4 * quarter + i)) =
+                make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
         }
         if constexpr (Q8) {
           // a lane's 32 columns are one block (columns beyond F hold the
           // next rows of W: they count as 0)
           if (f + 32 > p.F) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (f + j >= p.F) g[j] = u[j] = 0.f;
+            for (int i = 0; i < 32; ++i)
+              if (f + i >= p.F) g[i] = u[i] = 0.f;
           }
 #pragma unroll
           for (int part = 0; part < 2; ++part) {
             uint32_t w[8];
             const uint32_t byte = q8_block(part ? u : g, w);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              *reinterpret_cast<uint2*>(box + 8192 + 4096 * part + code_at(lane, 4 * quarter + j)) =
-                  make_uint2(w[2 * j], w[2 * j + 1]);
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<uint2*>(box + 8192 + 4096 * part + code_at(lane, 4 * quarter + i)) =
+                  make_uint2(w[2 * i], w[2 * i + 1]);
             if (ok && m0 + lane < p.M && f < p.F)
               p.e[(int64_t)(m0 + lane) * p.lde + part * p.nb + (f >> 5)] = (uint8_t)byte;
           }
         }
         ok = group_sync(1 + q, ok);
         if (!ok) break;
-        // 16 lanes to a row: 16 bytes of bf16 or 8 codes each
-        const int j = lane & 15, c = f0 + 8 * j;
         if (c < p.F) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -374,10 +388,6 @@ gated_cg2_kernel(const __grid_constant__ GtParams p) {
               uint8_t* o = p.q + (int64_t)m * p.ldq + c;
               *reinterpret_cast<uint2*>(o) = *reinterpret_cast<const uint2*>(box + 8192 + code_at(br, j));
               *reinterpret_cast<uint2*>(o + p.F) = *reinterpret_cast<const uint2*>(box + 12288 + code_at(br, j));
-            } else if (p.s) {
-              __nv_bfloat16* o = p.s + (int64_t)m * p.lds + c;
-              *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(box + 8192 + box_at(br, j));
-              *reinterpret_cast<uint4*>(o + p.F) = *reinterpret_cast<const uint4*>(box + 16384 + box_at(br, j));
             }
           }
         }
