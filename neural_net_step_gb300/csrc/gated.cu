@@ -15,6 +15,7 @@
 
 #include "common.cuh"
 #include "e4m3.cuh"
+#include "f32x2.cuh"
 #include "gated.cuh"
 #include "ops.h"
 
@@ -42,11 +43,6 @@ constexpr int GT = 128, GK = 16, GSTAGES = 4;
 __device__ __forceinline__ void copy4(uint32_t dst, const float* src, bool in) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
 }
-// d += a b on two fp32 values at once.
-__device__ __forceinline__ void fma2(uint64_t& d, uint64_t a, uint64_t b) {
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
-}
-
 template <bool FWD, int RM>   // RM rows and 8 columns per thread
 __global__ void __launch_bounds__(256) gated_simt_kernel(const __grid_constant__ GatedParams p) {
   pdl_enter();
@@ -83,11 +79,11 @@ __global__ void __launch_bounds__(256) gated_simt_kernel(const __grid_constant__
     }
   };
   // two columns to an accumulator: one instruction forms both products
-  uint64_t acc2[RM][4];
+  F2 acc2[RM][4];
 #pragma unroll
   for (int i = 0; i < RM; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc2[i][j] = 0ull;
+    for (int j = 0; j < 4; ++j) acc2[i][j] = pack2(0.f, 0.f);
   const int nt = (p.K + GK - 1) / GK;
 #pragma unroll
   for (int s = 0; s < GSTAGES - 1; ++s) {
@@ -116,12 +112,11 @@ __global__ void __launch_bounds__(256) gated_simt_kernel(const __grid_constant__
       b[1] = *reinterpret_cast<const ulonglong2*>(Bs + kk * PB + 64 + tx * 4);
 #pragma unroll
       for (int i = 0; i < RM; ++i) {
-        uint64_t aa;
-        asm("mov.b64 %0, {%1, %1};" : "=l"(aa) : "f"(a[i]));
-        fma2(acc2[i][0], aa, b[0].x);
-        fma2(acc2[i][1], aa, b[0].y);
-        fma2(acc2[i][2], aa, b[1].x);
-        fma2(acc2[i][3], aa, b[1].y);
+        const F2 aa = pack2(a[i], a[i]);
+        acc2[i][0] = fma2(aa, F2{b[0].x}, acc2[i][0]);
+        acc2[i][1] = fma2(aa, F2{b[0].y}, acc2[i][1]);
+        acc2[i][2] = fma2(aa, F2{b[1].x}, acc2[i][2]);
+        acc2[i][3] = fma2(aa, F2{b[1].y}, acc2[i][3]);
       }
     }
   }
@@ -130,7 +125,7 @@ __global__ void __launch_bounds__(256) gated_simt_kernel(const __grid_constant__
 #pragma unroll
   for (int i = 0; i < RM; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) asm("mov.b64 {%0, %1}, %2;" : "=f"(acc[i][2 * j]), "=f"(acc[i][2 * j + 1]) : "l"(acc2[i][j]));
+    for (int j = 0; j < 4; ++j) unpack2(acc2[i][j], acc[i][2 * j], acc[i][2 * j + 1]);
   // thread (ty, tx): its rows; tile columns tx*4 + 0..3 and 64 + tx*4 + 0..3 (the forward's second four are the up
   // columns of its first four)
   float* h = p.h;

@@ -25,6 +25,7 @@
 
 #include "common.cuh"
 #include "e4m3.cuh"
+#include "f32x2.cuh"
 #include "gated.cuh"
 #include "ops.h"
 #include "tc.cuh"
@@ -46,17 +47,21 @@ constexpr int GT_THREADS = 64 + 32 * GT_EPI_WARPS;
 // then moves 8 of the rows:
 //   forward: g and u in bf16, two boxes of 32 x 256 bytes, then h in the first
 //   of them (or h and the codes together);
-//   backward: dH in fp32, 32 x 1024 bytes; the gate's arithmetic is then done
-//   row by row, eight columns per lane, on g and u straight from global
-//   memory (fetched four rows ahead) and its results go straight back.
+//   backward: dH in fp32, 32 x 512 bytes, the tile's columns in two halves; the
+//   gate's arithmetic is then done row by row, eight columns per lane, on g and
+//   u straight from global memory (fetched four steps ahead) and its results
+//   go straight back.
+// Small boxes leave the main loop five stages (backward of 16384 x 4096 x 1024
+// with two, three, five: BWDTIMES; forward with s in bf16 and two to
+// five: 263, 201, 181, 173 us).
 template <bool FWD> struct GtCfg {
   static constexpr int TBM = 2 * BM;
   static constexpr int TF = FWD ? 128 : 256;             // F columns per tile
   static constexpr int A_BYTES = BM * BK * 2;
   static constexpr int B_BYTES = 128 * BK * 2;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;  // 32 KB
-  static constexpr int STAGES = FWD ? 5 : 3;
-  static constexpr int EPI_GROUP_BYTES = FWD ? 2 * 8192 : 32768;
+  static constexpr int STAGES = 5;
+  static constexpr int EPI_GROUP_BYTES = 16384 + 256;     // box(es), and the scale bytes of 32 rows
   static constexpr int EPI_BYTES = 4 * EPI_GROUP_BYTES;
   static constexpr int ACC_COLS = 256;
   static constexpr int TMEM_COLS = 2 * ACC_COLS;
@@ -77,6 +82,7 @@ struct GtParams {
   uint8_t* q; int64_t ldq;               // codes (forward writes, backward reads)
   uint8_t* e; int64_t lde;
   int nb;                                // scale bytes of half a row
+  int e_words;                           // scale bytes may be written four at a time
   uint32_t* err;
 };
 
@@ -125,14 +131,21 @@ __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar_cluster
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
 
+__device__ __forceinline__ uint32_t bf16_pair(F2 x) {
+  float a, b;
+  unpack2(x, a, b);
+  const __nv_bfloat162 b2 = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&b2);
+}
+
 // Byte offsets in the boxes: 16-byte unit j (0..15) of row r with 256-byte
 // rows, 8-byte unit j (0..15) of a row of codes (128 bytes), 16-byte unit j
-// (0..63) of a row of fp32 (1024 bytes).  Units are exchanged so that neither
+// (0..31) of a row of fp32 (512 bytes).  Units are exchanged so that neither
 // the same unit of a quarter-warp's rows nor a quarter-warp's units of one row
 // share banks (fp32: units 2 l and 2 l + 1 of lane l).
 __device__ __forceinline__ int box_at(int r, int j) { return r * 256 + ((j ^ (r & 7)) << 4); }
 __device__ __forceinline__ int code_at(int r, int j) { return r * 128 + ((j ^ (r & 15)) << 3); }
-__device__ __forceinline__ int fbox_at(int r, int j) { return r * 1024 + ((j ^ ((j >> 3) & 1) ^ (r & 7)) << 4); }
+__device__ __forceinline__ int fbox_at(int r, int j) { return r * 512 + ((j ^ ((j >> 3) & 1) ^ (r & 7)) << 4); }
 
 // A lane's 32 values in bf16 into its row of a box, from unit j0 on.
 __device__ __forceinline__ void stage_row32(uint8_t* box, int lane, int j0, const float* v) {
@@ -271,13 +284,13 @@ gated_cg2_kernel(const __grid_constant__ GtParams p) {
     uint8_t* box = base_ptr + (epi_base - base) + q * C::EPI_GROUP_BYTES;
     int tc = 0;
     bool ok = true;
-    // backward: the kept g and u of eight columns (8 lane ..) of the rows to
-    // come, as bf16 pairs or codes and their scale bytes, four rows ahead;
-    // row i of a tile in slot i % 4
+    // backward: the kept g and u of eight columns (8 (lane % 16) ..) of the rows
+    // to come (lanes 16 .. 31 one further), as bf16 pairs or codes and their
+    // scale bytes, four steps ahead; step i of a half tile in slot i
     constexpr int AHEAD = 4, NW = FWD ? 1 : Q8 ? 2 : 4;
     uint32_t ng[AHEAD][NW], nu[AHEAD][NW], ne[AHEAD];
-    auto fetch = [&](int slot, int r, int f) {   // row r, tile columns f ..
-      const int c = f + 8 * lane;
+    auto fetch = [&](int slot, int r, int f) {   // row r, columns f ..
+      const int c = f + 8 * (lane & 15);
       const bool in = r < p.M && c < p.F;   // (F is a multiple of 8)
       if constexpr (Q8 && !FWD) {
         const uint8_t* qr = p.q + (int64_t)r * p.ldq + c;
@@ -346,9 +359,9 @@ gated_cg2_kernel(const __grid_constant__ GtParams p) {
           uint32_t w[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const __nv_bfloat162 b2 =
-                __floats2bfloat162_rn(gate_act(g[2 * i], ACT) * u[2 * i], gate_act(g[2 * i + 1], ACT) * u[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t*>(&b2);
+            F2 a, da;
+            gate2<ACT>(pack2(g[2 * i], g[2 * i + 1]), a, da);
+            w[i] = bf16_pair(mul2(a, pack2(u[2 * i], u[2 * i + 1])));
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -371,8 +384,7 @@ gated_cg2_kernel(const __grid_constant__ GtParams p) {
             for (int i = 0; i < 4; ++i)
               *reinterpret_cast<uint2*>(box + 8192 + 4096 * part + code_at(lane, 4 * quarter + i)) =
                   make_uint2(w[2 * i], w[2 * i + 1]);
-            if (ok && m0 + lane < p.M && f < p.F)
-              p.e[(int64_t)(m0 + lane) * p.lde + part * p.nb + (f >> 5)] = (uint8_t)byte;
+            box[16384 + 128 * part + 4 * lane + quarter] = (uint8_t)byte;
           }
         }
         ok = group_sync(1 + q, ok);
@@ -391,84 +403,105 @@ gated_cg2_kernel(const __grid_constant__ GtParams p) {
             }
           }
         }
+        if constexpr (Q8) {
+          // the four scale bytes of a row's gate or up blocks, a lane to each
+          // (a byte at a time from every lane cost 12 us of 185)
+          const int part = lane >> 3, br = 8 * quarter + (lane & 7), m = mr + (lane & 7);
+          if (part < 2 && m < p.M) {
+            uint8_t* o = p.e + (int64_t)m * p.lde + part * p.nb + (f0 >> 5);
+            const uint32_t four = *reinterpret_cast<const uint32_t*>(box + 16384 + 128 * part + 4 * br);
+            if (p.e_words && f0 + 128 <= p.F) {
+              *reinterpret_cast<uint32_t*>(o) = four;
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (f0 + 32 * i < p.F) o[i] = (uint8_t)(four >> (8 * i));
+            }
+          }
+        }
         named_bar_sync(1 + q, 128);   // the boxes are read before the next tile fills them
       } else {
+        const int up = lane >> 4;   // which of a step's two rows
         if (tc == 0) {
 #pragma unroll
-          for (int i = 0; i < AHEAD; ++i) fetch(i, mr + i, f0);
+          for (int i = 0; i < AHEAD; ++i) fetch(i, mr + 2 * i + up, f0);
         }
         ok = __all_sync(0xffffffffu, mbar_wait_cluster(tfull_bar(buf), ((uint32_t)tc >> 1) & 1u, p.err));
         tc_fence_after();
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float d[16];
-          tmem_ld16(trow + (uint32_t)(quarter * 64 + 16 * c), d);
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<float4*>(box + fbox_at(lane, 16 * quarter + 4 * c + j)) =
-                make_float4(d[4 * j], d[4 * j + 1], d[4 * j + 2], d[4 * j + 3]);
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster_relaxed(lead_tempty0 + 8u * (uint32_t)buf);
-        ok = group_sync(1 + q, ok);
-        if (!ok) break;
-        // the next tile's rows, to fetch while this one's last rows are worked on
+        // the rows to fetch while the second half's are worked on: the next tile's
         int next_m = p.M, next_f = 0;   // (none: nothing is read)
         if (t + tstep < p.num_tiles) {
           origin(t + tstep, next_m, next_f);
           next_m += q * 32 + 8 * quarter;
         }
-        const int c = f0 + 8 * lane;
 #pragma unroll 1
-        for (int i0 = 0; i0 < 8; i0 += AHEAD) {
-        const int fm = i0 + AHEAD < 8 ? mr + i0 + AHEAD : next_m, ff = i0 + AHEAD < 8 ? f0 : next_f;
+        for (int hc = 0; hc < 256; hc += 128) {   // half a tile's columns
 #pragma unroll
-        for (int slot = 0; slot < AHEAD; ++slot) {
-          const int i = i0 + slot, m = mr + i;
-          float g[8], u[8], d[8];
-          if constexpr (Q8) {
-            const float eg = q8_scale(ne[slot] & 0xffu), eu = q8_scale(ne[slot] >> 8);
-            q8_unpack(ng[slot][0], eg, g);
-            q8_unpack(ng[slot][1], eg, g + 4);
-            q8_unpack(nu[slot][0], eu, u);
-            q8_unpack(nu[slot][1], eu, u + 4);
-          } else {
+          for (int c = 0; c < 2; ++c) {
+            float d[16];
+            tmem_ld16(trow + (uint32_t)(hc + quarter * 32 + 16 * c), d);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              *reinterpret_cast<float4*>(box + fbox_at(lane, 8 * quarter + 4 * c + j)) =
+                  make_float4(d[4 * j], d[4 * j + 1], d[4 * j + 2], d[4 * j + 3]);
+          }
+          if (hc > 0) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster_relaxed(lead_tempty0 + 8u * (uint32_t)buf);
+          }
+          ok = group_sync(1 + q, ok);
+          if (!ok) break;
+          const int c = f0 + hc + 8 * (lane & 15);
+          const int fm = (hc == 0 ? mr : next_m) + up, ff = hc == 0 ? f0 + 128 : next_f;
+#pragma unroll
+          for (int slot = 0; slot < AHEAD; ++slot) {   // two rows a step
+            const int m = mr + 2 * slot + up;
+            F2 g[4], u[4];
+            if constexpr (Q8) {
+              float v[8];
+              const float eg = q8_scale(ne[slot] & 0xffu), eu = q8_scale(ne[slot] >> 8);
+              const F2 sg = pack2(eg, eg), su = pack2(eu, eu);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                q8_unpack(ng[slot][h], 1.0f, v);
+                q8_unpack(nu[slot][h], 1.0f, v + 4);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  g[2 * h + i] = mul2(pack2(v[2 * i], v[2 * i + 1]), sg);
+                  u[2 * h + i] = mul2(pack2(v[4 + 2 * i], v[5 + 2 * i]), su);
+                }
+              }
+            } else {
+#pragma unroll
+              for (int h = 0; h < 4; ++h) {
+                g[h] = pack2(__uint_as_float(ng[slot][h % NW] << 16), __uint_as_float(ng[slot][h % NW] & 0xFFFF0000u));
+                u[h] = pack2(__uint_as_float(nu[slot][h % NW] << 16), __uint_as_float(nu[slot][h % NW] & 0xFFFF0000u));
+              }
+            }
+            fetch(slot, fm + 2 * slot, ff);
+            const int br = 8 * quarter + 2 * slot + up;
+            const ulonglong2 lo = *reinterpret_cast<const ulonglong2*>(box + fbox_at(br, 2 * (lane & 15)));
+            const ulonglong2 hi = *reinterpret_cast<const ulonglong2*>(box + fbox_at(br, 2 * (lane & 15) + 1));
+            const F2 d[4] = {F2{lo.x}, F2{lo.y}, F2{hi.x}, F2{hi.y}};
+            uint32_t wg[4], wu[4], wh[4];
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
-              g[2 * h] = __uint_as_float(ng[slot][h % NW] << 16);
-              g[2 * h + 1] = __uint_as_float(ng[slot][h % NW] & 0xFFFF0000u);
-              u[2 * h] = __uint_as_float(nu[slot][h % NW] << 16);
-              u[2 * h + 1] = __uint_as_float(nu[slot][h % NW] & 0xFFFF0000u);
+              F2 a, da;
+              gate2<ACT>(g[h], a, da);
+              wg[h] = bf16_pair(mul2(mul2(d[h], u[h]), da));
+              wu[h] = bf16_pair(mul2(d[h], a));
+              wh[h] = bf16_pair(mul2(a, u[h]));
+            }
+            if (m < p.M && c < p.F) {
+              __nv_bfloat16* o = p.ds + (int64_t)m * p.ldds + c;
+              *reinterpret_cast<uint4*>(o) = make_uint4(wg[0], wg[1], wg[2], wg[3]);
+              *reinterpret_cast<uint4*>(o + p.F) = make_uint4(wu[0], wu[1], wu[2], wu[3]);
+              if (p.h) *reinterpret_cast<uint4*>(p.h + (int64_t)m * p.ldh + c) = make_uint4(wh[0], wh[1], wh[2], wh[3]);
             }
           }
-          fetch(slot, fm + slot, ff);
-          *reinterpret_cast<float4*>(d) = *reinterpret_cast<const float4*>(box + fbox_at(8 * quarter + i, 2 * lane));
-          *reinterpret_cast<float4*>(d + 4) =
-              *reinterpret_cast<const float4*>(box + fbox_at(8 * quarter + i, 2 * lane + 1));
-          uint32_t wg[4], wu[4], wh[4];
-#pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            float a0, a1, d0, d1;
-            gate_act_grad(g[2 * h], ACT, a0, d0);
-            gate_act_grad(g[2 * h + 1], ACT, a1, d1);
-            const float e0 = d[2 * h], e1 = d[2 * h + 1];
-            const __nv_bfloat162 x = __floats2bfloat162_rn(e0 * u[2 * h] * d0, e1 * u[2 * h + 1] * d1);
-            const __nv_bfloat162 y = __floats2bfloat162_rn(e0 * a0, e1 * a1);
-            const __nv_bfloat162 z = __floats2bfloat162_rn(a0 * u[2 * h], a1 * u[2 * h + 1]);
-            wg[h] = *reinterpret_cast<const uint32_t*>(&x);
-            wu[h] = *reinterpret_cast<const uint32_t*>(&y);
-            wh[h] = *reinterpret_cast<const uint32_t*>(&z);
-          }
-          if (m < p.M && c < p.F) {
-            __nv_bfloat16* o = p.ds + (int64_t)m * p.ldds + c;
-            *reinterpret_cast<uint4*>(o) = make_uint4(wg[0], wg[1], wg[2], wg[3]);
-            *reinterpret_cast<uint4*>(o + p.F) = make_uint4(wu[0], wu[1], wu[2], wu[3]);
-            if (p.h) *reinterpret_cast<uint4*>(p.h + (int64_t)m * p.ldh + c) = make_uint4(wh[0], wh[1], wh[2], wh[3]);
-          }
+          named_bar_sync(1 + q, 128);   // the box is read before the next half fills it
         }
-        }
-        named_bar_sync(1 + q, 128);   // the box is read before the next tile fills it
       }
     }
   }
@@ -535,6 +568,7 @@ int gated_tc_plan(const GatedOp& op, LaunchRec* rec, char* err, size_t errlen) {
     p.s = (__nv_bfloat16*)op.s; p.lds = op.lds;
   }
   p.nb = (int)q8_blocks(op.F);
+  p.e_words = (uintptr_t)op.se % 4 == 0 && op.ldse % 4 == 0 && p.nb % 4 == 0;
   p.err = op.err;
   rec->func = op.fwd ? (op.se ? gated_pick<true, true>(op.act) : gated_pick<true, false>(op.act))
                      : (op.se ? gated_pick<false, true>(op.act) : gated_pick<false, false>(op.act));

@@ -20,6 +20,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "ops.h"
 
 namespace mlpk {
@@ -99,36 +100,6 @@ __device__ __forceinline__ void row_sums(float (&v)[NS], float (&sh)[NS][WARPS])
 __device__ __forceinline__ void finish_stats(const float (&s)[2], float inv_d, float eps, float& rest, float& rstd) {
   rest = s[0] * inv_d;
   rstd = rsqrtf(fmaxf(fmaf(-rest, rest, s[1] * inv_d), 0.f) + eps);   // (2 ulp)
-}
-
-// Two fp32 values in a register pair: one instruction does both (the kernels
-// below are bound by instruction issue before they are by DRAM otherwise).
-struct F2 { uint64_t v; };
-__device__ __forceinline__ F2 pack2(float a, float b) {
-  F2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void unpack2(F2 x, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x.v)); }
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-  F2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
-__device__ __forceinline__ float sum2(F2 x) {
-  float a, b;
-  unpack2(x, a, b);
-  return a + b;
 }
 
 // How rows of at most kMaxRow elements are walked, forward and backward: tpr
