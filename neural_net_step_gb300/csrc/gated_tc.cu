@@ -285,27 +285,37 @@ gated_cg2_kernel(const __grid_constant__ GtParams p) {
     int tc = 0;
     bool ok = true;
     // backward: the kept g and u of eight columns (8 (lane % 16) ..) of the rows
-    // to come (lanes 16 .. 31 one further), as bf16 pairs or codes and their
-    // scale bytes, four steps ahead; step i of a half tile in slot i
+    // to come (lanes 16 .. 31 one further), as bf16 pairs or codes, four steps
+    // ahead; step i of a half tile in slot i
     constexpr int AHEAD = 4, NW = FWD ? 1 : Q8 ? 2 : 4;
-    uint32_t ng[AHEAD][NW], nu[AHEAD][NW], ne[AHEAD];
+    uint32_t ng[AHEAD][NW], nu[AHEAD][NW];
+    // scale bytes a half tile ahead: lane l holds those of row l / 4 and block
+    // l % 4 of the 8 rows' gate and up parts (a load of its own for every lane
+    // and step cost 20 us of 141)
+    uint32_t eg = 0, eu = 0;
     auto fetch = [&](int slot, int r, int f) {   // row r, columns f ..
       const int c = f + 8 * (lane & 15);
       const bool in = r < p.M && c < p.F;   // (F is a multiple of 8)
       if constexpr (Q8 && !FWD) {
         const uint8_t* qr = p.q + (int64_t)r * p.ldq + c;
-        const uint8_t* er = p.e + (int64_t)r * p.lde + (c >> 5);
         const uint2 a = in ? __ldg(reinterpret_cast<const uint2*>(qr)) : make_uint2(0u, 0u);
         const uint2 b = in ? __ldg(reinterpret_cast<const uint2*>(qr + p.F)) : make_uint2(0u, 0u);
         ng[slot][0] = a.x; ng[slot][1] = a.y;
         nu[slot][0] = b.x; nu[slot][1] = b.y;
-        ne[slot] = in ? (uint32_t)__ldg(er) | ((uint32_t)__ldg(er + p.nb) << 8) : 0u;
       } else if constexpr (!FWD) {
         const __nv_bfloat16* sr = p.s + (int64_t)r * p.lds + c;
         const uint4 a = in ? __ldg(reinterpret_cast<const uint4*>(sr)) : make_uint4(0u, 0u, 0u, 0u);
         const uint4 b = in ? __ldg(reinterpret_cast<const uint4*>(sr + p.F)) : make_uint4(0u, 0u, 0u, 0u);
         ng[slot][0] = a.x; ng[slot][1] = a.y; ng[slot][2] = a.z; ng[slot][3] = a.w;
         nu[slot][0] = b.x; nu[slot][1] = b.y; nu[slot][2] = b.z; nu[slot][3] = b.w;
+      }
+    };
+    auto fetch_scales = [&](int m, int f) {   // rows m .. m + 7, columns f .. f + 127
+      const int r = m + (lane >> 2), c = f + 32 * (lane & 3);
+      if (Q8 && !FWD && r < p.M && c < p.F) {
+        const uint8_t* er = p.e + (int64_t)r * p.lde + (c >> 5);
+        eg = __ldg(er);
+        eu = __ldg(er + p.nb);
       }
     };
     for (int t = t0; t < p.num_tiles && ok; t += tstep, ++tc) {
@@ -425,6 +435,7 @@ gated_cg2_kernel(const __grid_constant__ GtParams p) {
         if (tc == 0) {
 #pragma unroll
           for (int i = 0; i < AHEAD; ++i) fetch(i, mr + 2 * i + up, f0);
+          fetch_scales(mr, f0);
         }
         ok = __all_sync(0xffffffffu, mbar_wait_cluster(tfull_bar(buf), ((uint32_t)tc >> 1) & 1u, p.err));
         tc_fence_after();
@@ -454,14 +465,18 @@ gated_cg2_kernel(const __grid_constant__ GtParams p) {
           if (!ok) break;
           const int c = f0 + hc + 8 * (lane & 15);
           const int fm = (hc == 0 ? mr : next_m) + up, ff = hc == 0 ? f0 + 128 : next_f;
+          const uint32_t cg = eg, cu = eu;
+          fetch_scales(fm - up, ff);
 #pragma unroll
           for (int slot = 0; slot < AHEAD; ++slot) {   // two rows a step
             const int m = mr + 2 * slot + up;
             F2 g[4], u[4];
             if constexpr (Q8) {
               float v[8];
-              const float eg = q8_scale(ne[slot] & 0xffu), eu = q8_scale(ne[slot] >> 8);
-              const F2 sg = pack2(eg, eg), su = pack2(eu, eu);
+              const int from = 4 * (2 * slot + up) + ((lane & 15) >> 2);
+              const float xg = q8_scale(__shfl_sync(0xffffffffu, cg, from));
+              const float xu = q8_scale(__shfl_sync(0xffffffffu, cu, from));
+              const F2 sg = pack2(xg, xg), su = pack2(xu, xu);
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 q8_unpack(ng[slot][h], 1.0f, v);
