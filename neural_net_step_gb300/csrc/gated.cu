@@ -38,17 +38,20 @@ struct GatedParams {
 // Tile of 16 RM rows by GT columns, GK deep, in a ring of GSTAGES slices that
 // cp.async fills an element at a time (any alignment; elements outside the
 // matrices as zeros) and transposes on the way.
-constexpr int GT = 128, GK = 16, GSTAGES = 4;
+// Every kChunk slices (256 k) the accumulators are added to sums in shared
+// memory, which keeps the error of a long reduction near that of a short one
+// (K = 2000: 1.2e-6 of the result in one sequence of FMAs).
+constexpr int GT = 128, GK = 16, GSTAGES = 4, kChunk = 16;
 
 __device__ __forceinline__ void copy4(uint32_t dst, const float* src, bool in) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
 }
 template <bool FWD, int RM>   // RM rows and 8 columns per thread
-__global__ void __launch_bounds__(256) gated_simt_kernel(const __grid_constant__ GatedParams p) {
+__global__ void __launch_bounds__(256, 2) gated_simt_kernel(const __grid_constant__ GatedParams p) {
   pdl_enter();
   constexpr int BM = 16 * RM, PA = BM + 4, PB = GT + 4;   // rows, pitches of the two slices
   constexpr int SLICE = GK * (PA + PB);
-  extern __shared__ __align__(16) float gated_smem[];     // [GSTAGES][GK][PA], [GK][PB]
+  extern __shared__ __align__(16) float gated_smem[];     // [GSTAGES]([GK][PA], [GK][PB]), [8 RM][256]
   constexpr int TF = FWD ? GT / 2 : GT;   // F columns per tile
   const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
   const int m0 = blockIdx.y * BM, f0 = blockIdx.x * TF;
@@ -84,6 +87,7 @@ __global__ void __launch_bounds__(256) gated_simt_kernel(const __grid_constant__
   for (int i = 0; i < RM; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc2[i][j] = pack2(0.f, 0.f);
+  float* sums = gated_smem + GSTAGES * SLICE + tid;
   const int nt = (p.K + GK - 1) / GK;
 #pragma unroll
   for (int s = 0; s < GSTAGES - 1; ++s) {
@@ -119,13 +123,27 @@ __global__ void __launch_bounds__(256) gated_simt_kernel(const __grid_constant__
         acc2[i][3] = fma2(aa, F2{b[1].y}, acc2[i][3]);
       }
     }
+    if ((t + 1) % kChunk == 0 && t + 1 < nt) {
+#pragma unroll
+      for (int i = 0; i < RM; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float* sum = sums + (i * 8 + 2 * j) * 256;
+          const F2 old = t + 1 == kChunk ? pack2(0.f, 0.f) : pack2(sum[0], sum[256]);
+          unpack2(add2(acc2[i][j], old), sum[0], sum[256]);
+          acc2[i][j] = pack2(0.f, 0.f);
+        }
+    }
   }
 
   float acc[RM][8];
 #pragma unroll
   for (int i = 0; i < RM; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) unpack2(acc2[i][j], acc[i][2 * j], acc[i][2 * j + 1]);
+    for (int j = 0; j < 4; ++j) {
+      const float* sum = sums + (i * 8 + 2 * j) * 256;
+      unpack2(nt > kChunk ? add2(acc2[i][j], pack2(sum[0], sum[256])) : acc2[i][j], acc[i][2 * j], acc[i][2 * j + 1]);
+    }
   // thread (ty, tx): its rows; tile columns tx*4 + 0..3 and 64 + tx*4 + 0..3 (the forward's second four are the up
   // columns of its first four)
   float* h = p.h;
@@ -213,13 +231,16 @@ __global__ void __launch_bounds__(256) gated_simt_kernel(const __grid_constant__
   }
 }
 
-unsigned simt_smem(int rm) { return (unsigned)(GSTAGES * GK * (16 * rm + 4 + GT + 4) * 4); }
+// the ring, and the chunks' sums where there are several
+unsigned simt_smem(int rm, int64_t K) {
+  return (unsigned)((GSTAGES * GK * (16 * rm + 4 + GT + 4) + (K > GK * kChunk ? 8 * rm * 256 : 0)) * 4);
+}
 template <bool FWD, int RM>
 const void* simt_kernel() {
   static std::once_flag once;
   std::call_once(once, [] {
     cudaFuncSetAttribute((const void*)gated_simt_kernel<FWD, RM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                         simt_smem(RM));
+                         (int)simt_smem(RM, INT32_MAX));
   });
   return (const void*)gated_simt_kernel<FWD, RM>;
 }
@@ -240,11 +261,12 @@ int gated_plan(const GatedOp& op, LaunchRec* rec, char* err, size_t errlen) {
   const GatedParams p{(const float*)op.A, op.lda, (const float*)op.B, op.ldb, op.bias, (float*)op.h, op.ldh,
                       op.s, op.lds, op.se, op.ldse, (float*)op.ds, op.ldds, (int)op.M, (int)op.F, (int)op.K, op.act};
   const int64_t cols = ceil_div(op.F, op.fwd ? GT / 2 : GT);
-  // the tallest tile that still gives most SMs one (fp32, forward / backward of
-  // 1000 x 1000 x 784 with rm = 8, 4, 2: 90, 107, 152 us from 128, 256, 512
-  // tiles; 97, 66, 87 us from 64, 128, 256; one row: 82, 58, 48 us)
+  // the tallest tile that still gives half the SMs one (fp32, rm = 8, 4, 2:
+  // forward of 1000 x 1000 x 784 90, 107, 152 us from 128, 256, 512 tiles, of
+  // 300 x 2000 x 1000 115, 140, 158 from 96, 160, 320; backward of the first 97,
+  // 66, 87 us from 64, 128, 256; one row forward 82, 58, 48 us)
   int rm = 8;
-  while (rm > 2 && cols * ceil_div(op.M, 16 * rm) < 100) rm /= 2;
+  while (rm > 2 && cols * ceil_div(op.M, 16 * rm) < 76) rm /= 2;
   rec->func = op.fwd ? simt_pick<true>(rm) : simt_pick<false>(rm);
   rec->grid = dim3((unsigned)cols, (unsigned)ceil_div(op.M, 16 * rm));
   if (rec->grid.y > 65535) {
@@ -252,7 +274,7 @@ int gated_plan(const GatedOp& op, LaunchRec* rec, char* err, size_t errlen) {
     return -1;
   }
   rec->block = dim3(256);
-  rec->smem = simt_smem(rm);
+  rec->smem = simt_smem(rm, op.K);
   rec->name = op.fwd ? "gated_fwd" : "gated_dgrad";
   rec->set_args(p);
   return 1;
