@@ -172,7 +172,7 @@ mlp_status mlp_op_argmax(int dtype, int64_t B, int64_t C, const void* z, int64_t
  *   mean_i = sum_j X_ij / D,  rstd_i = 1 / sqrt(sum_j (X_ij - mean_i)^2 / D
  *   + eps),  Y_ij = (X_ij - mean_i) rstd_i gamma_j + beta_j.
  *   gamma, beta fp32 [D] (nullable: 1 and 0); Y [M, D] (ldy, dtype; may be
- *   X); mean, rstd fp32 [M] (nullable: not kept).  eps >= 0 and finite.
+ *   X with X's pitch); mean, rstd fp32 [M] (nullable: not kept).  eps >= 0 and finite.
  * Any D up to 65535 * 256 and any alignment of the elements; rows whose base
  * and pitch are 16-byte aligned move by 16-byte accesses.  Statistics are
  * fp32, from the elements as stored. */
@@ -181,7 +181,8 @@ mlp_status mlp_op_layernorm(int dtype, int64_t M, int64_t D, const void* X, int6
                             void* stream);
 
 /* Its vector-Jacobian product: with xh = (X - mean) rstd and w = gamma dY,
- *   dX = rstd (w - mean_j(w) - xh mean_j(w xh))   (dtype, lddx; may be dY),
+ *   dX = rstd (w - mean_j(w) - xh mean_j(w xh))   (dtype, lddx; may be dY with
+ *   dY's pitch),
  *   dgamma_j = sum_i dY_ij xh_ij,  dbeta_j = sum_i dY_ij  (fp32 [D], nullable).
  * X, mean and rstd are what the forward read and kept.  workspace (device, at
  * least the bytes below for this shape) holds per-block partial sums of
@@ -223,7 +224,8 @@ mlp_status mlp_op_dequant8(int dtype, int64_t rows, int64_t cols, const uint8_t*
  * first (gate and up half each as one matrix of F columns).  H comes from the
  * fp32 sums, before s is rounded.  MLP_F32 or MLP_BF16; MLP_BF16 takes K, F
  * and the leading dimensions (but ldse) in multiples of 8 and 16-byte aligned
- * matrices (S codes: 8-byte).  M from one token on. */
+ * matrices (S codes: 8-byte).  M from one token on.  Nothing written may
+ * overlap anything read. */
 enum { MLP_ACT_SILU = 3 };   /* the gated operations only */
 mlp_status mlp_op_gated_linear(int dtype, int act, int64_t M, int64_t F, int64_t K, const void* X, int64_t ldx,
                                const void* W, int64_t ldw, const float* b, void* H, int64_t ldh, void* S, int64_t lds,
@@ -237,7 +239,8 @@ mlp_status mlp_op_gated_linear(int dtype, int act, int64_t M, int64_t F, int64_t
  *   so that it need not be kept for dWd = dY^T H.
  * dX and the projections' gradients are mlp_op_dgrad(MLP_ACT_NONE) and
  * mlp_op_wgrad (or _wgrad8) of dS and W with 2F output columns.  ReLU's
- * derivative at 0 is 0.  Types and alignment as above, N a multiple of 8. */
+ * derivative at 0 is 0.  Types and alignment as above, N a multiple of 8;
+ * nothing written may overlap anything read. */
 mlp_status mlp_op_gated_dgrad(int dtype, int act, int64_t M, int64_t N, int64_t F, const void* dY, int64_t lddy,
                               const void* Wd, int64_t ldw, const void* S, int64_t lds, const uint8_t* SE, int64_t ldse,
                               void* dS, int64_t ldds, void* H, int64_t ldh, uint32_t* err_dev, void* stream);

@@ -252,10 +252,6 @@ const void* simt_pick(int rm) {
 }  // namespace
 
 int gated_plan(const GatedOp& op, LaunchRec* rec, char* err, size_t errlen) {
-  if (op.M < 1 || op.F < 1 || op.K < 1 || op.M > INT32_MAX || op.F > INT32_MAX / 2 || op.K > INT32_MAX - GK) {
-    snprintf(err, errlen, "bad gated shape M=%lld F=%lld K=%lld", (long long)op.M, (long long)op.F, (long long)op.K);
-    return -1;
-  }
   if (gated_small_takes(op)) return gated_small_plan(op, rec);
   if (op.dtype == DT_BF16) return gated_tc_plan(op, rec, err, errlen);
   const GatedParams p{(const float*)op.A, op.lda, (const float*)op.B, op.ldb, op.bias, (float*)op.h, op.ldh,

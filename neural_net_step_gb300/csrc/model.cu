@@ -1686,7 +1686,7 @@ static const char* gated_layout(const GatedOp& op) {
   return nullptr;
 }
 static mlp_status run_gated(const GatedOp& op, void* stream) {
-  const int64_t top = INT32_MAX;
+  const int64_t top = INT32_MAX - 1024;   // (tiles end past the last row and column)
   if (op.M < 1 || op.F < 1 || op.K < 1 || op.M > top || op.F > top / 2 || op.K > top)
     return fail(MLP_ERR_SHAPE, "bad gated shape %lld x %lld x %lld", (long long)op.M, (long long)op.F, (long long)op.K);
   if (const char* why = gated_layout(op)) return fail(MLP_ERR_SHAPE, "%s", why);

@@ -88,7 +88,7 @@ GB = dict(dtype=nn.BF16, act=nn.ACT_SILU, M=4, N=32, F=64, dY=P, lddy=32, Wd=P, 
 
 @pytest.mark.parametrize("bad", [
     dict(dtype=nn.F32X3), dict(act=4), dict(act=-1), dict(X=None), dict(W=None), dict(H=None), dict(S=None, SE=P),
-    dict(M=0), dict(F=0), dict(K=0), dict(M=1 << 33), dict(F=1 << 31), dict(K=1 << 33), dict(ldx=24), dict(ldw=24),
+    dict(M=0), dict(F=0), dict(K=0), dict(M=1 << 33), dict(M=(1 << 31) - 1), dict(F=1 << 31), dict(K=1 << 33), dict(ldx=24), dict(ldw=24),
     dict(ldh=56), dict(lds=120), dict(SE=P, ldse=3), dict(F=60), dict(K=28), dict(X=P + 2), dict(W=P + 8),
     dict(H=P + 4), dict(S=P + 8), dict(SE=P, S=P + 4), dict(ldx=33), dict(ldw=36), dict(ldh=68), dict(lds=132),
     dict(SE=P, lds=132)])
