@@ -105,10 +105,12 @@ __device__ __forceinline__ void finish_stats(const float (&s)[2], float inv_d, f
 // How rows of at most kMaxRow elements are walked, forward and backward: tpr
 // threads (whole warps) share a row, EPT elements each, and a block's groups of
 // tpr threads take rows in turn, so that the gradients' columns stay with
-// their threads.  Aligned rows are prefetched into a ring in shared memory
-// (cp.async), each thread only its own elements, so a thread waits for no
-// other; the rest are loaded when their turn comes.  The scale and the shift
-// lie in shared memory.
+// their threads.  Rows are prefetched into a ring in shared memory (cp.async, 16
+// bytes at a time where they are aligned, else 4), each thread only its own
+// elements, so a thread waits for no other; bf16 rows that start between two
+// words are loaded when their turn comes.  (bf16 21746 x 3086, whose rows are
+// 4-byte aligned: forward 136 us loaded so, 89 through the ring, backward 237
+// and 116.)  The scale and the shift lie in shared memory.
 //   EPT: with 8 elements a thread the kernels were bound by instruction issue
 // (about 250 instructions a row and warp besides the elements: 94 us for the
 // forward of 65536 x 1024 bf16); more elements share that.  The forward takes
@@ -123,29 +125,32 @@ template <bool FWD> struct RowCfg {   // one block to an SM
 template <typename T, int VEC, int EPT, int NT, bool FULL>   // NT tensors a row: x, or x and dy; FULL: no thread's elements end early
 struct RowFetch {
   static constexpr int NV = EPT / VEC;
-  static constexpr bool RING = VEC > 1;
+  static constexpr int CB = VEC * (int)sizeof(T);   // bytes of a unit
+  static constexpr bool RING = CB >= 4;
   static constexpr int FIT = RowCfg<NT == 1>::RING / (EPT * (int)sizeof(T) * NT);
   static constexpr int STAGES = FIT > 6 ? 6 : FIT;
   static_assert(!RING || STAGES >= 2, "a row ahead at least");
   const T* src[NT];      // the tensors, at this thread's first element
   int64_t ld[NT];
   int64_t M, step;       // rows, rows from one to the next
-  int cols;              // this thread's elements start below D from (cols) on: unit i is there while i * tpr * VEC < cols
+  int cols;              // elements from this thread's first one to D
   int hop;               // elements from unit to unit
-  uint32_t ring;         // this thread's 16 bytes of unit 0 of stage 0
+  uint32_t ring;         // this thread's place of unit 0 of stage 0
   uint32_t pitch;        // bytes from unit to unit
-  uint4 raw[NT][RING ? NV : 1];
+  uint32_t raw[NT][RING ? NV : 1][RING ? CB / 4 : 1];
   T one[NT][RING ? 1 : NV];
 
   __device__ __forceinline__ void setup(int t, int tpr, int D, uint32_t ring0) {
     cols = D - t * VEC;
     hop = tpr * VEC;
-    ring = ring0 + threadIdx.x * 16;
-    pitch = blockDim.x * 16;
+    ring = ring0 + threadIdx.x * CB;
+    pitch = blockDim.x * CB;
 #pragma unroll
     for (int k = 0; k < NT; ++k) src[k] += t * VEC;
   }
-  __device__ __forceinline__ bool in(int i) const { return FULL || i * hop < cols; }
+  // (tpr is the least multiple of 32 with tpr EPT >= D: with more than 8
+  // elements a thread the first half of its units is always there)
+  __device__ __forceinline__ bool in(int i) const { return FULL || (EPT > 8 && i < NV / 2) || i * hop < cols; }
   __device__ __forceinline__ void issue(int64_t row, int stage) {
     if constexpr (RING) {
       if (row < M) {
@@ -155,16 +160,35 @@ struct RowFetch {
           const uint32_t to = ring + (uint32_t)(stage * NT + k) * NV * pitch;
 #pragma unroll
           for (int i = 0; i < NV; ++i)
-            if (in(i))
-              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + (uint32_t)i * pitch), "l"(r + i * hop)
-                           : "memory");
+            if (in(i)) {
+              if constexpr (CB == 16)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + (uint32_t)i * pitch), "l"(r + i * hop)
+                             : "memory");
+              else
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + (uint32_t)i * pitch), "l"(r + i * hop)
+                             : "memory");
+            }
         }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     }
   }
+  __device__ __forceinline__ static void clear(uint32_t at) {
+    if constexpr (CB == 16)
+      asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0u) : "memory");
+    else
+      asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(0u) : "memory");
+  }
+  // The first rows' fetches.  Units that are not there are zeros in every
+  // stage: the sums run over them without a branch (bf16 16384 x 1000,
+  // forward: 16.7 us with branches, 15.5 without).
   __device__ __forceinline__ void start(int64_t row) {
     if constexpr (RING) {
+      if constexpr (!FULL)
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+          if (!in(i))
+            for (int s = 0; s < STAGES * NT; ++s) clear(ring + (uint32_t)(s * NV + i) * pitch);
 #pragma unroll
       for (int s = 0; s < STAGES - 1; ++s) issue(row + s * step, s);
     }
@@ -176,11 +200,16 @@ struct RowFetch {
 #pragma unroll
       for (int k = 0; k < NT; ++k)
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(raw[k][i].x), "=r"(raw[k][i].y), "=r"(raw[k][i].z), "=r"(raw[k][i].w)
-                       : "r"(ring + (uint32_t)((stage * NT + k) * NV + i) * pitch)
-                       : "memory");
+        for (int i = 0; i < NV; ++i) {
+          const uint32_t at = ring + (uint32_t)((stage * NT + k) * NV + i) * pitch;
+          if constexpr (CB == 16)
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(raw[k][i][0]), "=r"(raw[k][i][1]), "=r"(raw[k][i][2]), "=r"(raw[k][i][3])
+                         : "r"(at)
+                         : "memory");
+          else
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(raw[k][i][0]) : "r"(at) : "memory");
+        }
       issue(row + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);   // the row before's, read by now
       stage = stage + 1 == STAGES ? 0 : stage + 1;
     } else {
@@ -190,26 +219,28 @@ struct RowFetch {
         for (int i = 0; i < NV; ++i) one[k][i] = in(i) ? src[k][row * ld[k] + i * hop] : from_f32<T>(0.f);
     }
   }
-  // Elements 2 q and 2 q + 1 of this thread (of the order c(q) below); single
-  // elements beyond D are `fill`.
-  __device__ __forceinline__ F2 get(int k, int q, float fill) const {
+  // Elements 2 q and 2 q + 1 of this thread, zeros beyond D.
+  __device__ __forceinline__ F2 get(int k, int q) const {
     if constexpr (!RING) {
-      return pack2(to_f32(one[k][2 * q]), in(2 * q + 1) ? to_f32(one[k][2 * q + 1]) : fill);
+      return pack2(to_f32(one[k][2 * q]), to_f32(one[k][2 * q + 1]));
+    } else if constexpr (VEC == 1) {
+      return pack2(__uint_as_float(raw[k][2 * q][0]), __uint_as_float(raw[k][2 * q + 1][0]));
+    } else if constexpr (sizeof(T) == 4) {
+      return pack2(__uint_as_float(raw[k][q / 2][2 * (q & 1)]), __uint_as_float(raw[k][q / 2][2 * (q & 1) + 1]));
     } else {
-      const uint4& r = raw[k][2 * q / VEC];
-      if constexpr (sizeof(T) == 4) {
-        return (q & 1) ? pack2(__uint_as_float(r.z), __uint_as_float(r.w)) : pack2(__uint_as_float(r.x), __uint_as_float(r.y));
-      } else {
-        const uint32_t w = (q & 3) == 0 ? r.x : (q & 3) == 1 ? r.y : (q & 3) == 2 ? r.z : r.w;
-        return pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-      }
+      const uint32_t w = raw[k][2 * q / VEC][VEC == 2 ? 0 : q & 3];
+      return pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
     }
+  }
+  // v for pair q's elements, zeros beyond D.
+  __device__ __forceinline__ F2 only(int q, float v) const {
+    return pack2(has(q) ? v : 0.f, in((2 * q + 1) / VEC) ? v : 0.f);
   }
   // Whether pair q is there at all, and the row's elements it holds: offsets
   // from this thread's first one.
   __device__ __forceinline__ bool has(int q) const { return in(2 * q / VEC); }
   __device__ __forceinline__ int at(int q) const { return 2 * q / VEC * hop + (VEC == 1 ? 0 : 2 * q % VEC); }
-  // A vector of D floats in shared memory, in the order the threads use it:
+  // A vector of D floats (and zeros up to tpr EPT) in shared memory, in the order the threads use it:
   // four consecutive elements of thread t at 16 t, so that a warp's 16-byte
   // loads run through it (in memory order, lanes 32 bytes apart conflicted
   // four ways: 52 us for the forward of 65536 x 1024).
@@ -223,21 +254,24 @@ struct RowFetch {
   }
   // Pairs q and q + 1 (q even) of such a vector, v at this thread's first element.
   __device__ __forceinline__ void vec4(const float* v, int q, F2& a, F2& b) const {
-    if constexpr (RING) {
+    if constexpr (VEC >= 4) {
       const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(v + (2 * q / 4) * (hop / VEC) * 4);
       a.v = w.x;
       b.v = w.y;
+    } else if constexpr (VEC == 2) {
+      a.v = *reinterpret_cast<const uint64_t*>(v + at(q));
+      b.v = *reinterpret_cast<const uint64_t*>(v + at(q + 1));
     } else {
-      a = pack2(v[at(q)], in(2 * q + 1) ? v[at(q) + hop] : 0.f);
-      b = has(q + 1) ? pack2(v[at(q + 1)], in(2 * q + 3) ? v[at(q + 1) + hop] : 0.f) : pack2(0.f, 0.f);
+      a = pack2(v[at(q)], v[at(q) + hop]);
+      b = pack2(v[at(q + 1)], v[at(q + 1) + hop]);
     }
   }
 };
-// A thread's results to its elements of a row, a unit (unaligned: two pairs)
-// at a time: f(q, a, b) gives pairs q and q + 1.
+// A thread's results to its elements of a row, a unit (of less than 16 bytes:
+// two pairs) at a time: get(q, a, b) gives pairs q and q + 1.
 template <typename T, int VEC, int EPT, class F, class Get>
 __device__ __forceinline__ void put_row(const F& f, T* row, Get get) {
-  constexpr int PAIRS = VEC == 1 ? 2 : VEC / 2;
+  constexpr int PAIRS = VEC <= 4 ? 2 : VEC / 2;
 #pragma unroll
   for (int q = 0; q < EPT / 2; q += PAIRS) {
     if (!f.has(q)) continue;
@@ -253,6 +287,10 @@ __device__ __forceinline__ void put_row(const F& f, T* row, Get get) {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         if (f.in(2 * q + j)) row[(2 * q + j) * f.hop] = from_f32<T>(v[j]);
+    } else if constexpr (VEC == 2) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        if (f.has(q + j)) *reinterpret_cast<__nv_bfloat162*>(row + f.at(q + j)) = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
     } else {
       store_vec<T, VEC>(row + f.at(q), v);
     }
@@ -301,35 +339,29 @@ __global__ void __launch_bounds__(RowCfg<true>::THREADS, 1) ln_fwd_kernel(const 
     scale[F::place(c, tpr)] = p.gamma ? p.gamma[c] : 1.f;
     shift[F::place(c, tpr)] = p.beta ? p.beta[c] : 0.f;
   }
+  if constexpr (!FULL)
+    for (int c = p.D + threadIdx.x; c < tpr * EPT; c += blockDim.x) scale[F::place(c, tpr)] = shift[F::place(c, tpr)] = 0.f;
   __syncthreads();
   const float inv_d = 1.0f / (float)p.D;
-  const int my = VEC == 1 ? t : t * 4;   // this thread's first place in them
+  const int my = t * (VEC < 4 ? VEC : 4);   // this thread's first place in them
   int stage = 0;
   for (; row < p.M; row += f.step) {
     f.take(row, stage);
     F2 v[NP], a = pack2(0.f, 0.f), b = a;
 #pragma unroll
     for (int q = 0; q < NP; ++q) {
-      v[q] = f.get(0, q, 0.f);
-      if (f.has(q)) a = add2(a, v[q]);
+      v[q] = f.get(0, q);
+      a = add2(a, v[q]);
     }
     float s[1] = {sum2(a)}, sd[2];
     group_sums<1>(s, ln_smem, group, wpr);
     const float mean = s[0] * inv_d;
-    const F2 minus = pack2(-mean, -mean);
     a = b;
 #pragma unroll
     for (int q = 0; q < NP; ++q) {
-      v[q] = add2(v[q], minus);
-      if (VEC == 1 && !f.in(2 * q + 1)) {   // (a single last element)
-        float x, y;
-        unpack2(v[q], x, y);
-        v[q] = pack2(x, 0.f);
-      }
-      if (f.has(q)) {
-        a = add2(a, v[q]);
-        b = fma2(v[q], v[q], b);
-      }
+      v[q] = add2(v[q], f.only(q, -mean));
+      a = add2(a, v[q]);
+      b = fma2(v[q], v[q], b);
     }
     sd[0] = sum2(a);
     sd[1] = sum2(b);
@@ -416,6 +448,8 @@ __global__ void __launch_bounds__(RowCfg<false>::THREADS, 1) ln_bwd_kernel(const
   int64_t row = blockIdx.x * (int64_t)groups + group;
   f.start(row);
   for (int c = threadIdx.x; c < p.D; c += blockDim.x) scale[F::place(c, tpr)] = p.gamma ? p.gamma[c] : 1.f;
+  if constexpr (!FULL)
+    for (int c = p.D + threadIdx.x; c < tpr * EPT; c += blockDim.x) scale[F::place(c, tpr)] = 0.f;
   const float inv_d = 1.0f / (float)p.D;
   const F2 zero = pack2(0.f, 0.f);
   F2 dg[NP], db[NP];
@@ -424,23 +458,21 @@ __global__ void __launch_bounds__(RowCfg<false>::THREADS, 1) ln_bwd_kernel(const
   float mean = 0.f, rstd = 0.f;
   if (row < p.M) { mean = p.mean[row]; rstd = p.rstd[row]; }
   __syncthreads();
-  const float* sc = scale + (VEC == 1 ? t : t * 4);
+  const float* sc = scale + t * (VEC < 4 ? VEC : 4);
   int stage = 0, buf = 0;
   for (; row < p.M; row += f.step) {
     float next_mean = 0.f, next_rstd = 0.f;
     if (row + f.step < p.M) { next_mean = p.mean[row + f.step]; next_rstd = p.rstd[row + f.step]; }
     f.take(row, stage);
-    const F2 minus = pack2(-mean, -mean), times = pack2(rstd, rstd);
+    const F2 times = pack2(rstd, rstd);
     F2 a = zero, b = zero;
 #pragma unroll
     for (int q0 = 0; q0 < NP; q0 += 2) {
-      if (!f.has(q0)) continue;
       F2 g[2];
       f.vec4(sc, q0, g[0], g[1]);
 #pragma unroll
       for (int q = q0; q < q0 + 2; ++q) {
-        if (VEC == 1 && !f.has(q)) continue;
-        const F2 d = f.get(1, q, 0.f), xh = mul2(add2(f.get(0, q, mean), minus), times), w = mul2(d, g[q - q0]);
+        const F2 d = f.get(1, q), xh = mul2(add2(f.get(0, q), f.only(q, -mean)), times), w = mul2(d, g[q - q0]);
         dg[q] = fma2(d, xh, dg[q]);
         db[q] = add2(db[q], d);
         a = add2(a, w);
@@ -452,12 +484,12 @@ __global__ void __launch_bounds__(RowCfg<false>::THREADS, 1) ln_bwd_kernel(const
     buf ^= 1;
     // rstd (w - c1 - xh c2) = w rstd - c1 rstd - (x - mean) rstd^2 c2
     const float c1 = -s[0] * inv_d * rstd, c2 = -s[1] * inv_d * rstd * rstd;
-    const F2 p1 = pack2(c1, c1), p2 = pack2(c2, c2);
+    const F2 minus = pack2(-mean, -mean), p1 = pack2(c1, c1), p2 = pack2(c2, c2);
     put_row<T, VEC, EPT>(f, reinterpret_cast<T*>(p.dx) + row * p.lddx + t * VEC, [&](int q, F2& o0, F2& o1) {
       F2 g0, g1;
       f.vec4(sc, q, g0, g1);
-      o0 = fma2(add2(f.get(0, q, mean), minus), p2, fma2(mul2(f.get(1, q, 0.f), g0), times, p1));
-      o1 = fma2(add2(f.get(0, q + 1, mean), minus), p2, fma2(mul2(f.get(1, q + 1, 0.f), g1), times, p1));
+      o0 = fma2(add2(f.get(0, q), minus), p2, fma2(mul2(f.get(1, q), g0), times, p1));
+      o1 = fma2(add2(f.get(0, q + 1), minus), p2, fma2(mul2(f.get(1, q + 1), g1), times, p1));
     });
     mean = next_mean;
     rstd = next_rstd;
@@ -561,17 +593,20 @@ __global__ void __launch_bounds__(1024) ln_param_reduce_kernel(const __grid_cons
   }
 }
 
-bool aligned16(const void* p, int64_t ld, size_t es) {
-  return ((uintptr_t)p & 15) == 0 && (ld * (int64_t)es) % 16 == 0;
+// The elements that move at once: 16 bytes of them, 4 bytes, or (bf16 between
+// words) one.  bits: the row length, the pitches and the bases in bytes, or'ed.
+int unit_of(bool f32, uint64_t bits) {
+  const int es = f32 ? 4 : 2;
+  return (bits & 15) == 0 ? 16 / es : (bits & 3) == 0 ? 4 / es : 1;
 }
 
 // How a block walks rows of D elements: elements per thread, threads per row,
 // block and grid.
 struct RowShape { int ept, tpr, threads; int64_t blocks; };
 template <bool FWD>
-RowShape row_shape(bool f32, bool vec, int64_t M, int64_t D) {
+RowShape row_shape(bool f32, int unit, int64_t M, int64_t D) {
   RowShape s;
-  s.ept = D <= 256 ? 8 : D <= 512 || f32 || !vec || !FWD ? 16 : 32;
+  s.ept = D <= 256 ? 8 : D <= 512 || f32 || unit < 8 || !FWD ? 16 : 32;
   s.tpr = (int)(32 * ceil_div(D, 32 * s.ept));
   // (rows of two warps and more: 15 named barriers.  The forward's scale and
   // shift leave 768 threads' rings beside them from 4096 elements on.)
@@ -587,15 +622,17 @@ unsigned row_smem(const RowShape& s, bool ring, int64_t D) {
   return (unsigned)(fixed + std::max<int64_t>(ring ? s.threads * RowCfg<FWD>::RING : 0, FWD ? 0 : cols));
 }
 // Blocks of the backward, each with its partial rows of dgamma and dbeta (the
-// most that any alignment of this shape takes).
-int64_t bwd_blocks(bool f32, bool vec, int64_t M, int64_t D) {
-  return D > kMaxRow ? std::min<int64_t>(M, 32) : row_shape<false>(f32, vec, M, D).blocks;
+// same for every type and alignment).
+int64_t bwd_blocks(int64_t M, int64_t D) {
+  return D > kMaxRow ? std::min<int64_t>(M, 32) : row_shape<false>(false, 1, M, D).blocks;
 }
 
 template <typename T, int VEC, int EPT, bool FULL, bool FWD>
 const void* row_kernel() {
   static std::once_flag once;
-  const void* k = FWD ? (const void*)ln_fwd_kernel<T, VEC, EPT, FULL> : (const void*)ln_bwd_kernel<T, VEC, EPT, FULL>;
+  const void* k;
+  if constexpr (FWD) k = (const void*)ln_fwd_kernel<T, VEC, EPT, FULL>;
+  else k = (const void*)ln_bwd_kernel<T, VEC, EPT, FULL>;
   std::call_once(once, [k] { cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448); });
   return k;
 }
@@ -606,15 +643,18 @@ const void* row_full(bool full) {
   return full ? row_kernel<T, VEC, EPT, true, FWD>() : row_kernel<T, VEC, EPT, false, FWD>();
 }
 template <bool FWD>
-const void* row_pick(bool f32, bool vec, const RowShape& s, int64_t D) {
+const void* row_pick(bool f32, int unit, const RowShape& s, int64_t D) {
   using B = __nv_bfloat16;
   const bool e8 = s.ept == 8, full = D == (int64_t)s.tpr * s.ept;
-  if (!vec) {
-    if (f32) return e8 ? row_kernel<float, 1, 8, false, FWD>() : row_kernel<float, 1, 16, false, FWD>();
-    return e8 ? row_kernel<B, 1, 8, false, FWD>() : row_kernel<B, 1, 16, false, FWD>();
+  if (f32) {
+    if (unit == 1) return e8 ? row_kernel<float, 1, 8, false, FWD>() : row_kernel<float, 1, 16, false, FWD>();
+    return e8 ? row_full<float, 4, 8, FWD>(full) : row_full<float, 4, 16, FWD>(full);
   }
-  if (f32) return e8 ? row_full<float, 4, 8, FWD>(full) : row_full<float, 4, 16, FWD>(full);
-  return e8 ? row_full<B, 8, 8, FWD>(full) : s.ept == 16 ? row_full<B, 8, 16, FWD>(full) : row_full<B, 8, 32, FWD>(full);
+  if (unit == 1) return e8 ? row_kernel<B, 1, 8, false, FWD>() : row_kernel<B, 1, 16, false, FWD>();
+  if (unit == 2) return e8 ? row_kernel<B, 2, 8, false, FWD>() : row_kernel<B, 2, 16, false, FWD>();
+  if constexpr (FWD)
+    if (s.ept == 32) return row_full<B, 8, 32, FWD>(full);
+  return e8 ? row_full<B, 8, 8, FWD>(full) : row_full<B, 8, 16, FWD>(full);
 }
 
 }  // namespace
@@ -625,8 +665,7 @@ int layernorm_plan(const LayerNormOp& op, LaunchRec* rec, char* err, size_t errl
     return -1;
   }
   const bool f32 = op.dtype == DT_F32;
-  const size_t es = f32 ? 4 : 2;
-  const bool v = op.D % (f32 ? 4 : 8) == 0 && aligned16(op.x, op.ldx, es) && aligned16(op.y, op.ldy, es);
+  const int unit = unit_of(f32, (uintptr_t)op.x | (uintptr_t)op.y | (uint64_t)(op.D | op.ldx | op.ldy) * (f32 ? 4 : 2));
   LnFwdParams q{op.x, op.ldx, op.gamma, op.beta, op.y, op.ldy, op.mean, op.rstd, op.M, (int)op.D, op.eps, 0};
   if (op.D > kMaxRow) {
     rec->func = f32 ? (const void*)ln_fwd_wide_kernel<float> : (const void*)ln_fwd_wide_kernel<__nv_bfloat16>;
@@ -634,21 +673,20 @@ int layernorm_plan(const LayerNormOp& op, LaunchRec* rec, char* err, size_t errl
     rec->block = dim3(1024);
     rec->smem = 0;
   } else {
-    const RowShape s = row_shape<true>(f32, v, op.M, op.D);
+    const RowShape s = row_shape<true>(f32, unit, op.M, op.D);
     q.tpr = s.tpr;
-    rec->func = row_pick<true>(f32, v, s, op.D);
+    rec->func = row_pick<true>(f32, unit, s, op.D);
     rec->grid = dim3((unsigned)s.blocks);
     rec->block = dim3((unsigned)s.threads);
-    rec->smem = row_smem<true>(s, v, op.D);
+    rec->smem = row_smem<true>(s, f32 || unit > 1, op.D);
   }
   rec->name = "layernorm_fwd";
   rec->set_args(q);
   return 1;
 }
 
-size_t layernorm_bwd_workspace_bytes(int dtype, int64_t M, int64_t D) {
-  const bool f32 = dtype == DT_F32;
-  return (size_t)std::max(bwd_blocks(f32, true, M, D), bwd_blocks(f32, false, M, D)) * 2 * (size_t)D * sizeof(float);
+size_t layernorm_bwd_workspace_bytes(int64_t M, int64_t D) {
+  return (size_t)bwd_blocks(M, D) * 2 * (size_t)D * sizeof(float);
 }
 
 int layernorm_bwd_plan(const LayerNormBwdOp& op, LaunchRec* recs, char* err, size_t errlen) {
@@ -658,16 +696,15 @@ int layernorm_bwd_plan(const LayerNormBwdOp& op, LaunchRec* recs, char* err, siz
     return -1;
   }
   const bool params = op.dgamma || op.dbeta;
-  if (params && (!op.ws || op.ws_bytes < layernorm_bwd_workspace_bytes(op.dtype, op.M, op.D) || (uintptr_t)op.ws % 4)) {
+  if (params && (!op.ws || op.ws_bytes < layernorm_bwd_workspace_bytes(op.M, op.D) || (uintptr_t)op.ws % 4)) {
     snprintf(err, errlen, "layer-norm backward workspace too small (%zu < %zu) or misaligned", op.ws_bytes,
-             layernorm_bwd_workspace_bytes(op.dtype, op.M, op.D));
+             layernorm_bwd_workspace_bytes(op.M, op.D));
     return -1;
   }
   const bool f32 = op.dtype == DT_F32;
-  const size_t es = f32 ? 4 : 2;
-  const bool v = op.D % (f32 ? 4 : 8) == 0 && aligned16(op.x, op.ldx, es) && aligned16(op.dy, op.lddy, es) &&
-                 aligned16(op.dx, op.lddx, es);
-  const int64_t blocks = bwd_blocks(f32, v, op.M, op.D);
+  const int unit = unit_of(f32, (uintptr_t)op.x | (uintptr_t)op.dy | (uintptr_t)op.dx |
+                                    (uint64_t)(op.D | op.ldx | op.lddy | op.lddx) * (f32 ? 4 : 2));
+  const int64_t blocks = bwd_blocks(op.M, op.D);
   LnBwdParams q{op.dy, op.lddy, op.x, op.ldx, op.gamma, op.mean, op.rstd, op.dx, op.lddx,
                 params ? op.ws : nullptr, op.M, (int)op.D, 0};
   int n = 0;
@@ -684,12 +721,12 @@ int layernorm_bwd_plan(const LayerNormBwdOp& op, LaunchRec* recs, char* err, siz
     recs[n].grid = dim3((unsigned)op.M);
     recs[n].block = dim3(1024);
   } else {
-    const RowShape s = row_shape<false>(f32, v, op.M, op.D);
+    const RowShape s = row_shape<false>(f32, unit, op.M, op.D);
     q.tpr = s.tpr;
-    recs[n].func = row_pick<false>(f32, v, s, op.D);
+    recs[n].func = row_pick<false>(f32, unit, s, op.D);
     recs[n].grid = dim3((unsigned)s.blocks);
     recs[n].block = dim3((unsigned)s.threads);
-    recs[n].smem = row_smem<false>(s, v, op.D);
+    recs[n].smem = row_smem<false>(s, f32 || unit > 1, op.D);
   }
   recs[n].name = "layernorm_bwd";
   recs[n++].set_args(q);

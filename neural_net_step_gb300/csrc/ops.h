@@ -295,7 +295,7 @@ struct LayerNormBwdOp {
   float* dgamma = nullptr; float* dbeta = nullptr;             // nullable
   float* ws = nullptr; size_t ws_bytes = 0;
 };
-size_t layernorm_bwd_workspace_bytes(int dtype, int64_t M, int64_t D);
+size_t layernorm_bwd_workspace_bytes(int64_t M, int64_t D);
 // Up to three records.
 int layernorm_bwd_plan(const LayerNormBwdOp& op, LaunchRec* recs, char* err, size_t errlen);
 

@@ -22,7 +22,9 @@ SHAPES = [(dt, M, D, pad, off) for dt in (nn.F32, nn.BF16) for M, D, pad, off in
     (1, 1, 0, 0), (3, 2, 0, 0), (9, 7, 1, 1), (8, 8, 0, 0), (5, 31, 0, 0), (64, 64, 8, 8), (33, 250, 0, 0),
     (17, 256, 0, 0), (17, 257, 0, 3), (40, 512, 16, 0), (77, 784, 0, 0), (77, 1000, 0, 1), (1, 1024, 0, 0),
     (700, 1024, 0, 0), (12, 1025, 0, 0), (12, 1032, 0, 0), (30, 2048, 0, 0), (9, 4096, 8, 0), (9, 4100, 0, 0),
-    (5, 8192, 0, 0), (5, 8191, 1, 0), (3, 8193, 0, 0), (2, 20000, 0, 8)]]
+    (5, 8192, 0, 0), (5, 8191, 1, 0), (3, 8193, 0, 0), (2, 20000, 0, 8),
+    # rows that start between 16-byte units, at whole words for bf16 too
+    (21, 30, 2, 2), (21, 256, 2, 0), (41, 258, 0, 2), (41, 770, 2, 2), (1500, 2050, 0, 0), (7, 8190, 2, 2), (6, 8192, 0, 2)]]
 
 
 def _fwd_tol(x, gamma, y, mean, rstd, D, dtype):
