@@ -173,8 +173,8 @@ mlp_status mlp_op_argmax(int dtype, int64_t B, int64_t C, const void* z, int64_t
  *   + eps),  Y_ij = (X_ij - mean_i) rstd_i gamma_j + beta_j.
  *   gamma, beta fp32 [D] (nullable: 1 and 0); Y [M, D] (ldy, dtype; may be
  *   X with X's pitch); mean, rstd fp32 [M] (nullable: not kept).  eps >= 0 and finite.
- * Any D up to 65535 * 256 and any alignment of the elements; rows whose base
- * and pitch are 16-byte aligned move by 16-byte accesses.  Statistics are
+ * Any D up to 65535 * 256 and any pitch.  Rows move 16 bytes at a time where D,
+ * base and pitch allow it, else 4 bytes, else an element.  Statistics are
  * fp32, from the elements as stored. */
 mlp_status mlp_op_layernorm(int dtype, int64_t M, int64_t D, const void* X, int64_t ldx, const float* gamma,
                             const float* beta, float eps, void* Y, int64_t ldy, float* mean, float* rstd,
@@ -205,8 +205,8 @@ mlp_status mlp_op_layernorm_backward(int dtype, int64_t M, int64_t D, const void
  * reads back as infinite.
  *   X, Y [rows, cols] (ldx, ldy; MLP_F32 or MLP_BF16), Q uint8 [rows, cols]
  *   (ldq), E uint8 [rows, ceil(cols / 32)] (lde).
- * Any alignment; 16-byte aligned rows of X / Y with 8-byte aligned rows of Q
- * move by wide accesses. */
+ * Any pitch; 16-byte aligned rows of X / Y with 8-byte aligned rows of Q move
+ * by wide accesses.  Nothing written may overlap anything read. */
 mlp_status mlp_op_quant8(int dtype, int64_t rows, int64_t cols, const void* X, int64_t ldx, uint8_t* Q, int64_t ldq,
                          uint8_t* E, int64_t lde, void* stream);
 mlp_status mlp_op_dequant8(int dtype, int64_t rows, int64_t cols, const uint8_t* Q, int64_t ldq, const uint8_t* E,
@@ -224,8 +224,8 @@ mlp_status mlp_op_dequant8(int dtype, int64_t rows, int64_t cols, const uint8_t*
  * first (gate and up half each as one matrix of F columns).  H comes from the
  * fp32 sums, before s is rounded.  MLP_F32 or MLP_BF16; MLP_BF16 takes K, F
  * and the leading dimensions (but ldse) in multiples of 8 and 16-byte aligned
- * matrices (S codes: 8-byte).  M from one token on.  Nothing written may
- * overlap anything read. */
+ * matrices (S codes: 8-byte).  M from one token on (MLP_F32: to 65535 * 128).
+ * Nothing written may overlap anything read. */
 enum { MLP_ACT_SILU = 3 };   /* the gated operations only */
 mlp_status mlp_op_gated_linear(int dtype, int act, int64_t M, int64_t F, int64_t K, const void* X, int64_t ldx,
                                const void* W, int64_t ldw, const float* b, void* H, int64_t ldh, void* S, int64_t lds,
@@ -249,8 +249,10 @@ mlp_status mlp_op_gated_dgrad(int dtype, int act, int64_t M, int64_t N, int64_t 
  *   dW = dY^T X (fp32 [N, K], lddw), db = sum over rows of dY (nullable),
  *   dY [B, N] (ldy; MLP_F32 or MLP_BF16), X [B, K] the values of Q (ldq), E
  *   (lde).  The values are read back into the workspace (16-byte aligned, at
- *   least the bytes below; the dtype holds them exactly), so the result is
- *   that of mlp_op_wgrad on them. */
+ *   least the bytes below; the dtype holds them exactly): the result is that
+ *   of mlp_op_wgrad on them up to the order of its sums.  MLP_BF16 takes K and
+ *   lddw in multiples of 4, ldy of 8 and 16-byte aligned dY and dW.
+ *   Workspaces of calls that may overlap must not. */
 size_t mlp_op_wgrad8_workspace_bytes(int dtype, int64_t N, int64_t K, int64_t B);
 mlp_status mlp_op_wgrad8(int dtype, int64_t N, int64_t K, int64_t B, const void* dY, int64_t ldy, const uint8_t* Q,
                          int64_t ldq, const uint8_t* E, int64_t lde, float* dW, int64_t lddw, float* db,

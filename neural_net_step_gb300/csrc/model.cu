@@ -6,6 +6,7 @@
 #include <stdio.h>
 #include <string.h>
 
+#include <initializer_list>
 #include <mutex>
 #include <vector>
 
@@ -1356,6 +1357,14 @@ static mlp_status run_chain(LaunchRec* r, int n, void* stream) {
   return ok();
 }
 
+// Whether every address (null: absent) is a multiple of an element's size.
+static bool elements_aligned(size_t es, std::initializer_list<const void*> ps) {
+  uintptr_t all = 0;
+  for (const void* p : ps) all |= (uintptr_t)p;
+  return all % es == 0;
+}
+static size_t dtype_bytes(int d) { return d == MLP_BF16 ? 2 : 4; }
+
 static bool dtype_ok(int d) { return d == MLP_F32 || d == MLP_BF16; }
 static bool gemm_dtype_ok(int d) { return d == MLP_F32 || d == MLP_BF16 || d == MLP_F32X3; }
 static bool act_ok(int a) { return a >= MLP_ACT_NONE && a <= MLP_ACT_GELU_TANH; }
@@ -1619,6 +1628,8 @@ mlp_status mlp_op_layernorm(int dtype, int64_t M, int64_t D, const void* X, int6
   if (!dtype_ok(dtype)) return fail(MLP_ERR_DTYPE, "bad dtype");
   if (!X || !Y) return fail(MLP_ERR_ARG, "null pointer");
   if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(MLP_ERR_ARG, "eps must be finite and not negative");
+  if (!elements_aligned(dtype_bytes(dtype), {X, Y}) || !elements_aligned(4, {gamma, beta, mean, rstd}))
+    return fail(MLP_ERR_ARG, "misaligned elements");
   LayerNormOp op;
   op.dtype = dtype; op.M = M; op.D = D; op.x = X; op.ldx = ldx; op.gamma = gamma; op.beta = beta; op.eps = eps;
   op.y = Y; op.ldy = ldy; op.mean = mean; op.rstd = rstd;
@@ -1639,6 +1650,8 @@ mlp_status mlp_op_layernorm_backward(int dtype, int64_t M, int64_t D, const void
                                      void* stream) {
   if (!dtype_ok(dtype)) return fail(MLP_ERR_DTYPE, "bad dtype");
   if (!dY || !X || !mean || !rstd || !dX) return fail(MLP_ERR_ARG, "null pointer");
+  if (!elements_aligned(dtype_bytes(dtype), {dY, X, dX}) || !elements_aligned(4, {gamma, mean, rstd, dgamma, dbeta}))
+    return fail(MLP_ERR_ARG, "misaligned elements");
   LayerNormBwdOp op;
   op.dtype = dtype; op.M = M; op.D = D; op.dy = dY; op.lddy = lddy; op.x = X; op.ldx = ldx; op.gamma = gamma;
   op.mean = mean; op.rstd = rstd; op.dx = dX; op.lddx = lddx; op.dgamma = dgamma; op.dbeta = dbeta;
@@ -1654,6 +1667,7 @@ mlp_status mlp_op_quant8(int dtype, int64_t rows, int64_t cols, const void* X, i
                          uint8_t* E, int64_t lde, void* stream) {
   if (!dtype_ok(dtype)) return fail(MLP_ERR_DTYPE, "bad dtype");
   if (!X || !Q || !E) return fail(MLP_ERR_ARG, "null pointer");
+  if (!elements_aligned(dtype_bytes(dtype), {X})) return fail(MLP_ERR_ARG, "misaligned elements");
   LaunchRec r;
   char e_[512] = "";
   if (quant8_plan(dtype, rows, cols, X, ldx, Q, ldq, E, lde, &r, e_, sizeof(e_)) < 0)
@@ -1665,6 +1679,7 @@ mlp_status mlp_op_dequant8(int dtype, int64_t rows, int64_t cols, const uint8_t*
                            int64_t lde, void* Y, int64_t ldy, void* stream) {
   if (!dtype_ok(dtype)) return fail(MLP_ERR_DTYPE, "bad dtype");
   if (!Q || !E || !Y) return fail(MLP_ERR_ARG, "null pointer");
+  if (!elements_aligned(dtype_bytes(dtype), {Y})) return fail(MLP_ERR_ARG, "misaligned elements");
   LaunchRec r;
   char e_[512] = "";
   if (dequant8_plan(dtype, rows, cols, Q, ldq, E, lde, Y, ldy, &r, e_, sizeof(e_)) < 0)
@@ -1677,6 +1692,9 @@ static const char* gated_layout(const GatedOp& op) {
   if (op.lda < op.K || op.ldb < (op.fwd ? op.K : op.F) || (op.h && op.ldh < op.F) || (op.s && op.lds < 2 * op.F) ||
       (op.se && op.ldse < 2 * ceil_div(op.F, 32)) || (op.ds && op.ldds < 2 * op.F))
     return "leading dimension too small";
+  if (!elements_aligned(4, {op.bias}) ||
+      !elements_aligned(dtype_bytes(op.dtype), {op.A, op.B, op.h, op.ds, op.se ? nullptr : op.s}))
+    return "misaligned elements";
   if (op.dtype == MLP_F32) return nullptr;
   auto off16 = [](const void* p, int64_t ld) { return (uintptr_t)p % 16 != 0 || ld % 8 != 0; };
   if (op.F % 8 || op.K % 8) return "bf16: widths in multiples of 8";
@@ -1743,6 +1761,8 @@ mlp_status mlp_op_wgrad8(int dtype, int64_t N, int64_t K, int64_t B, const void*
                          void* workspace, size_t ws_bytes, uint32_t* err_dev, void* stream) {
   if (!dtype_ok(dtype)) return fail(MLP_ERR_DTYPE, "bad dtype");
   if (!dY || !Q || !E || !dW || !workspace) return fail(MLP_ERR_ARG, "null pointer");
+  if (!elements_aligned(dtype_bytes(dtype), {dY}) || !elements_aligned(4, {dW, db}))
+    return fail(MLP_ERR_ARG, "misaligned elements");
   const size_t need = mlp_op_wgrad8_workspace_bytes(dtype, N, K, B);
   if (need == 0 || ldy < N || lddw < K) return fail(MLP_ERR_SHAPE, "bad shape or leading dimension");
   // the tensor cores' dW leaves by TMA in units of 16 bytes: a row's last unit must be whole

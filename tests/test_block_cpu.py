@@ -110,3 +110,15 @@ def test_silu_belongs_to_the_gated_operations():
         nn.mlp_op_linear_act(nn.BF16, nn.ACT_SILU, 4, 64, 64, P, 64, P, 64, P, P, 64, None, 0, None, None)
     with pytest.raises(nn.MlpError):
         nn.mlp_arena_bytes([8, 8, 4], None, nn.ACT_SILU, nn.F32, 4)
+
+
+@pytest.mark.parametrize("f,good,names", [
+    (nn.mlp_op_layernorm, LN, "X Y gamma beta mean rstd"), (nn.mlp_op_layernorm_backward, LNB, "dY X dX gamma mean rstd dgamma dbeta"),
+    (nn.mlp_op_quant8, Q8, "X"), (nn.mlp_op_dequant8, D8, "Y"), (nn.mlp_op_wgrad8, W8, "dY dW db"),
+    (nn.mlp_op_gated_linear, GF, "X W b H S"), (nn.mlp_op_gated_dgrad, GB, "dY Wd S dS H")])
+@pytest.mark.parametrize("dtype", [nn.F32, nn.BF16])
+def test_addresses_between_elements_are_refused(f, good, names, dtype):
+    """An address that is no multiple of an element's size."""
+    for name in names.split():
+        _refused(f, dict(good, dtype=dtype), **{name: P + 1})
+        _refused(f, dict(good, dtype=nn.F32), **{name: P + 2})
