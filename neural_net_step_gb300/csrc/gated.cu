@@ -18,6 +18,7 @@
 #include "f32x2.cuh"
 #include "gated.cuh"
 #include "ops.h"
+#include "tc.cuh"
 
 namespace mlpk {
 
@@ -38,22 +39,33 @@ struct GatedParams {
 // Tile of 16 RM rows by GT columns, GK deep, in a ring of GSTAGES slices that
 // cp.async fills an element at a time (any alignment; elements outside the
 // matrices as zeros) and transposes on the way.
-// Every kChunk slices (256 k) the accumulators are added to sums in shared
+// Every kChunk slices (1024 k) the accumulators are added to sums in shared
 // memory, which keeps the error of a long reduction near that of a short one
-// (K = 2000: 1.2e-6 of the result in one sequence of FMAs).
-constexpr int GT = 128, GK = 16, GSTAGES = 4, kChunk = 16;
+// (K = 4000: 1.1e-6 of the result in one sequence of FMAs, 5.7e-7 so).  The
+// sums leave room for one block to an SM, shorter reductions run two: 10000 x
+// 784 x 500 410 us with sums (every 256 k), 359 without.
+constexpr int GT = 128, GK = 16, GSTAGES = 4, kChunk = 64;
+
+__host__ __device__ constexpr int simt_pitch(int rm) { return (rm > 4 ? 128 : 16 * rm) + 4; }
 
 __device__ __forceinline__ void copy4(uint32_t dst, const float* src, bool in) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
 }
-template <bool FWD, int RM>   // RM rows and 8 columns per thread
+// RM (2, 4 .. 8) rows and 8 columns per thread: rows ty R1 .. of the tile's first
+// 16 R1, and ty R2 .. of the 16 R2 after them.  In a slice the second rows of
+// a thread stand four apart, so that it reads them at once whatever R2 is.
+template <bool FWD, int RM>
 __global__ void __launch_bounds__(256, 2) gated_simt_kernel(const __grid_constant__ GatedParams p) {
   pdl_enter();
-  constexpr int BM = 16 * RM, PA = BM + 4, PB = GT + 4;   // rows, pitches of the two slices
+  constexpr int BM = 16 * RM, R1 = RM < 4 ? RM : 4, R2 = RM - R1;
+  constexpr int PA = simt_pitch(RM), PB = GT + 4;         // pitches of the two slices
   constexpr int SLICE = GK * (PA + PB);
   extern __shared__ __align__(16) float gated_smem[];     // [GSTAGES]([GK][PA], [GK][PB]), [8 RM][256]
   constexpr int TF = FWD ? GT / 2 : GT;   // F columns per tile
-  const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
+  const int tid = threadIdx.x;
+  // a warp takes 4 x 8 threads' results: as many elements of A as of B to read
+  // for them (shared memory serves half a warp at a time)
+  const int tx = (tid >> 5) % 2 * 8 + tid % 8, ty = (tid >> 5) / 2 * 4 + (tid >> 3) % 4;
   const int m0 = blockIdx.y * BM, f0 = blockIdx.x * TF;
   const float* A = p.A;
   const float* B = p.B;
@@ -65,7 +77,8 @@ __global__ void __launch_bounds__(256, 2) gated_simt_kernel(const __grid_constan
     for (int i = 0; i < RM; ++i) {
       const int idx = tid + i * 256, m = idx / GK, kk = idx % GK, k = k0 + kk;
       const bool in = m0 + m < p.M && k < p.K;
-      copy4(as + (uint32_t)(kk * PA + m) * 4u, in ? A + (int64_t)(m0 + m) * p.lda + k : A, in);
+      const int at = R2 == 0 || m < 16 * R1 ? m : 64 + (m - 64) / (R2 ? R2 : 1) * 4 + (m - 64) % (R2 ? R2 : 1);
+      copy4(as + (uint32_t)(kk * PA + at) * 4u, in ? A + (int64_t)(m0 + m) * p.lda + k : A, in);
     }
 #pragma unroll
     for (int i = 0; i < GT * GK / 256; ++i) {
@@ -103,13 +116,12 @@ __global__ void __launch_bounds__(256, 2) gated_simt_kernel(const __grid_constan
     const float* Bs = As + GK * PA;
 #pragma unroll
     for (int kk = 0; kk < GK; ++kk) {
-      // rows ty * 4 + 0..3 and 64 + the same (RM = 8), ty * 4 .. (4), ty * 2 .. (2)
-      float a[RM];
+      float a[8];
       if constexpr (RM == 2) {
         *reinterpret_cast<float2*>(a) = *reinterpret_cast<const float2*>(As + kk * PA + ty * 2);
       } else {
         *reinterpret_cast<float4*>(a) = *reinterpret_cast<const float4*>(As + kk * PA + ty * 4);
-        if constexpr (RM == 8) *reinterpret_cast<float4*>(a + 4) = *reinterpret_cast<const float4*>(As + kk * PA + 64 + ty * 4);
+        if constexpr (R2 > 0) *reinterpret_cast<float4*>(a + 4) = *reinterpret_cast<const float4*>(As + kk * PA + 64 + ty * 4);
       }
       ulonglong2 b[2];
       b[0] = *reinterpret_cast<const ulonglong2*>(Bs + kk * PB + tx * 4);
@@ -150,7 +162,7 @@ __global__ void __launch_bounds__(256, 2) gated_simt_kernel(const __grid_constan
   const int64_t nb = q8_blocks(p.F);
 #pragma unroll
   for (int i = 0; i < RM; ++i) {
-    const int m = m0 + (RM == 2 ? ty * 2 + i : i < 4 ? ty * 4 + i : 60 + ty * 4 + i);
+    const int m = m0 + (i < R1 ? ty * R1 + i : 16 * R1 + ty * R2 + i - R1);
     const bool row_ok = m < p.M;
     if (FWD) {
       const int f = f0 + tx * 4;
@@ -233,7 +245,7 @@ __global__ void __launch_bounds__(256, 2) gated_simt_kernel(const __grid_constan
 
 // the ring, and the chunks' sums where there are several
 unsigned simt_smem(int rm, int64_t K) {
-  return (unsigned)((GSTAGES * GK * (16 * rm + 4 + GT + 4) + (K > GK * kChunk ? 8 * rm * 256 : 0)) * 4);
+  return (unsigned)((GSTAGES * GK * (simt_pitch(rm) + GT + 4) + (K > GK * kChunk ? 8 * rm * 256 : 0)) * 4);
 }
 template <bool FWD, int RM>
 const void* simt_kernel() {
@@ -246,7 +258,14 @@ const void* simt_kernel() {
 }
 template <bool FWD>
 const void* simt_pick(int rm) {
-  return rm == 8 ? simt_kernel<FWD, 8>() : rm == 4 ? simt_kernel<FWD, 4>() : simt_kernel<FWD, 2>();
+  switch (rm) {
+    case 8: return simt_kernel<FWD, 8>();
+    case 7: return simt_kernel<FWD, 7>();
+    case 6: return simt_kernel<FWD, 6>();
+    case 5: return simt_kernel<FWD, 5>();
+    case 4: return simt_kernel<FWD, 4>();
+    default: return simt_kernel<FWD, 2>();
+  }
 }
 
 }  // namespace
@@ -257,12 +276,18 @@ int gated_plan(const GatedOp& op, LaunchRec* rec, char* err, size_t errlen) {
   const GatedParams p{(const float*)op.A, op.lda, (const float*)op.B, op.ldb, op.bias, (float*)op.h, op.ldh,
                       op.s, op.lds, op.se, op.ldse, (float*)op.ds, op.ldds, (int)op.M, (int)op.F, (int)op.K, op.act};
   const int64_t cols = ceil_div(op.F, op.fwd ? GT / 2 : GT);
-  // the tallest tile that still gives half the SMs one (fp32, rm = 8, 4, 2:
-  // forward of 1000 x 1000 x 784 90, 107, 152 us from 128, 256, 512 tiles, of
-  // 300 x 2000 x 1000 115, 140, 158 from 96, 160, 320; backward of the first 97,
-  // 66, 87 us from 64, 128, 256; one row forward 82, 58, 48 us)
+  // the tile height of least cost: rounds of tiles over the SMs, times a tile's
+  // time, about rm + 4 (forward of one tile, K = 784, rm = 2, 4 .. 8: 48, 58, 62,
+  // 66, 78, 82 us).  Of the heights timed it is the fastest at every size tried:
+  // forward of 1000 x 1000 x 784, rm = 2, 4 .. 8: 164, 103, 119, 130, 84, 88 us, of
+  // 300 x 2000 x 1000: 167, 132, 86, 95, 107, 113; backward of 2500 x 900 x 600:
+  // 166, 123, 103, 115, 135, 139
   int rm = 8;
-  while (rm > 2 && cols * ceil_div(op.M, 16 * rm) < 76) rm /= 2;
+  int64_t best = INT64_MAX;
+  for (int r : {8, 7, 6, 5, 4, 2}) {
+    const int64_t cost = ceil_div(cols * ceil_div(op.M, 16 * r), device_sms()) * (r + 4);
+    if (cost < best) { best = cost; rm = r; }
+  }
   rec->func = op.fwd ? simt_pick<true>(rm) : simt_pick<false>(rm);
   rec->grid = dim3((unsigned)cols, (unsigned)ceil_div(op.M, 16 * rm));
   if (rec->grid.y > 65535) {
