@@ -39,14 +39,18 @@ struct GatedParams {
 // Tile of 16 RM rows by GT columns, GK deep, in a ring of GSTAGES slices that
 // cp.async fills an element at a time (any alignment; elements outside the
 // matrices as zeros) and transposes on the way.
-// Every kChunk slices (1024 k) the accumulators are added to sums in shared
+// Every kChunk slices (512 k) the accumulators are added to sums in shared
 // memory, which keeps the error of a long reduction near that of a short one
-// (K = 4000: 1.1e-6 of the result in one sequence of FMAs, 5.7e-7 so).  The
-// sums leave room for one block to an SM, shorter reductions run two: 10000 x
-// 784 x 500 410 us with sums (every 256 k), 359 without.
-constexpr int GT = 128, GK = 16, GSTAGES = 4, kChunk = 64;
+// (K = 4000: 1.1e-6 of the result in one sequence of FMAs, 4.0e-7 so).  Ring
+// and sums of two blocks fit an SM (10000 x 784 x 500, forward: 359 us, 410 with
+// one block); a fourth slice, which they would not leave room for, gains
+// nothing, and chunks of 256 cost 1 to 3%.
+constexpr int GT = 128, GK = 16, GSTAGES = 3, kChunk = 32;
 
-__host__ __device__ constexpr int simt_pitch(int rm) { return (rm > 4 ? 128 : 16 * rm) + 4; }
+// A row of a slice: a k's elements of A, then of B, then four of padding (so
+// that the transposing copies of neighbouring k meet in two lanes at most).
+__host__ __device__ constexpr int simt_rows(int rm) { return rm > 4 ? 128 : 16 * rm; }
+__host__ __device__ constexpr int simt_pitch(int rm) { return simt_rows(rm) + GT + 4; }
 
 __device__ __forceinline__ void copy4(uint32_t dst, const float* src, bool in) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
@@ -58,9 +62,8 @@ template <bool FWD, int RM>
 __global__ void __launch_bounds__(256, 2) gated_simt_kernel(const __grid_constant__ GatedParams p) {
   pdl_enter();
   constexpr int BM = 16 * RM, R1 = RM < 4 ? RM : 4, R2 = RM - R1;
-  constexpr int PA = simt_pitch(RM), PB = GT + 4;         // pitches of the two slices
-  constexpr int SLICE = GK * (PA + PB);
-  extern __shared__ __align__(16) float gated_smem[];     // [GSTAGES]([GK][PA], [GK][PB]), [8 RM][256]
+  constexpr int P = simt_pitch(RM), SLICE = GK * P;
+  extern __shared__ __align__(16) float gated_smem[];     // [GSTAGES][GK][P], [8 RM][256]
   constexpr int TF = FWD ? GT / 2 : GT;   // F columns per tile
   const int tid = threadIdx.x;
   // a warp takes 4 x 8 threads' results: as many elements of A as of B to read
@@ -72,13 +75,13 @@ __global__ void __launch_bounds__(256, 2) gated_simt_kernel(const __grid_constan
   const uint32_t base = (uint32_t)__cvta_generic_to_shared(gated_smem);
   auto load = [&](int slice) {
     const int k0 = slice * GK;
-    const uint32_t as = base + (uint32_t)((slice % GSTAGES) * SLICE) * 4u, bs = as + GK * PA * 4u;
+    const uint32_t as = base + (uint32_t)((slice % GSTAGES) * SLICE) * 4u, bs = as + simt_rows(RM) * 4u;
 #pragma unroll
     for (int i = 0; i < RM; ++i) {
       const int idx = tid + i * 256, m = idx / GK, kk = idx % GK, k = k0 + kk;
       const bool in = m0 + m < p.M && k < p.K;
       const int at = R2 == 0 || m < 16 * R1 ? m : 64 + (m - 64) / (R2 ? R2 : 1) * 4 + (m - 64) % (R2 ? R2 : 1);
-      copy4(as + (uint32_t)(kk * PA + at) * 4u, in ? A + (int64_t)(m0 + m) * p.lda + k : A, in);
+      copy4(as + (uint32_t)(kk * P + at) * 4u, in ? A + (int64_t)(m0 + m) * p.lda + k : A, in);
     }
 #pragma unroll
     for (int i = 0; i < GT * GK / 256; ++i) {
@@ -86,11 +89,11 @@ __global__ void __launch_bounds__(256, 2) gated_simt_kernel(const __grid_constan
       if (FWD) {   // tile column n: gate row f0 + n, or up row F + f0 + n - 64
         const int n = idx / GK, kk = idx % GK, k = k0 + kk, f = f0 + (n & (TF - 1));
         const bool in = f < p.F && k < p.K;
-        copy4(bs + (uint32_t)(kk * PB + n) * 4u, in ? B + ((int64_t)f + (n < TF ? 0 : p.F)) * p.ldb + k : B, in);
+        copy4(bs + (uint32_t)(kk * P + n) * 4u, in ? B + ((int64_t)f + (n < TF ? 0 : p.F)) * p.ldb + k : B, in);
       } else {
         const int n = idx % GT, kk = idx / GT, k = k0 + kk;
         const bool in = f0 + n < p.F && k < p.K;
-        copy4(bs + (uint32_t)(kk * PB + n) * 4u, in ? B + (int64_t)k * p.ldb + f0 + n : B, in);
+        copy4(bs + (uint32_t)(kk * P + n) * 4u, in ? B + (int64_t)k * p.ldb + f0 + n : B, in);
       }
     }
   };
@@ -113,19 +116,19 @@ __global__ void __launch_bounds__(256, 2) gated_simt_kernel(const __grid_constan
     if (t + GSTAGES - 1 < nt) load(t + GSTAGES - 1);
     asm volatile("cp.async.commit_group;" ::: "memory");
     const float* As = gated_smem + (t % GSTAGES) * SLICE;
-    const float* Bs = As + GK * PA;
+    const float* Bs = As + simt_rows(RM);
 #pragma unroll
     for (int kk = 0; kk < GK; ++kk) {
       float a[8];
       if constexpr (RM == 2) {
-        *reinterpret_cast<float2*>(a) = *reinterpret_cast<const float2*>(As + kk * PA + ty * 2);
+        *reinterpret_cast<float2*>(a) = *reinterpret_cast<const float2*>(As + kk * P + ty * 2);
       } else {
-        *reinterpret_cast<float4*>(a) = *reinterpret_cast<const float4*>(As + kk * PA + ty * 4);
-        if constexpr (R2 > 0) *reinterpret_cast<float4*>(a + 4) = *reinterpret_cast<const float4*>(As + kk * PA + 64 + ty * 4);
+        *reinterpret_cast<float4*>(a) = *reinterpret_cast<const float4*>(As + kk * P + ty * 4);
+        if constexpr (R2 > 0) *reinterpret_cast<float4*>(a + 4) = *reinterpret_cast<const float4*>(As + kk * P + 64 + ty * 4);
       }
       ulonglong2 b[2];
-      b[0] = *reinterpret_cast<const ulonglong2*>(Bs + kk * PB + tx * 4);
-      b[1] = *reinterpret_cast<const ulonglong2*>(Bs + kk * PB + 64 + tx * 4);
+      b[0] = *reinterpret_cast<const ulonglong2*>(Bs + kk * P + tx * 4);
+      b[1] = *reinterpret_cast<const ulonglong2*>(Bs + kk * P + 64 + tx * 4);
 #pragma unroll
       for (int i = 0; i < RM; ++i) {
         const F2 aa = pack2(a[i], a[i]);
@@ -245,7 +248,7 @@ __global__ void __launch_bounds__(256, 2) gated_simt_kernel(const __grid_constan
 
 // the ring, and the chunks' sums where there are several
 unsigned simt_smem(int rm, int64_t K) {
-  return (unsigned)((GSTAGES * GK * (simt_pitch(rm) + GT + 4) + (K > GK * kChunk ? 8 * rm * 256 : 0)) * 4);
+  return (unsigned)((GSTAGES * GK * simt_pitch(rm) + (K > GK * kChunk ? 8 * rm * 256 : 0)) * 4);
 }
 template <bool FWD, int RM>
 const void* simt_kernel() {
