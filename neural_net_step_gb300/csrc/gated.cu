@@ -8,7 +8,9 @@
 // bf16 runs on the tensor cores (gated_tc.cu; a few rows: gated_small.cu).  fp32
 // on the FFMA pipes: tiles of 16 RM rows by 128 columns, RM x 8 results per
 // thread.  The forward's tile is 64 gate and the 64 up columns that belong to
-// them, so a thread holds both factors of its results.
+// them, so a thread holds both factors of its results.  Where there are few
+// tiles, the blocks of a cluster share a tile's reduction and add their sums
+// through one another's shared memory.
 #include <stdio.h>
 
 #include <mutex>
@@ -55,10 +57,15 @@ __host__ __device__ constexpr int simt_pitch(int rm) { return simt_rows(rm) + GT
 __device__ __forceinline__ void copy4(uint32_t dst, const float* src, bool in) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
 }
+__device__ __forceinline__ float ld_cluster(uint32_t a) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
 // RM (2, 4 .. 8) rows and 8 columns per thread: rows ty R1 .. of the tile's first
 // 16 R1, and ty R2 .. of the 16 R2 after them.  In a slice the second rows of
 // a thread stand four apart, so that it reads them at once whatever R2 is.
-template <bool FWD, int RM>
+template <bool FWD, int RM, bool SPLIT>
 __global__ void __launch_bounds__(256, 2) gated_simt_kernel(const __grid_constant__ GatedParams p) {
   pdl_enter();
   constexpr int BM = 16 * RM, R1 = RM < 4 ? RM : 4, R2 = RM - R1;
@@ -73,9 +80,12 @@ __global__ void __launch_bounds__(256, 2) gated_simt_kernel(const __grid_constan
   const float* A = p.A;
   const float* B = p.B;
   const uint32_t base = (uint32_t)__cvta_generic_to_shared(gated_smem);
-  auto load = [&](int slice) {
-    const int k0 = slice * GK;
-    const uint32_t as = base + (uint32_t)((slice % GSTAGES) * SLICE) * 4u, bs = as + simt_rows(RM) * 4u;
+  // this block's slices of the reduction
+  const int all = (p.K + GK - 1) / GK, parts = SPLIT ? (int)gridDim.z : 1, per = SPLIT ? (all + parts - 1) / parts : all;
+  const int first = SPLIT ? (int)blockIdx.z * per : 0, nt = SPLIT ? max(0, min(all - first, per)) : all;
+  auto load = [&](int t) {
+    const int k0 = (first + t) * GK;
+    const uint32_t as = base + (uint32_t)((t % GSTAGES) * SLICE) * 4u, bs = as + simt_rows(RM) * 4u;
 #pragma unroll
     for (int i = 0; i < RM; ++i) {
       const int idx = tid + i * 256, m = idx / GK, kk = idx % GK, k = k0 + kk;
@@ -104,7 +114,6 @@ __global__ void __launch_bounds__(256, 2) gated_simt_kernel(const __grid_constan
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc2[i][j] = pack2(0.f, 0.f);
   float* sums = gated_smem + GSTAGES * SLICE + tid;
-  const int nt = (p.K + GK - 1) / GK;
 #pragma unroll
   for (int s = 0; s < GSTAGES - 1; ++s) {
     if (s < nt) load(s);
@@ -159,6 +168,14 @@ __global__ void __launch_bounds__(256, 2) gated_simt_kernel(const __grid_constan
       const float* sum = sums + (i * 8 + 2 * j) * 256;
       unpack2(nt > kChunk ? add2(acc2[i][j], pack2(sum[0], sum[256])) : acc2[i][j], acc[i][2 * j], acc[i][2 * j + 1]);
     }
+  if constexpr (SPLIT) {
+    // the other blocks of the cluster read them from here
+#pragma unroll
+    for (int i = 0; i < RM; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sums[(i * 8 + j) * 256] = acc[i][j];
+    tc::cluster_sync_all();
+  }
   // thread (ty, tx): its rows; tile columns tx*4 + 0..3 and 64 + tx*4 + 0..3 (the forward's second four are the up
   // columns of its first four)
   float* h = p.h;
@@ -167,6 +184,16 @@ __global__ void __launch_bounds__(256, 2) gated_simt_kernel(const __grid_constan
   for (int i = 0; i < RM; ++i) {
     const int m = m0 + (i < R1 ? ty * R1 + i : 16 * R1 + ty * R2 + i - R1);
     const bool row_ok = m < p.M;
+    if constexpr (SPLIT) {   // a thread's rows go round the blocks, the parts' sums are added in their order
+      if (i % parts != (int)blockIdx.z) continue;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
+      for (int r = 0; r < parts; ++r) {
+        const uint32_t from = tc::mapa_cluster((uint32_t)__cvta_generic_to_shared(sums + i * 8 * 256), (uint32_t)r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[i][j] += ld_cluster(from + (uint32_t)j * 1024u);
+      }
+    }
     if (FWD) {
       const int f = f0 + tx * 4;
       float g[4], u[4];
@@ -244,31 +271,60 @@ __global__ void __launch_bounds__(256, 2) gated_simt_kernel(const __grid_constan
       }
     }
   }
+  if constexpr (SPLIT) tc::cluster_sync_all();   // no block leaves while another reads its sums
 }
 
-// the ring, and the chunks' sums where there are several
-unsigned simt_smem(int rm, int64_t K) {
-  return (unsigned)((GSTAGES * GK * simt_pitch(rm) + (K > GK * kChunk ? 8 * rm * 256 : 0)) * 4);
-}
-template <bool FWD, int RM>
+// the ring, and the sums of several chunks or parts
+unsigned simt_smem(int rm, bool sums) { return (unsigned)((GSTAGES * GK * simt_pitch(rm) + (sums ? 8 * rm * 256 : 0)) * 4); }
+template <bool FWD, int RM, bool SPLIT>
 const void* simt_kernel() {
   static std::once_flag once;
   std::call_once(once, [] {
-    cudaFuncSetAttribute((const void*)gated_simt_kernel<FWD, RM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                         (int)simt_smem(RM, INT32_MAX));
+    cudaFuncSetAttribute((const void*)gated_simt_kernel<FWD, RM, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                         (int)simt_smem(RM, true));
   });
-  return (const void*)gated_simt_kernel<FWD, RM>;
+  return (const void*)gated_simt_kernel<FWD, RM, SPLIT>;
 }
-template <bool FWD>
+template <bool FWD, bool SPLIT>
 const void* simt_pick(int rm) {
   switch (rm) {
-    case 8: return simt_kernel<FWD, 8>();
-    case 7: return simt_kernel<FWD, 7>();
-    case 6: return simt_kernel<FWD, 6>();
-    case 5: return simt_kernel<FWD, 5>();
-    case 4: return simt_kernel<FWD, 4>();
-    default: return simt_kernel<FWD, 2>();
+    case 8: return simt_kernel<FWD, 8, SPLIT>();
+    case 7: return simt_kernel<FWD, 7, SPLIT>();
+    case 6: return simt_kernel<FWD, 6, SPLIT>();
+    case 5: return simt_kernel<FWD, 5, SPLIT>();
+    case 4: return simt_kernel<FWD, 4, SPLIT>();
+    default: return simt_kernel<FWD, 2, SPLIT>();
   }
+}
+
+// Rows per thread and parts of the reduction (a block each, in clusters along
+// z) of least estimated time.  A slice of a tile takes about rm + 4 (forward of
+// one tile, K = 784, rm = 2, 4 .. 8: 48, 58, 62, 66, 78, 82 us), two blocks beside
+// one another on an SM 1.8 times as long, joining the parts about a slice;
+// clusters of 4 and 8 blocks find room on 136 and 120 SMs; several parts have to
+// promise 5%.  Of all heights and parts timed it takes the fastest or one within
+// 2% at 28 of 30 sizes, and one within 13% at two.  The tallest tile (few rows: the
+// lowest) in one part, and as chosen, in us:
+//   forward 1 x 553 x 1379    89 (rm = 2) -> 18     backward 401 x 1592 x 1125  91 -> 58
+//   forward 16 x 256 x 4000  240 (rm = 2) -> 37     backward 2500 x 900 x 600  139 -> 91
+//   forward 300 x 2000 x 1000 113 -> 85             backward 1000 x 1000 x 784  97 -> 56
+//   forward 2500 x 900 x 600  134, kept             forward 1000 x 1000 x 784   88 -> 85 (one part)
+struct Simt { int rm, parts; };
+Simt simt_choice(int64_t cols, int64_t M, int64_t K) {
+  constexpr int64_t room[4] = {152, 152, 136, 120};
+  const int64_t slices = ceil_div(K, GK);
+  Simt best{8, 1};
+  int64_t least = INT64_MAX;
+  for (int i = 0; i < 4; ++i) {
+    const int64_t per = ceil_div(slices, (int64_t)1 << i) + (i > 0);
+    for (int r : {8, 7, 6, 5, 4, 2}) {
+      const int64_t q = ceil_div((cols * ceil_div(M, 16 * r)) << i, room[i]);
+      const int64_t cost = (q / 2 * 9 + q % 2 * 5) * (r + 4) * per * (i > 0 ? 20 : 19);
+      if (cost < least) { least = cost; best = Simt{r, 1 << i}; }
+    }
+    if (cols * ceil_div(M, 128) > 8 * room[0]) break;   // (many tiles: in one part)
+  }
+  return best;
 }
 
 }  // namespace
@@ -279,26 +335,18 @@ int gated_plan(const GatedOp& op, LaunchRec* rec, char* err, size_t errlen) {
   const GatedParams p{(const float*)op.A, op.lda, (const float*)op.B, op.ldb, op.bias, (float*)op.h, op.ldh,
                       op.s, op.lds, op.se, op.ldse, (float*)op.ds, op.ldds, (int)op.M, (int)op.F, (int)op.K, op.act};
   const int64_t cols = ceil_div(op.F, op.fwd ? GT / 2 : GT);
-  // the tile height of least cost: rounds of tiles over the SMs, times a tile's
-  // time, about rm + 4 (forward of one tile, K = 784, rm = 2, 4 .. 8: 48, 58, 62,
-  // 66, 78, 82 us).  Of the heights timed it is the fastest at every size tried:
-  // forward of 1000 x 1000 x 784, rm = 2, 4 .. 8: 164, 103, 119, 130, 84, 88 us, of
-  // 300 x 2000 x 1000: 167, 132, 86, 95, 107, 113; backward of 2500 x 900 x 600:
-  // 166, 123, 103, 115, 135, 139
-  int rm = 8;
-  int64_t best = INT64_MAX;
-  for (int r : {8, 7, 6, 5, 4, 2}) {
-    const int64_t cost = ceil_div(cols * ceil_div(op.M, 16 * r), device_sms()) * (r + 4);
-    if (cost < best) { best = cost; rm = r; }
-  }
-  rec->func = op.fwd ? simt_pick<true>(rm) : simt_pick<false>(rm);
-  rec->grid = dim3((unsigned)cols, (unsigned)ceil_div(op.M, 16 * rm));
+  const Simt t = simt_choice(cols, op.M, op.K);
+  const int rm = t.rm, parts = t.parts;
+  rec->func = parts > 1 ? (op.fwd ? simt_pick<true, true>(rm) : simt_pick<false, true>(rm))
+                        : (op.fwd ? simt_pick<true, false>(rm) : simt_pick<false, false>(rm));
+  rec->grid = dim3((unsigned)cols, (unsigned)ceil_div(op.M, 16 * rm), (unsigned)parts);
+  rec->cluster = (unsigned)parts;
   if (rec->grid.y > 65535) {
     snprintf(err, errlen, "gated: %lld rows are too many", (long long)op.M);
     return -1;
   }
   rec->block = dim3(256);
-  rec->smem = simt_smem(rm, op.K);
+  rec->smem = simt_smem(rm, parts > 1 || op.K > GK * kChunk);
   rec->name = op.fwd ? "gated_fwd" : "gated_dgrad";
   rec->set_args(p);
   return 1;

@@ -15,6 +15,7 @@ struct LaunchRec {
   dim3 grid{1, 1, 1};
   dim3 block{1, 1, 1};
   unsigned smem = 0;
+  unsigned cluster = 1;   // blocks of a cluster (along z), for kernels that take it at launch; eager launches only
   unsigned args_size = 0;
   const char* name = "";
   // Graph dependencies: indices of earlier records in the same plan that this
@@ -79,7 +80,22 @@ struct LaunchRec {
 
 inline cudaError_t launch_rec(const LaunchRec& r, cudaStream_t s) {
   void* argp[1] = {const_cast<unsigned char*>(r.args)};
-  return cudaLaunchKernel(r.func, r.grid, r.block, argp, r.smem, s);
+  if (r.cluster == 1) return cudaLaunchKernel(r.func, r.grid, r.block, argp, r.smem, s);
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = r.grid;
+  cfg.blockDim = r.block;
+  cfg.dynamicSmemBytes = r.smem;
+  cfg.stream = s;
+  cudaLaunchAttribute a;
+  memset(&a, 0, sizeof(a));
+  a.id = cudaLaunchAttributeClusterDimension;
+  a.val.clusterDim.x = 1;
+  a.val.clusterDim.y = 1;
+  a.val.clusterDim.z = r.cluster;
+  cfg.attrs = &a;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelExC(&cfg, r.func, argp);
 }
 
 inline cudaKernelNodeParams node_params(const LaunchRec& r, void** argp) {

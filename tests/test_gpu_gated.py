@@ -68,9 +68,10 @@ BWD = [(nn.BF16, *s, ACTS[(i + 2) % 4], i % 2 == 0, SAVES[1 + i % 2]) for i, s i
 BWD += [(nn.F32, *s, ACTS[i % 4], i % 2 == 1, SAVES[1 + i % 2]) for i, s in enumerate(F32_SHAPES)]
 BWD += [(nn.BF16, m, 264, 136, 0, a, True, sv) for m in (5, 40, 300) for a in ACTS for sv in SAVES[1:]]
 BWD += [(nn.F32, 40, 100, 70, 0, a, True, sv) for a in ACTS for sv in SAVES[1:]]
-# fp32 tiles of every height (chosen by the number of tiles), reductions in one piece and in several
+# fp32 tiles of every height (chosen by the number of tiles), reductions in one part and in several, in one chunk and in several
 F32_HEIGHTS = [(5, 100, 2050), (300, 2000, 24), (383, 2047, 1030), (383, 4095, 20), (1000, 1000, 1040), (2500, 900, 24),
-               (2500, 900, 1040), (4096, 1024, 16), (10000, 784, 20)]
+               (2500, 900, 1040), (4096, 1024, 16), (10000, 784, 20), (64, 512, 512), (200, 200, 200), (16, 256, 4000),
+               (401, 1592, 1125), (1, 553, 1379)]
 FWD += [(nn.F32, *s, 0, ACTS[i % 4], i % 2 == 0, SAVES[(i + 2) % 3]) for i, s in enumerate(F32_HEIGHTS)]
 BWD += [(nn.F32, *s, 0, ACTS[(i + 1) % 4], i % 2 == 0, SAVES[1 + i % 2]) for i, s in enumerate(F32_HEIGHTS)]
 
