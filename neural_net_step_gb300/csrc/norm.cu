@@ -182,6 +182,7 @@ struct RowFetch {
   // The first rows' fetches.  Units that are not there are zeros in every
   // stage: the sums run over them without a branch (bf16 16384 x 1000,
   // forward: 16.7 us with branches, 15.5 without).
+  template <int AHEAD>   // rows that are fetched before their turn
   __device__ __forceinline__ void start(int64_t row) {
     if constexpr (RING) {
       if constexpr (!FULL)
@@ -190,13 +191,12 @@ struct RowFetch {
           if (!in(i))
             for (int s = 0; s < STAGES * NT; ++s) clear(ring + (uint32_t)(s * NV + i) * pitch);
 #pragma unroll
-      for (int s = 0; s < STAGES - 1; ++s) issue(row + s * step, s);
+      for (int s = 0; s < AHEAD; ++s) issue(row + s * step, s);
     }
   }
-  // Row `row`'s elements into raw (stage by stage), the next fetch under way.
-  __device__ __forceinline__ void take(int64_t row, int& stage) {
+  // A stage's elements into raw.
+  __device__ __forceinline__ void read(int stage) {
     if constexpr (RING) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
 #pragma unroll
       for (int k = 0; k < NT; ++k)
 #pragma unroll
@@ -210,7 +210,17 @@ struct RowFetch {
           else
             asm volatile("ld.shared.u32 %0, [%1];" : "=r"(raw[k][i][0]) : "r"(at) : "memory");
         }
-      issue(row + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);   // the row before's, read by now
+    }
+  }
+  // Row `row`'s elements into raw (stage by stage), the next fetch under way.
+  template <int AHEAD>
+  __device__ __forceinline__ void take(int64_t row, int& stage) {
+    if constexpr (RING) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD - 1) : "memory");
+      read(stage);
+      // into a stage whose row has been read for the last time: the row before's
+      // (AHEAD = STAGES - 1), or that of the one before it
+      issue(row + AHEAD * step, stage + AHEAD >= STAGES ? stage + AHEAD - STAGES : stage + AHEAD);
       stage = stage + 1 == STAGES ? 0 : stage + 1;
     } else {
 #pragma unroll
@@ -301,19 +311,27 @@ __device__ __forceinline__ void put_row(const F& f, T* row, Get get) {
 // of it.  w: the block's [32 * NS] floats of one of two buffers used in turn
 // (a group's next use of the same buffer lies two barriers later).
 template <int NS>
-__device__ __forceinline__ void group_sums(float (&v)[NS], float* w, int group, int wpr) {
+__device__ __forceinline__ void post_sums(float (&v)[NS], float* w, int wpr) {
 #pragma unroll
   for (int k = 0; k < NS; ++k) v[k] = warp_sum(v[k]);
-  if (wpr == 1) return;
-  if ((threadIdx.x & 31) == 0)
+  if (wpr > 1 && (threadIdx.x & 31) == 0)
 #pragma unroll
     for (int k = 0; k < NS; ++k) w[NS * (threadIdx.x >> 5) + k] = v[k];
-  asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(wpr * 32) : "memory");
+}
+template <int NS>
+__device__ __forceinline__ void read_sums(float (&v)[NS], const float* w, int group, int wpr) {   // (one warp: v as posted)
+  if (wpr == 1) return;
 #pragma unroll
   for (int k = 0; k < NS; ++k) v[k] = 0.f;
   for (int i = 0; i < wpr; ++i)
 #pragma unroll
     for (int k = 0; k < NS; ++k) v[k] += w[NS * (group * wpr + i) + k];
+}
+template <int NS>
+__device__ __forceinline__ void group_sums(float (&v)[NS], float* w, int group, int wpr) {
+  post_sums<NS>(v, w, wpr);
+  if (wpr > 1) asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(wpr * 32) : "memory");
+  read_sums<NS>(v, w, group, wpr);
 }
 
 constexpr int kSumBytes = 2 * 32 * 2 * 4;   // group_sums' two buffers
@@ -334,7 +352,7 @@ __global__ void __launch_bounds__(RowCfg<true>::THREADS, 1) ln_fwd_kernel(const 
   f.M = p.M; f.step = (int64_t)gridDim.x * groups;
   f.setup(t, tpr, p.D, (uint32_t)__cvta_generic_to_shared(shift + tpr * EPT));
   int64_t row = blockIdx.x * (int64_t)groups + group;
-  f.start(row);
+  f.template start<F::STAGES - 1>(row);
   for (int c = threadIdx.x; c < p.D; c += blockDim.x) {
     scale[F::place(c, tpr)] = p.gamma ? p.gamma[c] : 1.f;
     shift[F::place(c, tpr)] = p.beta ? p.beta[c] : 0.f;
@@ -346,7 +364,7 @@ __global__ void __launch_bounds__(RowCfg<true>::THREADS, 1) ln_fwd_kernel(const 
   const int my = t * (VEC < 4 ? VEC : 4);   // this thread's first place in them
   int stage = 0;
   for (; row < p.M; row += f.step) {
-    f.take(row, stage);
+    f.template take<F::STAGES - 1>(row, stage);
     F2 v[NP], a = pack2(0.f, 0.f), b = a;
 #pragma unroll
     for (int q = 0; q < NP; ++q) {
@@ -434,6 +452,8 @@ __global__ void __launch_bounds__(RowCfg<false>::THREADS, 1) ln_bwd_kernel(const
   pdl_enter();
   using F = RowFetch<T, VEC, EPT, 2, FULL>;
   constexpr int NP = EPT / 2;
+  constexpr bool DEFER = VEC == 8 && EPT == 16 && !FULL;
+  constexpr int AHEAD = DEFER ? F::STAGES - 2 : F::STAGES - 1;
   extern __shared__ __align__(16) float ln_smem[];
   const int tpr = p.tpr, groups = (int)blockDim.x / tpr, wpr = tpr >> 5;
   float* scale = ln_smem + kSumBytes / 4;                 // [tpr EPT]
@@ -446,7 +466,7 @@ __global__ void __launch_bounds__(RowCfg<false>::THREADS, 1) ln_bwd_kernel(const
   f.M = p.M; f.step = (int64_t)gridDim.x * groups;
   f.setup(t, tpr, p.D, (uint32_t)__cvta_generic_to_shared(colsum));
   int64_t row = blockIdx.x * (int64_t)groups + group;
-  f.start(row);
+  f.template start<AHEAD>(row);
   for (int c = threadIdx.x; c < p.D; c += blockDim.x) scale[F::place(c, tpr)] = p.gamma ? p.gamma[c] : 1.f;
   if constexpr (!FULL)
     for (int c = p.D + threadIdx.x; c < tpr * EPT; c += blockDim.x) scale[F::place(c, tpr)] = 0.f;
@@ -459,11 +479,8 @@ __global__ void __launch_bounds__(RowCfg<false>::THREADS, 1) ln_bwd_kernel(const
   if (row < p.M) { mean = p.mean[row]; rstd = p.rstd[row]; }
   __syncthreads();
   const float* sc = scale + t * (VEC < 4 ? VEC : 4);
-  int stage = 0, buf = 0;
-  for (; row < p.M; row += f.step) {
-    float next_mean = 0.f, next_rstd = 0.f;
-    if (row + f.step < p.M) { next_mean = p.mean[row + f.step]; next_rstd = p.rstd[row + f.step]; }
-    f.take(row, stage);
+  // a row's two sums (this warp's share of them), the columns' sums on the way
+  auto row_sums = [&](float (&s)[2]) {
     const F2 times = pack2(rstd, rstd);
     F2 a = zero, b = zero;
 #pragma unroll
@@ -479,20 +496,69 @@ __global__ void __launch_bounds__(RowCfg<false>::THREADS, 1) ln_bwd_kernel(const
         b = fma2(w, xh, b);
       }
     }
-    float s[2] = {sum2(a), sum2(b)};
-    group_sums<2>(s, ln_smem + 64 * buf, group, wpr);
-    buf ^= 1;
+    s[0] = sum2(a);
+    s[1] = sum2(b);
+  };
+  auto put = [&](int64_t to, float mean, float rstd, const float (&s)[2]) {
     // rstd (w - c1 - xh c2) = w rstd - c1 rstd - (x - mean) rstd^2 c2
     const float c1 = -s[0] * inv_d * rstd, c2 = -s[1] * inv_d * rstd * rstd;
-    const F2 minus = pack2(-mean, -mean), p1 = pack2(c1, c1), p2 = pack2(c2, c2);
-    put_row<T, VEC, EPT>(f, reinterpret_cast<T*>(p.dx) + row * p.lddx + t * VEC, [&](int q, F2& o0, F2& o1) {
+    const F2 times = pack2(rstd, rstd), minus = pack2(-mean, -mean), p1 = pack2(c1, c1), p2 = pack2(c2, c2);
+    put_row<T, VEC, EPT>(f, reinterpret_cast<T*>(p.dx) + to * p.lddx + t * VEC, [&](int q, F2& o0, F2& o1) {
       F2 g0, g1;
       f.vec4(sc, q, g0, g1);
       o0 = fma2(add2(f.get(0, q), minus), p2, fma2(mul2(f.get(1, q), g0), times, p1));
       o1 = fma2(add2(f.get(0, q + 1), minus), p2, fma2(mul2(f.get(1, q + 1), g1), times, p1));
     });
-    mean = next_mean;
-    rstd = next_rstd;
+  };
+  int stage = 0, buf = 0;
+  if constexpr (DEFER) {
+    // a row's results a turn after its sums, so that no warp waits for the
+    // others' with nothing to do; the row is read a second time from its stage,
+    // which makes room for the column tests' registers (bf16 11503 x 5520: 146 us
+    // at once, 106 so; 16384 x 1000: 31 and 27; full rows 16384 x 4096: 79 and 83,
+    // rows in 4-byte units 21746 x 3086: 116 and 129)
+    int64_t last = -1;
+    float last_mean = 0.f, last_rstd = 0.f, s[2], last_s[2] = {0.f, 0.f};
+    int last_stage = 0;
+    for (; row < p.M; row += f.step) {
+      float next_mean = 0.f, next_rstd = 0.f;
+      if (row + f.step < p.M) { next_mean = p.mean[row + f.step]; next_rstd = p.rstd[row + f.step]; }
+      const int at = stage;
+      f.template take<AHEAD>(row, stage);
+      row_sums(s);
+      post_sums<2>(s, ln_smem + 64 * buf, wpr);
+      if (last >= 0) {
+        f.read(last_stage);
+        read_sums<2>(last_s, ln_smem + 64 * (buf ^ 1), group, wpr);
+        put(last, last_mean, last_rstd, last_s);
+      }
+      if (wpr > 1) asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(wpr * 32) : "memory");
+      last = row;
+      last_mean = mean; last_rstd = rstd;
+      last_s[0] = s[0]; last_s[1] = s[1];
+      last_stage = at;
+      buf ^= 1;
+      mean = next_mean;
+      rstd = next_rstd;
+    }
+    if (last >= 0) {
+      f.read(last_stage);
+      read_sums<2>(last_s, ln_smem + 64 * (buf ^ 1), group, wpr);
+      put(last, last_mean, last_rstd, last_s);
+    }
+  } else {
+    for (; row < p.M; row += f.step) {
+      float next_mean = 0.f, next_rstd = 0.f;
+      if (row + f.step < p.M) { next_mean = p.mean[row + f.step]; next_rstd = p.rstd[row + f.step]; }
+      f.template take<AHEAD>(row, stage);
+      float s[2];
+      row_sums(s);
+      group_sums<2>(s, ln_smem + 64 * buf, group, wpr);
+      buf ^= 1;
+      put(row, mean, rstd, s);
+      mean = next_mean;
+      rstd = next_rstd;
+    }
   }
   if (!p.part) return;
   // every group's column sums, added in the groups' order
