@@ -26,7 +26,8 @@ SHAPES = [(dt, M, D, pad, off) for dt in (nn.F32, nn.BF16) for M, D, pad, off in
     # rows that start between 16-byte units, at whole words for bf16 too
     (21, 30, 2, 2), (21, 256, 2, 0), (41, 258, 0, 2), (41, 770, 2, 2), (1500, 2050, 0, 0), (7, 8190, 2, 2), (6, 8192, 0, 2),
     # several rows to a group of threads, the groups of one block at different counts
-    (5003, 784, 0, 0), (1000, 5520, 0, 8), (2600, 1000, 24, 0), (3001, 1001, 0, 0), (3001, 2048, 0, 0), (20001, 96, 0, 0)]]
+    (5003, 784, 0, 0), (1000, 5520, 0, 8), (2600, 1000, 24, 0), (3001, 1001, 0, 0), (3001, 2048, 0, 0), (20001, 96, 0, 0), (6001, 400, 0, 0),
+    (7001, 280, 8, 8)]]
 
 
 def _fwd_tol(x, gamma, y, mean, rstd, D, dtype):
