@@ -96,10 +96,13 @@ __device__ __forceinline__ void row_sums(float (&v)[NS], float (&sh)[NS][WARPS])
   }
 }
 // What the sums of differences from a row's first mean say: the rest of the
-// mean and 1 / sqrt(variance + eps).
+// mean and 1 / sqrt(variance + eps).  The variance is kept from falling below
+// zero by a comparison that NaN fails (fmaxf would turn it into 0): a row that
+// holds NaN or an infinity has rstd NaN.
 __device__ __forceinline__ void finish_stats(const float (&s)[2], float inv_d, float eps, float& rest, float& rstd) {
   rest = s[0] * inv_d;
-  rstd = rsqrtf(fmaxf(fmaf(-rest, rest, s[1] * inv_d), 0.f) + eps);   // (2 ulp)
+  const float var = fmaf(-rest, rest, s[1] * inv_d);
+  rstd = rsqrtf((var < 0.f ? 0.f : var) + eps);   // (2 ulp)
 }
 
 // How rows of at most kMaxRow elements are walked, forward and backward: tpr
