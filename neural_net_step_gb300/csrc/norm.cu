@@ -503,14 +503,15 @@ __global__ void __launch_bounds__(RowCfg<false>::THREADS, 1) ln_bwd_kernel(const
     s[1] = sum2(b);
   };
   auto put = [&](int64_t to, float mean, float rstd, const float (&s)[2]) {
-    // rstd (w - c1 - xh c2) = w rstd - c1 rstd - (x - mean) rstd^2 c2
-    const float c1 = -s[0] * inv_d * rstd, c2 = -s[1] * inv_d * rstd * rstd;
+    // rstd (w - c1 - xh c2), the last factor over all of it: rstd^2 would leave
+    // fp32 where rstd does not (rows below 5e-20)
+    const float c1 = -s[0] * inv_d, c2 = -s[1] * inv_d * rstd;
     const F2 times = pack2(rstd, rstd), minus = pack2(-mean, -mean), p1 = pack2(c1, c1), p2 = pack2(c2, c2);
     put_row<T, VEC, EPT>(f, reinterpret_cast<T*>(p.dx) + to * p.lddx + t * VEC, [&](int q, F2& o0, F2& o1) {
       F2 g0, g1;
       f.vec4(sc, q, g0, g1);
-      o0 = fma2(add2(f.get(0, q), minus), p2, fma2(mul2(f.get(1, q), g0), times, p1));
-      o1 = fma2(add2(f.get(0, q + 1), minus), p2, fma2(mul2(f.get(1, q + 1), g1), times, p1));
+      o0 = mul2(fma2(add2(f.get(0, q), minus), p2, fma2(f.get(1, q), g0, p1)), times);
+      o1 = mul2(fma2(add2(f.get(0, q + 1), minus), p2, fma2(f.get(1, q + 1), g1, p1)), times);
     });
   };
   int stage = 0, buf = 0;
