@@ -1753,7 +1753,7 @@ static size_t wgrad8_values_bytes(int dtype, int64_t K, int64_t B) {
 size_t mlp_op_wgrad8_workspace_bytes(int dtype, int64_t N, int64_t K, int64_t B) {
   if (!dtype_ok(dtype) || N < 1 || K < 1 || B < 1 || N > INT32_MAX || K > INT32_MAX || B > INT32_MAX) return 0;
   if ((double)B * (double)K > 1e15 || (double)N * (double)K > 1e15) return 0;   // (more than any device holds)
-  return wgrad8_values_bytes(dtype, K, B) + wgrad_workspace_bytes(dtype, N, K, B, wgrad_splits(dtype, N, K, B));
+  return wgrad8_values_bytes(dtype, K, B) + wgrad_workspace_bytes(dtype, N, K, B, wgrad_splits(dtype, N, K, B, true));
 }
 
 mlp_status mlp_op_wgrad8(int dtype, int64_t N, int64_t K, int64_t B, const void* dY, int64_t ldy, const uint8_t* Q,

@@ -69,9 +69,9 @@ struct GemmOp {
   // -1 where there is at least one full wave of pair tiles, 0 never, 1
   // wherever the form allows (N and M of at least 256, no softmax-CE)
   int cg2 = -1;
-  // weight gradient on CTA pairs: the reduction in chunks whose sums are added
-  // in fp32 registers (the tensor cores' accumulation loses more over a long
-  // one); elsewhere it has no effect
+  // bf16 weight gradient: no chain of MMAs over more than 2048 rows (the tensor
+  // cores' accumulation loses more over a long one): on CTA pairs, in chunks
+  // whose sums are added in fp32 registers, or in splits that short
   bool promote = false;
   float2* ce_stats = nullptr; float* ce_zy = nullptr;
   const float2* ce_rowstat = nullptr;
@@ -95,8 +95,8 @@ struct GemmOp {
   float beta1 = 0.9f, beta2 = 0.999f;
 };
 
-// Number of K splits the wgrad of this shape uses, and the workspace bytes.
-int wgrad_splits(int dtype, int64_t M, int64_t N, int64_t K);
+// Number of K splits the wgrad of this shape uses (promote: GemmOp's), and the workspace bytes.
+int wgrad_splits(int dtype, int64_t M, int64_t N, int64_t K, bool promote = false);
 size_t wgrad_workspace_bytes(int dtype, int64_t M, int64_t N, int64_t K, int splits);
 // The largest workspace any kernel choice for this shape uses (one-SM or CTA
 // pairs, whatever GemmOp::cg2 says): a layout sized by it fits either.

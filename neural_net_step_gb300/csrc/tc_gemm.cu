@@ -2408,9 +2408,23 @@ static bool cg2_wgrad_default(int dtype, int64_t M, int64_t N, int64_t K) {
   return ceil_div(ceil_div(K, tc::BK), cg2_wgrad_splits(M, N, K)) >= 16;
 }
 
-int wgrad_splits(int dtype, int64_t M, int64_t N, int64_t K) {
+// Where GemmOp::promote takes the CTA pairs: by their default policy, and
+// wherever the one-SM kernel, which adds nothing apart, would run a chain of
+// more than kPromoteStages stages (their tiles are zero-filled beyond a narrow
+// output).  With the read-back, in us, and off by (2-norm), one-SM kernel ->
+// pairs: 200 x 4096 over 65536 rows 289 -> 259, 8.8e-6 -> below 1e-6;
+// 4096 x 200 over 30001 128 -> 91, 1.4e-6; 8 x 2048 over 50000 104 -> 109, 1.1e-6.
+static bool promote_on_pairs(int64_t M, int64_t N, int64_t K) {
+  if (cg2_wgrad_default(DT_BF16, M, N, K)) return true;
+  int bn, s;
+  tc_wgrad_choice(DT_BF16, M, N, K, &bn, &s);
+  return ceil_div(ceil_div(K, tc::BK), s) > tc::kPromoteStages;
+}
+
+int wgrad_splits(int dtype, int64_t M, int64_t N, int64_t K, bool promote) {
   if (dtype == DT_F32) return simt_gemm_splits(M, N, K);
-  if (cg2_wgrad_default(dtype, M, N, K)) return cg2_wgrad_splits(M, N, K);
+  if (cg2_wgrad_default(dtype, M, N, K) || (promote && dtype == DT_BF16 && promote_on_pairs(M, N, K)))
+    return cg2_wgrad_splits(M, N, K);
   int bn, s;
   tc_wgrad_choice(dtype, M, N, K, &bn, &s);
   return s;
@@ -2570,6 +2584,8 @@ int tc_wgrad_cg2_plan(const GemmOp& op, LaunchRec* recs, char* err, size_t errle
 int tc_wgrad_plan(const GemmOp& op, LaunchRec* recs, char* err, size_t errlen) {
   if (op.dtype == DT_BF16 && !op.ce_rowstat && op.cg2 != 0 && op.M >= 256 && op.N >= 256 &&
       (op.cg2 > 0 || cg2_wgrad_default(op.dtype, op.M, op.N, op.K)))
+    return tc_wgrad_cg2_plan(op, recs, err, errlen);
+  if (op.promote && op.dtype == DT_BF16 && promote_on_pairs(op.M, op.N, op.K))
     return tc_wgrad_cg2_plan(op, recs, err, errlen);
   tc::WParams p;
   memset(&p, 0, sizeof(p));
