@@ -14,25 +14,35 @@ __device__ __forceinline__ float gate_act(float g, int act) {
   if (act == ACT_SILU) return g * rcp_fast(1.0f + ex2_fast(-kLog2e * g));
   return apply_act(g, act);
 }
+// g, but no further from zero than c; NaN stays NaN.
+__device__ __forceinline__ float clamp_gate(float g, float c) {
+  float r;
+  asm("min.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(g), "f"(c));
+  return r;
+}
 // act(g) and act'(g) together.  Both smooth activations are g s with s =
 // 1 / (1 + e): for SiLU e = e^{-g}, for GELU (tanh form) e = e^{-2a}
-// (common.cuh); the exponent is clamped so that e stays finite, and 1 - s =
-// e s keeps its relative accuracy in the tails.
+// (common.cuh), and 1 - s = e s keeps its relative accuracy in the tails.  The
+// gate is clamped where e would leave 2^-126 .. 2^126 (SiLU: 87.3, GELU: 10):
+// act' has reached 1 there, or 0 but for 2^-118, while e (s) held at its bound
+// would still be multiplied by g (GELU: g^3).  Beyond, act is g, or 0 but for 2^-119.
 __device__ __forceinline__ void gate_act_grad(float g, int act, float& a, float& da) {
   if (act == ACT_RELU) {
     a = fmaxf(g, 0.0f);
     da = g > 0.0f ? 1.0f : 0.0f;
   } else if (act == ACT_GELU_TANH) {
-    const float g2 = g * g;
-    const float e = ex2_fast(fminf(fmaxf(g * fmaf(kGeluC1, g2, kGeluC0), -126.f), 126.f));
+    const float c = clamp_gate(g, 10.0f);
+    const float g2 = c * c;
+    const float e = ex2_fast(c * fmaf(kGeluC1, g2, kGeluC0));
     const float s = rcp_fast(1.0f + e);
-    a = g * s;
-    da = fmaf(2.0f * a * (e * s), fmaf(kGeluK3, g2, kGeluK0), s);
+    a = (g < c ? c : g) * s;
+    da = fmaf(2.0f * (c * s) * (e * s), fmaf(kGeluK3, g2, kGeluK0), s);
   } else if (act == ACT_SILU) {
-    const float e = ex2_fast(fminf(-kLog2e * g, 126.f));
+    const float c = clamp_gate(g, 87.3f);
+    const float e = ex2_fast(-kLog2e * c);
     const float s = rcp_fast(1.0f + e);
-    a = g * s;
-    da = fmaf(a, e * s, s);
+    a = (g < c ? c : g) * s;
+    da = fmaf(c * s, e * s, s);
   } else {
     a = g;
     da = 1.0f;
@@ -40,8 +50,10 @@ __device__ __forceinline__ void gate_act_grad(float g, int act, float& a, float&
 }
 
 // The same for two gates whose results are rounded to bf16.  1 - s stands for
-// e s here: off by 2^-24 where s is near 1 (act' is too), and with no clamp an
-// infinite e leaves s = 0, a = -0, act' = -0.
+// e s here: off by 2^-24 where s is near 1, which GELU's other factor (35 at g =
+// 5) makes 2e-6 of act' at most; from g = 6 on 1 - s is 0.  With no clamp of e an
+// infinite one leaves s = 0, a = -0, act' = 0; in act' g^2 is held at 256, so that
+// 1 - s = 0 or a = 0 meets no infinity.
 template <int ACT>
 __device__ __forceinline__ void gate2(F2 g, F2& a, F2& da) {
   if constexpr (ACT == ACT_NONE) {
@@ -63,9 +75,11 @@ __device__ __forceinline__ void gate2(F2 g, F2& a, F2& da) {
     const F2 s = pack2(rcp_fast(x0), rcp_fast(x1));
     a = mul2(g, s);
     const F2 rest = fma2(s, minus, one);   // 1 - s
+    unpack2(g2, x0, x1);
+    const F2 near2 = pack2(fminf(x0, 256.f), fminf(x1, 256.f));
     da = ACT == ACT_SILU
              ? fma2(a, rest, s)
-             : fma2(mul2(a, rest), fma2(g2, pack2(2 * kGeluK3, 2 * kGeluK3), pack2(2 * kGeluK0, 2 * kGeluK0)), s);
+             : fma2(mul2(a, rest), fma2(near2, pack2(2 * kGeluK3, 2 * kGeluK3), pack2(2 * kGeluK0, 2 * kGeluK0)), s);
   }
 }
 
