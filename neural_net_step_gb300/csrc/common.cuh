@@ -63,15 +63,23 @@ __device__ __forceinline__ float gelu_tanh(float u) {
   const float e = ex2_fast(u * fmaf(kGeluC1, u * u, kGeluC0));
   return u * rcp_fast(1.0f + e);
 }
+// u, but no further from zero than c; NaN stays NaN.
+__device__ __forceinline__ float clamp_abs(float u, float c) {
+  float r;
+  asm("min.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(u), "f"(c));
+  return r;
+}
 // s + 2 u s (1 - s) a', a' = sqrt(2/pi) (1 + 3 * 0.044715 u^2), with
-// 1 - s = e s; the exponent is clamped so that e stays finite.
+// 1 - s = e s; u is clamped to +-10, where e is still finite and the value has
+// reached 1, or 0 but for 2^-118 (e held at its bound alone would still be
+// multiplied by u^3).
 __device__ __forceinline__ float gelu_tanh_grad(float u) {
-  const float u2 = u * u;
-  const float x = fminf(fmaxf(u * fmaf(kGeluC1, u2, kGeluC0), -126.f), 126.f);
-  const float e = ex2_fast(x);
+  const float c = clamp_abs(u, 10.0f);
+  const float c2 = c * c;
+  const float e = ex2_fast(c * fmaf(kGeluC1, c2, kGeluC0));
   const float s = rcp_fast(1.0f + e);
-  const float d = fmaf(kGeluK3, u2, kGeluK0);
-  return fmaf(2.0f * u * s * (e * s), d, s);
+  const float d = fmaf(kGeluK3, c2, kGeluK0);
+  return fmaf(2.0f * c * s * (e * s), d, s);
 }
 __device__ __forceinline__ float apply_act(float v, int act) {
   if (act == ACT_RELU) return fmaxf(v, 0.0f);

@@ -14,12 +14,6 @@ __device__ __forceinline__ float gate_act(float g, int act) {
   if (act == ACT_SILU) return g * rcp_fast(1.0f + ex2_fast(-kLog2e * g));
   return apply_act(g, act);
 }
-// g, but no further from zero than c; NaN stays NaN.
-__device__ __forceinline__ float clamp_gate(float g, float c) {
-  float r;
-  asm("min.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(g), "f"(c));
-  return r;
-}
 // act(g) and act'(g) together.  Both smooth activations are g s with s =
 // 1 / (1 + e): for SiLU e = e^{-g}, for GELU (tanh form) e = e^{-2a}
 // (common.cuh), and 1 - s = e s keeps its relative accuracy in the tails.  The
@@ -31,14 +25,14 @@ __device__ __forceinline__ void gate_act_grad(float g, int act, float& a, float&
     a = fmaxf(g, 0.0f);
     da = g > 0.0f ? 1.0f : 0.0f;
   } else if (act == ACT_GELU_TANH) {
-    const float c = clamp_gate(g, 10.0f);
+    const float c = clamp_abs(g, 10.0f);
     const float g2 = c * c;
     const float e = ex2_fast(c * fmaf(kGeluC1, g2, kGeluC0));
     const float s = rcp_fast(1.0f + e);
     a = (g < c ? c : g) * s;
     da = fmaf(2.0f * (c * s) * (e * s), fmaf(kGeluK3, g2, kGeluK0), s);
   } else if (act == ACT_SILU) {
-    const float c = clamp_gate(g, 87.3f);
+    const float c = clamp_abs(g, 87.3f);
     const float e = ex2_fast(-kLog2e * c);
     const float s = rcp_fast(1.0f + e);
     a = (g < c ? c : g) * s;
