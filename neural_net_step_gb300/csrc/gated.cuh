@@ -10,7 +10,14 @@ constexpr int ACT_SILU = 3;   // g / (1 + e^{-g}); the gated operations only
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// max(g, 0); NaN stays NaN (fmaxf would return 0 and hide a broken gate).
+__device__ __forceinline__ float gate_relu(float g) {
+  float r;
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(g));
+  return r;
+}
 __device__ __forceinline__ float gate_act(float g, int act) {
+  if (act == ACT_RELU) return gate_relu(g);
   if (act == ACT_SILU) return g * rcp_fast(1.0f + ex2_fast(-kLog2e * g));
   return apply_act(g, act);
 }
@@ -22,7 +29,7 @@ __device__ __forceinline__ float gate_act(float g, int act) {
 // would still be multiplied by g (GELU: g^3).  Beyond, act is g, or 0 but for 2^-119.
 __device__ __forceinline__ void gate_act_grad(float g, int act, float& a, float& da) {
   if (act == ACT_RELU) {
-    a = fmaxf(g, 0.0f);
+    a = gate_relu(g);
     da = g > 0.0f ? 1.0f : 0.0f;
   } else if (act == ACT_GELU_TANH) {
     const float c = clamp_abs(g, 10.0f);
@@ -56,7 +63,7 @@ __device__ __forceinline__ void gate2(F2 g, F2& a, F2& da) {
   } else if constexpr (ACT == ACT_RELU) {
     float x, y;
     unpack2(g, x, y);
-    a = pack2(fmaxf(x, 0.0f), fmaxf(y, 0.0f));
+    a = pack2(gate_relu(x), gate_relu(y));
     da = pack2(x > 0.0f ? 1.0f : 0.0f, y > 0.0f ? 1.0f : 0.0f);
   } else {
     const F2 one = pack2(1.0f, 1.0f), minus = pack2(-1.0f, -1.0f);
