@@ -13,8 +13,6 @@
 // through one another's shared memory.
 #include <stdio.h>
 
-#include <mutex>
-
 #include "common.cuh"
 #include "e4m3.cuh"
 #include "f32x2.cuh"
@@ -278,11 +276,6 @@ __global__ void __launch_bounds__(256, 2) gated_simt_kernel(const __grid_constan
 unsigned simt_smem(int rm, bool sums) { return (unsigned)((GSTAGES * GK * simt_pitch(rm) + (sums ? 8 * rm * 256 : 0)) * 4); }
 template <bool FWD, int RM, bool SPLIT>
 const void* simt_kernel() {
-  static std::once_flag once;
-  std::call_once(once, [] {
-    cudaFuncSetAttribute((const void*)gated_simt_kernel<FWD, RM, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                         (int)simt_smem(RM, true));
-  });
   return (const void*)gated_simt_kernel<FWD, RM, SPLIT>;
 }
 template <bool FWD, bool SPLIT>

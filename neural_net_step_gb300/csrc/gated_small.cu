@@ -16,7 +16,6 @@
 #include <stdio.h>
 
 #include <algorithm>
-#include <mutex>
 
 #include "common.cuh"
 #include "gated.cuh"
@@ -122,11 +121,6 @@ __global__ void __launch_bounds__(512) gated_small_kernel(const __grid_constant_
 
 template <int NT, int ACT>
 const void* small_kernel() {
-  static std::once_flag once;
-  std::call_once(once, [] {
-    cudaFuncSetAttribute((const void*)gated_small_kernel<NT, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                         16 * 32 * (8 * NT + 1) * 4);
-  });
   return (const void*)gated_small_kernel<NT, ACT>;
 }
 template <int NT>

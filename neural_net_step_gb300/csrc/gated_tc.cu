@@ -21,7 +21,6 @@
 #include <string.h>
 
 #include <algorithm>
-#include <mutex>
 
 #include "common.cuh"
 #include "e4m3.cuh"
@@ -536,11 +535,6 @@ gated_cg2_kernel(const __grid_constant__ GtParams p) {
 namespace {
 template <bool FWD, bool Q8, int ACT>
 const void* gated_kernel_ptr() {
-  static std::once_flag once;
-  std::call_once(once, [] {
-    cudaFuncSetAttribute((const void*)tc::gated_cg2_kernel<FWD, Q8, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                         tc::GtCfg<FWD>::SMEM_BYTES);
-  });
   return (const void*)tc::gated_cg2_kernel<FWD, Q8, ACT>;
 }
 template <bool FWD, bool Q8>

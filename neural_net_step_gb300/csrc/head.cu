@@ -23,8 +23,6 @@
 #include <cooperative_groups.h>
 #include <stdio.h>
 
-#include <mutex>
-
 #include "common.cuh"
 #include "ops.h"
 
@@ -433,11 +431,6 @@ int head_plan(const HeadOp& op, LaunchRec* rec, char* err, size_t errlen) {
                         (const void*)head_kernel<float, true>, (const void*)head_kernel<float, false, true>,
                         (const void*)head_kernel<__nv_bfloat16, false, true>,
                         (const void*)head_kernel<float, true, true>};
-  static std::once_flag once;
-  std::call_once(once, [&] {
-    for (const void* f : fns)
-      cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(HeadSmem));
-  });
   rec->func = fns[(mse ? 3 : 0) + (x3 ? 2 : op.dtype == DT_F32 ? 0 : 1)];
   rec->grid = dim3(head_grid(op.B));
   rec->block = dim3(kHT);

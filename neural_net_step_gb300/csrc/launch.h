@@ -6,6 +6,8 @@
 #include <stdint.h>
 #include <string.h>
 
+#include "smem_limit.h"
+
 namespace mlpk {
 
 constexpr unsigned kMaxArgBytes = 1024;
@@ -79,6 +81,8 @@ struct LaunchRec {
 };
 
 inline cudaError_t launch_rec(const LaunchRec& r, cudaStream_t s) {
+  const cudaError_t e = allow_smem(r.func, r.smem);
+  if (e != cudaSuccess) return e;
   void* argp[1] = {const_cast<unsigned char*>(r.args)};
   if (r.cluster == 1) return cudaLaunchKernel(r.func, r.grid, r.block, argp, r.smem, s);
   cudaLaunchConfig_t cfg;
@@ -98,6 +102,7 @@ inline cudaError_t launch_rec(const LaunchRec& r, cudaStream_t s) {
   return cudaLaunchKernelExC(&cfg, r.func, argp);
 }
 
+// (the caller asks allow_smem)
 inline cudaKernelNodeParams node_params(const LaunchRec& r, void** argp) {
   cudaKernelNodeParams kp;
   memset(&kp, 0, sizeof(kp));

@@ -755,6 +755,7 @@ mlp_status launch_graph(mlp* m, int key, std::vector<LaunchRec>& recs, cudaStrea
         }
       }
       void* argp[1];
+      CUDA_TRY(allow_smem(r.func, r.smem));
       cudaKernelNodeParams kp = node_params(r, argp);
       cudaGraphNode_t node;
       if (nd >= 1 && m->pdl && r.early) {
@@ -773,6 +774,7 @@ mlp_status launch_graph(mlp* m, int key, std::vector<LaunchRec>& recs, cudaStrea
     for (size_t i = 0; i < recs.size(); ++i) {
       if (recs[i].same_as(gc->recs[i])) continue;
       void* argp[1];
+      CUDA_TRY(allow_smem(recs[i].func, recs[i].smem));
       cudaKernelNodeParams kp = node_params(recs[i], argp);
       CUDA_TRY(cudaGraphExecKernelNodeSetParams(gc->exec, gc->nodes[i], &kp));
       gc->recs[i] = recs[i];
@@ -1351,7 +1353,8 @@ static mlp_status run_chain(LaunchRec* r, int n, void* stream) {
     cfg.attrs = &a;
     cfg.numAttrs = i > 0 ? 1 : 0;
     void* argp[1] = {r[i].args};
-    cudaError_t e = cudaLaunchKernelExC(&cfg, r[i].func, argp);
+    cudaError_t e = allow_smem(r[i].func, r[i].smem);
+    if (e == cudaSuccess) e = cudaLaunchKernelExC(&cfg, r[i].func, argp);
     if (e != cudaSuccess) return fail(MLP_ERR_CUDA, "launch of %s failed: %s", r[i].name, cudaGetErrorString(e));
   }
   return ok();

@@ -17,7 +17,6 @@
 #include <stdio.h>
 
 #include <algorithm>
-#include <mutex>
 
 #include "common.cuh"
 #include "f32x2.cuh"
@@ -699,12 +698,8 @@ int64_t bwd_blocks(int64_t M, int64_t D) {
 
 template <typename T, int VEC, int EPT, bool FULL, bool FWD>
 const void* row_kernel() {
-  static std::once_flag once;
-  const void* k;
-  if constexpr (FWD) k = (const void*)ln_fwd_kernel<T, VEC, EPT, FULL>;
-  else k = (const void*)ln_bwd_kernel<T, VEC, EPT, FULL>;
-  std::call_once(once, [k] { cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448); });
-  return k;
+  if constexpr (FWD) return (const void*)ln_fwd_kernel<T, VEC, EPT, FULL>;
+  else return (const void*)ln_bwd_kernel<T, VEC, EPT, FULL>;
 }
 // FULL where every thread's elements are all there (a row length that is a
 // multiple of 32 EPT): no tests of the columns, half the instructions.

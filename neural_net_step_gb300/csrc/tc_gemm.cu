@@ -2301,11 +2301,6 @@ bool make_tmap_op(CUtensorMap* tm, bool x3, const void* ptr, int64_t inner, int6
 
 template <int BN>
 const void* tc_kernel_ptr() {
-  static std::once_flag once;
-  std::call_once(once, [] {
-    cudaFuncSetAttribute((const void*)tc::tc_gemm_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                         tc::Cfg<BN>::SMEM_BYTES);
-  });
   return (const void*)tc::tc_gemm_kernel<BN>;
 }
 
@@ -2449,21 +2444,11 @@ size_t wgrad_workspace_bytes(int dtype, int64_t M, int64_t N, int64_t K, int spl
 
 namespace {
 const void* tcpair_kernel_ptr() {
-  static std::once_flag once;
-  std::call_once(once, [] {
-    cudaFuncSetAttribute((const void*)tc::tc_gemm_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                         tc::PCfg<128, true>::SMEM_BYTES);
-  });
   return (const void*)tc::tc_gemm_pair_kernel;
 }
 
 template <int BN, bool X3>
 const void* tcp_kernel_ptr() {
-  static std::once_flag once;
-  std::call_once(once, [] {
-    cudaFuncSetAttribute((const void*)tc::tc_gemm_persistent_kernel<BN, X3>,
-                         cudaFuncAttributeMaxDynamicSharedMemorySize, tc::PCfg<BN, X3>::SMEM_BYTES);
-  });
   return (const void*)tc::tc_gemm_persistent_kernel<BN, X3>;
 }
 
@@ -2507,21 +2492,11 @@ bool make_tmap_f32_3d(CUtensorMap* tm, const void* ptr, int64_t inner, int64_t r
 
 template <bool X3, int WBN>
 const void* tcw_kernel_ptr() {
-  static std::once_flag once;
-  std::call_once(once, [] {
-    cudaFuncSetAttribute((const void*)tc::tc_wgrad_persistent_kernel<X3, WBN>,
-                         cudaFuncAttributeMaxDynamicSharedMemorySize, tc::WCfg<X3, WBN>::SMEM_BYTES);
-  });
   return (const void*)tc::tc_wgrad_persistent_kernel<X3, WBN>;
 }
 
 template <bool PROMOTE>
 const void* tcw2_kernel_ptr() {
-  static std::once_flag once;
-  std::call_once(once, [] {
-    cudaFuncSetAttribute((const void*)tc::tc_wgrad_cg2_kernel<PROMOTE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                         tc::W2Cfg::SMEM_BYTES);
-  });
   return (const void*)tc::tc_wgrad_cg2_kernel<PROMOTE>;
 }
 
@@ -2647,11 +2622,6 @@ int tc_wgrad_plan(const GemmOp& op, LaunchRec* recs, char* err, size_t errlen) {
 
 template <bool FWD>
 const void* tcg2_kernel_ptr() {
-  static std::once_flag once;
-  std::call_once(once, [] {
-    cudaFuncSetAttribute((const void*)tc::tc_gemm_cg2_kernel<FWD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                         tc::G2Cfg::SMEM_BYTES);
-  });
   return (const void*)tc::tc_gemm_cg2_kernel<FWD>;
 }
 
@@ -2673,7 +2643,8 @@ int cg2_max_clusters() {
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     int c = 0;
-    if (cudaOccupancyMaxActiveClusters(&c, tcg2_kernel_ptr<true>(), &cfg) != cudaSuccess || c < 1) {
+    if (allow_smem(tcg2_kernel_ptr<true>(), tc::G2Cfg::SMEM_BYTES) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&c, tcg2_kernel_ptr<true>(), &cfg) != cudaSuccess || c < 1) {
       cudaGetLastError();
       c = sms / 2;
     }
