@@ -202,7 +202,8 @@ mlp_status mlp_op_layernorm_backward(int dtype, int64_t M, int64_t D, const void
  * even).  A code stands for e4m3 * 2^k, exact in fp32 and in bf16, off by at
  * most 2^-4 of the value (2^-17.8 of the block's amax where that is more).
  * Infinities and NaN are kept as NaN; a magnitude of 2^128 (1 - 2^-5) or more
- * reads back as infinite.
+ * reads back as infinite.  Read back, E may hold any byte: 255, which stands for
+ * no k, makes its block's values NaN.
  *   X, Y [rows, cols] (ldx, ldy; MLP_F32 or MLP_BF16), Q uint8 [rows, cols]
  *   (ldq), E uint8 [rows, ceil(cols / 32)] (lde).
  * Any pitch; 16-byte aligned rows of X / Y with 8-byte aligned rows of Q move

@@ -50,10 +50,11 @@ __device__ __forceinline__ void q8_unpack(uint32_t w, float scale, float* v) {
   const float2 a = __half22float2(lo), b = __half22float2(hi);
   v[0] = a.x * scale; v[1] = a.y * scale; v[2] = b.x * scale; v[3] = b.y * scale;
 }
-// 2^(byte - 127) of a scale byte (0 stands for fp32's subnormal 2^-127; a
-// program may hand in scales below the encoder's).
+// 2^(byte - 127) of a scale byte; a program may hand in ones that the encoder
+// does not write: 0 stands for fp32's subnormal 2^-127, and 255 is NaN (as in the
+// microscaling formats' scales), which makes every value of its block NaN.
 __device__ __forceinline__ float q8_scale(uint32_t byte) {
-  return byte ? __uint_as_float(byte << 23) : __uint_as_float(0x00400000u);
+  return __uint_as_float(byte << 23 | (((byte + 1u) & 0xfeu) == 0u ? 0x00400000u : 0u));
 }
 __device__ __forceinline__ float q8_value(uint32_t code, uint32_t byte) {
   float v[4];

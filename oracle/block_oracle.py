@@ -113,8 +113,8 @@ def q8_encode(x):
 
 
 def q8_decode(q, e):
-    """The values that codes and scale bytes stand for (fp64)."""
+    """The values that codes and scale bytes stand for (fp64); scale byte 255 is NaN."""
     table = np.append(_e4m3_table(), np.nan)
     sign = np.where(q >> 7, -1.0, 1.0)
     k = np.repeat(e.astype(np.int64) - 127, Q8_BLOCK, axis=1)[:, :q.shape[1]]
-    return sign * table[q & 127] * 2.0 ** k.astype(np.float64)
+    return sign * table[q & 127] * np.where(k == 128, np.nan, 2.0 ** k.astype(np.float64))
