@@ -200,7 +200,8 @@ mlp_status mlp_op_layernorm_backward(int dtype, int64_t M, int64_t D, const void
  * finite magnitude, k is the smallest exponent >= -120 with amax <= 448 2^k;
  * E holds k + 127, Q the values X 2^-k rounded to e4m3 (to nearest, ties to
  * even).  A code stands for e4m3 * 2^k, exact in fp32 and in bf16, off by at
- * most 2^-4 of the value (2^-17.8 of the block's amax where that is more).
+ * most 2^-4 of the value, or 2^(k - 10) where that is more: 2^-17.8 of the
+ * block's amax, but 2^-130 where amax is below 224 * 2^-120 and k stays at -120.
  * Infinities and NaN are kept as NaN; a magnitude of 2^128 (1 - 2^-5) or more
  * reads back as infinite.  Read back, E may hold any byte: 255, which stands for
  * no k, makes its block's values NaN.
