@@ -1695,7 +1695,7 @@ static const char* gated_layout(const GatedOp& op) {
   if (op.lda < op.K || op.ldb < (op.fwd ? op.K : op.F) || (op.h && op.ldh < op.F) || (op.s && op.lds < 2 * op.F) ||
       (op.se && op.ldse < 2 * ceil_div(op.F, 32)) || (op.ds && op.ldds < 2 * op.F))
     return "leading dimension too small";
-  if (!elements_aligned(4, {op.bias}) ||
+  if (!elements_aligned(4, {op.bias, op.err}) ||
       !elements_aligned(dtype_bytes(op.dtype), {op.A, op.B, op.h, op.ds, op.se ? nullptr : op.s}))
     return "misaligned elements";
   if (op.dtype == MLP_F32) return nullptr;
@@ -1764,7 +1764,7 @@ mlp_status mlp_op_wgrad8(int dtype, int64_t N, int64_t K, int64_t B, const void*
                          void* workspace, size_t ws_bytes, uint32_t* err_dev, void* stream) {
   if (!dtype_ok(dtype)) return fail(MLP_ERR_DTYPE, "bad dtype");
   if (!dY || !Q || !E || !dW || !workspace) return fail(MLP_ERR_ARG, "null pointer");
-  if (!elements_aligned(dtype_bytes(dtype), {dY}) || !elements_aligned(4, {dW, db}))
+  if (!elements_aligned(dtype_bytes(dtype), {dY}) || !elements_aligned(4, {dW, db, err_dev}))
     return fail(MLP_ERR_ARG, "misaligned elements");
   const size_t need = mlp_op_wgrad8_workspace_bytes(dtype, N, K, B);
   if (need == 0 || ldy < N || lddw < K) return fail(MLP_ERR_SHAPE, "bad shape or leading dimension");
