@@ -1643,8 +1643,7 @@ mlp_status mlp_op_layernorm(int dtype, int64_t M, int64_t D, const void* X, int6
 }
 
 size_t mlp_op_layernorm_backward_workspace_bytes(int dtype, int64_t M, int64_t D) {
-  if (!dtype_ok(dtype) || M < 1 || D < 1) return 0;
-  return layernorm_bwd_workspace_bytes(M, D);
+  return dtype_ok(dtype) ? layernorm_bwd_workspace_bytes(M, D) : 0;
 }
 
 mlp_status mlp_op_layernorm_backward(int dtype, int64_t M, int64_t D, const void* dY, int64_t lddy, const void* X,

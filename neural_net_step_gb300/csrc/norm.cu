@@ -722,10 +722,13 @@ const void* row_pick(bool f32, int unit, const RowShape& s, int64_t D) {
   return e8 ? row_full<B, 8, 8, FWD>(full) : row_full<B, 8, 16, FWD>(full);
 }
 
+// The shapes taken, forward and backward.
+bool shape_ok(int64_t M, int64_t D) { return M >= 1 && D >= 1 && M <= INT32_MAX && D <= kMaxD; }
+
 }  // namespace
 
 int layernorm_plan(const LayerNormOp& op, LaunchRec* rec, char* err, size_t errlen) {
-  if (op.M < 1 || op.D < 1 || op.M > INT32_MAX || op.D > kMaxD || op.ldx < op.D || op.ldy < op.D) {
+  if (!shape_ok(op.M, op.D) || op.ldx < op.D || op.ldy < op.D) {
     snprintf(err, errlen, "bad layer-norm shape %lld x %lld", (long long)op.M, (long long)op.D);
     return -1;
   }
@@ -751,11 +754,11 @@ int layernorm_plan(const LayerNormOp& op, LaunchRec* rec, char* err, size_t errl
 }
 
 size_t layernorm_bwd_workspace_bytes(int64_t M, int64_t D) {
-  return (size_t)bwd_blocks(M, D) * 2 * (size_t)D * sizeof(float);
+  return !shape_ok(M, D) ? 0 : (size_t)bwd_blocks(M, D) * 2 * (size_t)D * sizeof(float);
 }
 
 int layernorm_bwd_plan(const LayerNormBwdOp& op, LaunchRec* recs, char* err, size_t errlen) {
-  if (op.M < 1 || op.D < 1 || op.M > INT32_MAX || op.D > kMaxD || op.ldx < op.D || op.lddy < op.D ||
+  if (!shape_ok(op.M, op.D) || op.ldx < op.D || op.lddy < op.D ||
       op.lddx < op.D) {
     snprintf(err, errlen, "bad layer-norm shape %lld x %lld", (long long)op.M, (long long)op.D);
     return -1;
