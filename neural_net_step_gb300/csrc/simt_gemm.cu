@@ -250,6 +250,10 @@ int simt_gemm_plan(const GemmOp& op, LaunchRec* recs, char* err, size_t errlen) 
   p.k_chunk = (int)chunk;
   splits = (int)ceil_div(op.K, chunk);
   constexpr int BM = 64, BN = 64;
+  if (ceil_div(op.M, BM) > 65535) {   // (a grid's y)
+    snprintf(err, errlen, "fp32 GEMM: %lld rows are too many", (long long)op.M);
+    return -1;
+  }
   recs[0].func = pick<BM, BN>(op.a_kmajor, op.b_kmajor);
   recs[0].grid = dim3((unsigned)ceil_div(op.N, BN), (unsigned)ceil_div(op.M, BM), (unsigned)splits);
   recs[0].block = dim3((BM / 8) * (BN / 8));

@@ -25,3 +25,15 @@ def test_workspace_size_of_the_largest_norms():
     most = (1 << 31) - 1
     assert nn.mlp_op_layernorm_backward_workspace_bytes(nn.BF16, most, 65535 * 256) == 32 * 2 * 65535 * 256 * 4
     assert nn.mlp_op_layernorm_backward_workspace_bytes(nn.BF16, most, 8192) > 0
+
+
+@pytest.mark.parametrize("f,good,rows", [
+    (nn.mlp_op_wgrad8, dict(W8, dtype=nn.F32, K=1, lddw=1, ldq=1, lde=1, ws_bytes=1 << 40), "N"),
+    (nn.mlp_op_wgrad, dict(dtype=nn.F32, N=4, K=1, B=1, dY=P, ldy=4, X=P, ldx=1, dW=P, lddw=1, db=P, ws=P, ws_bytes=1 << 40,
+                           err=None, stream=None), "N"),
+    (nn.mlp_op_dgrad, dict(dtype=nn.F32, act=0, M=4, N=4, K=4, dY=P, ldy=4, W=P, ldw=4, S=None, lds=0, dX=P, ldx=4,
+                           err=None, stream=None), "M")])
+def test_more_fp32_rows_than_a_grid_has(f, good, rows):
+    """More rows of 64-row tiles than a grid takes: refused before the first of a call's kernels is enqueued."""
+    pitch = dict(ldy=1 << 23) if rows == "N" else {}
+    _refused(f, dict(good, **pitch), **{rows: 64 * 65535 + 1})
