@@ -37,3 +37,8 @@ def test_more_fp32_rows_than_a_grid_has(f, good, rows):
     """More rows of 64-row tiles than a grid takes: refused before the first of a call's kernels is enqueued."""
     pitch = dict(ldy=1 << 23) if rows == "N" else {}
     _refused(f, dict(good, **pitch), **{rows: 64 * 65535 + 1})
+
+
+@pytest.mark.parametrize("f,good", [(nn.mlp_op_gated_linear, GF), (nn.mlp_op_gated_dgrad, GB)])
+def test_gated_fp32_rows_beyond_the_stated_most(f, good):
+    _refused(f, dict(good, dtype=nn.F32), M=65535 * 128 + 1)
