@@ -175,7 +175,9 @@ mlp_status mlp_op_argmax(int dtype, int64_t B, int64_t C, const void* z, int64_t
  *   X with X's pitch); mean, rstd fp32 [M] (nullable: not kept).  eps >= 0 and finite.
  * Any D up to 65535 * 256 and any pitch.  Rows move 16 bytes at a time where D,
  * base and pitch allow it, else 4 bytes, else an element.  Statistics are
- * fp32, from the elements as stored. */
+ * fp32, from the elements as stored: squares of differences from the mean
+ * leave fp32 above 1e19 (rstd 0) and lose bits below 1e-19.  A row that holds
+ * NaN or an infinity has y and rstd NaN. */
 mlp_status mlp_op_layernorm(int dtype, int64_t M, int64_t D, const void* X, int64_t ldx, const float* gamma,
                             const float* beta, float eps, void* Y, int64_t ldy, float* mean, float* rstd,
                             void* stream);
@@ -224,7 +226,7 @@ mlp_status mlp_op_dequant8(int dtype, int64_t rows, int64_t cols, const uint8_t*
  * with SE set as an 8-bit checkpoint (mlp_op_quant8), S uint8 [M, 2F] the
  * codes and SE uint8 [M, 2 ceil(F / 32)] (ldse) the scales, the gate's blocks
  * first (gate and up half each as one matrix of F columns).  H comes from the
- * fp32 sums, before s is rounded.  MLP_F32 or MLP_BF16; MLP_BF16 takes K, F
+ * fp32 sums, before s is rounded; a gate that is NaN gives NaN with every act.  MLP_F32 or MLP_BF16; MLP_BF16 takes K, F
  * and the leading dimensions (but ldse) in multiples of 8 and 16-byte aligned
  * matrices (S codes: 8-byte).  M from one token on (MLP_F32: to 65535 * 128).
  * Nothing written may overlap anything read. */
@@ -252,7 +254,8 @@ mlp_status mlp_op_gated_dgrad(int dtype, int act, int64_t M, int64_t N, int64_t 
  *   dY [B, N] (ldy; MLP_F32 or MLP_BF16), X [B, K] the values of Q (ldq), E
  *   (lde).  The values are read back into the workspace (16-byte aligned, at
  *   least the bytes below; the dtype holds them exactly): the result is that
- *   of mlp_op_wgrad on them up to the order of its sums.  MLP_BF16 takes K and
+ *   of mlp_op_wgrad on them up to the order of its sums (bf16: none of them over
+ *   more than 2048 rows on the tensor cores).  MLP_BF16 takes K and
  *   lddw in multiples of 4, ldy of 8 and 16-byte aligned dY and dW.
  *   Workspaces of calls that may overlap must not. */
 size_t mlp_op_wgrad8_workspace_bytes(int dtype, int64_t N, int64_t K, int64_t B);

@@ -5,6 +5,8 @@ and only marshal arguments: pointers are passed as integers (device addresses
 from torch tensors' data_ptr()), streams as cudaStream_t integers.  Every
 step of the path runs in the library's CUDA kernels; there is no CPU path.
 `Model` is a small convenience wrapper that lets torch allocate the arena.
+Addresses' alignment and pitches are checked; that matrices do not overlap where
+the headers forbid it is the caller's word.
 """
 from __future__ import annotations
 

@@ -117,7 +117,7 @@ __device__ __forceinline__ void finish_stats(const float (&s)[2], float inv_d, f
 // (about 250 instructions a row and warp besides the elements: 94 us for the
 // forward of 65536 x 1024 bf16); more elements share that.  The forward takes
 // 32 of bf16 (47 us); the backward, whose 2 EPT column sums stay in registers,
-// and fp32 and unaligned rows take 16 (backward of the same: 75 us; with 32
+// and fp32 and unaligned rows take 16 (backward of the same: 73 us; with 32
 // the sums spill, 142 us); short rows 8.
 template <bool FWD> struct RowCfg {   // one block to an SM
   static constexpr int THREADS = FWD ? 1024 : 512;   // at most (64 and 128 registers)
