@@ -253,9 +253,11 @@ def _own(s):
         return {"loss": s["loss"], "dz": s["dz"]}
     if kind == "select":
         batch, W, C, m = s["batch"], s["W"], s["C"], s["m"]
+        n = nn.mlp_op_beam_select_workspace_bytes(dt, batch, W, C, m)
+        ws = torch.empty(n, dtype=torch.uint8, device=DEV)
         nn.mlp_op_beam_select(dt, batch, W, C, m, s["z"].data_ptr(), C, s["scores"].data_ptr(), s["done"].data_ptr(),
                               s["eos"], s["scores_out"].data_ptr(), s["parents"].data_ptr(), s["tokens"].data_ptr(),
-                              s["done_out"].data_ptr(), st)
+                              s["done_out"].data_ptr(), ws.data_ptr(), n, st)
         return {"scores": s["scores_out"], "parents": s["parents"], "tokens": s["tokens"], "done": s["done_out"]}
     planes, batch, W = s["planes"], s["batch"], s["W"]
     row = s["n"] * s["src"].element_size()
