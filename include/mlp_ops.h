@@ -11,7 +11,7 @@
  * enqueuing anything when they are invalid; it returns once its kernels are
  * enqueued.  Device-side conditions (label range, wait timeouts) are OR-ed
  * into `err_dev` (a device uint32, nullable) with the bits
- *   1 = label outside [0, C), 2 = non-finite loss, 4 = bounded wait gave up.
+ *   1 = label or index outside its range, 2 = non-finite loss, 4 = bounded wait gave up.
  * For MLP_BF16 the GEMM operands are read by TMA: every operand base must be
  * 16-byte aligned and every leading dimension a multiple of 8 elements.
  * The GEMM entry points (linear_act, dgrad, wgrad) also take MLP_F32X3:
@@ -166,6 +166,93 @@ mlp_status mlp_op_wait_timeout_check(uint64_t limit_ns, uint32_t* err_dev, void*
 
 /* Row argmax of z [B, C] (ldz) into int32 out [B]; lowest index on ties. */
 mlp_status mlp_op_argmax(int dtype, int64_t B, int64_t C, const void* z, int64_t ldz, int32_t* out, void* stream);
+
+/* The k largest entries of every row of z [B, C] (ldz; MLP_F32 or MLP_BF16),
+ * descending, the lowest column first among equals; NaN is below everything
+ * and -0 equals +0:
+ *   values fp32 [B, k] (ldv), indices int32 [B, k] (ldi),
+ *   lse[i] = log sum_c exp(z_ic / T)  (fp32 [B], nullable),
+ *   tail[i] the same over the columns not among the k  (fp32 [B], nullable;
+ *   -infinity where nothing is left), as mlp_op_distill takes it.
+ * 1 <= k <= 256, k <= C <= 393216; T = temperature, 1e-6 to 1e6 (it changes the two sums
+ * alone).  Entries of -infinity are taken like others, last.  Where a row holds NaN or
+ * +infinity its lse is NaN, and its tail too unless only the k entries hold it.  Any
+ * base and pitch.  Nothing written may overlap anything read. */
+enum { MLP_TOPK_MAX = 256, MLP_TOPK_MAX_COLUMNS = 393216 };
+mlp_status mlp_op_topk(int dtype, int64_t B, int64_t C, int64_t k, const void* z, int64_t ldz, float temperature,
+                       float* values, int64_t ldv, int32_t* indices, int64_t ldi, float* lse, float* tail,
+                       void* stream);
+
+/* Distillation from a teacher's top logits: softmax cross-entropy's soft
+ * sibling, forward and backward in one pass over each row of the student's
+ * logits z [B, C] (ldz).  The teacher's row is k logits t_values fp32 [B, k]
+ * (ldtv) at columns t_indices int32 [B, k] (ldti; distinct; -1: unused entry) and
+ * t_tail fp32 [B] (nullable: -infinity), the log of what its other columns
+ * add up to at temperature T (mlp_op_topk's tail).  With
+ *   p_j = e^(t_j / T) / (sum_j e^(t_j / T) + e^tail),  p_r = 1 - sum_j p_j,
+ *   q = softmax(z / T),  R = the sum of q over the columns not given:
+ *   KD = sum_j p_j log(p_j / q_j) + p_r log(p_r / R)   (0 log 0 = 0),
+ *   CE = logsumexp(z) - z_y   (labels int32 [B]; nullable where ce_weight is 0, not
+ *   read then),
+ *   loss_rows = w (ce_weight CE + kd_weight KD)   (fp32 [B]),
+ *   dz = w grad_scale (ce_weight (softmax(z) - onehot(y)) + kd_weight / T g)
+ *   (dtype, lddz; nullable: the loss alone; may be z with z's pitch),
+ *   g = q_j - p_j at the teacher's columns, q (1 - p_r / R) at the others.
+ * Without a tail that is the teacher's top renormalised (p_r = 0).  kd_weight = T^2
+ * keeps the gradient's size over T.  w = row_weights fp32 [B] (nullable: 1); where
+ * it is 0, loss and gradient are 0 whatever the row, its label and its teacher
+ * hold.  A teacher's row with nothing in it (no entry above -infinity, no tail)
+ * has KD 0.  A label or column out of range, or a column given twice, sets bit 1 of
+ * err_dev, and that row's loss and gradient are 0.  A teacher that gives weight
+ * where the student has none (z = -infinity) has an infinite loss; a row of z that
+ * holds NaN or +infinity, or nothing but -infinity, gives NaN.
+ * 1 <= k <= 256, k <= C <= 393216; T from 1e-6 to 1e6.  Any base and pitch; rows of dz with
+ * another address modulo 16 than z's are written element by element. */
+mlp_status mlp_op_distill(int dtype, int64_t B, int64_t C, int64_t k, const void* z, int64_t ldz,
+                          const float* t_values, int64_t ldtv, const int32_t* t_indices, int64_t ldti,
+                          const float* t_tail, const int32_t* labels, const float* row_weights, float temperature,
+                          float ce_weight, float kd_weight, float grad_scale, void* dz, int64_t lddz,
+                          float* loss_rows, uint32_t* err_dev, void* stream);
+
+/* Beam search's step: of every batch entry's beams x C pairs (beam, token) the m
+ * best, best first, by
+ *   total(w, c) = scores[w] + z_wc - logsumexp(z_w),
+ * z [batch * beams, C] (ldz; MLP_F32 or MLP_BF16), scores fp32 [batch, beams] the beams'
+ * log-probabilities so far.  A finished beam (done uint8 [batch, beams] not 0;
+ * nullable: none) offers token eos at total scores[w] and every other at -infinity,
+ * and its logits are not read.
+ *   scores_out fp32, parents int32 (the beam), tokens int32 [batch, m]; done_out
+ *   uint8 [batch, m] (nullable): the parent was finished or the token is eos (eos
+ *   may be -1, no end token, where done is null).
+ * Totals are formed and compared in 64 bits; equal ones go by beam, then by logit
+ * and token.  A beam of score -infinity has every total -infinity (a search starts with
+ * scores 0, -infinity, ...), and so has a row of nothing but -infinity; one whose score is
+ * NaN or +infinity or whose row holds NaN or +infinity has NaN, below everything.
+ * beams <= 32, m <= 64, m <= beams * C, C <= 393216.  With m = beams, scores_out may be scores
+ * and done_out may be done.  workspace: 8-byte aligned, at least the bytes below (0: a
+ * shape that is refused); workspaces of calls that may overlap must not. */
+size_t mlp_op_beam_select_workspace_bytes(int dtype, int64_t batch, int64_t beams, int64_t C, int64_t m);
+mlp_status mlp_op_beam_select(int dtype, int64_t batch, int64_t beams, int64_t C, int64_t m, const void* z,
+                              int64_t ldz, const float* scores, const uint8_t* done, int32_t eos, float* scores_out,
+                              int32_t* parents, int32_t* tokens, uint8_t* done_out, void* workspace, size_t ws_bytes,
+                              void* stream);
+
+/* The states that go with the beams (keys and values, recurrent states, token
+ * histories), after a selection: for every plane p (a layer's tensor), batch entry b
+ * and new beam i
+ *   dst(p, b, i) = src(p, b, parents[b, i]),
+ * rows of row_bytes bytes at src + p src_plane + (b beams_in + beam) src_pitch, likewise
+ * dst (pitches and planes in bytes), parents int32 [batch, beams_out] (ldp: a
+ * selection's m entries of which beams_out are taken).  dst may be src with the
+ * same layout: rows that stay where they are are not touched then.  Otherwise
+ * nothing written may overlap anything read.  A parent outside [0, beams_in) sets bit 1 of
+ * err_dev and leaves its row as it was.  beams <= 32; moved in units of 16 bytes (8 for more
+ * than 8 beams, 4 for more than 16) where bases, pitches and row_bytes allow it, else
+ * of 4, 2 or 1. */
+mlp_status mlp_op_beam_reorder(int64_t planes, int64_t batch, int64_t beams_in, int64_t beams_out, int64_t row_bytes,
+                               const void* src, int64_t src_pitch, int64_t src_plane, const int32_t* parents,
+                               int64_t ldp, void* dst, int64_t dst_pitch, int64_t dst_plane, uint32_t* err_dev,
+                               void* stream);
 
 /* Layer norm over the rows of X [M, D] (ldx; MLP_F32 or MLP_BF16), the norm
  * in front of a feed-forward block:

@@ -28,6 +28,7 @@ PLANE_P, PLANE_G, PLANE_M, PLANE_V = 0, 1, 2, 3
 OPTIM_ADAMW, OPTIM_ADAM, OPTIM_SGD = 0, 1, 2
 OPTIM_WS_FLOATS = 1216   # op-level clipping workspace (floats)
 LOSS_CE, LOSS_MSE = 0, 1
+TOPK_MAX, TOPK_MAX_COLUMNS = 256, 393216
 
 
 class MlpError(RuntimeError):
@@ -85,6 +86,12 @@ _SIGS = {
     "mlp_op_adamw": (_I32, [_I64, _P, _P, _P, _P, _P, _I64, _F, _F, _F, _F, _F, _P]),
     "mlp_op_optim": (_I32, [_I32, _I64, _P, _P, _P, _P, _P, _I64, _F, _F, _F, _F, _F, _F, _P, _P, _P]),
     "mlp_op_argmax": (_I32, [_I32, _I64, _I64, _P, _I64, _P, _P]),
+    "mlp_op_topk": (_I32, [_I32, _I64, _I64, _I64, _P, _I64, _F, _P, _I64, _P, _I64, _P, _P, _P]),
+    "mlp_op_distill": (_I32, [_I32, _I64, _I64, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _F, _F, _F, _F, _P, _I64,
+                              _P, _P, _P]),
+    "mlp_op_beam_select_workspace_bytes": (_SZ, [_I32, _I64, _I64, _I64, _I64]),
+    "mlp_op_beam_select": (_I32, [_I32, _I64, _I64, _I64, _I64, _P, _I64, _P, _P, _I32, _P, _P, _P, _P, _P, _SZ, _P]),
+    "mlp_op_beam_reorder": (_I32, [_I64, _I64, _I64, _I64, _I64, _P, _I64, _I64, _P, _I64, _P, _I64, _I64, _P, _P]),
     "mlp_op_layernorm": (_I32, [_I32, _I64, _I64, _P, _I64, _P, _P, _F, _P, _I64, _P, _P, _P]),
     "mlp_op_layernorm_backward_workspace_bytes": (_SZ, [_I32, _I64, _I64]),
     "mlp_op_layernorm_backward": (_I32, [_I32, _I64, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _I64, _P, _P, _P, _SZ,
@@ -343,6 +350,32 @@ def mlp_op_wait_timeout_check(limit_ns, err, stream) -> None:
 
 def mlp_op_argmax(dtype, B, C, z, ldz, out, stream) -> None:
     _check(lib().mlp_op_argmax(dtype, B, C, z, ldz, out, stream))
+
+
+def mlp_op_topk(dtype, B, C, k, z, ldz, temperature, values, ldv, indices, ldi, lse, tail, stream) -> None:
+    _check(lib().mlp_op_topk(dtype, B, C, k, z, ldz, temperature, values, ldv, indices, ldi, lse, tail, stream))
+
+
+def mlp_op_distill(dtype, B, C, k, z, ldz, t_values, ldtv, t_indices, ldti, t_tail, labels, row_weights, temperature,
+                   ce_weight, kd_weight, grad_scale, dz, lddz, loss_rows, err, stream) -> None:
+    _check(lib().mlp_op_distill(dtype, B, C, k, z, ldz, t_values, ldtv, t_indices, ldti, t_tail, labels, row_weights,
+                                temperature, ce_weight, kd_weight, grad_scale, dz, lddz, loss_rows, err, stream))
+
+
+def mlp_op_beam_select_workspace_bytes(dtype, batch, beams, C, m) -> int:
+    return lib().mlp_op_beam_select_workspace_bytes(dtype, batch, beams, C, m)
+
+
+def mlp_op_beam_select(dtype, batch, beams, C, m, z, ldz, scores, done, eos, scores_out, parents, tokens, done_out,
+                       ws, ws_bytes, stream) -> None:
+    _check(lib().mlp_op_beam_select(dtype, batch, beams, C, m, z, ldz, scores, done, eos, scores_out, parents, tokens,
+                                    done_out, ws, ws_bytes, stream))
+
+
+def mlp_op_beam_reorder(planes, batch, beams_in, beams_out, row_bytes, src, src_pitch, src_plane, parents, ldp, dst,
+                        dst_pitch, dst_plane, err, stream) -> None:
+    _check(lib().mlp_op_beam_reorder(planes, batch, beams_in, beams_out, row_bytes, src, src_pitch, src_plane, parents,
+                                     ldp, dst, dst_pitch, dst_plane, err, stream))
 
 
 def mlp_op_layernorm(dtype, M, D, X, ldx, gamma, beta, eps, Y, ldy, mean, rstd, stream) -> None:

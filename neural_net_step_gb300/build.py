@@ -17,7 +17,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmlpstep.so")
-SOURCES = ["simt_gemm.cu", "tc_gemm.cu", "rowops.cu", "model.cu", "noalloc.cu", "head.cu", "norm.cu", "ckpt8.cu", "gated.cu", "gated_tc.cu", "gated_small.cu"]
+SOURCES = ["simt_gemm.cu", "tc_gemm.cu", "rowops.cu", "model.cu", "noalloc.cu", "head.cu", "norm.cu", "ckpt8.cu", "gated.cu", "gated_tc.cu", "gated_small.cu",
+           "topk.cu", "distill.cu", "beam.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

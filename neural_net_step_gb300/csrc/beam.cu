@@ -1,0 +1,254 @@
+// Beam search: which (beam, token) pairs go on, and the reordering of the states
+// that belong to the beams.
+//
+// Selection.  total(w, c) = score_w + z_wc - logsumexp(z_w); a finished beam offers
+// its end token at its score.  Only the m best tokens of a beam can be among the m
+// best pairs: the top-k kernel (topk.cu) leaves them per beam with the row's
+// largest logit and sum of exponentials, and one block per batch entry merges the
+// lists.  Totals are formed and compared in 64 bits: scores of -50 leave an fp32
+// sum a step of 4e-6, which would make equals of tokens of different beams.
+//
+// Reordering.  Bound by DRAM.  A thread owns a column of all beams: it reads the
+// columns of the parents and then writes, so that source and destination may be
+// the same memory, and rows that stay are not written there.
+#include <stdio.h>
+
+#include <algorithm>
+
+#include "logits.cuh"
+#include "ops.h"
+
+namespace mlpk {
+
+namespace {
+
+using namespace lg;
+
+constexpr int kMaxBeams = 32;
+constexpr int kMaxOut = 64;
+
+struct BeamMergeParams {
+  const uint64_t* entries; const float2* stats;   // [batch * beams][per], [batch * beams]
+  const float* scores; const uint8_t* done;
+  int beams, C, m, per, eos;                      // per = min(m, C) entries of a beam
+  float* scores_out; int32_t* parents; int32_t* tokens; uint8_t* done_out;
+};
+
+// Order of totals as unsigned integers; NaN is 0, below -infinity.
+__device__ __forceinline__ uint64_t total_key(double t) {
+  const uint64_t u = (uint64_t)__double_as_longlong(t + 0.0);
+  const uint64_t k = (u >> 63) ? ~u : (u | 0x8000000000000000ull);
+  return t == t ? k : 0ull;
+}
+__device__ __forceinline__ double total_of(uint64_t k) {
+  const uint64_t u = (k >> 63) ? (k & 0x7FFFFFFFFFFFFFFFull) : ~k;
+  return __longlong_as_double(k ? (long long)u : 0x7FF8000000000000ll);
+}
+
+// Pairs of equal totals go by beam, then by their place in the beam's list.
+__global__ void __launch_bounds__(256) beam_merge_kernel(const __grid_constant__ BeamMergeParams p) {
+  pdl_enter();
+  extern __shared__ __align__(16) unsigned char smem[];
+  uint64_t* keys = reinterpret_cast<uint64_t*>(smem);                     // [beams][per], descending
+  int* toks = reinterpret_cast<int*>(keys + p.beams * p.per);
+  __shared__ double base[kMaxBeams];   // what a beam's logits are added to
+  __shared__ int kind[kMaxBeams];      // 0: base + logit; 1: every token at base; 2: finished
+  const int tid = threadIdx.x;
+  const int64_t r0 = (int64_t)blockIdx.x * p.beams;
+  if (tid < p.beams) {
+    const float score = p.scores[r0 + tid];
+    double b = (double)score;
+    int k = 0;
+    if (p.done && p.done[r0 + tid]) {
+      k = 2;
+    } else if (!(fabsf(score) < INFINITY)) {
+      k = 1;
+      if (!(score < 0.f)) b = __longlong_as_double(0x7FF8000000000000ll);
+    } else {
+      const float2 st = p.stats[r0 + tid];
+      if (st.x == -INFINITY && !(st.y != 0.f)) {   // nothing but -infinity
+        k = 1;
+        b = -(double)INFINITY;
+      } else {
+        b -= (double)st.x + log((double)st.y);
+        if (!(st.x < INFINITY) || !(b == b)) {
+          k = 1;
+          b = __longlong_as_double(0x7FF8000000000000ll);
+        }
+      }
+    }
+    base[tid] = b;
+    kind[tid] = k;
+  }
+  __syncthreads();
+  const int all = p.beams * p.per;
+  for (int a = tid; a < all; a += blockDim.x) {
+    const int w = a / p.per, j = a - w * p.per;
+    uint64_t key;
+    int tok;
+    if (kind[w] == 0) {
+      const uint64_t e = p.entries[(r0 + w) * p.per + j];
+      tok = entry_col(e);
+      key = total_key(base[w] + (double)value_of(entry_key(e)));
+    } else if (kind[w] == 1) {
+      tok = j;
+      key = total_key(base[w]);
+    } else {   // the end token, then the others in order, at -infinity
+      tok = j == 0 ? p.eos : j - 1 + (j - 1 >= p.eos);
+      key = total_key(j == 0 ? base[w] : -(double)INFINITY);
+    }
+    keys[a] = key;
+    toks[a] = tok;
+  }
+  __syncthreads();
+  for (int a = tid; a < all; a += blockDim.x) {
+    const int w = a / p.per;
+    const uint64_t key = keys[a];
+    int place = a - w * p.per;
+    for (int o = 0; o < p.beams; ++o) {
+      if (o == w) continue;
+      const uint64_t* l = keys + o * p.per;   // those before this pair: larger, or equal of a lower beam
+      int lo = 0, hi = p.per;
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (l[mid] > key || (l[mid] == key && o < w)) lo = mid + 1;
+        else hi = mid;
+      }
+      place += lo;
+    }
+    if (place < p.m) {
+      const int64_t at = (int64_t)blockIdx.x * p.m + place;
+      p.scores_out[at] = (float)total_of(key);
+      p.parents[at] = w;
+      p.tokens[at] = toks[a];
+      if (p.done_out) p.done_out[at] = (kind[w] == 2 || toks[a] == p.eos) ? 1 : 0;
+    }
+  }
+}
+
+struct ReorderParams {
+  const unsigned char* src; int64_t src_pitch, src_plane;
+  unsigned char* dst; int64_t dst_pitch, dst_plane;
+  const int32_t* parents; int64_t ldp;
+  int batch, beams_in, beams_out;
+  int64_t units;                // of U bytes in a row
+  int64_t chunks;               // blocks along a row
+  uint32_t* err;
+};
+
+// One block: blockDim.x units of all beams of one batch entry in one plane.
+template <typename U, int W>
+__global__ void __launch_bounds__(256) beam_reorder_kernel(const __grid_constant__ ReorderParams p) {
+  pdl_enter();
+  __shared__ int from[W];
+  const int64_t row = blockIdx.x / p.chunks, chunk = blockIdx.x - row * p.chunks;   // row: (plane, batch entry)
+  const int64_t plane = row / p.batch, b = row - plane * p.batch;
+  if (threadIdx.x < W) {
+    int f = -1;
+    if ((int)threadIdx.x < p.beams_out) {
+      f = p.parents[b * p.ldp + threadIdx.x];
+      if (f < 0 || f >= p.beams_in) {
+        if (p.err && plane == 0 && chunk == 0) atomicOr(p.err, ERRBIT_LABEL_RANGE);
+        f = -1;
+      }
+      if (p.dst == p.src && f == (int)threadIdx.x) f = -1;   // (stays)
+    }
+    from[threadIdx.x] = f;
+  }
+  __syncthreads();
+  const unsigned char* src = p.src + plane * p.src_plane + b * p.beams_in * p.src_pitch;
+  unsigned char* dst = p.dst + plane * p.dst_plane + b * p.beams_out * p.dst_pitch;
+  const int64_t u = chunk * blockDim.x + threadIdx.x;
+  if (u >= p.units) return;
+  U v[W];
+#pragma unroll
+  for (int i = 0; i < W; ++i)
+    if (from[i] >= 0) v[i] = *reinterpret_cast<const U*>(src + from[i] * p.src_pitch + u * (int64_t)sizeof(U));
+#pragma unroll
+  for (int i = 0; i < W; ++i)
+    if (from[i] >= 0) *reinterpret_cast<U*>(dst + i * p.dst_pitch + u * (int64_t)sizeof(U)) = v[i];
+}
+
+template <typename U>
+const void* reorder_func(int W) {
+  if (W <= 4) return (const void*)beam_reorder_kernel<U, 4>;
+  if (W <= 8) return (const void*)beam_reorder_kernel<U, 8>;
+  if (W <= 16) return (const void*)beam_reorder_kernel<U, 16>;
+  return (const void*)beam_reorder_kernel<U, 32>;
+}
+
+}  // namespace
+
+size_t beam_select_workspace(int64_t batch, int64_t beams, int64_t C, int64_t m) {
+  if (batch < 1 || beams < 1 || beams > kMaxBeams || C < 1 || C > kMaxC || m < 1 || m > kMaxOut || m > beams * C ||
+      batch > INT32_MAX / beams)
+    return 0;
+  return (size_t)(batch * beams) * (8 * (size_t)std::min(m, C) + 8);
+}
+
+int beam_select_plan(const BeamSelectOp& op, LaunchRec* recs, char* err, size_t errlen) {
+  if (beam_select_workspace(op.batch, op.beams, op.C, op.m) == 0 || op.ldz < op.C) {
+    snprintf(err, errlen, "beam_select: bad shape batch=%lld beams=%lld C=%lld m=%lld or leading dimension",
+             (long long)op.batch, (long long)op.beams, (long long)op.C, (long long)op.m);
+    return -1;
+  }
+  const int per = (int)std::min(op.m, op.C);
+  const int64_t rows = op.batch * op.beams;
+  uint64_t* entries = reinterpret_cast<uint64_t*>(op.ws);
+  float* stats = reinterpret_cast<float*>(entries + rows * per);
+  beam_rows_plan(op, per, entries, stats, &recs[0]);
+  BeamMergeParams p{};
+  p.entries = entries; p.stats = reinterpret_cast<const float2*>(stats);
+  p.scores = op.scores; p.done = op.done;
+  p.beams = (int)op.beams; p.C = (int)op.C; p.m = (int)op.m; p.per = per; p.eos = op.eos;
+  p.scores_out = op.scores_out; p.parents = op.parents; p.tokens = op.tokens; p.done_out = op.done_out;
+  recs[1].func = (const void*)beam_merge_kernel;
+  recs[1].grid = dim3((unsigned)op.batch);
+  recs[1].block = dim3(p.beams * per <= 64 ? 64 : p.beams * per <= 128 ? 128 : 256);
+  recs[1].smem = (unsigned)(p.beams * per * 12);
+  recs[1].name = "beam_merge";
+  recs[1].set_args(p);
+  return 2;
+}
+
+int beam_reorder_plan(const BeamReorderOp& op, LaunchRec* rec, char* err, size_t errlen) {
+  const auto bad = [&](const char* what) {
+    snprintf(err, errlen, "beam_reorder: %s", what);
+    return -1;
+  };
+  if (op.planes < 1 || op.batch < 1 || op.beams_in < 1 || op.beams_out < 1 || op.beams_in > kMaxBeams ||
+      op.beams_out > kMaxBeams || op.row_bytes < 1 || op.batch > INT32_MAX)
+    return bad("bad shape");
+  if (op.ldp < op.beams_out || op.src_pitch < op.row_bytes || op.dst_pitch < op.row_bytes)
+    return bad("pitch too small");
+  if (op.src == op.dst &&
+      (op.beams_in != op.beams_out || op.src_pitch != op.dst_pitch || (op.planes > 1 && op.src_plane != op.dst_plane)))
+    return bad("in place, source and destination have the same layout");
+  const uint64_t any = (uint64_t)(uintptr_t)op.src | (uint64_t)(uintptr_t)op.dst | (uint64_t)op.src_pitch |
+                       (uint64_t)op.dst_pitch | (uint64_t)op.row_bytes |
+                       (op.planes > 1 ? (uint64_t)op.src_plane | (uint64_t)op.dst_plane : 0);
+  // a thread's units stay in registers: 16 bytes for up to 8 beams, 8 for up to 16, 4 beyond
+  const int W = (int)op.beams_out;
+  const int widest = W <= 8 ? 16 : W <= 16 ? 8 : 4;
+  const int ub = any % 16 == 0 && widest == 16 ? 16 : any % 8 == 0 && widest >= 8 ? 8 : any % 4 == 0 ? 4 : any % 2 == 0 ? 2 : 1;
+  ReorderParams p{};
+  p.src = static_cast<const unsigned char*>(op.src); p.src_pitch = op.src_pitch; p.src_plane = op.src_plane;
+  p.dst = static_cast<unsigned char*>(op.dst); p.dst_pitch = op.dst_pitch; p.dst_plane = op.dst_plane;
+  p.parents = op.parents; p.ldp = op.ldp;
+  p.batch = (int)op.batch; p.beams_in = (int)op.beams_in; p.beams_out = W;
+  p.units = op.row_bytes / ub;
+  p.err = op.err;
+  const int threads = p.units >= 256 ? 256 : p.units >= 128 ? 128 : 64;
+  p.chunks = ceil_div(p.units, threads);
+  if (op.planes > INT32_MAX / op.batch || p.chunks > INT32_MAX / (op.planes * op.batch)) return bad("too many bytes");
+  rec->grid = dim3((unsigned)(op.planes * op.batch * p.chunks));
+  rec->block = dim3((unsigned)threads);
+  rec->smem = 0;
+  rec->func = ub == 16 ? reorder_func<uint4>(W) : ub == 8 ? reorder_func<uint2>(W) : ub == 4 ? reorder_func<uint32_t>(W)
+              : ub == 2 ? reorder_func<uint16_t>(W) : reorder_func<uint8_t>(W);
+  rec->name = "beam_reorder";
+  rec->set_args(p);
+  return 1;
+}
+
+}  // namespace mlpk

@@ -1,0 +1,322 @@
+// Distillation from a teacher's top logits: the loss of every row and its
+// gradient, hard labels besides where they are given.
+//
+// The teacher keeps k logits t_j of a row with their columns i_j, and the log of
+// what its other columns add up to, r = log sum_{others} exp(t / T).  With
+//   L = log(sum_j exp(t_j / T) + exp(r)),  p_j = exp(t_j / T - L),  p_r = exp(r - L),
+//   q = softmax(z / T),  R = sum of q over the columns that are no i_j:
+//   KD = sum_j p_j log(p_j / q_{i_j}) + p_r log(p_r / R),  CE = logsumexp(z) - z_y,
+//   loss = w (a CE + b KD),
+//   dz_i = w g (a (softmax(z)_i - [i = y]) + (b / T) (q_i - p_j             at i = i_j,
+//                                                      q_i (1 - p_r / R)    elsewhere)).
+//
+// Bound by DRAM: the row is read once into shared memory, becomes its gradient
+// there, and leaves by one bulk copy.  The k columns are taken out first (what
+// stays in their place is -infinity), so the others' sum needs no subtraction,
+// the pass over the row needs no test, and 1 - p_r / R is exact to fp32 however
+// small R is; the k gradients are written over the row's before it leaves.  All
+// logarithms are of ratios of sums, so that a student that is nearly its teacher
+// has a nearly exact small loss.
+#include <stdio.h>
+
+#include <algorithm>
+
+#include "logits.cuh"
+#include "ops.h"
+
+namespace mlpk {
+
+namespace {
+
+using namespace lg;
+
+struct DistillParams {
+  const void* z; int64_t ldz;
+  void* dz; int64_t lddz;           // nullable
+  const float* tv; int64_t ldtv;
+  const int32_t* ti; int64_t ldti;
+  const float* tail;                // nullable: nothing else
+  const int32_t* labels;            // nullable: a is 0
+  const float* w;                   // nullable: 1
+  float* loss;
+  int C, k, per;
+  float T, inv_T, c, a, b, g;       // c: log2(e) / T
+  uint32_t* err;
+};
+
+// What a block knows of its slice's columns besides the k.
+struct DistillPart {
+  float most, sum, sum1;            // largest, sums of exp((z - most) / T) and exp(z - most)
+  uint32_t bad;
+};
+struct DistillShared {
+  float red[10][16];
+  DistillPart part[8];
+  float zy;
+};
+
+template <typename T> struct BitsOf { typedef uint32_t type; };
+template <> struct BitsOf<__nv_bfloat16> { typedef uint16_t type; };
+
+// Zeros over a block's slice of the gradient: 16 bytes at a time but at its ends.
+template <typename T>
+__device__ __forceinline__ void clear(T* dz, int n) {
+  constexpr int E = kPer16<T>;
+  const int head = min(n, (int)((16 - ((uintptr_t)dz & 15)) & 15) / (int)sizeof(T)), units = (n - head) / E;
+  for (int v = threadIdx.x; v < units; v += blockDim.x) reinterpret_cast<uint4*>(dz + head)[v] = make_uint4(0, 0, 0, 0);
+  for (int i = threadIdx.x; i < head; i += blockDim.x) dz[i] = from_f32<T>(0.f);
+  for (int i = head + units * E + threadIdx.x; i < n; i += blockDim.x) dz[i] = from_f32<T>(0.f);
+}
+
+// TWO: the hard labels' softmax is at another temperature than the soft ones'.
+template <typename T, bool CLUSTER, bool TWO>
+__global__ void __launch_bounds__(512) distill_kernel(const __grid_constant__ DistillParams p) {
+  pdl_enter();
+  constexpr int E = kPer16<T>;
+  typedef typename BitsOf<T>::type Bits;
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ DistillShared sh;
+  const int tid = threadIdx.x, NT = blockDim.x;
+  const int64_t row = blockIdx.x;
+  const int rank = CLUSTER ? (int)blockIdx.z : 0, blocks = CLUSTER ? (int)gridDim.z : 1;
+  const int lo = rank * p.per, n = max(0, min(p.per, p.C - lo));
+  T* dz = p.dz ? reinterpret_cast<T*>(p.dz) + row * p.lddz + lo : nullptr;
+  const float w = p.w ? p.w[row] : 1.f;
+  if (w == 0.f) {   // a row that does not count, whatever it holds
+    if (dz) clear(dz, n);
+    if (rank == 0 && tid == 0) p.loss[row] = 0.f;
+    return;
+  }
+
+  float* zt = reinterpret_cast<float*>(smem);   // [k] the student's logits at the teacher's columns
+  unsigned char* buf = smem + (p.k * 4 + 15) / 16 * 16;
+  const bool mine = tid < p.k;                  // (at least k threads)
+  if (mine) zt[tid] = -INFINITY;
+  if (CLUSTER) cluster_arrive();
+  Slice<T> s;
+  s.load(buf, reinterpret_cast<const T*>(p.z) + row * p.ldz, lo, n);
+
+  // ---- the teacher, while the row is on its way
+  int col = -1;
+  float t = -INFINITY;
+  bool bad = false;
+  if (mine) {
+    col = p.ti[row * p.ldti + tid];
+    bad = col < -1 || col >= p.C;
+    if (col >= 0) t = p.tv[row * p.ldtv + tid];
+  }
+  const int y = p.labels ? p.labels[row] : -1;
+  if (p.labels) bad |= y < 0 || y >= p.C;
+  const float tm = block_max(t, sh.red[0]);
+  const float tail = p.tail ? p.tail[row] : -INFINITY;
+  const float tm0 = tm > -INFINITY ? tm : 0.f;
+  float tref = fmaxf(tm * p.inv_T, tail);
+  if (!(tref > -INFINITY)) tref = 0.f;
+  const float dl = tm0 * p.inv_T - tref;        // what the largest is below the reference
+  const float pe = mine ? expf((t - tm0) / p.T + dl) : 0.f;
+  const float U = expf(tail - tref);
+  const float St = block_sum(pe, sh.red[1]) + U;
+  const bool has = !(St == 0.f);
+
+  // ---- the k columns out of the row
+  copies_wait();
+  const int own = col - lo;
+  const bool here = mine && col >= 0 && own >= 0 && own < n;
+  const bool label_here = p.labels && y >= lo && y < lo + n;
+  const bool label_in_top = __syncthreads_or(mine && col >= 0 && col == y) != 0;   // (and the row is there)
+  float ztj = -INFINITY;
+  if (here) ztj = to_f32(s.at(own));
+  if (label_here && tid == 0) sh.zy = to_f32(s.at(y - lo));
+  __syncthreads();
+  if (here) reinterpret_cast<Bits*>(s.elems())[s.ph + own] = (Bits)tid;
+  __syncthreads();
+  bad |= here && reinterpret_cast<Bits*>(s.elems())[s.ph + own] != (Bits)tid;   // a column given twice
+  bad = __syncthreads_or(bad) != 0;
+  if (here) s.at(own) = minus_inf<T>();
+  __syncthreads();
+
+  // ---- the sums over the others
+  float most = -INFINITY;
+  for (int v = tid; v < s.nvec; v += NT) most = fmaxf(most, unit_max<T>(s.units()[v]));
+  most = block_max(most, sh.red[2]);
+  float sum = 0.f, sum1 = 0.f;
+  {
+    const float ref = most > -INFINITY ? most : 0.f;
+    for (int v = tid; v < s.nvec; v += NT) {
+      float x[E];
+      unit_floats<T>(s.units()[v], x);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float d = x[e] - ref;
+        sum += ex2(d * p.c);
+        if constexpr (TWO) sum1 += ex2(d * kLog2e);
+      }
+    }
+  }
+  sum = block_sum(sum, sh.red[3]);
+  if constexpr (TWO) sum1 = block_sum(sum1, sh.red[4]);
+
+  // ---- all slices together
+  float zy = 0.f;
+  if (CLUSTER) {
+    cluster_wait();   // (every block of the cluster runs and has cleared its zt)
+    for (int b = 0; b < blocks; ++b) {
+      if (here) put32(in_block(smem_addr(zt + tid), b), __float_as_uint(ztj));
+      if (tid == 0) {
+        const uint32_t to = in_block(smem_addr(&sh.part[rank]), b);
+        put32(to, __float_as_uint(most));
+        put32(to + 4, __float_as_uint(sum));
+        put32(to + 8, __float_as_uint(sum1));
+        put32(to + 12, bad);
+        if (label_here) put32(in_block(smem_addr(&sh.zy), b), __float_as_uint(sh.zy));
+      }
+    }
+    cluster_arrive();
+    cluster_wait();
+    most = -INFINITY;
+    for (int b = 0; b < blocks; ++b) {
+      most = fmaxf(most, sh.part[b].most);
+      bad |= sh.part[b].bad != 0;
+    }
+    const float ref = most > -INFINITY ? most : 0.f;
+    sum = sum1 = 0.f;
+    for (int b = 0; b < blocks; ++b) {
+      const DistillPart q = sh.part[b];
+      const float d = (q.most > -INFINITY ? q.most : 0.f) - ref;
+      if (q.sum != 0.f) sum += q.sum * ex2(d * p.c);
+      if (TWO && q.sum1 != 0.f) sum1 += q.sum1 * ex2(d * kLog2e);
+    }
+    if (mine) ztj = zt[tid];
+  }
+  if (p.labels) zy = sh.zy;
+  if (bad) {
+    if (dz) clear(dz, n);
+    if (rank == 0 && tid == 0) {
+      p.loss[row] = 0.f;
+      if (p.err) atomicOr(p.err, ERRBIT_LABEL_RANGE);
+    }
+    return;
+  }
+  const float rest = most > -INFINITY ? most : 0.f;   // the others' exponents are relative to this
+  const float m = fmaxf(most, block_max(mine ? ztj : -INFINITY, sh.red[5]));
+  const float m0 = m > -INFINITY ? m : 0.f;
+  const float q = mine ? expf((ztj - m0) / p.T) : 0.f;
+  const float f = sum != 0.f ? ex2((rest - m0) * p.c) : 0.f;
+  const float S = fmaf(sum, f, block_sum(q, sh.red[6]));
+  float q1 = q, f1 = f, S1 = S;
+  if constexpr (TWO) {
+    q1 = mine ? expf(ztj - m0) : 0.f;
+    f1 = sum1 != 0.f ? ex2((rest - m0) * kLog2e) : 0.f;
+    S1 = fmaf(sum1, f1, block_sum(q1, sh.red[7]));
+  }
+  const float pj = has ? pe / St : 0.f, pr = has ? U / St : 0.f;
+
+  if (rank == 0) {
+    float kd = 0.f;
+    if (has && p.b != 0.f) {
+      const float ln = logf(St / S);
+      if (mine && !(pj == 0.f)) kd = pj * (((t - ztj) - (tm0 - m0)) / p.T + dl - ln);
+      kd = block_sum(kd, sh.red[8]);
+      const float R = sum * f / S;
+      if (!(pr == 0.f))
+        kd += pr * (R > 1e-30f ? logf(pr / R) : logf(pr) - ((rest - m0) / p.T + logf(sum) - logf(S)));
+      kd *= p.b;
+    }
+    if (tid == 0) p.loss[row] = w * (kd + (p.labels ? p.a * (logf(S1) + (m0 - zy)) : 0.f));
+  }
+  if (!dz) return;
+
+  // ---- the gradient, in the row's place
+  const float wg = w * p.g, kb = has ? wg * p.b * p.inv_T : 0.f, ka = p.labels ? wg * p.a : 0.f;
+  float A = sum == 0.f ? 0.f : kb * (f / S - pr / sum);
+  const float A1 = sum1 == 0.f && TWO ? 0.f : ka * (f1 / S1);
+  if constexpr (!TWO) A += p.labels ? A1 : 0.f;
+  const auto grad = [&](float x) {
+    const float d = x - rest;
+    float r = ex2(d * p.c) * A;
+    if constexpr (TWO) r = fmaf(ex2(d * kLog2e), A1, r);
+    return r;
+  };
+  for (int v = tid; v < s.nvec; v += NT) {
+    float x[E];
+    unit_floats<T>(s.units()[v], x);
+    uint32_t o[4];
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      if constexpr (sizeof(T) == 4) {
+        o[h] = __float_as_uint(grad(x[h]));
+      } else {
+        const __nv_bfloat162 b2 = __floats2bfloat162_rn(grad(x[2 * h]), grad(x[2 * h + 1]));
+        o[h] = *reinterpret_cast<const uint32_t*>(&b2);
+      }
+    }
+    s.units()[v] = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+  __syncthreads();
+  if (here) {
+    float r = kb * (q / S - pj);
+    if (p.labels) r += ka * (q1 / S1 - (col == y ? 1.f : 0.f));
+    s.at(own) = from_f32<T>(r);
+  }
+  if (label_here && !label_in_top && tid == 0) s.at(y - lo) = from_f32<T>(grad(zy) - ka);
+
+  // ---- and out
+  if ((((uintptr_t)dz) & 15) / sizeof(T) == (unsigned)s.ph) {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncthreads();
+    const int v0 = s.ph > 0 ? 1 : 0, v1 = (s.ph + n) / E;   // the whole units
+    if (tid == 0 && v1 > v0) {
+      asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dz - s.ph + v0 * E),
+                   "r"(smem_addr(s.units() + v0)), "r"((v1 - v0) * 16)
+                   : "memory");
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    }
+    if (tid < 2 * E) {   // the units that the slice only partly covers
+      const int i = tid < E ? tid - s.ph : max(v1, v0) * E + (tid - E) - s.ph;
+      if (i >= 0 && i < n && (tid < E ? v0 == 1 : true) && !(tid >= E && v1 < v0)) dz[i] = s.at(i);
+    }
+    if (tid == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  } else {
+    __syncthreads();
+    for (int i = tid; i < n; i += NT) dz[i] = s.at(i);
+  }
+}
+
+template <typename T>
+const void* distill_func(bool cluster, bool two) {
+  if (cluster) return two ? (const void*)distill_kernel<T, true, true> : (const void*)distill_kernel<T, true, false>;
+  return two ? (const void*)distill_kernel<T, false, true> : (const void*)distill_kernel<T, false, false>;
+}
+
+}  // namespace
+
+int distill_plan(const DistillOp& op, LaunchRec* rec, char* err, size_t errlen) {
+  if (op.B < 1 || op.B > INT32_MAX || op.C < 1 || op.C > kMaxC || op.k < 1 || op.k > kMaxK || op.k > op.C ||
+      op.ldz < op.C || (op.dz && op.lddz < op.C) || op.ldtv < op.k || op.ldti < op.k) {
+    snprintf(err, errlen, "distill: bad shape B=%lld C=%lld k=%lld or leading dimension", (long long)op.B,
+             (long long)op.C, (long long)op.k);
+    return -1;
+  }
+  const int es = op.dtype == DT_F32 ? 4 : 2;
+  const Cut cut = cut_rows(op.B, op.C, es, (int)op.k);
+  DistillParams p{};
+  p.z = op.z; p.ldz = op.ldz; p.dz = op.dz; p.lddz = op.lddz;
+  p.tv = op.t_values; p.ldtv = op.ldtv; p.ti = op.t_indices; p.ldti = op.ldti; p.tail = op.t_tail;
+  p.labels = op.ce_weight != 0.f ? op.labels : nullptr; p.w = op.row_weights; p.loss = op.loss_rows;
+  p.C = (int)op.C; p.k = (int)op.k; p.per = cut.per;
+  p.T = op.temperature; p.inv_T = 1.f / op.temperature; p.c = kLog2e / op.temperature;
+  p.a = op.ce_weight; p.b = op.kd_weight; p.g = op.grad_scale;
+  p.err = op.err;
+  const bool two = p.labels && op.temperature != 1.f;
+  rec->grid = dim3((unsigned)op.B, 1, (unsigned)cut.cluster);
+  rec->block = dim3((unsigned)cut.threads);
+  rec->cluster = (unsigned)cut.cluster;
+  rec->smem = (unsigned)((op.k * 4 + 15) / 16 * 16 + slice_buffer(cut.per, es));
+  rec->func = op.dtype == DT_F32 ? distill_func<float>(cut.cluster > 1, two)
+                                 : distill_func<__nv_bfloat16>(cut.cluster > 1, two);
+  rec->name = "distill";
+  rec->set_args(p);
+  return 1;
+}
+
+}  // namespace mlpk

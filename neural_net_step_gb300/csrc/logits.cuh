@@ -1,0 +1,181 @@
+// A row of logits, or a slice of it, in shared memory: what the top-k,
+// distillation and beam kernels share.
+//
+// A row of C elements is cut into slices of `per` elements, one for each block
+// of a cluster.  The slice is copied in 16-byte units whatever the row's
+// alignment: shared memory keeps the row's phase (its address modulo 16), the
+// units that the row only partly covers are copied element by element, and
+// their other elements are -infinity, so that every pass runs over whole
+// units without tests.  A thread copies the units that it later reads first
+// (tid, tid + NT, ...) and need not wait for other threads to read them.
+#pragma once
+#include "common.cuh"
+
+namespace mlpk {
+namespace lg {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kSMs = 152;
+constexpr int kMaxK = 256;                 // entries kept of a row
+constexpr int kCand = 1024;                // candidates ranked at most
+constexpr int64_t kMaxC = 393216;          // columns: eight slices of 192 KB of fp32
+constexpr int64_t kSliceBytes = 72 * 1024; // a slice of at most this leaves room for three blocks on an SM
+
+// 2^t; subnormal results are flushed to zero (PTX ex2.approx).
+__device__ __forceinline__ float ex2(float t) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(t));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// The blocks of a cluster.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+__device__ __forceinline__ uint32_t in_block(uint32_t addr, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void put64(uint32_t addr, uint64_t v) {
+  asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
+__device__ __forceinline__ void put32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// Order of logits as unsigned integers: NaN is 0, below -infinity; -0 is +0.
+__device__ __forceinline__ uint32_t key_of(float f) {
+  const uint32_t u = __float_as_uint(f + 0.f);
+  const uint32_t k = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  return f == f ? k : 0u;
+}
+__device__ __forceinline__ float value_of(uint32_t k) {
+  const uint32_t u = (k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k;
+  return k ? __uint_as_float(u) : __uint_as_float(0x7FC00000u);
+}
+// A candidate: larger is better, lower column first among equals; 0 is none.
+__device__ __forceinline__ uint64_t entry_of(uint32_t key, int col) {
+  return ((uint64_t)key << 32) | (uint32_t)~col;
+}
+__device__ __forceinline__ int entry_col(uint64_t e) { return (int)~(uint32_t)e; }
+__device__ __forceinline__ uint32_t entry_key(uint64_t e) { return (uint32_t)(e >> 32); }
+
+template <typename T> constexpr int kPer16 = 16 / (int)sizeof(T);
+
+// The E elements of a unit as fp32.
+template <typename T>
+__device__ __forceinline__ void unit_floats(uint4 a, float (&v)[kPer16<T>]) {
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int h = 0; h < 4; ++h) {
+    if constexpr (sizeof(T) == 4) {
+      v[h] = __uint_as_float(w[h]);
+    } else {
+      v[2 * h] = __uint_as_float(w[h] << 16);
+      v[2 * h + 1] = __uint_as_float(w[h] & 0xFFFF0000u);
+    }
+  }
+}
+// Its largest element; NaN is passed over (-infinity where all are NaN).
+template <typename T>
+__device__ __forceinline__ float unit_max(uint4 a) {
+  if constexpr (sizeof(T) == 4) {
+    return fmaxf(fmaxf(fmaxf(__uint_as_float(a.x), __uint_as_float(a.y)), fmaxf(__uint_as_float(a.z), __uint_as_float(a.w))),
+                 -INFINITY);
+  } else {
+    const auto b = [](uint32_t w) { return *reinterpret_cast<__nv_bfloat162*>(&w); };
+    const __nv_bfloat162 m = __hmax2(__hmax2(b(a.x), b(a.y)), __hmax2(b(a.z), b(a.w)));
+    return fmaxf(fmaxf(__low2float(m), __high2float(m)), -INFINITY);
+  }
+}
+template <typename T> __device__ __forceinline__ T minus_inf();
+template <> __device__ __forceinline__ float minus_inf<float>() { return -INFINITY; }
+template <> __device__ __forceinline__ __nv_bfloat16 minus_inf<__nv_bfloat16>() { return __ushort_as_bfloat16(0xFF80); }
+
+// The slice [lo, lo + n) of a row as shared memory holds it: element i is at
+// elems()[ph + i], units() unit v holds the elements v E - ph .. + E.
+template <typename T>
+struct Slice {
+  unsigned char* buf;
+  int lo, n, ph, nvec;
+
+  __device__ __forceinline__ T* elems() const { return reinterpret_cast<T*>(buf); }
+  __device__ __forceinline__ uint4* units() const { return reinterpret_cast<uint4*>(buf); }
+  __device__ __forceinline__ T& at(int i) const { return elems()[ph + i]; }
+
+  // Starts the copies of this thread's units.
+  __device__ __forceinline__ void load(unsigned char* buf_, const T* row, int lo_, int n_) {
+    constexpr int E = kPer16<T>;
+    buf = buf_;
+    lo = lo_;
+    n = n_ > 0 ? n_ : 0;
+    const T* g = row + lo;
+    ph = (int)(((uintptr_t)g & 15) / sizeof(T));
+    nvec = n > 0 ? (ph + n + E - 1) / E : 0;
+    const unsigned char* g0 = reinterpret_cast<const unsigned char*>(g - ph);
+    const uint32_t s0 = smem_addr(buf);
+    for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
+      if (v * E >= ph && (v + 1) * E <= ph + n) {
+        copy16_async(s0 + 16u * v, g0 + 16ll * v);
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const int i = v * E + e - ph;
+          elems()[v * E + e] = i >= 0 && i < n ? g[i] : minus_inf<T>();
+        }
+      }
+    }
+  }
+  // f(i, value) for the elements of this thread's units.
+  template <typename F>
+  __device__ __forceinline__ void each(F f) const {
+    constexpr int E = kPer16<T>;
+    for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
+      float x[E];
+      unit_floats<T>(units()[v], x);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int i = v * E + e - ph;
+        if (i >= 0 && i < n) f(i, x[e]);
+      }
+    }
+  }
+};
+// Bytes of a slice's buffer (the phase can add a unit).
+inline int64_t slice_buffer(int64_t per, int es) { return (per * es + 15) / 16 * 16 + 16; }
+
+// Sums and maxima over the block, the same in every thread; red: one float a
+// warp and a place of its own for each call between two barriers.
+__device__ __forceinline__ float block_sum(float v, float* red) {
+  v = warp_sum(v);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  float s = 0.f;
+  for (int w = 0; w < (int)blockDim.x / 32; ++w) s += red[w];
+  return s;
+}
+__device__ __forceinline__ float block_max(float v, float* red) {
+  v = warp_max(v);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  float s = -INFINITY;
+  for (int w = 0; w < (int)blockDim.x / 32; ++w) s = fmaxf(s, red[w]);
+  return s;
+}
+
+// How rows are cut: `cluster` blocks of `threads` threads share a row, `per`
+// columns each.
+struct Cut {
+  int cluster, per, threads;
+};
+Cut cut_rows(int64_t rows, int64_t C, int es, int k);
+
+}  // namespace lg
+}  // namespace mlpk

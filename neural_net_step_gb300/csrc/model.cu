@@ -1347,11 +1347,18 @@ static mlp_status run_chain(LaunchRec* r, int n, void* stream) {
     cfg.blockDim = r[i].block;
     cfg.dynamicSmemBytes = r[i].smem;
     cfg.stream = (cudaStream_t)stream;
-    cudaLaunchAttribute a;
-    a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    a.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &a;
-    cfg.numAttrs = i > 0 ? 1 : 0;
+    cudaLaunchAttribute a[2];
+    memset(a, 0, sizeof(a));
+    if (i > 0) {
+      a[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      a[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (r[i].cluster > 1) {
+      a[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+      a[cfg.numAttrs].val.clusterDim.x = a[cfg.numAttrs].val.clusterDim.y = 1;
+      a[cfg.numAttrs++].val.clusterDim.z = r[i].cluster;
+    }
+    cfg.attrs = a;
     void* argp[1] = {r[i].args};
     cudaError_t e = allow_smem(r[i].func, r[i].smem);
     if (e == cudaSuccess) e = cudaLaunchKernelExC(&cfg, r[i].func, argp);
@@ -1369,6 +1376,8 @@ static bool elements_aligned(size_t es, std::initializer_list<const void*> ps) {
 static size_t dtype_bytes(int d) { return d == MLP_BF16 ? 2 : 4; }
 
 static bool dtype_ok(int d) { return d == MLP_F32 || d == MLP_BF16; }
+// (its inverse stays a normal fp32 number)
+static bool temperature_ok(float t) { return t >= 1e-6f && t <= 1e6f; }
 static bool gemm_dtype_ok(int d) { return d == MLP_F32 || d == MLP_BF16 || d == MLP_F32X3; }
 static bool act_ok(int a) { return a >= MLP_ACT_NONE && a <= MLP_ACT_GELU_TANH; }
 
@@ -1622,6 +1631,92 @@ mlp_status mlp_op_argmax(int dtype, int64_t B, int64_t C, const void* z, int64_t
   LaunchRec r;
   char e_[512] = "";
   if (argmax_plan(op, &r, e_, sizeof(e_)) < 0) return fail(MLP_ERR_SHAPE, "%s", e_);
+  return run_ops(&r, 1, stream);
+}
+
+mlp_status mlp_op_topk(int dtype, int64_t B, int64_t C, int64_t k, const void* z, int64_t ldz, float temperature,
+                       float* values, int64_t ldv, int32_t* indices, int64_t ldi, float* lse, float* tail,
+                       void* stream) {
+  if (!dtype_ok(dtype)) return fail(MLP_ERR_DTYPE, "bad dtype");
+  if (!z || !values || !indices) return fail(MLP_ERR_ARG, "null pointer");
+  if (!temperature_ok(temperature)) return fail(MLP_ERR_ARG, "temperature must lie between 1e-6 and 1e6");
+  if (!elements_aligned(dtype_bytes(dtype), {z}) || !elements_aligned(4, {values, indices, lse, tail}))
+    return fail(MLP_ERR_ARG, "misaligned elements");
+  TopkOp op;
+  op.dtype = dtype; op.B = B; op.C = C; op.k = k; op.z = z; op.ldz = ldz; op.temperature = temperature;
+  op.values = values; op.ldv = ldv; op.indices = indices; op.ldi = ldi; op.lse = lse; op.tail = tail;
+  LaunchRec r;
+  char e_[512] = "";
+  if (topk_plan(op, &r, e_, sizeof(e_)) < 0) return fail(MLP_ERR_SHAPE, "%s", e_);
+  return run_ops(&r, 1, stream);
+}
+
+mlp_status mlp_op_distill(int dtype, int64_t B, int64_t C, int64_t k, const void* z, int64_t ldz,
+                          const float* t_values, int64_t ldtv, const int32_t* t_indices, int64_t ldti,
+                          const float* t_tail, const int32_t* labels, const float* row_weights, float temperature,
+                          float ce_weight, float kd_weight, float grad_scale, void* dz, int64_t lddz,
+                          float* loss_rows, uint32_t* err_dev, void* stream) {
+  if (!dtype_ok(dtype)) return fail(MLP_ERR_DTYPE, "bad dtype");
+  if (!z || !t_values || !t_indices || !loss_rows) return fail(MLP_ERR_ARG, "null pointer");
+  if (!temperature_ok(temperature)) return fail(MLP_ERR_ARG, "temperature must lie between 1e-6 and 1e6");
+  if (!std::isfinite(ce_weight) || !std::isfinite(kd_weight) || !std::isfinite(grad_scale))
+    return fail(MLP_ERR_ARG, "weights must be finite");
+  if (ce_weight != 0.f && !labels) return fail(MLP_ERR_ARG, "ce_weight without labels");
+  if (!elements_aligned(dtype_bytes(dtype), {z, dz}) ||
+      !elements_aligned(4, {t_values, t_indices, t_tail, labels, row_weights, loss_rows, err_dev}))
+    return fail(MLP_ERR_ARG, "misaligned elements");
+  if (dz == z && lddz != ldz) return fail(MLP_ERR_ARG, "in place, dz has z's pitch");
+  DistillOp op;
+  op.dtype = dtype; op.B = B; op.C = C; op.k = k; op.z = z; op.ldz = ldz;
+  op.t_values = t_values; op.ldtv = ldtv; op.t_indices = t_indices; op.ldti = ldti; op.t_tail = t_tail;
+  op.labels = labels; op.row_weights = row_weights;
+  op.temperature = temperature; op.ce_weight = ce_weight; op.kd_weight = kd_weight; op.grad_scale = grad_scale;
+  op.dz = dz; op.lddz = lddz; op.loss_rows = loss_rows; op.err = err_dev;
+  LaunchRec r;
+  char e_[512] = "";
+  if (distill_plan(op, &r, e_, sizeof(e_)) < 0) return fail(MLP_ERR_SHAPE, "%s", e_);
+  return run_ops(&r, 1, stream);
+}
+
+size_t mlp_op_beam_select_workspace_bytes(int dtype, int64_t batch, int64_t beams, int64_t C, int64_t m) {
+  return dtype_ok(dtype) ? beam_select_workspace(batch, beams, C, m) : 0;
+}
+
+mlp_status mlp_op_beam_select(int dtype, int64_t batch, int64_t beams, int64_t C, int64_t m, const void* z,
+                              int64_t ldz, const float* scores, const uint8_t* done, int32_t eos, float* scores_out,
+                              int32_t* parents, int32_t* tokens, uint8_t* done_out, void* workspace, size_t ws_bytes,
+                              void* stream) {
+  if (!dtype_ok(dtype)) return fail(MLP_ERR_DTYPE, "bad dtype");
+  if (!z || !scores || !scores_out || !parents || !tokens) return fail(MLP_ERR_ARG, "null pointer");
+  if (done && (eos < 0 || eos >= C)) return fail(MLP_ERR_ARG, "finished beams need an end token in [0, C)");
+  if (!elements_aligned(dtype_bytes(dtype), {z}) || !elements_aligned(4, {scores, scores_out, parents, tokens}))
+    return fail(MLP_ERR_ARG, "misaligned elements");
+  BeamSelectOp op;
+  op.dtype = dtype; op.batch = batch; op.beams = beams; op.C = C; op.m = m; op.z = z; op.ldz = ldz;
+  op.scores = scores; op.done = done; op.eos = eos;
+  op.scores_out = scores_out; op.parents = parents; op.tokens = tokens; op.done_out = done_out; op.ws = workspace;
+  LaunchRec r[2];
+  char e_[512] = "";
+  if (beam_select_plan(op, r, e_, sizeof(e_)) < 0) return fail(MLP_ERR_SHAPE, "%s", e_);
+  if (!workspace || ws_bytes < beam_select_workspace(batch, beams, C, m))
+    return fail(MLP_ERR_ARG, "beam_select: workspace of %zu bytes is too small", ws_bytes);
+  if (!elements_aligned(8, {workspace})) return fail(MLP_ERR_ARG, "misaligned workspace");
+  return run_chain(r, 2, stream);
+}
+
+mlp_status mlp_op_beam_reorder(int64_t planes, int64_t batch, int64_t beams_in, int64_t beams_out, int64_t row_bytes,
+                               const void* src, int64_t src_pitch, int64_t src_plane, const int32_t* parents,
+                               int64_t ldp, void* dst, int64_t dst_pitch, int64_t dst_plane, uint32_t* err_dev,
+                               void* stream) {
+  if (!src || !dst || !parents) return fail(MLP_ERR_ARG, "null pointer");
+  if (!elements_aligned(4, {parents, err_dev})) return fail(MLP_ERR_ARG, "misaligned elements");
+  BeamReorderOp op;
+  op.planes = planes; op.batch = batch; op.beams_in = beams_in; op.beams_out = beams_out; op.row_bytes = row_bytes;
+  op.src = src; op.src_pitch = src_pitch; op.src_plane = src_plane; op.parents = parents; op.ldp = ldp;
+  op.dst = dst; op.dst_pitch = dst_pitch; op.dst_plane = dst_plane; op.err = err_dev;
+  LaunchRec r;
+  char e_[512] = "";
+  if (beam_reorder_plan(op, &r, e_, sizeof(e_)) < 0) return fail(MLP_ERR_SHAPE, "%s", e_);
   return run_ops(&r, 1, stream);
 }
 

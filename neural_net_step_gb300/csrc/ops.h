@@ -213,6 +213,61 @@ struct ArgmaxOp {
 };
 int argmax_plan(const ArgmaxOp& op, LaunchRec* rec, char* err, size_t errlen);
 
+// The k largest of every row with the log-sums of the row and of the rest
+// (topk.cu).
+struct TopkOp {
+  int dtype = 0;
+  int64_t B = 0, C = 0, k = 0;
+  const void* z = nullptr; int64_t ldz = 0;
+  float temperature = 1.f;
+  float* values = nullptr; int64_t ldv = 0;
+  int32_t* indices = nullptr; int64_t ldi = 0;
+  float* lse = nullptr; float* tail = nullptr;                 // nullable
+};
+int topk_plan(const TopkOp& op, LaunchRec* rec, char* err, size_t errlen);
+
+// Distillation from a teacher's top logits, forward and backward (distill.cu).
+struct DistillOp {
+  int dtype = 0;
+  int64_t B = 0, C = 0, k = 0;
+  const void* z = nullptr; int64_t ldz = 0;
+  const float* t_values = nullptr; int64_t ldtv = 0;
+  const int32_t* t_indices = nullptr; int64_t ldti = 0;
+  const float* t_tail = nullptr;                               // nullable
+  const int32_t* labels = nullptr;                             // nullable
+  const float* row_weights = nullptr;                          // nullable
+  float temperature = 1.f, ce_weight = 0.f, kd_weight = 1.f, grad_scale = 1.f;
+  void* dz = nullptr; int64_t lddz = 0;                        // nullable
+  float* loss_rows = nullptr;
+  uint32_t* err = nullptr;
+};
+int distill_plan(const DistillOp& op, LaunchRec* rec, char* err, size_t errlen);
+
+// Beam search (beam.cu): the selection is two records, the rows' best entries
+// (topk.cu) and their merge, joined by the workspace.
+struct BeamSelectOp {
+  int dtype = 0;
+  int64_t batch = 0, beams = 0, C = 0, m = 0;
+  const void* z = nullptr; int64_t ldz = 0;
+  const float* scores = nullptr;
+  const uint8_t* done = nullptr;                               // nullable
+  int eos = -1;
+  float* scores_out = nullptr; int32_t* parents = nullptr; int32_t* tokens = nullptr;
+  uint8_t* done_out = nullptr;                                 // nullable
+  void* ws = nullptr;
+};
+size_t beam_select_workspace(int64_t batch, int64_t beams, int64_t C, int64_t m);   // 0: a shape not taken
+int beam_select_plan(const BeamSelectOp& op, LaunchRec* recs, char* err, size_t errlen);
+int beam_rows_plan(const BeamSelectOp& op, int entries, uint64_t* lists, float* stats, LaunchRec* rec);
+struct BeamReorderOp {
+  int64_t planes = 0, batch = 0, beams_in = 0, beams_out = 0, row_bytes = 0;
+  const void* src = nullptr; int64_t src_pitch = 0, src_plane = 0;   // bytes
+  const int32_t* parents = nullptr; int64_t ldp = 0;
+  void* dst = nullptr; int64_t dst_pitch = 0, dst_plane = 0;
+  uint32_t* err = nullptr;
+};
+int beam_reorder_plan(const BeamReorderOp& op, LaunchRec* rec, char* err, size_t errlen);
+
 // Copy rows of a padded [B, ld] matrix into a dense [B, C] one.
 struct CopyRowsOp {
   int dtype = 0;
