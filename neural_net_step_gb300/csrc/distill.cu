@@ -14,9 +14,12 @@
 // there, and leaves by one bulk copy.  The k columns are taken out first (what
 // stays in their place is -infinity), so the others' sum needs no subtraction,
 // the pass over the row needs no test, and 1 - p_r / R is exact to fp32 however
-// small R is; the k gradients are written over the row's before it leaves.  All
-// logarithms are of ratios of sums, so that a student that is nearly its teacher
-// has a nearly exact small loss.
+// small R is; the k gradients are written over the row's before it leaves.
+//
+// Near the teacher KD is a small difference of large terms.  It is summed as
+//   KD = sum over the k columns and the rest of  p log(p / q) - p + q,
+// which is the same (both distributions add up to 1), and of which every term is
+// positive and as exact as its p / q.
 #include <stdio.h>
 
 #include <algorithm>
@@ -50,7 +53,7 @@ struct DistillPart {
   uint32_t bad;
 };
 struct DistillShared {
-  float red[10][16];
+  Red red[9];
   DistillPart part[8];
   float zy;
 };
@@ -66,6 +69,20 @@ __device__ __forceinline__ void clear(T* dz, int n) {
   for (int v = threadIdx.x; v < units; v += blockDim.x) reinterpret_cast<uint4*>(dz + head)[v] = make_uint4(0, 0, 0, 0);
   for (int i = threadIdx.x; i < head; i += blockDim.x) dz[i] = from_f32<T>(0.f);
   for (int i = head + units * E + threadIdx.x; i < n; i += blockDim.x) dz[i] = from_f32<T>(0.f);
+}
+
+// p log(p / q) - p + q for r = log(p / q): p (r - 1 + e^-r), for small r by its
+// series (the terms left out are below 2^-24 of it at 1/2).
+__device__ __forceinline__ float divergence(float p, float q, float r) {
+  if (p == 0.f) return q;
+  if (!(fabsf(r) < 0.5f)) return fmaf(p, r - 1.f, q);
+  float h = fmaf(r, 1.f / 40320.f, -1.f / 5040.f);
+  h = fmaf(r, h, 1.f / 720.f);
+  h = fmaf(r, h, -1.f / 120.f);
+  h = fmaf(r, h, 1.f / 24.f);
+  h = fmaf(r, h, -1.f / 6.f);
+  h = fmaf(r, h, 0.5f);
+  return p * (r * r) * h;
 }
 
 // TWO: the hard labels' softmax is at another temperature than the soft ones'.
@@ -110,9 +127,9 @@ __global__ void __launch_bounds__(512) distill_kernel(const __grid_constant__ Di
   const float tm = block_max(t, sh.red[0]);
   const float tail = p.tail ? p.tail[row] : -INFINITY;
   const float tm0 = tm > -INFINITY ? tm : 0.f;
-  float tref = fmaxf(tm * p.inv_T, tail);
+  float tref = fmaxf(tm / p.T, tail);
   if (!(tref > -INFINITY)) tref = 0.f;
-  const float dl = tm0 * p.inv_T - tref;        // what the largest is below the reference
+  const float dl = tm0 / p.T - tref;            // what the largest is below the reference
   const float pe = mine ? expf((t - tm0) / p.T + dl) : 0.f;
   const float U = expf(tail - tref);
   const float St = block_sum(pe, sh.red[1]) + U;
@@ -136,25 +153,10 @@ __global__ void __launch_bounds__(512) distill_kernel(const __grid_constant__ Di
   __syncthreads();
 
   // ---- the sums over the others
-  float most = -INFINITY;
-  for (int v = tid; v < s.nvec; v += NT) most = fmaxf(most, unit_max<T>(s.units()[v]));
-  most = block_max(most, sh.red[2]);
-  float sum = 0.f, sum1 = 0.f;
-  {
-    const float ref = most > -INFINITY ? most : 0.f;
-    for (int v = tid; v < s.nvec; v += NT) {
-      float x[E];
-      unit_floats<T>(s.units()[v], x);
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float d = x[e] - ref;
-        sum += ex2(d * p.c);
-        if constexpr (TWO) sum1 += ex2(d * kLog2e);
-      }
-    }
-  }
-  sum = block_sum(sum, sh.red[3]);
-  if constexpr (TWO) sum1 = block_sum(sum1, sh.red[4]);
+  float most = block_max(max_of(s), sh.red[2]);
+  const float ref = most > -INFINITY ? most : 0.f;
+  float sum = block_sum(sum_exp(s, Exponent(ref, p.c)), sh.red[3]), sum1 = 0.f;
+  if constexpr (TWO) sum1 = block_sum(sum_exp(s, Exponent(ref, kLog2e)), sh.red[4]);
 
   // ---- all slices together
   float zy = 0.f;
@@ -173,16 +175,16 @@ __global__ void __launch_bounds__(512) distill_kernel(const __grid_constant__ Di
     }
     cluster_arrive();
     cluster_wait();
-    most = -INFINITY;
+    most = -INFINITY;   // (of all slices from here on)
     for (int b = 0; b < blocks; ++b) {
       most = fmaxf(most, sh.part[b].most);
       bad |= sh.part[b].bad != 0;
     }
-    const float ref = most > -INFINITY ? most : 0.f;
+    const float all = most > -INFINITY ? most : 0.f;
     sum = sum1 = 0.f;
     for (int b = 0; b < blocks; ++b) {
       const DistillPart q = sh.part[b];
-      const float d = (q.most > -INFINITY ? q.most : 0.f) - ref;
+      const float d = (q.most > -INFINITY ? q.most : 0.f) - all;
       if (q.sum != 0.f) sum += q.sum * ex2(d * p.c);
       if (TWO && q.sum1 != 0.f) sum1 += q.sum1 * ex2(d * kLog2e);
     }
@@ -214,12 +216,10 @@ __global__ void __launch_bounds__(512) distill_kernel(const __grid_constant__ Di
   if (rank == 0) {
     float kd = 0.f;
     if (has && p.b != 0.f) {
-      const float ln = logf(St / S);
-      if (mine && !(pj == 0.f)) kd = pj * (((t - ztj) - (tm0 - m0)) / p.T + dl - ln);
+      const float ln = logf(St / S), R = sum * f / S;
+      if (mine && col >= 0) kd = divergence(pj, q / S, ((t - ztj) - (tm0 - m0)) / p.T + dl - ln);
       kd = block_sum(kd, sh.red[8]);
-      const float R = sum * f / S;
-      if (!(pr == 0.f))
-        kd += pr * (R > 1e-30f ? logf(pr / R) : logf(pr) - ((rest - m0) / p.T + logf(sum) - logf(S)));
+      kd += divergence(pr, R, R > 1e-30f ? logf(pr / R) : logf(pr) - ((rest - m0) / p.T + logf(sum) - logf(S)));
       kd *= p.b;
     }
     if (tid == 0) p.loss[row] = w * (kd + (p.labels ? p.a * (logf(S1) + (m0 - zy)) : 0.f));
@@ -231,26 +231,40 @@ __global__ void __launch_bounds__(512) distill_kernel(const __grid_constant__ Di
   float A = sum == 0.f ? 0.f : kb * (f / S - pr / sum);
   const float A1 = sum1 == 0.f && TWO ? 0.f : ka * (f1 / S1);
   if constexpr (!TWO) A += p.labels ? A1 : 0.f;
-  const auto grad = [&](float x) {
-    const float d = x - rest;
-    float r = ex2(d * p.c) * A;
-    if constexpr (TWO) r = fmaf(ex2(d * kLog2e), A1, r);
-    return r;
-  };
-  for (int v = tid; v < s.nvec; v += NT) {
-    float x[E];
-    unit_floats<T>(s.units()[v], x);
-    uint32_t o[4];
+  const Exponent eg(rest, p.c), eg1(rest, kLog2e);
+  A *= eg.scale;
+  const float B1 = A1 * eg1.scale;
+  const auto grad = [&](float x) { return TWO ? fmaf(eg1.one(x), B1, eg.one(x) * A) : eg.one(x) * A; };
+  if (eg.far || (TWO && eg1.far)) {
+    for (int i = tid; i < s.nvec * E; i += NT) s.elems()[i] = from_f32<T>(grad(to_f32(s.elems()[i])));
+  } else {
+    const F2 c2 = pack2(p.c, p.c), r2 = pack2(-eg.rc, -eg.rc), A2 = pack2(A, A);
+    const F2 c12 = pack2(kLog2e, kLog2e), r12 = pack2(-eg1.rc, -eg1.rc), B2 = pack2(B1, B1);
+#pragma unroll 2
+    for (int v = tid; v < s.nvec; v += NT) {
+      const uint4 u = s.units()[v];
+      uint32_t o[4];
 #pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      if constexpr (sizeof(T) == 4) {
-        o[h] = __float_as_uint(grad(x[h]));
-      } else {
-        const __nv_bfloat162 b2 = __floats2bfloat162_rn(grad(x[2 * h]), grad(x[2 * h + 1]));
-        o[h] = *reinterpret_cast<const uint32_t*>(&b2);
+      for (int h = 0; h < E / 2; ++h) {
+        const F2 x2 = pair_of<T>(u, h);
+        float x, y;
+        unpack2(fma2(x2, c2, r2), x, y);
+        F2 d = mul2(pack2(ex2(x), ex2(y)), A2);
+        if constexpr (TWO) {
+          unpack2(fma2(x2, c12, r12), x, y);
+          d = fma2(pack2(ex2(x), ex2(y)), B2, d);
+        }
+        unpack2(d, x, y);
+        if constexpr (sizeof(T) == 4) {
+          o[2 * h] = __float_as_uint(x);
+          o[2 * h + 1] = __float_as_uint(y);
+        } else {
+          const __nv_bfloat162 b2 = __floats2bfloat162_rn(x, y);
+          o[h] = *reinterpret_cast<const uint32_t*>(&b2);
+        }
       }
+      s.units()[v] = make_uint4(o[0], o[1], o[2], o[3]);
     }
-    s.units()[v] = make_uint4(o[0], o[1], o[2], o[3]);
   }
   __syncthreads();
   if (here) {

@@ -10,6 +10,7 @@
 // (tid, tid + NT, ...) and need not wait for other threads to read them.
 #pragma once
 #include "common.cuh"
+#include "f32x2.cuh"
 
 namespace mlpk {
 namespace lg {
@@ -20,7 +21,7 @@ constexpr int kSMs = 152;
 constexpr int kMaxK = 256;                 // entries kept of a row
 constexpr int kCand = 1024;                // candidates ranked at most
 constexpr int64_t kMaxC = 393216;          // columns: eight slices of 192 KB of fp32
-constexpr int64_t kSliceBytes = 72 * 1024; // a slice of at most this leaves room for three blocks on an SM
+constexpr int64_t kSliceBytes = 64 * 1024; // a slice of at most this leaves room for three blocks on an SM
 
 // 2^t; subnormal results are flushed to zero (PTX ex2.approx).
 __device__ __forceinline__ float ex2(float t) {
@@ -151,23 +152,97 @@ struct Slice {
 // Bytes of a slice's buffer (the phase can add a unit).
 inline int64_t slice_buffer(int64_t per, int es) { return (per * es + 15) / 16 * 16 + 16; }
 
-// Sums and maxima over the block, the same in every thread; red: one float a
-// warp and a place of its own for each call between two barriers.
-__device__ __forceinline__ float block_sum(float v, float* red) {
+// Sums and maxima over the block (4, 8 or 16 warps), the same in every thread;
+// red: a place of its own for each call.
+struct __align__(16) Red { float v[16]; };
+__device__ __forceinline__ float block_sum(float v, Red& red) {
   v = warp_sum(v);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  if ((threadIdx.x & 31) == 0) red.v[threadIdx.x >> 5] = v;
   __syncthreads();
   float s = 0.f;
-  for (int w = 0; w < (int)blockDim.x / 32; ++w) s += red[w];
+  for (int w = 0; w < (int)blockDim.x / 32; w += 4) {
+    const float4 a = *reinterpret_cast<const float4*>(red.v + w);
+    s += (a.x + a.y) + (a.z + a.w);
+  }
   return s;
 }
-__device__ __forceinline__ float block_max(float v, float* red) {
+__device__ __forceinline__ float block_max(float v, Red& red) {
   v = warp_max(v);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  if ((threadIdx.x & 31) == 0) red.v[threadIdx.x >> 5] = v;
   __syncthreads();
   float s = -INFINITY;
-  for (int w = 0; w < (int)blockDim.x / 32; ++w) s = fmaxf(s, red[w]);
+  for (int w = 0; w < (int)blockDim.x / 32; w += 4) {
+    const float4 a = *reinterpret_cast<const float4*>(red.v + w);
+    s = fmaxf(s, fmaxf(fmaxf(a.x, a.y), fmaxf(a.z, a.w)));
+  }
   return s;
+}
+
+// Two neighbouring elements (bf16: of one word) as fp32.
+template <typename T>
+__device__ __forceinline__ F2 pair_of(const uint4& a, int h) {
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+  if constexpr (sizeof(T) == 4) return pack2(__uint_as_float(w[2 * h]), __uint_as_float(w[2 * h + 1]));
+  else return pack2(__uint_as_float(w[h] << 16), __uint_as_float(w[h] & 0xFFFF0000u));
+}
+
+// exp((x - ref) / T) for many x as 2^(x c - ref c), one FMA and one ex2 each.
+// ref c is rounded once for all of them, which scales every term alike by
+// 2^(its rounding): `scale` takes that out of their sum.  Where ref c leaves fp32
+// (masks of the lowest value, small T) the difference is formed first.
+struct Exponent {
+  float c, ref, rc, scale;
+  bool far;
+  __device__ __forceinline__ Exponent(float ref_, float c_) : c(c_), ref(ref_), rc(ref_ * c_) {
+    far = !(fabsf(rc) < 1e37f);
+    scale = far ? 1.f : fmaf(-kLn2, fmaf(ref, c, -rc), 1.f);
+  }
+  // of one x, without the scale
+  __device__ __forceinline__ float one(float x) const { return ex2(far ? (x - ref) * c : fmaf(x, c, -rc)); }
+};
+// The sum over this thread's units of exp((x - ref) / T).
+template <typename T>
+__device__ __forceinline__ float sum_exp(const Slice<T>& s, const Exponent& q) {
+  float sum;
+  if (q.far) {
+    sum = 0.f;
+    s.each([&](int, float x) { sum += ex2((x - q.ref) * q.c); });
+  } else {
+    F2 a0 = pack2(0.f, 0.f), a1 = a0;
+    const F2 c2 = pack2(q.c, q.c), r2 = pack2(-q.rc, -q.rc);
+#pragma unroll 2
+    for (int v = threadIdx.x; v < s.nvec; v += blockDim.x) {
+      const uint4 u = s.units()[v];
+#pragma unroll
+      for (int h = 0; h < kPer16<T> / 2; ++h) {
+        float x, y;
+        unpack2(fma2(pair_of<T>(u, h), c2, r2), x, y);
+        const F2 e = pack2(ex2(x), ex2(y));
+        if (h & 1) a1 = add2(a1, e);
+        else a0 = add2(a0, e);
+      }
+    }
+    sum = sum2(add2(a0, a1));
+  }
+  return sum * q.scale;
+}
+template <typename T>
+__device__ __forceinline__ float max_of(const Slice<T>& s) {
+  float m = -INFINITY;
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll 4
+    for (int v = threadIdx.x; v < s.nvec; v += blockDim.x) m = fmaxf(m, unit_max<T>(s.units()[v]));
+  } else {
+    const auto b = [](uint32_t w) { return *reinterpret_cast<__nv_bfloat162*>(&w); };
+    __nv_bfloat162 m2 = b(0xFF80FF80u);
+#pragma unroll 4
+    for (int v = threadIdx.x; v < s.nvec; v += blockDim.x) {
+      const uint4 a = s.units()[v];
+      m2 = __hmax2(m2, __hmax2(__hmax2(b(a.x), b(a.y)), __hmax2(b(a.z), b(a.w))));
+    }
+    m = fmaxf(__low2float(m2), __high2float(m2));
+  }
+  return m;
 }
 
 // How rows are cut: `cluster` blocks of `threads` threads share a row, `per`
