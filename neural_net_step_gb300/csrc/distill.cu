@@ -98,7 +98,13 @@ __global__ void __launch_bounds__(512) distill_kernel(const __grid_constant__ Di
   const int rank = CLUSTER ? (int)blockIdx.z : 0, blocks = CLUSTER ? (int)gridDim.z : 1;
   const int lo = rank * p.per, n = max(0, min(p.per, p.C - lo));
   T* dz = p.dz ? reinterpret_cast<T*>(p.dz) + row * p.lddz + lo : nullptr;
+  // the small reads first: behind the row's they would wait for it
+  const bool mine = tid < p.k;                  // (at least k threads)
   const float w = p.w ? p.w[row] : 1.f;
+  int col = mine ? p.ti[row * p.ldti + tid] : -1;
+  float t = mine ? p.tv[row * p.ldtv + tid] : -INFINITY;
+  const int y = p.labels ? p.labels[row] : -1;
+  const float tail = p.tail ? p.tail[row] : -INFINITY;
   if (w == 0.f) {   // a row that does not count, whatever it holds
     if (dz) clear(dz, n);
     if (rank == 0 && tid == 0) p.loss[row] = 0.f;
@@ -107,25 +113,16 @@ __global__ void __launch_bounds__(512) distill_kernel(const __grid_constant__ Di
 
   float* zt = reinterpret_cast<float*>(smem);   // [k] the student's logits at the teacher's columns
   unsigned char* buf = smem + (p.k * 4 + 15) / 16 * 16;
-  const bool mine = tid < p.k;                  // (at least k threads)
   if (mine) zt[tid] = -INFINITY;
   if (CLUSTER) cluster_arrive();
   Slice<T> s;
   s.load(buf, reinterpret_cast<const T*>(p.z) + row * p.ldz, lo, n);
 
   // ---- the teacher, while the row is on its way
-  int col = -1;
-  float t = -INFINITY;
-  bool bad = false;
-  if (mine) {
-    col = p.ti[row * p.ldti + tid];
-    bad = col < -1 || col >= p.C;
-    if (col >= 0) t = p.tv[row * p.ldtv + tid];
-  }
-  const int y = p.labels ? p.labels[row] : -1;
+  bool bad = mine && (col < -1 || col >= p.C);
   if (p.labels) bad |= y < 0 || y >= p.C;
+  if (col < 0) t = -INFINITY;                   // (unused entries' values are not looked at)
   const float tm = block_max(t, sh.red[0]);
-  const float tail = p.tail ? p.tail[row] : -INFINITY;
   const float tm0 = tm > -INFINITY ? tm : 0.f;
   float tref = fmaxf(tm / p.T, tail);
   if (!(tref > -INFINITY)) tref = 0.f;
@@ -213,6 +210,84 @@ __global__ void __launch_bounds__(512) distill_kernel(const __grid_constant__ Di
   }
   const float pj = has ? pe / St : 0.f, pr = has ? U / St : 0.f;
 
+  // ---- the gradient, in the row's place
+  if (dz) {
+    const float wg = w * p.g, kb = has ? wg * p.b * p.inv_T : 0.f, ka = p.labels ? wg * p.a : 0.f;
+    float A = sum == 0.f ? 0.f : kb * (f / S - pr / sum);
+    const float A1 = sum1 == 0.f && TWO ? 0.f : ka * (f1 / S1);
+    if constexpr (!TWO) A += p.labels ? A1 : 0.f;
+    const Exponent eg(rest, p.c), eg1(rest, kLog2e);
+    A *= eg.scale;
+    const float B1 = A1 * eg1.scale;
+    const auto grad = [&](float x) { return TWO ? fmaf(eg1.one(x), B1, eg.one(x) * A) : eg.one(x) * A; };
+    if (eg.far || (TWO && eg1.far)) {
+      for (int i = tid; i < s.nvec * E; i += NT) s.elems()[i] = from_f32<T>(grad(to_f32(s.elems()[i])));
+    } else {
+      const F2 c2 = pack2(p.c, p.c), r2 = pack2(-eg.rc, -eg.rc), A2 = pack2(A, A);
+      const F2 c12 = pack2(kLog2e, kLog2e), r12 = pack2(-eg1.rc, -eg1.rc), B2 = pack2(B1, B1);
+      const auto step = [&](const uint4& u) {
+        uint32_t o[4];
+#pragma unroll
+        for (int h = 0; h < E / 2; ++h) {
+          const F2 x2 = pair_of<T>(u, h);
+          float x, y;
+          unpack2(fma2(x2, c2, r2), x, y);
+          F2 d = mul2(pack2(ex2(x), ex2(y)), A2);
+          if constexpr (TWO) {
+            unpack2(fma2(x2, c12, r12), x, y);
+            d = fma2(pack2(ex2(x), ex2(y)), B2, d);
+          }
+          unpack2(d, x, y);
+          if constexpr (sizeof(T) == 4) {
+            o[2 * h] = __float_as_uint(x);
+            o[2 * h + 1] = __float_as_uint(y);
+          } else {
+            const __nv_bfloat162 b2 = __floats2bfloat162_rn(x, y);
+            o[h] = *reinterpret_cast<const uint32_t*>(&b2);
+          }
+        }
+        return make_uint4(o[0], o[1], o[2], o[3]);
+      };
+      int v = tid;
+      for (; v + 3 * NT < s.nvec; v += 4 * NT) {   // four loads in flight
+        const uint4 u0 = s.units()[v], u1 = s.units()[v + NT], u2 = s.units()[v + 2 * NT], u3 = s.units()[v + 3 * NT];
+        s.units()[v] = step(u0);
+        s.units()[v + NT] = step(u1);
+        s.units()[v + 2 * NT] = step(u2);
+        s.units()[v + 3 * NT] = step(u3);
+      }
+      for (; v < s.nvec; v += NT) s.units()[v] = step(s.units()[v]);
+    }
+    __syncthreads();
+    if (here) {
+      float r = kb * (q / S - pj);
+      if (p.labels) r += ka * (q1 / S1 - (col == y ? 1.f : 0.f));
+      s.at(own) = from_f32<T>(r);
+    }
+    if (label_here && !label_in_top && tid == 0) s.at(y - lo) = from_f32<T>(grad(zy) - ka);
+
+    // ---- and out
+    if ((((uintptr_t)dz) & 15) / sizeof(T) == (unsigned)s.ph) {
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncthreads();
+      const int v0 = s.ph > 0 ? 1 : 0, v1 = (s.ph + n) / E;   // the whole units
+      if (tid == 0 && v1 > v0) {
+        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dz - s.ph + v0 * E),
+                     "r"(smem_addr(s.units() + v0)), "r"((v1 - v0) * 16)
+                     : "memory");
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+      }
+      if (tid < 2 * E) {   // the units that the slice only partly covers
+        const int i = tid < E ? tid - s.ph : max(v1, v0) * E + (tid - E) - s.ph;
+        if (i >= 0 && i < n && (tid < E ? v0 == 1 : true) && !(tid >= E && v1 < v0)) dz[i] = s.at(i);
+      }
+    } else {
+      __syncthreads();
+      for (int i = tid; i < n; i += NT) dz[i] = s.at(i);
+    }
+  }
+
+  // ---- the loss, while the gradient leaves
   if (rank == 0) {
     float kd = 0.f;
     if (has && p.b != 0.f) {
@@ -224,76 +299,7 @@ __global__ void __launch_bounds__(512) distill_kernel(const __grid_constant__ Di
     }
     if (tid == 0) p.loss[row] = w * (kd + (p.labels ? p.a * (logf(S1) + (m0 - zy)) : 0.f));
   }
-  if (!dz) return;
-
-  // ---- the gradient, in the row's place
-  const float wg = w * p.g, kb = has ? wg * p.b * p.inv_T : 0.f, ka = p.labels ? wg * p.a : 0.f;
-  float A = sum == 0.f ? 0.f : kb * (f / S - pr / sum);
-  const float A1 = sum1 == 0.f && TWO ? 0.f : ka * (f1 / S1);
-  if constexpr (!TWO) A += p.labels ? A1 : 0.f;
-  const Exponent eg(rest, p.c), eg1(rest, kLog2e);
-  A *= eg.scale;
-  const float B1 = A1 * eg1.scale;
-  const auto grad = [&](float x) { return TWO ? fmaf(eg1.one(x), B1, eg.one(x) * A) : eg.one(x) * A; };
-  if (eg.far || (TWO && eg1.far)) {
-    for (int i = tid; i < s.nvec * E; i += NT) s.elems()[i] = from_f32<T>(grad(to_f32(s.elems()[i])));
-  } else {
-    const F2 c2 = pack2(p.c, p.c), r2 = pack2(-eg.rc, -eg.rc), A2 = pack2(A, A);
-    const F2 c12 = pack2(kLog2e, kLog2e), r12 = pack2(-eg1.rc, -eg1.rc), B2 = pack2(B1, B1);
-#pragma unroll 2
-    for (int v = tid; v < s.nvec; v += NT) {
-      const uint4 u = s.units()[v];
-      uint32_t o[4];
-#pragma unroll
-      for (int h = 0; h < E / 2; ++h) {
-        const F2 x2 = pair_of<T>(u, h);
-        float x, y;
-        unpack2(fma2(x2, c2, r2), x, y);
-        F2 d = mul2(pack2(ex2(x), ex2(y)), A2);
-        if constexpr (TWO) {
-          unpack2(fma2(x2, c12, r12), x, y);
-          d = fma2(pack2(ex2(x), ex2(y)), B2, d);
-        }
-        unpack2(d, x, y);
-        if constexpr (sizeof(T) == 4) {
-          o[2 * h] = __float_as_uint(x);
-          o[2 * h + 1] = __float_as_uint(y);
-        } else {
-          const __nv_bfloat162 b2 = __floats2bfloat162_rn(x, y);
-          o[h] = *reinterpret_cast<const uint32_t*>(&b2);
-        }
-      }
-      s.units()[v] = make_uint4(o[0], o[1], o[2], o[3]);
-    }
-  }
-  __syncthreads();
-  if (here) {
-    float r = kb * (q / S - pj);
-    if (p.labels) r += ka * (q1 / S1 - (col == y ? 1.f : 0.f));
-    s.at(own) = from_f32<T>(r);
-  }
-  if (label_here && !label_in_top && tid == 0) s.at(y - lo) = from_f32<T>(grad(zy) - ka);
-
-  // ---- and out
-  if ((((uintptr_t)dz) & 15) / sizeof(T) == (unsigned)s.ph) {
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    __syncthreads();
-    const int v0 = s.ph > 0 ? 1 : 0, v1 = (s.ph + n) / E;   // the whole units
-    if (tid == 0 && v1 > v0) {
-      asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dz - s.ph + v0 * E),
-                   "r"(smem_addr(s.units() + v0)), "r"((v1 - v0) * 16)
-                   : "memory");
-      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-    }
-    if (tid < 2 * E) {   // the units that the slice only partly covers
-      const int i = tid < E ? tid - s.ph : max(v1, v0) * E + (tid - E) - s.ph;
-      if (i >= 0 && i < n && (tid < E ? v0 == 1 : true) && !(tid >= E && v1 < v0)) dz[i] = s.at(i);
-    }
-    if (tid == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-  } else {
-    __syncthreads();
-    for (int i = tid; i < n; i += NT) dz[i] = s.at(i);
-  }
+  if (tid == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 
 template <typename T>

@@ -20,6 +20,8 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kSMs = 152;
 constexpr int kMaxK = 256;                 // entries kept of a row
 constexpr int kCand = 1024;                // candidates ranked at most
+constexpr int kCounted = 256;              // of which so many by counting
+constexpr int kHits = 2048;                // 16-byte units looked through for them at most, shared out to the warps
 constexpr int64_t kMaxC = 393216;          // columns: eight slices of 192 KB of fp32
 constexpr int64_t kSliceBytes = 64 * 1024; // a slice of at most this leaves room for three blocks on an SM
 
@@ -166,6 +168,21 @@ __device__ __forceinline__ float block_sum(float v, Red& red) {
   }
   return s;
 }
+__device__ __forceinline__ void block_sums(float& u, float& v, Red& ru, Red& rv) {
+  u = warp_sum(u);
+  v = warp_sum(v);
+  if ((threadIdx.x & 31) == 0) {
+    ru.v[threadIdx.x >> 5] = u;
+    rv.v[threadIdx.x >> 5] = v;
+  }
+  __syncthreads();
+  u = v = 0.f;
+  for (int w = 0; w < (int)blockDim.x / 32; w += 4) {
+    const float4 a = *reinterpret_cast<const float4*>(ru.v + w), b = *reinterpret_cast<const float4*>(rv.v + w);
+    u += (a.x + a.y) + (a.z + a.w);
+    v += (b.x + b.y) + (b.z + b.w);
+  }
+}
 __device__ __forceinline__ float block_max(float v, Red& red) {
   v = warp_max(v);
   if ((threadIdx.x & 31) == 0) red.v[threadIdx.x >> 5] = v;
@@ -210,9 +227,7 @@ __device__ __forceinline__ float sum_exp(const Slice<T>& s, const Exponent& q) {
   } else {
     F2 a0 = pack2(0.f, 0.f), a1 = a0;
     const F2 c2 = pack2(q.c, q.c), r2 = pack2(-q.rc, -q.rc);
-#pragma unroll 2
-    for (int v = threadIdx.x; v < s.nvec; v += blockDim.x) {
-      const uint4 u = s.units()[v];
+    const auto add = [&](const uint4& u) {
 #pragma unroll
       for (int h = 0; h < kPer16<T> / 2; ++h) {
         float x, y;
@@ -221,7 +236,17 @@ __device__ __forceinline__ float sum_exp(const Slice<T>& s, const Exponent& q) {
         if (h & 1) a1 = add2(a1, e);
         else a0 = add2(a0, e);
       }
+    };
+    const int step = blockDim.x;
+    int v = threadIdx.x;
+    for (; v + 3 * step < s.nvec; v += 4 * step) {   // four loads in flight
+      const uint4 u0 = s.units()[v], u1 = s.units()[v + step], u2 = s.units()[v + 2 * step], u3 = s.units()[v + 3 * step];
+      add(u0);
+      add(u1);
+      add(u2);
+      add(u3);
     }
+    for (; v < s.nvec; v += step) add(s.units()[v]);
     sum = sum2(add2(a0, a1));
   }
   return sum * q.scale;

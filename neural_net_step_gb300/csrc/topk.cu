@@ -9,20 +9,22 @@
 //      warps, of each warp's ceil(k / warps)-th largest lane is a threshold that at
 //      least k elements reach, and not many more do where the row is in no
 //      particular order.
-//   2. The elements that reach it are the candidates; each counts those before it,
-//      which is its place (where they are many, warps sort them 32 at a time and
-//      each searches the other runs).  Where they are too many (equal values,
-//      sorted rows) or too few (padding, NaN), the k-th largest is found by halving
-//      the range of keys, then of columns among equals, counting each time.
+//   2. Every warp lists its units that reach it, then their elements that do: the
+//      candidates.  Each counts those before it, which is its place; where they are
+//      64 bits wide, warps sort them 32 at a time instead and each searches the
+//      other runs.  Where they are too many
+//      (equal values, sorted rows) or too few (padding, NaN), the k-th largest is
+//      found by halving the range of keys, then of columns among equals.
 //   3. The elements taken become -infinity in shared memory, and the sum of the
-//      others is relative to the smallest taken: the tail needs no subtraction
-//      and cannot underflow before its largest term does.
+//      others is relative to the smallest taken, or to their own largest where that
+//      leaves next to nothing: the tail needs no subtraction and does not underflow.
 // The blocks of a cluster do this for their slices and send lists and sums to the
 // first, which finds the entries' places in the row and adds what a slice took
 // and the row does not to the rest.
 #include <stdio.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "logits.cuh"
 #include "ops.h"
@@ -33,7 +35,6 @@ namespace lg {
 Cut cut_rows(int64_t rows, int64_t C, int es, int k) {
   int cs = 1;
   while (cs < 8 && ceil_div(C, cs) * es > kSliceBytes) cs *= 2;
-  while (cs < 8 && rows * cs * 2 <= kSMs * 2 && C / (cs * 2) >= 2048) cs *= 2;
   Cut c;
   c.cluster = cs;
   c.per = (int)round_up(ceil_div(C, cs), 16 / es);
@@ -63,8 +64,8 @@ struct TopkParams {
 };
 
 struct TopkShared {
-  Red red[3];
-  uint32_t tau[16];
+  Red red[7];
+  uint32_t tau[16];                 // (16-byte aligned)
   int count;
   int total[16];
   float2 part[8];                   // of each block of the cluster: reference and sum of the rest
@@ -95,23 +96,46 @@ __device__ __forceinline__ U warp_sort_down(U x) {
   }
   return x;
 }
-// The n-th largest of the warp's values, n from 1.
-__device__ __forceinline__ uint32_t warp_nth(uint32_t x, int n) {
-  if (n > 8) return __shfl_sync(0xffffffffu, warp_sort_down(x), n - 1);
-  uint32_t m = 0;
-  while (true) {
-    m = __reduce_max_sync(0xffffffffu, x);
-    if (--n <= 0) return m;
-    const unsigned who = __ballot_sync(0xffffffffu, x == m);
-    if ((threadIdx.x & 31) == __ffs(who) - 1) x = 0;
+// The n-th largest of the warp's values, n from 1: each lane counts the larger
+// ones (room: 32 places).
+__device__ __forceinline__ uint32_t warp_nth(uint32_t x, int n, uint32_t* room) {
+  room[threadIdx.x & 31] = x;
+  __syncwarp();
+  int larger = 0;
+#pragma unroll
+  for (int b = 0; b < 8; ++b) {
+    const uint4 o = reinterpret_cast<const uint4*>(room)[b];
+    larger += (o.x > x) + (o.y > x) + (o.z > x) + (o.w > x);
   }
+  __syncwarp();
+  return __reduce_min_sync(0xffffffffu, larger < n ? x : 0xFFFFFFFFu);
 }
+
+// A candidate of a slice: larger is better, lower element first among equals; 0
+// is none.  bf16 slices of at most 65535 elements need 32 bits.
+template <typename K> struct Cand;
+template <> struct Cand<uint64_t> {
+  static __device__ __forceinline__ uint64_t of(float x, int i) { return entry_of(key_of(x), i); }
+  static __device__ __forceinline__ int at(uint64_t c) { return entry_col(c); }
+  static __device__ __forceinline__ uint32_t key(uint64_t c) { return entry_key(c); }
+};
+template <> struct Cand<uint32_t> {
+  static __device__ __forceinline__ uint32_t of(float x, int i) {
+    return (key_of(x) & 0xFFFF0000u) | (uint32_t)(0xFFFF - i);
+  }
+  static __device__ __forceinline__ int at(uint32_t c) { return 0xFFFF - (int)(c & 0xFFFFu); }
+  // (the low half of a bf16's key: zeros, or ones below zero)
+  static __device__ __forceinline__ uint32_t key(uint32_t c) {
+    const uint32_t h = c & 0xFFFF0000u;
+    return h == 0 ? 0u : (c & 0x80000000u) ? h : h | 0xFFFFu;
+  }
+};
 
 // Candidates where the threshold did not leave a fit number of them: exactly
 // those not below the kk-th largest, or the kk largest themselves.  tau: a first
 // guess of the kk-th largest's key, or 0.
-template <typename T>
-__device__ __noinline__ void search(const Slice<T>& s, int kk, uint32_t tau, uint64_t* cand, TopkShared& sh) {
+template <typename T, typename K>
+__device__ __noinline__ void search(const Slice<T>& s, int kk, uint32_t tau, K* cand, TopkShared& sh) {
   const auto reach = [&](uint32_t key) {
     int c = 0;
     s.each([&](int, float x) { c += key_of(x) >= key; });
@@ -143,7 +167,7 @@ __device__ __noinline__ void search(const Slice<T>& s, int kk, uint32_t tau, uin
     const uint32_t key = key_of(x);
     if (key > v || (key == v && i <= last)) {
       const int at = atomicAdd(&sh.count, 1);
-      if (at < kCand) cand[at] = entry_of(key, s.lo + i);
+      if (at < kCand) cand[at] = Cand<K>::of(x, i);
     }
   });
   __syncthreads();
@@ -152,20 +176,37 @@ __device__ __noinline__ void search(const Slice<T>& s, int kk, uint32_t tau, uin
 // Adds to `place` how many entries of the descending lists 0 .. n - 1 but `not_in`
 // are larger than e.  Lists are `len` entries long and lie one behind the other;
 // eight of them are searched side by side.
-__device__ __forceinline__ void add_larger(int& place, const uint64_t* lists, int n, int not_in, int len, uint64_t e) {
+template <typename K>
+__device__ __forceinline__ void add_larger(int& place, const K* lists, int n, int not_in, int len, K e) {
   const int top = 1 << (31 - __clz(len));
   for (int b0 = 0; b0 < n; b0 += 8) {
     int at[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     for (int step = top; step > 0; step >>= 1) {
 #pragma unroll
       for (int b = 0; b < 8; ++b) {
-        const int to = at[b] + step;
-        if (b0 + b < n && to <= len && lists[(b0 + b) * len + to - 1] > e) at[b] = to;
+        const int to = at[b] + step;   // (every load has a place to go: none waits for a branch)
+        const K v = lists[min(b0 + b, n - 1) * len + min(to, len) - 1];
+        at[b] = to <= len && v > e ? to : at[b];
       }
     }
 #pragma unroll
-    for (int b = 0; b < 8; ++b) place += b0 + b == not_in ? 0 : at[b];
+    for (int b = 0; b < 8; ++b) place += b0 + b == not_in || b0 + b >= n ? 0 : at[b];
   }
+}
+
+// Sum of n over the lanes before this one and over all, n < 2^BITS.
+template <int BITS>
+__device__ __forceinline__ int before_lane(int n, int& all) {
+  const uint32_t below = (1u << (threadIdx.x & 31)) - 1;
+  int before = 0;
+  all = 0;
+#pragma unroll
+  for (int b = 0; b < BITS; ++b) {
+    const uint32_t who = __ballot_sync(0xffffffffu, n >> b & 1);
+    before += __popc(who & below) << b;
+    all += __popc(who) << b;
+  }
+  return before;
 }
 
 // U: units a thread has at most.
@@ -182,15 +223,19 @@ __global__ void __launch_bounds__(U <= 16 ? 256 : 512, U <= 16 ? 3 : 1) topk_ker
   if (p.stats && ((p.done && p.done[row]) || !(fabsf(p.scores[row]) < INFINITY))) return;
   if (CLUSTER) cluster_arrive();
 
-  uint64_t* cand = reinterpret_cast<uint64_t*>(smem);    // [kCand]
-  uint64_t* lists = cand + kCand;                        // [blocks][k], descending (0: none); the first block has all
-  uint64_t* own = lists + (int64_t)rank * p.k;
-  unsigned char* buf = reinterpret_cast<unsigned char*>(((uintptr_t)(lists + (int64_t)blocks * p.k) + 15) & ~(uintptr_t)15);
+  typedef typename std::conditional<U <= 16 && sizeof(T) == 2, uint32_t, uint64_t>::type K;
+  uint64_t* best = reinterpret_cast<uint64_t*>(smem);    // [k, even]: the row's, descending
+  uint64_t* lists = best + ((p.k + 1) & ~1);             // [blocks][k], descending (0: none); the first block has all
+  uint64_t* own = CLUSTER ? lists + (int64_t)rank * p.k : best;
+  K* cand = reinterpret_cast<K*>(lists + (CLUSTER ? blocks * p.k : 0));   // [kCand]
+  uint16_t* hits = reinterpret_cast<uint16_t*>(cand + kCand);                      // [kHits]
+  unsigned char* buf = reinterpret_cast<unsigned char*>(((uintptr_t)(hits + kHits) + 15) & ~(uintptr_t)15);
 
   Slice<T> s;
   s.load(buf, reinterpret_cast<const T*>(p.z) + row * p.ldz, rank * p.per, min(p.per, p.C - rank * p.per));
   const int kk = min(p.k, s.n);
   if (tid == 0) sh.count = 0;
+  for (int a = tid; a < kCounted + 16; a += NT) cand[a] = 0;
   copies_wait();
 
   // 1. a threshold that at least kk elements reach
@@ -201,28 +246,47 @@ __global__ void __launch_bounds__(U <= 16 ? 256 : 512, U <= 16 ? 3 : 1) topk_ker
     um[u] = v < s.nvec ? unit_max<T>(s.units()[v]) : -INFINITY;
     most = fmaxf(most, um[u]);
   }
-  const uint32_t nth = warp_nth(key_of(most), (kk + warps - 1) / warps);
+  const uint32_t nth = warp_nth(key_of(most), (kk + warps - 1) / warps, reinterpret_cast<uint32_t*>(hits) + warp * 32);
   if (lane == 0) sh.tau[warp] = nth;
   __syncthreads();
-  uint32_t tau = sh.tau[0];
-  for (int w = 1; w < warps; ++w) tau = min(tau, sh.tau[w]);
+  uint32_t tau = 0xFFFFFFFFu;
+  for (int w = 0; w < warps; w += 4) {
+    const uint4 q = *reinterpret_cast<const uint4*>(sh.tau + w);
+    tau = min(tau, min(min(q.x, q.y), min(q.z, q.w)));
+  }
   const float least = value_of(tau);
 
   // 2. candidates and their places
   uint32_t reach = 0;
 #pragma unroll
-  for (int u = 0; u < U; ++u) reach |= (uint32_t)(um[u] >= least && tid + u * NT < s.nvec) << u;
-  for (; reach; reach &= reach - 1) {
-    const int v = tid + (__ffs(reach) - 1) * NT, i0 = v * E - s.ph;
-    float x[E];
-    unit_floats<T>(s.units()[v], x);
+  for (int u = 0; u < U; ++u) reach |= (uint32_t)(um[u] >= least) << u;
+  const int room = kHits / warps;
+  uint16_t* hit = hits + warp * room;
+  int n_hits;
+  for (int at = before_lane<5>(__popc(reach), n_hits); reach && at < room; reach &= reach - 1, ++at)
+    hit[at] = (uint16_t)(tid + (__ffs(reach) - 1) * NT);
+  __syncwarp();
+  if (n_hits > room && lane == 0) atomicAdd(&sh.count, kCand + 1);
+  for (int a = lane; a - lane < min(n_hits, room); a += 32) {
     uint32_t in = 0;
+    int v = 0;
+    if (a < min(n_hits, room) && hit[a] < s.nvec) {
+      v = hit[a];
+      float x[E];
+      unit_floats<T>(s.units()[v], x);
 #pragma unroll
-    for (int e = 0; e < E; ++e) in |= (uint32_t)(x[e] >= least && i0 + e >= 0 && i0 + e < s.n) << e;
-    int at = atomicAdd(&sh.count, __popc(in));
+      for (int e = 0; e < E; ++e) in |= (uint32_t)(x[e] >= least) << e;
+      if (least == -INFINITY)   // (what fills the units at a slice's ends does not count)
+        for (int e = 0; e < E; ++e)
+          if (v * E + e < s.ph || v * E + e >= s.ph + s.n) in &= ~(1u << e);
+    }
+    int n_in, at = 0;
+    const int before = before_lane<4>(__popc(in), n_in);
+    if (lane == 0) at = atomicAdd(&sh.count, n_in);
+    at = __shfl_sync(0xffffffffu, at, 0) + before;
     for (; in && at < kCand; in &= in - 1, ++at) {
-      const int i = i0 + __ffs(in) - 1;
-      cand[at] = entry_of(key_of(to_f32(s.at(i))), s.lo + i);
+      const int i = v * E + __ffs(in) - 1 - s.ph;
+      cand[at] = Cand<K>::of(to_f32(s.at(i)), i);
     }
   }
   __syncthreads();
@@ -230,48 +294,79 @@ __global__ void __launch_bounds__(U <= 16 ? 256 : 512, U <= 16 ? 3 : 1) topk_ker
   if (count > kCand || count < kk) {
     search<T>(s, kk, count > kCand ? tau : 0u, cand, sh);
     count = sh.count;
+    for (int a = count + tid; a < kCounted + 16; a += NT) cand[a] = 0;
+    __syncthreads();
   }
-  if (count <= 256) {
-    for (int a = tid; a < count; a += NT) {
-      const uint64_t e = cand[a];
-      const ulonglong2* c2 = reinterpret_cast<const ulonglong2*>(cand);
-      int place = 0;
-#pragma unroll 4
-      for (int b = 0; b < count >> 1; ++b) {
-        const ulonglong2 o = c2[b];
-        place += (o.x > e) + (o.y > e);
+  const bool sums = p.lse || p.tail || p.stats;
+  const auto place_at = [&](int place, K c) {   // (an element taken leaves the row)
+    const int i = Cand<K>::at(c);
+    own[place] = entry_of(Cand<K>::key(c), s.lo + i);
+    if (sums) s.at(i) = minus_inf<T>();
+  };
+  if (sizeof(K) == 4 && count <= kCounted) {
+    // 2^part neighbouring threads count for one candidate, sixteen others at a time
+    const int part = count * 4 <= NT ? 2 : count * 2 <= NT ? 1 : 0;
+    const int a = tid >> part, first = tid & ((1 << part) - 1);
+    const uint4* c4 = reinterpret_cast<const uint4*>(cand);   // (zeros behind the last)
+    for (int a0 = 0; a0 < count; a0 += NT) {
+      const uint32_t c = (uint32_t)cand[a0 + a < count ? a0 + a : 0];
+      int n[4] = {0, 0, 0, 0};
+      for (int b = first; b * 16 < count; b += 1 << part) {
+        uint4 o[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) o[q] = c4[b * 4 + q];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) n[q] += (o[q].x > c) + (o[q].y > c) + (o[q].z > c) + (o[q].w > c);
       }
-      if (count & 1) place += cand[count - 1] > e;
-      if (place < kk) own[place] = e;
+      int place = (n[0] + n[1]) + (n[2] + n[3]);
+      if (part >= 1) place += __shfl_xor_sync(0xffffffffu, place, 1);
+      if (part == 2) place += __shfl_xor_sync(0xffffffffu, place, 2);
+      if (a0 + a < count && first == 0 && place < kk) place_at(place, (K)c);
     }
   } else {
     const int runs = (count + 31) / 32;
     for (int r = warp; r < runs; r += warps)
-      cand[r * 32 + lane] = warp_sort_down(r * 32 + lane < count ? cand[r * 32 + lane] : 0ull);
+      cand[r * 32 + lane] = warp_sort_down(r * 32 + lane < count ? cand[r * 32 + lane] : (K)0);
     __syncthreads();
     for (int a = tid; a < count; a += NT) {
+      const K c = cand[a];
       int place = a & 31;
-      add_larger(place, cand, runs, a >> 5, 32, cand[a]);
-      if (place < kk) own[place] = cand[a];
+      add_larger(place, cand, runs, a >> 5, 32, c);
+      if (place < kk) place_at(place, c);
     }
   }
   __syncthreads();
 
   // 3. the sum of what is not taken, relative to the smallest that is
-  const bool sums = p.lse || p.tail || p.stats;
   const uint64_t e = tid < kk ? own[tid] : 0;            // (at least k threads)
+  const auto write = [&](uint64_t c) {
+    if (p.stats) {
+      p.entries[row * p.k + tid] = c;
+    } else {
+      p.values[row * p.ldv + tid] = value_of(entry_key(c));
+      p.indices[row * p.ldi + tid] = entry_col(c);
+    }
+  };
+  if (!CLUSTER && tid < p.k) write(e);
   float ref = 0.f, rest = 0.f;                           // (with nothing but -infinity and NaN left any reference will do)
   if (sums && kk > 0) {
-    if (tid < kk) s.at(entry_col(e) - s.lo) = minus_inf<T>();
-    __syncthreads();
     ref = value_of(entry_key(own[kk - 1]));
-    if (ref == INFINITY) ref = block_max(max_of(s), sh.red[2]);
+    if (ref == INFINITY) ref = block_max(max_of(s), sh.red[6]);
     if (!(ref > -INFINITY)) ref = 0.f;
-    rest = block_sum(sum_exp(s, Exponent(ref, p.c)), sh.red[0]);
+    rest = sum_exp(s, Exponent(ref, p.c));
   }
 
-  uint64_t* best = own;
+  // where the others are so far below that nothing is left of them
+  const auto look_closer = [&]() {
+    if (!sums || !(rest < 0x1p-60f)) return;
+    const float m = block_max(max_of(s), sh.red[3]);
+    if (!(m > -INFINITY)) return;
+    ref = m;
+    rest = block_sum(sum_exp(s, Exponent(ref, p.c)), sh.red[4]);
+  };
   if (CLUSTER) {
+    rest = block_sum(rest, sh.red[0]);
+    look_closer();
     cluster_wait();   // (every block of the cluster runs)
     if (rank != 0) {
       if (tid < p.k) put64(in_block(smem_addr(own + tid), 0), e);
@@ -287,57 +382,59 @@ __global__ void __launch_bounds__(U <= 16 ? 256 : 512, U <= 16 ? 3 : 1) topk_ker
     cluster_arrive();
     cluster_wait();
     if (rank != 0) return;
-    best = cand;
-    for (int a = tid; a < blocks * p.k; a += NT) {
-      const uint64_t c = lists[a];
-      const int from = a / p.k;
-      int place = a - from * p.k;
-      if (c == 0) continue;
-      add_larger(place, lists, blocks, from, p.k, c);
-      if (place < p.k) best[place] = c;
+    // the k-th is no smaller than the smallest of the slices' ceil(k / blocks)-th
+    // (a slice with fewer entries bounds nothing)
+    const int each = (p.k + blocks - 1) / blocks;
+    uint64_t bound = ~0ull;
+    for (int b = 0; b < blocks; ++b) bound = min(bound, lists[b * p.k + each - 1]);
+    const int groups = min(warps, blocks);   // (powers of two both)
+    for (int from = warp % groups; from < blocks; from += groups) {
+      for (int j = warp / groups * 32 + lane; j < p.k; j += warps / groups * 32) {
+        const uint64_t c = lists[from * p.k + j];
+        if (c == 0 || c < bound) break;
+        int place = j;
+        add_larger(place, lists, blocks, from, p.k, c);
+        if (place < p.k) best[place] = c;
+      }
     }
     __syncthreads();
   }
 
-  const uint64_t mine = tid < p.k ? best[tid] : 0;
-  const float x = value_of(entry_key(mine)), first = value_of(entry_key(best[0]));
-  if (tid < p.k) {
-    if (p.stats) {
-      p.entries[row * p.k + tid] = mine;
-    } else {
-      p.values[row * p.ldv + tid] = x;
-      p.indices[row * p.ldi + tid] = entry_col(mine);
-    }
-  }
+  if (CLUSTER && tid < p.k) write(best[tid]);
   if (!sums) return;
-  const float first0 = first > -INFINITY ? first : 0.f;
-  const float taken = block_sum(tid < p.k ? ex2((x - first0) * p.c) : 0.f, sh.red[1]);
+  const float first = value_of(entry_key(best[0])), first0 = first > -INFINITY ? first : 0.f;
+  float taken = tid < p.k ? ex2((value_of(entry_key(best[tid])) - first0) * p.c) : 0.f;
   if (CLUSTER) {
     // the rests of the slices and what they took and the row does not, relative to the largest of those
     const uint64_t last = best[p.k - 1];
     ref = -INFINITY;
     for (int b = 0; b < blocks; ++b)
       if (sh.part[b].y != 0.f) ref = fmaxf(ref, sh.part[b].x);
-    const float l = value_of(entry_key(last));
-    if (l < INFINITY) ref = fmaxf(ref, l);
+    float left = -INFINITY;
+    for (int a = tid; a < blocks * p.k; a += NT)
+      if (lists[a] != 0 && lists[a] < last) left = fmaxf(left, value_of(entry_key(lists[a])));
+    ref = fmaxf(ref, block_max(left, sh.red[5]));
     if (!(ref > -INFINITY)) ref = 0.f;
     rest = 0.f;
     for (int a = tid; a < blocks * p.k; a += NT)
       if (lists[a] != 0 && lists[a] < last) rest += ex2((value_of(entry_key(lists[a])) - ref) * p.c);
     if (tid < blocks && sh.part[tid].y != 0.f) rest += sh.part[tid].y * ex2((sh.part[tid].x - ref) * p.c);
-    rest = block_sum(rest, sh.red[0]);
   }
+  block_sums(taken, rest, sh.red[1], sh.red[2]);
+  if (!CLUSTER) look_closer();
+  const float all = taken + (rest != 0.f ? rest * ex2((ref - first0) * p.c) : 0.f);
   if (tid == 0) {
-    const float all = taken + (rest != 0.f ? rest * ex2((ref - first0) * p.c) : 0.f);
     if (p.stats) p.stats[row] = make_float2(first, all);
     if (p.lse) p.lse[row] = first0 / p.T + logf(all);
-    if (p.tail) p.tail[row] = ref / p.T + logf(rest);
   }
+  if (tid == 32 && p.tail) p.tail[row] = ref / p.T + logf(rest);
 }
 
 // Places for the row in shared memory behind the lists.
 unsigned topk_smem(const Cut& cut, int k, int es) {
-  return (unsigned)(((int64_t)cut.cluster * k + kCand) * 8 + 16 + slice_buffer(cut.per, es));
+  const int64_t entries = (k + 1) / 2 * 2 + (cut.cluster > 1 ? (int64_t)cut.cluster * k : 0);
+  return (unsigned)(entries * 8 + kCand * (cut.threads <= 256 && es == 2 ? 4 : 8) + kHits * 2 + 16 +
+                    slice_buffer(cut.per, es));
 }
 
 template <typename T>

@@ -85,6 +85,20 @@ def test_rows_in_order_with_equals_and_masks(dtype, B, kind):
 
 
 @pytest.mark.parametrize("dtype", [F, H])
+@pytest.mark.parametrize("B,C,k,T", [(3, 3000, 1, 1.0), (3, 32000, 8, 0.05), (2, 100000, 5, 1.0), (2, 300000, 3, 0.1)])
+def test_a_tail_far_below_what_is_taken(dtype, B, C, k, T):
+    """The tail is the log of its own sum, however far the k entries stand out."""
+    rng = np.random.default_rng(8)
+    z = logits(rng, B, C, TDT[dtype])
+    for b in range(B):
+        z[b, torch.from_numpy(rng.permutation(C)[:k])] += 200.0
+    check(dtype, z, k, T)
+    z[:, 5] = 500.0                                # and one of the tail above the others
+    z[:, 6] = 505.0
+    check(dtype, z, k + 1, T)
+
+
+@pytest.mark.parametrize("dtype", [F, H])
 def test_nan_is_last_and_reaches_the_sums(dtype):
     rng = np.random.default_rng(4)
     z = logits(rng, 6, 3001, TDT[dtype])
