@@ -174,11 +174,11 @@ mlp_status mlp_op_argmax(int dtype, int64_t B, int64_t C, const void* z, int64_t
  *   lse[i] = log sum_c exp(z_ic / T)  (fp32 [B], nullable),
  *   tail[i] the same over the columns not among the k  (fp32 [B], nullable;
  *   -infinity where nothing is left), as mlp_op_distill takes it.
- * 1 <= k <= 256, k <= C <= 393216; T = temperature, 1e-6 to 1e6 (it changes the two sums
+ * 1 <= k <= 256, k <= C <= 384000; T = temperature, 1e-6 to 1e6 (it changes the two sums
  * alone).  Entries of -infinity are taken like others, last.  Where a row holds NaN or
  * +infinity its lse is NaN, and its tail too unless only the k entries hold it.  Any
  * base and pitch.  Nothing written may overlap anything read. */
-enum { MLP_TOPK_MAX = 256, MLP_TOPK_MAX_COLUMNS = 393216 };
+enum { MLP_TOPK_MAX = 256, MLP_TOPK_MAX_COLUMNS = 384000 };
 mlp_status mlp_op_topk(int dtype, int64_t B, int64_t C, int64_t k, const void* z, int64_t ldz, float temperature,
                        float* values, int64_t ldv, int32_t* indices, int64_t ldi, float* lse, float* tail,
                        void* stream);
@@ -206,7 +206,7 @@ mlp_status mlp_op_topk(int dtype, int64_t B, int64_t C, int64_t k, const void* z
  * err_dev, and that row's loss and gradient are 0.  A teacher that gives weight
  * where the student has none (z = -infinity) has an infinite loss; a row of z that
  * holds NaN or +infinity, or nothing but -infinity, gives NaN.
- * 1 <= k <= 256, k <= C <= 393216; T from 1e-6 to 1e6.  Any base and pitch; rows of dz with
+ * 1 <= k <= 256, k <= C <= 384000; T from 1e-6 to 1e6.  Any base and pitch; rows of dz with
  * another address modulo 16 than z's are written element by element. */
 mlp_status mlp_op_distill(int dtype, int64_t B, int64_t C, int64_t k, const void* z, int64_t ldz,
                           const float* t_values, int64_t ldtv, const int32_t* t_indices, int64_t ldti,
@@ -228,7 +228,7 @@ mlp_status mlp_op_distill(int dtype, int64_t B, int64_t C, int64_t k, const void
  * and token.  A beam of score -infinity has every total -infinity (a search starts with
  * scores 0, -infinity, ...), and so has a row of nothing but -infinity; one whose score is
  * NaN or +infinity or whose row holds NaN or +infinity has NaN, below everything.
- * beams <= 32, m <= 64, m <= beams * C, C <= 393216.  With m = beams, scores_out may be scores
+ * beams <= 32, m <= 64, m <= beams * C, C <= 384000.  With m = beams, scores_out may be scores
  * and done_out may be done.  workspace: 8-byte aligned, at least the bytes below (0: a
  * shape that is refused); workspaces of calls that may overlap must not. */
 size_t mlp_op_beam_select_workspace_bytes(int dtype, int64_t batch, int64_t beams, int64_t C, int64_t m);

@@ -28,7 +28,7 @@ PLANE_P, PLANE_G, PLANE_M, PLANE_V = 0, 1, 2, 3
 OPTIM_ADAMW, OPTIM_ADAM, OPTIM_SGD = 0, 1, 2
 OPTIM_WS_FLOATS = 1216   # op-level clipping workspace (floats)
 LOSS_CE, LOSS_MSE = 0, 1
-TOPK_MAX, TOPK_MAX_COLUMNS = 256, 393216
+TOPK_MAX, TOPK_MAX_COLUMNS = 256, 384000
 
 
 class MlpError(RuntimeError):

@@ -86,14 +86,14 @@ __device__ __forceinline__ float divergence(float p, float q, float r) {
 }
 
 // TWO: the hard labels' softmax is at another temperature than the soft ones'.
-template <typename T, bool CLUSTER, bool TWO>
-__global__ void __launch_bounds__(512) distill_kernel(const __grid_constant__ DistillParams p) {
+template <typename T, bool CLUSTER, bool TWO, int NT>
+__global__ void __launch_bounds__(NT, NT <= 256 ? 3 : 1) distill_kernel(const __grid_constant__ DistillParams p) {
   pdl_enter();
   constexpr int E = kPer16<T>;
   typedef typename BitsOf<T>::type Bits;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ DistillShared sh;
-  const int tid = threadIdx.x, NT = blockDim.x;
+  const int tid = threadIdx.x;
   const int64_t row = blockIdx.x;
   const int rank = CLUSTER ? (int)blockIdx.z : 0, blocks = CLUSTER ? (int)gridDim.z : 1;
   const int lo = rank * p.per, n = max(0, min(p.per, p.C - lo));
@@ -115,21 +115,21 @@ __global__ void __launch_bounds__(512) distill_kernel(const __grid_constant__ Di
   unsigned char* buf = smem + (p.k * 4 + 15) / 16 * 16;
   if (mine) zt[tid] = -INFINITY;
   if (CLUSTER) cluster_arrive();
-  Slice<T> s;
+  Slice<T, NT> s;
   s.load(buf, reinterpret_cast<const T*>(p.z) + row * p.ldz, lo, n);
 
   // ---- the teacher, while the row is on its way
   bool bad = mine && (col < -1 || col >= p.C);
   if (p.labels) bad |= y < 0 || y >= p.C;
   if (col < 0) t = -INFINITY;                   // (unused entries' values are not looked at)
-  const float tm = block_max(t, sh.red[0]);
+  const float tm = block_max<NT>(t, sh.red[0]);
   const float tm0 = tm > -INFINITY ? tm : 0.f;
   float tref = fmaxf(tm / p.T, tail);
   if (!(tref > -INFINITY)) tref = 0.f;
   const float dl = tm0 / p.T - tref;            // what the largest is below the reference
   const float pe = mine ? expf((t - tm0) / p.T + dl) : 0.f;
   const float U = expf(tail - tref);
-  const float St = block_sum(pe, sh.red[1]) + U;
+  const float St = block_sum<NT>(pe, sh.red[1]) + U;
   const bool has = !(St == 0.f);
 
   // ---- the k columns out of the row
@@ -150,10 +150,10 @@ __global__ void __launch_bounds__(512) distill_kernel(const __grid_constant__ Di
   __syncthreads();
 
   // ---- the sums over the others
-  float most = block_max(max_of(s), sh.red[2]);
+  float most = block_max<NT>(max_of(s), sh.red[2]);
   const float ref = most > -INFINITY ? most : 0.f;
-  float sum = block_sum(sum_exp(s, Exponent(ref, p.c)), sh.red[3]), sum1 = 0.f;
-  if constexpr (TWO) sum1 = block_sum(sum_exp(s, Exponent(ref, kLog2e)), sh.red[4]);
+  float sum = block_sum<NT>(sum_exp(s, Exponent(ref, p.c)), sh.red[3]), sum1 = 0.f;
+  if constexpr (TWO) sum1 = block_sum<NT>(sum_exp(s, Exponent(ref, kLog2e)), sh.red[4]);
 
   // ---- all slices together
   float zy = 0.f;
@@ -197,16 +197,16 @@ __global__ void __launch_bounds__(512) distill_kernel(const __grid_constant__ Di
     return;
   }
   const float rest = most > -INFINITY ? most : 0.f;   // the others' exponents are relative to this
-  const float m = fmaxf(most, block_max(mine ? ztj : -INFINITY, sh.red[5]));
+  const float m = fmaxf(most, block_max<NT>(mine ? ztj : -INFINITY, sh.red[5]));
   const float m0 = m > -INFINITY ? m : 0.f;
   const float q = mine ? expf((ztj - m0) / p.T) : 0.f;
   const float f = sum != 0.f ? ex2((rest - m0) * p.c) : 0.f;
-  const float S = fmaf(sum, f, block_sum(q, sh.red[6]));
+  const float S = fmaf(sum, f, block_sum<NT>(q, sh.red[6]));
   float q1 = q, f1 = f, S1 = S;
   if constexpr (TWO) {
     q1 = mine ? expf(ztj - m0) : 0.f;
     f1 = sum1 != 0.f ? ex2((rest - m0) * kLog2e) : 0.f;
-    S1 = fmaf(sum1, f1, block_sum(q1, sh.red[7]));
+    S1 = fmaf(sum1, f1, block_sum<NT>(q1, sh.red[7]));
   }
   const float pj = has ? pe / St : 0.f, pr = has ? U / St : 0.f;
 
@@ -225,11 +225,11 @@ __global__ void __launch_bounds__(512) distill_kernel(const __grid_constant__ Di
     } else {
       const F2 c2 = pack2(p.c, p.c), r2 = pack2(-eg.rc, -eg.rc), A2 = pack2(A, A);
       const F2 c12 = pack2(kLog2e, kLog2e), r12 = pack2(-eg1.rc, -eg1.rc), B2 = pack2(B1, B1);
-      const auto step = [&](const uint4& u) {
+      const auto step = [&](const uint4& in) {
         uint32_t o[4];
 #pragma unroll
         for (int h = 0; h < E / 2; ++h) {
-          const F2 x2 = pair_of<T>(u, h);
+          const F2 x2 = pair_of<T>(in, h);
           float x, y;
           unpack2(fma2(x2, c2, r2), x, y);
           F2 d = mul2(pack2(ex2(x), ex2(y)), A2);
@@ -248,15 +248,15 @@ __global__ void __launch_bounds__(512) distill_kernel(const __grid_constant__ Di
         }
         return make_uint4(o[0], o[1], o[2], o[3]);
       };
-      int v = tid;
-      for (; v + 3 * NT < s.nvec; v += 4 * NT) {   // four loads in flight
-        const uint4 u0 = s.units()[v], u1 = s.units()[v + NT], u2 = s.units()[v + 2 * NT], u3 = s.units()[v + 3 * NT];
-        s.units()[v] = step(u0);
-        s.units()[v + NT] = step(u1);
-        s.units()[v + 2 * NT] = step(u2);
-        s.units()[v + 3 * NT] = step(u3);
+      int u = 0;
+      for (; u + 4 <= s.nu; u += 4) {   // (four loads in flight)
+        const uint4 u0 = s.mine(u), u1 = s.mine(u + 1), u2 = s.mine(u + 2), u3 = s.mine(u + 3);
+        s.mine(u) = step(u0);
+        s.mine(u + 1) = step(u1);
+        s.mine(u + 2) = step(u2);
+        s.mine(u + 3) = step(u3);
       }
-      for (; v < s.nvec; v += NT) s.units()[v] = step(s.units()[v]);
+      for (; u < s.nu; ++u) s.mine(u) = step(s.mine(u));
     }
     __syncthreads();
     if (here) {
@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(512) distill_kernel(const __grid_constant__ Di
     if (has && p.b != 0.f) {
       const float ln = logf(St / S), R = sum * f / S;
       if (mine && col >= 0) kd = divergence(pj, q / S, ((t - ztj) - (tm0 - m0)) / p.T + dl - ln);
-      kd = block_sum(kd, sh.red[8]);
+      kd = block_sum<NT>(kd, sh.red[8]);
       kd += divergence(pr, R, R > 1e-30f ? logf(pr / R) : logf(pr) - ((rest - m0) / p.T + logf(sum) - logf(S)));
       kd *= p.b;
     }
@@ -302,10 +302,16 @@ __global__ void __launch_bounds__(512) distill_kernel(const __grid_constant__ Di
   if (tid == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 
+template <typename T, bool CLUSTER, bool TWO>
+const void* distill_func(int threads) {
+  return threads == 128   ? (const void*)distill_kernel<T, CLUSTER, TWO, 128>
+         : threads == 256 ? (const void*)distill_kernel<T, CLUSTER, TWO, 256>
+                          : (const void*)distill_kernel<T, CLUSTER, TWO, 512>;
+}
 template <typename T>
-const void* distill_func(bool cluster, bool two) {
-  if (cluster) return two ? (const void*)distill_kernel<T, true, true> : (const void*)distill_kernel<T, true, false>;
-  return two ? (const void*)distill_kernel<T, false, true> : (const void*)distill_kernel<T, false, false>;
+const void* distill_func(bool cluster, bool two, int threads) {
+  if (cluster) return two ? distill_func<T, true, true>(threads) : distill_func<T, true, false>(threads);
+  return two ? distill_func<T, false, true>(threads) : distill_func<T, false, false>(threads);
 }
 
 }  // namespace
@@ -318,7 +324,7 @@ int distill_plan(const DistillOp& op, LaunchRec* rec, char* err, size_t errlen) 
     return -1;
   }
   const int es = op.dtype == DT_F32 ? 4 : 2;
-  const Cut cut = cut_rows(op.B, op.C, es, (int)op.k);
+  const Cut cut = cut_rows(op.C, es, (int)op.k);
   DistillParams p{};
   p.z = op.z; p.ldz = op.ldz; p.dz = op.dz; p.lddz = op.lddz;
   p.tv = op.t_values; p.ldtv = op.ldtv; p.ti = op.t_indices; p.ldti = op.ldti; p.tail = op.t_tail;
@@ -331,9 +337,9 @@ int distill_plan(const DistillOp& op, LaunchRec* rec, char* err, size_t errlen) 
   rec->grid = dim3((unsigned)op.B, 1, (unsigned)cut.cluster);
   rec->block = dim3((unsigned)cut.threads);
   rec->cluster = (unsigned)cut.cluster;
-  rec->smem = (unsigned)((op.k * 4 + 15) / 16 * 16 + slice_buffer(cut.per, es));
-  rec->func = op.dtype == DT_F32 ? distill_func<float>(cut.cluster > 1, two)
-                                 : distill_func<__nv_bfloat16>(cut.cluster > 1, two);
+  rec->smem = (unsigned)((op.k * 4 + 15) / 16 * 16 + slice_buffer(cut.per, es, cut.threads));
+  rec->func = op.dtype == DT_F32 ? distill_func<float>(cut.cluster > 1, two, cut.threads)
+                                 : distill_func<__nv_bfloat16>(cut.cluster > 1, two, cut.threads);
   rec->name = "distill";
   rec->set_args(p);
   return 1;

@@ -5,9 +5,14 @@
 // of a cluster.  The slice is copied in 16-byte units whatever the row's
 // alignment: shared memory keeps the row's phase (its address modulo 16), the
 // units that the row only partly covers are copied element by element, and
-// their other elements are -infinity, so that every pass runs over whole
-// units without tests.  A thread copies the units that it later reads first
-// (tid, tid + NT, ...) and need not wait for other threads to read them.
+// what they and the units behind them hold besides is -infinity, so that
+// every pass runs over whole units, as many for each thread, without tests.  A
+// thread copies the units that it later reads first (tid, tid + NT, ...) and need
+// not wait for other threads to read them.
+//
+// These kernels are bound by instruction issue before they are by DRAM (a row of
+// 32000 bf16 leaves an SM about 11000 issue slots), so block sizes are constants
+// and loops have uniform counts.
 #pragma once
 #include "common.cuh"
 #include "f32x2.cuh"
@@ -20,9 +25,8 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kSMs = 152;
 constexpr int kMaxK = 256;                 // entries kept of a row
 constexpr int kCand = 1024;                // candidates ranked at most
-constexpr int kCounted = 256;              // of which so many by counting
 constexpr int kHits = 2048;                // 16-byte units looked through for them at most, shared out to the warps
-constexpr int64_t kMaxC = 393216;          // columns: eight slices of 192 KB of fp32
+constexpr int64_t kMaxC = 384000;          // columns: eight slices of 192000 bytes of fp32
 constexpr int64_t kSliceBytes = 64 * 1024; // a slice of at most this leaves room for three blocks on an SM
 
 // 2^t; subnormal results are flushed to zero (PTX ex2.approx).
@@ -86,31 +90,49 @@ __device__ __forceinline__ void unit_floats(uint4 a, float (&v)[kPer16<T>]) {
     }
   }
 }
-// Its largest element; NaN is passed over (-infinity where all are NaN).
-template <typename T>
-__device__ __forceinline__ float unit_max(uint4 a) {
-  if constexpr (sizeof(T) == 4) {
-    return fmaxf(fmaxf(fmaxf(__uint_as_float(a.x), __uint_as_float(a.y)), fmaxf(__uint_as_float(a.z), __uint_as_float(a.w))),
-                 -INFINITY);
-  } else {
-    const auto b = [](uint32_t w) { return *reinterpret_cast<__nv_bfloat162*>(&w); };
-    const __nv_bfloat162 m = __hmax2(__hmax2(b(a.x), b(a.y)), __hmax2(b(a.z), b(a.w)));
-    return fmaxf(fmaxf(__low2float(m), __high2float(m)), -INFINITY);
+// The largest element of a unit, or of several, NaN passed over; bf16: of the
+// even elements and of the odd ones, side by side.
+template <typename T> struct Most;
+template <> struct Most<float> {
+  float m = -INFINITY;
+  __device__ __forceinline__ Most() {}
+  __device__ __forceinline__ explicit Most(const uint4& a) {
+    m = fmaxf(fmaxf(__uint_as_float(a.x), __uint_as_float(a.y)), fmaxf(__uint_as_float(a.z), __uint_as_float(a.w)));
   }
-}
+  __device__ __forceinline__ void take(const Most& o) { m = fmaxf(m, o.m); }
+  __device__ __forceinline__ bool reaches(float x) const { return m >= x; }
+  __device__ __forceinline__ float value() const { return fmaxf(m, -INFINITY); }
+};
+template <> struct Most<__nv_bfloat16> {
+  __nv_bfloat162 m;
+  static __device__ __forceinline__ __nv_bfloat162 two(uint32_t w) { return *reinterpret_cast<__nv_bfloat162*>(&w); }
+  __device__ __forceinline__ Most() { m = two(0xFF80FF80u); }
+  __device__ __forceinline__ explicit Most(const uint4& a) {
+    m = __hmax2(__hmax2(two(a.x), two(a.y)), __hmax2(two(a.z), two(a.w)));
+  }
+  __device__ __forceinline__ void take(const Most& o) { m = __hmax2(m, o.m); }
+  __device__ __forceinline__ bool reaches(float x) const {
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(&m);
+    return __uint_as_float(w << 16) >= x || __uint_as_float(w & 0xFFFF0000u) >= x;
+  }
+  __device__ __forceinline__ float value() const { return fmaxf(fmaxf(__low2float(m), __high2float(m)), -INFINITY); }
+};
 template <typename T> __device__ __forceinline__ T minus_inf();
 template <> __device__ __forceinline__ float minus_inf<float>() { return -INFINITY; }
 template <> __device__ __forceinline__ __nv_bfloat16 minus_inf<__nv_bfloat16>() { return __ushort_as_bfloat16(0xFF80); }
 
 // The slice [lo, lo + n) of a row as shared memory holds it: element i is at
-// elems()[ph + i], units() unit v holds the elements v E - ph .. + E.
-template <typename T>
+// elems()[ph + i], units() unit v holds the elements v E - ph .. + E.  Thread tid
+// has the units tid + u NT, u < nu; unit nvec is the first behind the slice.
+template <typename T, int NT_>
 struct Slice {
+  static constexpr int NT = NT_;
   unsigned char* buf;
-  int lo, n, ph, nvec;
+  int lo, n, ph, nvec, nu;
 
   __device__ __forceinline__ T* elems() const { return reinterpret_cast<T*>(buf); }
   __device__ __forceinline__ uint4* units() const { return reinterpret_cast<uint4*>(buf); }
+  __device__ __forceinline__ uint4& mine(int u) const { return units()[threadIdx.x + u * NT]; }
   __device__ __forceinline__ T& at(int i) const { return elems()[ph + i]; }
 
   // Starts the copies of this thread's units.
@@ -122,52 +144,79 @@ struct Slice {
     const T* g = row + lo;
     ph = (int)(((uintptr_t)g & 15) / sizeof(T));
     nvec = n > 0 ? (ph + n + E - 1) / E : 0;
-    const unsigned char* g0 = reinterpret_cast<const unsigned char*>(g - ph);
-    const uint32_t s0 = smem_addr(buf);
-    for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
-      if (v * E >= ph && (v + 1) * E <= ph + n) {
-        copy16_async(s0 + 16u * v, g0 + 16ll * v);
+    nu = (nvec + NT - 1) / NT;
+    const int whole = (ph + n) / E;   // the units from ph > 0 on to here are the row's alone
+    const int full = whole / NT;
+    const unsigned char* g0 = reinterpret_cast<const unsigned char*>(g - ph) + 16 * threadIdx.x;
+    const uint32_t s0 = smem_addr(buf) + 16u * threadIdx.x;
+    const auto edge = [&](int u) {
+      const int v = threadIdx.x + u * NT;
+      if (v >= (ph > 0) && v < whole) {
+        copy16_async(s0 + 16u * NT * u, g0 + 16ll * NT * u);
       } else {
-#pragma unroll
         for (int e = 0; e < E; ++e) {
           const int i = v * E + e - ph;
           elems()[v * E + e] = i >= 0 && i < n ? g[i] : minus_inf<T>();
         }
       }
+    };
+    int u = 0;
+    if (ph > 0 && nu > 0) edge(u++);
+#pragma unroll 4
+    for (; u < full; ++u) copy16_async(s0 + 16u * NT * u, g0 + 16ll * NT * u);
+    for (; u < nu; ++u) edge(u);
+  }
+  // f(unit) for this thread's units, four loads in flight.
+  template <typename F>
+  __device__ __forceinline__ void each_unit(F f) const {
+    int u = 0;
+    for (; u + 4 <= nu; u += 4) {
+      const uint4 a = mine(u), b = mine(u + 1), c = mine(u + 2), d = mine(u + 3);
+      f(a);
+      f(b);
+      f(c);
+      f(d);
     }
+    for (; u < nu; ++u) f(mine(u));
   }
   // f(i, value) for the elements of this thread's units.
   template <typename F>
   __device__ __forceinline__ void each(F f) const {
     constexpr int E = kPer16<T>;
-    for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
+    for (int u = 0; u < nu; ++u) {
       float x[E];
-      unit_floats<T>(units()[v], x);
+      unit_floats<T>(mine(u), x);
+      const int i0 = ((int)threadIdx.x + u * NT) * E - ph;
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const int i = v * E + e - ph;
-        if (i >= 0 && i < n) f(i, x[e]);
-      }
+      for (int e = 0; e < E; ++e)
+        if (i0 + e >= 0 && i0 + e < n) f(i0 + e, x[e]);
     }
   }
 };
-// Bytes of a slice's buffer (the phase can add a unit).
-inline int64_t slice_buffer(int64_t per, int es) { return (per * es + 15) / 16 * 16 + 16; }
+// Bytes of a slice's buffer: whole rounds of units (the phase can add one).
+inline int64_t slice_buffer(int64_t per, int es, int threads) { return round_up(per * es / 16 + 1, threads) * 16; }
 
-// Sums and maxima over the block (4, 8 or 16 warps), the same in every thread;
+// Sums and maxima over the block of NT threads, the same in every thread;
 // red: a place of its own for each call.
 struct __align__(16) Red { float v[16]; };
-__device__ __forceinline__ float block_sum(float v, Red& red) {
-  v = warp_sum(v);
-  if ((threadIdx.x & 31) == 0) red.v[threadIdx.x >> 5] = v;
-  __syncthreads();
+template <int NT>
+__device__ __forceinline__ float red_sum(const Red& red) {
   float s = 0.f;
-  for (int w = 0; w < (int)blockDim.x / 32; w += 4) {
+#pragma unroll
+  for (int w = 0; w < NT / 32; w += 4) {
     const float4 a = *reinterpret_cast<const float4*>(red.v + w);
     s += (a.x + a.y) + (a.z + a.w);
   }
   return s;
 }
+template <int NT>
+__device__ __forceinline__ float block_sum(float v, Red& red) {
+  v = warp_sum(v);
+  if ((threadIdx.x & 31) == 0) red.v[threadIdx.x >> 5] = v;
+  __syncthreads();
+  return red_sum<NT>(red);
+}
+template <int NT>
 __device__ __forceinline__ void block_sums(float& u, float& v, Red& ru, Red& rv) {
   u = warp_sum(u);
   v = warp_sum(v);
@@ -176,19 +225,17 @@ __device__ __forceinline__ void block_sums(float& u, float& v, Red& ru, Red& rv)
     rv.v[threadIdx.x >> 5] = v;
   }
   __syncthreads();
-  u = v = 0.f;
-  for (int w = 0; w < (int)blockDim.x / 32; w += 4) {
-    const float4 a = *reinterpret_cast<const float4*>(ru.v + w), b = *reinterpret_cast<const float4*>(rv.v + w);
-    u += (a.x + a.y) + (a.z + a.w);
-    v += (b.x + b.y) + (b.z + b.w);
-  }
+  u = red_sum<NT>(ru);
+  v = red_sum<NT>(rv);
 }
+template <int NT>
 __device__ __forceinline__ float block_max(float v, Red& red) {
   v = warp_max(v);
   if ((threadIdx.x & 31) == 0) red.v[threadIdx.x >> 5] = v;
   __syncthreads();
   float s = -INFINITY;
-  for (int w = 0; w < (int)blockDim.x / 32; w += 4) {
+#pragma unroll
+  for (int w = 0; w < NT / 32; w += 4) {
     const float4 a = *reinterpret_cast<const float4*>(red.v + w);
     s = fmaxf(s, fmaxf(fmaxf(a.x, a.y), fmaxf(a.z, a.w)));
   }
@@ -218,8 +265,8 @@ struct Exponent {
   __device__ __forceinline__ float one(float x) const { return ex2(far ? (x - ref) * c : fmaf(x, c, -rc)); }
 };
 // The sum over this thread's units of exp((x - ref) / T).
-template <typename T>
-__device__ __forceinline__ float sum_exp(const Slice<T>& s, const Exponent& q) {
+template <typename T, int NT>
+__device__ __forceinline__ float sum_exp(const Slice<T, NT>& s, const Exponent& q) {
   float sum;
   if (q.far) {
     sum = 0.f;
@@ -227,7 +274,7 @@ __device__ __forceinline__ float sum_exp(const Slice<T>& s, const Exponent& q) {
   } else {
     F2 a0 = pack2(0.f, 0.f), a1 = a0;
     const F2 c2 = pack2(q.c, q.c), r2 = pack2(-q.rc, -q.rc);
-    const auto add = [&](const uint4& u) {
+    s.each_unit([&](const uint4& u) {
 #pragma unroll
       for (int h = 0; h < kPer16<T> / 2; ++h) {
         float x, y;
@@ -236,46 +283,25 @@ __device__ __forceinline__ float sum_exp(const Slice<T>& s, const Exponent& q) {
         if (h & 1) a1 = add2(a1, e);
         else a0 = add2(a0, e);
       }
-    };
-    const int step = blockDim.x;
-    int v = threadIdx.x;
-    for (; v + 3 * step < s.nvec; v += 4 * step) {   // four loads in flight
-      const uint4 u0 = s.units()[v], u1 = s.units()[v + step], u2 = s.units()[v + 2 * step], u3 = s.units()[v + 3 * step];
-      add(u0);
-      add(u1);
-      add(u2);
-      add(u3);
-    }
-    for (; v < s.nvec; v += step) add(s.units()[v]);
+    });
     sum = sum2(add2(a0, a1));
   }
   return sum * q.scale;
 }
-template <typename T>
-__device__ __forceinline__ float max_of(const Slice<T>& s) {
-  float m = -INFINITY;
-  if constexpr (sizeof(T) == 4) {
-#pragma unroll 4
-    for (int v = threadIdx.x; v < s.nvec; v += blockDim.x) m = fmaxf(m, unit_max<T>(s.units()[v]));
-  } else {
-    const auto b = [](uint32_t w) { return *reinterpret_cast<__nv_bfloat162*>(&w); };
-    __nv_bfloat162 m2 = b(0xFF80FF80u);
-#pragma unroll 4
-    for (int v = threadIdx.x; v < s.nvec; v += blockDim.x) {
-      const uint4 a = s.units()[v];
-      m2 = __hmax2(m2, __hmax2(__hmax2(b(a.x), b(a.y)), __hmax2(b(a.z), b(a.w))));
-    }
-    m = fmaxf(__low2float(m2), __high2float(m2));
-  }
-  return m;
+template <typename T, int NT>
+__device__ __forceinline__ float max_of(const Slice<T, NT>& s) {
+  Most<T> m;
+  s.each_unit([&](const uint4& u) { m.take(Most<T>(u)); });
+  return m.value();
 }
 
 // How rows are cut: `cluster` blocks of `threads` threads share a row, `per`
-// columns each.
+// columns each, at most `units` units a thread.
 struct Cut {
-  int cluster, per, threads;
+  int cluster, per, threads, units;
 };
-Cut cut_rows(int64_t rows, int64_t C, int es, int k);
+// `threads`: at least so many.
+Cut cut_rows(int64_t C, int es, int threads);
 
 }  // namespace lg
 }  // namespace mlpk

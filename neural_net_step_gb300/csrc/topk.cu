@@ -32,15 +32,19 @@
 namespace mlpk {
 namespace lg {
 
-Cut cut_rows(int64_t rows, int64_t C, int es, int k) {
+// A slice of at most 64 KB leaves room for three blocks on an SM.  Rows are not
+// cut further where they are few: what the blocks of a cluster then have to tell
+// one another takes longer than a block for the whole row (one row of 32000 bf16,
+// k = 50: 6.6 us, eight blocks 8.1).
+Cut cut_rows(int64_t C, int es, int threads) {
   int cs = 1;
   while (cs < 8 && ceil_div(C, cs) * es > kSliceBytes) cs *= 2;
   Cut c;
   c.cluster = cs;
   c.per = (int)round_up(ceil_div(C, cs), 16 / es);
-  const int64_t units = c.per * es / 16;
-  c.threads = units <= 256 ? 128 : units < 4096 ? 256 : 512;   // (a row's phase adds a unit)
-  while (c.threads < 2 * k && c.threads < 512) c.threads *= 2;
+  const int64_t units = c.per * es / 16 + 1;   // (a row's phase adds one)
+  c.threads = units <= 3 * 128 && threads <= 128 ? 128 : units <= 16 * 256 && threads <= 256 ? 256 : 512;
+  c.units = c.threads == 128 ? 3 : c.threads == 256 ? 16 : units <= 9 * 512 ? 9 : 24;
   return c;
 }
 
@@ -72,13 +76,14 @@ struct TopkShared {
 };
 
 // Number of set flags over the block, the same in every thread.
+template <int NT>
 __device__ __forceinline__ int block_count(int v, TopkShared& sh) {
   v = __reduce_add_sync(0xffffffffu, v);
   __syncthreads();
   if ((threadIdx.x & 31) == 0) sh.total[threadIdx.x >> 5] = v;
   __syncthreads();
   int s = 0;
-  for (int w = 0; w < (int)blockDim.x / 32; ++w) s += sh.total[w];
+  for (int w = 0; w < NT / 32; ++w) s += sh.total[w];
   return s;
 }
 
@@ -96,19 +101,14 @@ __device__ __forceinline__ U warp_sort_down(U x) {
   }
   return x;
 }
-// The n-th largest of the warp's values, n from 1: each lane counts the larger
-// ones (room: 32 places).
-__device__ __forceinline__ uint32_t warp_nth(uint32_t x, int n, uint32_t* room) {
-  room[threadIdx.x & 31] = x;
-  __syncwarp();
-  int larger = 0;
-#pragma unroll
-  for (int b = 0; b < 8; ++b) {
-    const uint4 o = reinterpret_cast<const uint4*>(room)[b];
-    larger += (o.x > x) + (o.y > x) + (o.z > x) + (o.w > x);
+// The n-th largest of the warp's values, n from 1.
+__device__ __forceinline__ uint32_t warp_nth(uint32_t x, int n) {
+  if (n > 4) return __shfl_sync(0xffffffffu, warp_sort_down(x), n - 1);
+  while (true) {
+    const uint32_t m = __reduce_max_sync(0xffffffffu, x);
+    if (--n <= 0) return m;
+    if ((threadIdx.x & 31) == __ffs(__ballot_sync(0xffffffffu, x == m)) - 1) x = 0;
   }
-  __syncwarp();
-  return __reduce_min_sync(0xffffffffu, larger < n ? x : 0xFFFFFFFFu);
 }
 
 // A candidate of a slice: larger is better, lower element first among equals; 0
@@ -134,12 +134,12 @@ template <> struct Cand<uint32_t> {
 // Candidates where the threshold did not leave a fit number of them: exactly
 // those not below the kk-th largest, or the kk largest themselves.  tau: a first
 // guess of the kk-th largest's key, or 0.
-template <typename T, typename K>
-__device__ __noinline__ void search(const Slice<T>& s, int kk, uint32_t tau, K* cand, TopkShared& sh) {
+template <typename T, typename K, int NT>
+__device__ __noinline__ void search(const Slice<T, NT>& s, int kk, uint32_t tau, K* cand, TopkShared& sh) {
   const auto reach = [&](uint32_t key) {
     int c = 0;
     s.each([&](int, float x) { c += key_of(x) >= key; });
-    return block_count(c, sh);
+    return block_count<NT>(c, sh);
   };
   uint32_t v = tau;
   if (tau == 0 || tau == 0xFFFFFFFFu || reach(tau) < kk || reach(tau + 1) >= kk) {
@@ -155,7 +155,7 @@ __device__ __noinline__ void search(const Slice<T>& s, int kk, uint32_t tau, K* 
       const int mid = (lo + hi) / 2;
       int c = 0;
       s.each([&](int i, float x) { c += i <= mid && key_of(x) == v; });
-      if (above + block_count(c, sh) >= kk) hi = mid;
+      if (above + block_count<NT>(c, sh) >= kk) hi = mid;
       else lo = mid + 1;
     }
     last = lo;
@@ -173,25 +173,38 @@ __device__ __noinline__ void search(const Slice<T>& s, int kk, uint32_t tau, K* 
   __syncthreads();
 }
 
-// Adds to `place` how many entries of the descending lists 0 .. n - 1 but `not_in`
-// are larger than e.  Lists are `len` entries long and lie one behind the other;
-// eight of them are searched side by side.
-template <typename K>
-__device__ __forceinline__ void add_larger(int& place, const K* lists, int n, int not_in, int len, K e) {
-  const int top = 1 << (31 - __clz(len));
-  for (int b0 = 0; b0 < n; b0 += 8) {
-    int at[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    for (int step = top; step > 0; step >>= 1) {
+// Entries larger than e in N lists side by side, `stride` apart, each `len` long and
+// descending.  Every load has a place to go: none waits for a branch.
+template <int N, typename K>
+__device__ __forceinline__ void larger_in(int (&at)[N], const K* lists, int stride, int len, K e) {
 #pragma unroll
-      for (int b = 0; b < 8; ++b) {
-        const int to = at[b] + step;   // (every load has a place to go: none waits for a branch)
-        const K v = lists[min(b0 + b, n - 1) * len + min(to, len) - 1];
-        at[b] = to <= len && v > e ? to : at[b];
-      }
+  for (int b = 0; b < N; ++b) at[b] = 0;
+  for (int step = 1 << (31 - __clz(len)); step > 0; step >>= 1) {
+#pragma unroll
+    for (int b = 0; b < N; ++b) {
+      const int to = at[b] + step;
+      const K v = lists[b * stride + min(to, len) - 1];
+      at[b] = to <= len && v > e ? to : at[b];
     }
-#pragma unroll
-    for (int b = 0; b < 8; ++b) place += b0 + b == not_in || b0 + b >= n ? 0 : at[b];
   }
+}
+// The same for runs of 32 one behind the other.
+template <int N, typename K>
+__device__ __forceinline__ int larger_in_runs(const K* runs, int not_in, K e) {
+  int at[N], sum = 0;
+#pragma unroll
+  for (int b = 0; b < N; ++b) at[b] = 0;
+#pragma unroll
+  for (int step = 16; step > 0; step >>= 1)
+#pragma unroll
+    for (int b = 0; b < N; ++b)
+      if (runs[b * 32 + at[b] + step - 1] > e) at[b] += step;
+#pragma unroll
+  for (int b = 0; b < N; ++b) {
+    at[b] += runs[b * 32 + at[b]] > e;
+    if (b != not_in) sum += at[b];
+  }
+  return sum;
 }
 
 // Sum of n over the lanes before this one and over all, n < 2^BITS.
@@ -210,46 +223,59 @@ __device__ __forceinline__ int before_lane(int n, int& all) {
 }
 
 // U: units a thread has at most.
-template <typename T, bool CLUSTER, int U>
-__global__ void __launch_bounds__(U <= 16 ? 256 : 512, U <= 16 ? 3 : 1) topk_kernel(const __grid_constant__ TopkParams p) {
+template <typename T, bool CLUSTER, int NT, int U>
+__global__ void __launch_bounds__(NT, U <= 16 ? (NT <= 256 ? 3 : 2) : 1) topk_kernel(const __grid_constant__ TopkParams p) {
   pdl_enter();
   constexpr int E = kPer16<T>;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ TopkShared sh;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, NT = blockDim.x, warps = NT >> 5;
+  constexpr int warps = NT / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t row = blockIdx.x;
   const int rank = CLUSTER ? (int)blockIdx.z : 0, blocks = CLUSTER ? (int)gridDim.z : 1;
   // beams that offer nothing of their row: the merge knows without it
   if (p.stats && ((p.done && p.done[row]) || !(fabsf(p.scores[row]) < INFINITY))) return;
   if (CLUSTER) cluster_arrive();
 
-  typedef typename std::conditional<U <= 16 && sizeof(T) == 2, uint32_t, uint64_t>::type K;
+  typedef typename std::conditional<sizeof(T) == 2 && NT * U * 8 <= 65536, uint32_t, uint64_t>::type K;
   uint64_t* best = reinterpret_cast<uint64_t*>(smem);    // [k, even]: the row's, descending
   uint64_t* lists = best + ((p.k + 1) & ~1);             // [blocks][k], descending (0: none); the first block has all
   uint64_t* own = CLUSTER ? lists + (int64_t)rank * p.k : best;
-  K* cand = reinterpret_cast<K*>(lists + (CLUSTER ? blocks * p.k : 0));   // [kCand]
+  K* cand = reinterpret_cast<K*>(lists + (CLUSTER ? 8 * p.k : 0));   // [kCand]
   uint16_t* hits = reinterpret_cast<uint16_t*>(cand + kCand);                      // [kHits]
   unsigned char* buf = reinterpret_cast<unsigned char*>(((uintptr_t)(hits + kHits) + 15) & ~(uintptr_t)15);
 
-  Slice<T> s;
+  Slice<T, NT> s;
   s.load(buf, reinterpret_cast<const T*>(p.z) + row * p.ldz, rank * p.per, min(p.per, p.C - rank * p.per));
   const int kk = min(p.k, s.n);
   if (tid == 0) sh.count = 0;
-  for (int a = tid; a < kCounted + 16; a += NT) cand[a] = 0;
   copies_wait();
 
   // 1. a threshold that at least kk elements reach
-  float um[U], most = -INFINITY;
+  Most<T> um[U], most;
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int v = tid + u * NT;
-    um[u] = v < s.nvec ? unit_max<T>(s.units()[v]) : -INFINITY;
-    most = fmaxf(most, um[u]);
+  for (int u0 = 0; u0 < U; u0 += 4) {   // (four loads in flight)
+    if (u0 + 4 <= U && u0 + 4 <= s.nu) {
+      uint4 a[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) a[q] = s.mine(u0 + q);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (u0 + q < U) um[u0 + q] = Most<T>(a[q]);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (u0 + q < U && u0 + q < s.nu) um[u0 + q] = Most<T>(s.mine(u0 + q));
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (u0 + q < U) most.take(um[u0 + q]);
   }
-  const uint32_t nth = warp_nth(key_of(most), (kk + warps - 1) / warps, reinterpret_cast<uint32_t*>(hits) + warp * 32);
+  const uint32_t nth = warp_nth(key_of(most.value()), (kk + warps - 1) / warps);
   if (lane == 0) sh.tau[warp] = nth;
   __syncthreads();
   uint32_t tau = 0xFFFFFFFFu;
+#pragma unroll
   for (int w = 0; w < warps; w += 4) {
     const uint4 q = *reinterpret_cast<const uint4*>(sh.tau + w);
     tau = min(tau, min(min(q.x, q.y), min(q.z, q.w)));
@@ -259,8 +285,8 @@ __global__ void __launch_bounds__(U <= 16 ? 256 : 512, U <= 16 ? 3 : 1) topk_ker
   // 2. candidates and their places
   uint32_t reach = 0;
 #pragma unroll
-  for (int u = 0; u < U; ++u) reach |= (uint32_t)(um[u] >= least) << u;
-  const int room = kHits / warps;
+  for (int u = 0; u < U; ++u) reach |= (uint32_t)um[u].reaches(least) << u;
+  constexpr int room = kHits / warps;
   uint16_t* hit = hits + warp * room;
   int n_hits;
   for (int at = before_lane<5>(__popc(reach), n_hits); reach && at < room; reach &= reach - 1, ++at)
@@ -294,8 +320,6 @@ __global__ void __launch_bounds__(U <= 16 ? 256 : 512, U <= 16 ? 3 : 1) topk_ker
   if (count > kCand || count < kk) {
     search<T>(s, kk, count > kCand ? tau : 0u, cand, sh);
     count = sh.count;
-    for (int a = count + tid; a < kCounted + 16; a += NT) cand[a] = 0;
-    __syncthreads();
   }
   const bool sums = p.lse || p.tail || p.stats;
   const auto place_at = [&](int place, K c) {   // (an element taken leaves the row)
@@ -303,37 +327,17 @@ __global__ void __launch_bounds__(U <= 16 ? 256 : 512, U <= 16 ? 3 : 1) topk_ker
     own[place] = entry_of(Cand<K>::key(c), s.lo + i);
     if (sums) s.at(i) = minus_inf<T>();
   };
-  if (sizeof(K) == 4 && count <= kCounted) {
-    // 2^part neighbouring threads count for one candidate, sixteen others at a time
-    const int part = count * 4 <= NT ? 2 : count * 2 <= NT ? 1 : 0;
-    const int a = tid >> part, first = tid & ((1 << part) - 1);
-    const uint4* c4 = reinterpret_cast<const uint4*>(cand);   // (zeros behind the last)
-    for (int a0 = 0; a0 < count; a0 += NT) {
-      const uint32_t c = (uint32_t)cand[a0 + a < count ? a0 + a : 0];
-      int n[4] = {0, 0, 0, 0};
-      for (int b = first; b * 16 < count; b += 1 << part) {
-        uint4 o[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) o[q] = c4[b * 4 + q];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) n[q] += (o[q].x > c) + (o[q].y > c) + (o[q].z > c) + (o[q].w > c);
-      }
-      int place = (n[0] + n[1]) + (n[2] + n[3]);
-      if (part >= 1) place += __shfl_xor_sync(0xffffffffu, place, 1);
-      if (part == 2) place += __shfl_xor_sync(0xffffffffu, place, 2);
-      if (a0 + a < count && first == 0 && place < kk) place_at(place, (K)c);
-    }
-  } else {
-    const int runs = (count + 31) / 32;
-    for (int r = warp; r < runs; r += warps)
-      cand[r * 32 + lane] = warp_sort_down(r * 32 + lane < count ? cand[r * 32 + lane] : (K)0);
-    __syncthreads();
-    for (int a = tid; a < count; a += NT) {
-      const K c = cand[a];
-      int place = a & 31;
-      add_larger(place, cand, runs, a >> 5, 32, c);
-      if (place < kk) place_at(place, c);
-    }
+  const int runs = (count + 31) / 32, width = runs <= 4 ? 4 : 8;
+  for (int r = warp; r < (runs + width - 1) / width * width; r += warps)
+    cand[r * 32 + lane] = warp_sort_down(r * 32 + lane < count ? cand[r * 32 + lane] : (K)0);
+  __syncthreads();
+  for (int a = tid; a < count; a += NT) {
+    const K c = cand[a];
+    int place = a & 31;
+    if (width == 4) place += larger_in_runs<4>(cand, a >> 5, c);
+    else
+      for (int r = 0; r < runs; r += 8) place += larger_in_runs<8>(cand + r * 32, (a >> 5) - r, c);
+    if (place < kk) place_at(place, c);
   }
   __syncthreads();
 
@@ -351,7 +355,7 @@ __global__ void __launch_bounds__(U <= 16 ? 256 : 512, U <= 16 ? 3 : 1) topk_ker
   float ref = 0.f, rest = 0.f;                           // (with nothing but -infinity and NaN left any reference will do)
   if (sums && kk > 0) {
     ref = value_of(entry_key(own[kk - 1]));
-    if (ref == INFINITY) ref = block_max(max_of(s), sh.red[6]);
+    if (ref == INFINITY) ref = block_max<NT>(max_of(s), sh.red[6]);
     if (!(ref > -INFINITY)) ref = 0.f;
     rest = sum_exp(s, Exponent(ref, p.c));
   }
@@ -359,13 +363,13 @@ __global__ void __launch_bounds__(U <= 16 ? 256 : 512, U <= 16 ? 3 : 1) topk_ker
   // where the others are so far below that nothing is left of them
   const auto look_closer = [&]() {
     if (!sums || !(rest < 0x1p-60f)) return;
-    const float m = block_max(max_of(s), sh.red[3]);
+    const float m = block_max<NT>(max_of(s), sh.red[3]);
     if (!(m > -INFINITY)) return;
     ref = m;
-    rest = block_sum(sum_exp(s, Exponent(ref, p.c)), sh.red[4]);
+    rest = block_sum<NT>(sum_exp(s, Exponent(ref, p.c)), sh.red[4]);
   };
   if (CLUSTER) {
-    rest = block_sum(rest, sh.red[0]);
+    rest = block_sum<NT>(rest, sh.red[0]);
     look_closer();
     cluster_wait();   // (every block of the cluster runs)
     if (rank != 0) {
@@ -392,8 +396,9 @@ __global__ void __launch_bounds__(U <= 16 ? 256 : 512, U <= 16 ? 3 : 1) topk_ker
       for (int j = warp / groups * 32 + lane; j < p.k; j += warps / groups * 32) {
         const uint64_t c = lists[from * p.k + j];
         if (c == 0 || c < bound) break;
-        int place = j;
-        add_larger(place, lists, blocks, from, p.k, c);
+        int place = 0, at[8];
+        larger_in(at, lists, p.k, p.k, c);   // (its own list too: its place there)
+        for (int b = 0; b < 8; ++b) place += b < blocks ? at[b] : 0;
         if (place < p.k) best[place] = c;
       }
     }
@@ -413,14 +418,14 @@ __global__ void __launch_bounds__(U <= 16 ? 256 : 512, U <= 16 ? 3 : 1) topk_ker
     float left = -INFINITY;
     for (int a = tid; a < blocks * p.k; a += NT)
       if (lists[a] != 0 && lists[a] < last) left = fmaxf(left, value_of(entry_key(lists[a])));
-    ref = fmaxf(ref, block_max(left, sh.red[5]));
+    ref = fmaxf(ref, block_max<NT>(left, sh.red[5]));
     if (!(ref > -INFINITY)) ref = 0.f;
     rest = 0.f;
     for (int a = tid; a < blocks * p.k; a += NT)
       if (lists[a] != 0 && lists[a] < last) rest += ex2((value_of(entry_key(lists[a])) - ref) * p.c);
     if (tid < blocks && sh.part[tid].y != 0.f) rest += sh.part[tid].y * ex2((sh.part[tid].x - ref) * p.c);
   }
-  block_sums(taken, rest, sh.red[1], sh.red[2]);
+  block_sums<NT>(taken, rest, sh.red[1], sh.red[2]);
   if (!CLUSTER) look_closer();
   const float all = taken + (rest != 0.f ? rest * ex2((ref - first0) * p.c) : 0.f);
   if (tid == 0) {
@@ -432,28 +437,30 @@ __global__ void __launch_bounds__(U <= 16 ? 256 : 512, U <= 16 ? 3 : 1) topk_ker
 
 // Places for the row in shared memory behind the lists.
 unsigned topk_smem(const Cut& cut, int k, int es) {
-  const int64_t entries = (k + 1) / 2 * 2 + (cut.cluster > 1 ? (int64_t)cut.cluster * k : 0);
-  return (unsigned)(entries * 8 + kCand * (cut.threads <= 256 && es == 2 ? 4 : 8) + kHits * 2 + 16 +
-                    slice_buffer(cut.per, es));
+  const int64_t entries = (k + 1) / 2 * 2 + (cut.cluster > 1 ? 8 * k : 0);   // (eight lists are looked through)
+  const int64_t word = es == 2 && cut.threads * cut.units * 8 <= 65536 ? 4 : 8;
+  return (unsigned)(entries * 8 + kCand * word + kHits * 2 + 16 + slice_buffer(cut.per, es, cut.threads));
 }
 
-template <typename T>
+template <typename T, bool CLUSTER>
 const void* topk_func(const Cut& cut) {
-  if (cut.threads <= 256)   // (slices below 64 KB)
-    return cut.cluster > 1 ? (const void*)topk_kernel<T, true, 16> : (const void*)topk_kernel<T, false, 16>;
-  return cut.cluster > 1 ? (const void*)topk_kernel<T, true, 25> : (const void*)topk_kernel<T, false, 25>;
+  if (cut.threads == 128) return (const void*)topk_kernel<T, CLUSTER, 128, 3>;
+  if (cut.threads == 256) return (const void*)topk_kernel<T, CLUSTER, 256, 16>;
+  return cut.units == 9 ? (const void*)topk_kernel<T, CLUSTER, 512, 9> : (const void*)topk_kernel<T, CLUSTER, 512, 24>;
 }
 
 void topk_launch(int dtype, int64_t rows, const TopkParams& q, LaunchRec* rec) {
   const int es = dtype == DT_F32 ? 4 : 2;
-  const Cut cut = cut_rows(rows, q.C, es, q.k);
+  // twice as many threads as entries: their largest elements set the threshold
+  const Cut cut = cut_rows(q.C, es, 2 * q.k);
   TopkParams p = q;
   p.per = cut.per;
   rec->grid = dim3((unsigned)rows, 1, (unsigned)cut.cluster);
   rec->block = dim3((unsigned)cut.threads);
   rec->cluster = (unsigned)cut.cluster;
   rec->smem = topk_smem(cut, p.k, es);
-  rec->func = dtype == DT_F32 ? topk_func<float>(cut) : topk_func<__nv_bfloat16>(cut);
+  if (cut.cluster > 1) rec->func = dtype == DT_F32 ? topk_func<float, true>(cut) : topk_func<__nv_bfloat16, true>(cut);
+  else rec->func = dtype == DT_F32 ? topk_func<float, false>(cut) : topk_func<__nv_bfloat16, false>(cut);
   rec->name = "topk";
   rec->set_args(p);
 }

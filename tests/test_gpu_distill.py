@@ -51,7 +51,7 @@ def test_against_the_oracle(dtype, B, C, k, T, tail, labels, weights, pad, off, 
           dpad=dpad, doff=doff)
 
 
-@pytest.mark.parametrize("dtype,C,k", [(F, 393216, 256), (H, 393216, 100)])
+@pytest.mark.parametrize("dtype,C,k", [(F, 384000, 256), (H, 384000, 100)])
 def test_widest_rows(dtype, C, k):
     rng = np.random.default_rng([2, C])
     z = logits(rng, 2, C, TDT[dtype])
