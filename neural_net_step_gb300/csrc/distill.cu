@@ -117,6 +117,11 @@ __global__ void __launch_bounds__(NT, NT <= 256 ? 3 : 1) distill_kernel(const __
   if (CLUSTER) cluster_arrive();
   Slice<T, NT> s;
   s.load(buf, reinterpret_cast<const T*>(p.z) + row * p.ldz, lo, n);
+  if (tid == 0) {
+    const int64_t next = row + kAhead / blocks;
+    if (next < gridDim.x && n > 0 && !(p.w && p.w[next] == 0.f))
+      prefetch_row(reinterpret_cast<const T*>(p.z) + next * p.ldz, lo, n);
+  }
 
   // ---- the teacher, while the row is on its way
   bool bad = mine && (col < -1 || col >= p.C);

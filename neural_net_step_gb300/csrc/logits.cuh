@@ -27,6 +27,7 @@ constexpr int kMaxK = 256;                 // entries kept of a row
 constexpr int kCand = 1024;                // candidates ranked at most
 constexpr int kHits = 2048;                // 16-byte units looked through for them at most, shared out to the warps
 constexpr int64_t kMaxC = 384000;          // columns: eight slices of 192000 bytes of fp32
+constexpr int kAhead = 2 * kSMs;            // rows are asked for so many blocks ahead
 constexpr int64_t kSliceBytes = 64 * 1024; // a slice of at most this leaves room for three blocks on an SM
 
 // 2^t; subnormal results are flushed to zero (PTX ex2.approx).
@@ -193,6 +194,13 @@ struct Slice {
     }
   }
 };
+// Asks for elements [lo, lo + n) of a row to be in L2 (the whole 16-byte units).
+template <typename T>
+__device__ __forceinline__ void prefetch_row(const T* row, int lo, int n) {
+  const uintptr_t a = ((uintptr_t)(row + lo) + 15) & ~(uintptr_t)15, b = (uintptr_t)(row + lo + n) & ~(uintptr_t)15;
+  if (b > a)
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a), "r"((uint32_t)(b - a)) : "memory");
+}
 // Bytes of a slice's buffer: whole rounds of units (the phase can add one).
 inline int64_t slice_buffer(int64_t per, int es, int threads) { return round_up(per * es / 16 + 1, threads) * 16; }
 

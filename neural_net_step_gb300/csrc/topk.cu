@@ -248,7 +248,11 @@ __global__ void __launch_bounds__(NT, U <= 16 ? (NT <= 256 ? 3 : 2) : 1) topk_ke
   Slice<T, NT> s;
   s.load(buf, reinterpret_cast<const T*>(p.z) + row * p.ldz, rank * p.per, min(p.per, p.C - rank * p.per));
   const int kk = min(p.k, s.n);
-  if (tid == 0) sh.count = 0;
+  if (tid == 0) {
+    sh.count = 0;
+    const int64_t next = row + kAhead / blocks;
+    if (next < gridDim.x && s.n > 0) prefetch_row(reinterpret_cast<const T*>(p.z) + next * p.ldz, s.lo, s.n);
+  }
   copies_wait();
 
   // 1. a threshold that at least kk elements reach
