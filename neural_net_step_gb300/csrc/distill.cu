@@ -307,6 +307,23 @@ __global__ void __launch_bounds__(NT, NT <= 256 ? 3 : 1) distill_kernel(const __
   if (tid == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 
+// How rows are cut: `cluster` blocks of `threads` threads (at least k) share a
+// row, `per` columns each; a slice of at most 64 KB leaves room for three blocks on
+// an SM.
+struct Cut {
+  int cluster, per, threads;
+};
+Cut cut_rows(int64_t C, int es, int k) {
+  int cs = 1;
+  while (cs < 8 && ceil_div(C, cs) * es > kSliceBytes) cs *= 2;
+  Cut c;
+  c.cluster = cs;
+  c.per = (int)round_up(ceil_div(C, cs), 16 / es);
+  const int64_t units = c.per * es / 16 + 1;   // (a row's phase adds one)
+  c.threads = units <= 3 * 128 && k <= 128 ? 128 : units <= 16 * 256 ? 256 : 512;
+  return c;
+}
+
 template <typename T, bool CLUSTER, bool TWO>
 const void* distill_func(int threads) {
   return threads == 128   ? (const void*)distill_kernel<T, CLUSTER, TWO, 128>

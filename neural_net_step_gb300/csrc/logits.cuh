@@ -24,8 +24,6 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kSMs = 152;
 constexpr int kMaxK = 256;                 // entries kept of a row
-constexpr int kCand = 1024;                // candidates ranked at most
-constexpr int kHits = 2048;                // 16-byte units looked through for them at most, shared out to the warps
 constexpr int64_t kMaxC = 384000;          // columns: eight slices of 192000 bytes of fp32
 constexpr int kAhead = 2 * kSMs;            // rows are asked for so many blocks ahead
 constexpr int64_t kSliceBytes = 64 * 1024; // a slice of at most this leaves room for three blocks on an SM
@@ -302,14 +300,6 @@ __device__ __forceinline__ float max_of(const Slice<T, NT>& s) {
   s.each_unit([&](const uint4& u) { m.take(Most<T>(u)); });
   return m.value();
 }
-
-// How rows are cut: `cluster` blocks of `threads` threads share a row, `per`
-// columns each, at most `units` units a thread.
-struct Cut {
-  int cluster, per, threads, units;
-};
-// `threads`: at least so many.
-Cut cut_rows(int64_t C, int es, int threads);
 
 }  // namespace lg
 }  // namespace mlpk

@@ -3,24 +3,27 @@
 //   v_j, i_j  in descending order, lowest column first among equals,
 //   lse = log sum_i exp(z_i / T),  tail = log sum_{i not taken} exp(z_i / T).
 //
-// Bound by DRAM: the row is read once into shared memory and everything else
-// happens there.
-//   1. Every thread keeps the largest of each of its units.  The smallest, over the
+// Bound by DRAM, and by instruction issue close behind it.  A row is read twice, the
+// second time from L2 and backwards (what was read last is nearest), so that
+// nothing of it is held on the SM and many rows are under way there.
+//   1. Every thread finds the largest of its elements.  The smallest, over the
 //      warps, of each warp's ceil(k / warps)-th largest lane is a threshold that at
 //      least k elements reach, and not many more do where the row is in no
 //      particular order.
-//   2. Every warp lists its units that reach it, then their elements that do: the
-//      candidates.  Each counts those before it, which is its place; where they are
-//      64 bits wide, warps sort them 32 at a time instead and each searches the
-//      other runs.  Where they are too many
-//      (equal values, sorted rows) or too few (padding, NaN), the k-th largest is
-//      found by halving the range of keys, then of columns among equals.
-//   3. The elements taken become -infinity in shared memory, and the sum of the
-//      others is relative to the smallest taken, or to their own largest where that
-//      leaves next to nothing: the tail needs no subtraction and does not underflow.
-// The blocks of a cluster do this for their slices and send lists and sums to the
-// first, which finds the entries' places in the row and adds what a slice took
+//   2. The second time, 16-byte units that reach it are listed by every warp and the
+//      others' exponentials summed; then the listed units' elements are
+//      candidates or join the sum.  Where candidates are too many (equal values, sorted
+//      rows) or too few (NaN), the k-th largest is found by halving the range of
+//      keys, counting each time, and the columns of equals in their order.
+//   3. Warps sort the candidates 32 at a time; each one's place is its own in its run
+//      and what binary searches in the other runs say.  Those that are not taken
+//      join the sum: the tail needs no subtraction, and where next to nothing is left of it
+//      relative to the smallest taken it is formed again relative to its own largest.
+// The blocks of a cluster do this for their slices of a row and send lists and sums to
+// the first, which finds the entries' places in the row and adds what a slice took
 // and the row does not to the rest.
+//   Staged in shared memory instead, once from DRAM, three rows of 32000 bf16 fit an SM,
+// and 16384 of them with k = 64 took 260 us.
 #include <stdio.h>
 
 #include <algorithm>
@@ -30,25 +33,6 @@
 #include "ops.h"
 
 namespace mlpk {
-namespace lg {
-
-// A slice of at most 64 KB leaves room for three blocks on an SM.  Rows are not
-// cut further where they are few: what the blocks of a cluster then have to tell
-// one another takes longer than a block for the whole row (one row of 32000 bf16,
-// k = 50: 6.6 us, eight blocks 8.1).
-Cut cut_rows(int64_t C, int es, int threads) {
-  int cs = 1;
-  while (cs < 8 && ceil_div(C, cs) * es > kSliceBytes) cs *= 2;
-  Cut c;
-  c.cluster = cs;
-  c.per = (int)round_up(ceil_div(C, cs), 16 / es);
-  const int64_t units = c.per * es / 16 + 1;   // (a row's phase adds one)
-  c.threads = units <= 3 * 128 && threads <= 128 ? 128 : units <= 16 * 256 && threads <= 256 ? 256 : 512;
-  c.units = c.threads == 128 ? 3 : c.threads == 256 ? 16 : units <= 9 * 512 ? 9 : 24;
-  return c;
-}
-
-}  // namespace lg
 
 namespace {
 
@@ -67,12 +51,52 @@ struct TopkParams {
   const float* scores; const uint8_t* done;
 };
 
-struct TopkShared {
+struct __align__(16) TopkShared {
   Red red[7];
-  uint32_t tau[16];                 // (16-byte aligned)
-  int count;
+  uint32_t tau[16], top[16];        // of each warp
+  int count, over;                  // candidates; units found no place in a warp's list
   int total[16];
+  int found;
+  uint32_t last_key;                // the smallest taken
+  int last_at;
+  uint32_t row_last, row_first;
   float2 part[8];                   // of each block of the cluster: reference and sum of the rest
+};
+
+// Candidates of a slice at most, and units listed at most, shared out to the warps.
+template <int NT> constexpr int kRoom = NT < 256 ? 512 : 1024;
+
+// The slice of a row that a block walks: elements [lo, lo + n) from g on, whole
+// 16-byte units from element `head` on.
+template <typename T, int NT>
+struct Walk {
+  const T* g;
+  int lo, n, head, units;
+
+  __device__ __forceinline__ Walk(const T* row, int lo_, int n_) : g(row + lo_), lo(lo_), n(n_ > 0 ? n_ : 0) {
+    head = min(n, (int)((16 - ((uintptr_t)g & 15)) & 15) / (int)sizeof(T));
+    units = (n - head) / kPer16<T>;
+  }
+  __device__ __forceinline__ const uint4* unit(int v) const { return reinterpret_cast<const uint4*>(g + head) + v; }
+  __device__ __forceinline__ int at(int v) const { return head + v * kPer16<T>; }   // a unit's first element
+  // The elements at the ends: this thread's at most one of each (-1: none).
+  __device__ __forceinline__ int first_edge() const { return (int)threadIdx.x < head ? (int)threadIdx.x : -1; }
+  __device__ __forceinline__ int last_edge() const {
+    const int i = at(units) + (int)threadIdx.x;
+    return i < n ? i : -1;
+  }
+  // f(i, value), every element once over the block.
+  template <typename F>
+  __device__ __forceinline__ void each(F f) const {
+    for (int v = threadIdx.x; v < units; v += NT) {
+      float x[kPer16<T>];
+      unit_floats<T>(*unit(v), x);
+#pragma unroll
+      for (int e = 0; e < kPer16<T>; ++e) f(at(v) + e, x[e]);
+    }
+    if (first_edge() >= 0) f(first_edge(), to_f32(g[first_edge()]));
+    if (last_edge() >= 0) f(last_edge(), to_f32(g[last_edge()]));
+  }
 };
 
 // Number of set flags over the block, the same in every thread.
@@ -131,46 +155,66 @@ template <> struct Cand<uint32_t> {
   }
 };
 
+// What makes an element a candidate: a key above `key`, or `key` up to element `last`.
+struct Limit {
+  uint32_t key;
+  int last;
+  __device__ __forceinline__ bool takes(uint32_t k, int i) const { return k > key || (k == key && i <= last); }
+};
+
 // Candidates where the threshold did not leave a fit number of them: exactly
 // those not below the kk-th largest, or the kk largest themselves.  tau: a first
 // guess of the kk-th largest's key, or 0.
 template <typename T, typename K, int NT>
-__device__ __noinline__ void search(const Slice<T, NT>& s, int kk, uint32_t tau, K* cand, TopkShared& sh) {
+__device__ __noinline__ Limit search(const Walk<T, NT> s, int kk, uint32_t tau, K* cand, TopkShared& sh) {
   const auto reach = [&](uint32_t key) {
     int c = 0;
     s.each([&](int, float x) { c += key_of(x) >= key; });
     return block_count<NT>(c, sh);
   };
-  uint32_t v = tau;
+  Limit l;
+  l.key = tau;
+  l.last = s.n;
   if (tau == 0 || tau == 0xFFFFFFFFu || reach(tau) < kk || reach(tau + 1) >= kk) {
-    v = 0;
+    l.key = 0;
     for (int b = 31; b >= 0; --b)
-      if (reach(v | (1u << b)) >= kk) v |= 1u << b;
+      if (reach(l.key | (1u << b)) >= kk) l.key |= 1u << b;
   }
-  int last = s.n;   // among those equal to v: columns up to here
-  if (reach(v) > kCand) {
-    const int above = v == 0xFFFFFFFFu ? 0 : reach(v + 1);
-    int lo = 0, hi = s.n - 1;   // the smallest column with enough of them up to it
-    while (lo < hi) {
-      const int mid = (lo + hi) / 2;
-      int c = 0;
-      s.each([&](int i, float x) { c += i <= mid && key_of(x) == v; });
-      if (above + block_count<NT>(c, sh) >= kk) hi = mid;
-      else lo = mid + 1;
+  if (reach(l.key) > kRoom<NT>) {
+    // of those equal to it the first that are needed, NT elements at a time
+    int need = kk - (l.key == 0xFFFFFFFFu ? 0 : reach(l.key + 1));
+    for (int i0 = 0; i0 < s.n; i0 += NT) {
+      const int i = i0 + (int)threadIdx.x;
+      const bool equal = i < s.n && key_of(to_f32(s.g[i])) == l.key;
+      const uint32_t who = __ballot_sync(0xffffffffu, equal);
+      __syncthreads();
+      if ((threadIdx.x & 31) == 0) sh.total[threadIdx.x >> 5] = __popc(who);
+      __syncthreads();
+      int before = 0, all = 0;
+      for (int w = 0; w < NT / 32; ++w) {
+        before += w < (int)threadIdx.x >> 5 ? sh.total[w] : 0;
+        all += sh.total[w];
+      }
+      if (all >= need) {
+        if (equal && before + __popc(who & ((1u << (threadIdx.x & 31)) - 1)) == need - 1) sh.found = i;
+        __syncthreads();
+        l.last = sh.found;
+        break;
+      }
+      need -= all;
     }
-    last = lo;
   }
   __syncthreads();
   if (threadIdx.x == 0) sh.count = 0;
   __syncthreads();
   s.each([&](int i, float x) {
-    const uint32_t key = key_of(x);
-    if (key > v || (key == v && i <= last)) {
+    if (l.takes(key_of(x), i)) {
       const int at = atomicAdd(&sh.count, 1);
-      if (at < kCand) cand[at] = Cand<K>::of(x, i);
+      if (at < kRoom<NT>) cand[at] = Cand<K>::of(x, i);
     }
   });
   __syncthreads();
+  return l;
 }
 
 // Entries larger than e in N lists side by side, `stride` apart, each `len` long and
@@ -222,14 +266,12 @@ __device__ __forceinline__ int before_lane(int n, int& all) {
   return before;
 }
 
-// U: units a thread has at most.
-template <typename T, bool CLUSTER, int NT, int U>
-__global__ void __launch_bounds__(NT, U <= 16 ? (NT <= 256 ? 3 : 2) : 1) topk_kernel(const __grid_constant__ TopkParams p) {
+template <typename T, bool CLUSTER, int NT, typename K>
+__global__ void __launch_bounds__(NT, 1280 / NT) topk_kernel(const __grid_constant__ TopkParams p) {
   pdl_enter();
-  constexpr int E = kPer16<T>;
+  constexpr int E = kPer16<T>, warps = NT / 32, room = kRoom<NT> / warps;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ TopkShared sh;
-  constexpr int warps = NT / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t row = blockIdx.x;
   const int rank = CLUSTER ? (int)blockIdx.z : 0, blocks = CLUSTER ? (int)gridDim.z : 1;
@@ -237,147 +279,225 @@ __global__ void __launch_bounds__(NT, U <= 16 ? (NT <= 256 ? 3 : 2) : 1) topk_ke
   if (p.stats && ((p.done && p.done[row]) || !(fabsf(p.scores[row]) < INFINITY))) return;
   if (CLUSTER) cluster_arrive();
 
-  typedef typename std::conditional<sizeof(T) == 2 && NT * U * 8 <= 65536, uint32_t, uint64_t>::type K;
-  uint64_t* best = reinterpret_cast<uint64_t*>(smem);    // [k, even]: the row's, descending
-  uint64_t* lists = best + ((p.k + 1) & ~1);             // [blocks][k], descending (0: none); the first block has all
-  uint64_t* own = CLUSTER ? lists + (int64_t)rank * p.k : best;
-  K* cand = reinterpret_cast<K*>(lists + (CLUSTER ? 8 * p.k : 0));   // [kCand]
-  uint16_t* hits = reinterpret_cast<uint16_t*>(cand + kCand);                      // [kHits]
-  unsigned char* buf = reinterpret_cast<unsigned char*>(((uintptr_t)(hits + kHits) + 15) & ~(uintptr_t)15);
+  K* cand = reinterpret_cast<K*>(smem);                            // [kRoom]
+  int* hits = reinterpret_cast<int*>(cand + kRoom<NT>);            // [kRoom]: units, warp by warp; then
+  float* sorted = reinterpret_cast<float*>(hits);                  //   the candidates' values by place
+  uint64_t* best = reinterpret_cast<uint64_t*>(hits + kRoom<NT>);  // of a cluster's first block: [k] the row's, descending,
+  uint64_t* lists = best + p.k;                                    //   [blocks][k] every block's (0: none)
+  uint64_t* own = lists + (int64_t)rank * p.k;
 
-  Slice<T, NT> s;
-  s.load(buf, reinterpret_cast<const T*>(p.z) + row * p.ldz, rank * p.per, min(p.per, p.C - rank * p.per));
-  const int kk = min(p.k, s.n);
-  if (tid == 0) {
-    sh.count = 0;
-    const int64_t next = row + kAhead / blocks;
-    if (next < gridDim.x && s.n > 0) prefetch_row(reinterpret_cast<const T*>(p.z) + next * p.ldz, s.lo, s.n);
-  }
-  copies_wait();
+  const Walk<T, NT> s(reinterpret_cast<const T*>(p.z) + row * p.ldz, rank * p.per, min(p.per, p.C - rank * p.per));
+  const int kk = min(p.k, s.n), e0 = s.first_edge(), e1 = s.last_edge();
+  const float x0 = e0 >= 0 ? to_f32(s.g[e0]) : -INFINITY, x1 = e1 >= 0 ? to_f32(s.g[e1]) : -INFINITY;
+  if (tid == 0) sh.count = sh.over = 0;
 
   // 1. a threshold that at least kk elements reach
-  Most<T> um[U], most;
+  Most<T> most;
+  {
+    int v = tid;
+    for (; v + 7 * NT < s.units; v += 8 * NT) {
+      uint4 a[8];
 #pragma unroll
-  for (int u0 = 0; u0 < U; u0 += 4) {   // (four loads in flight)
-    if (u0 + 4 <= U && u0 + 4 <= s.nu) {
-      uint4 a[4];
+      for (int q = 0; q < 8; ++q) a[q] = *s.unit(v + q * NT);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) a[q] = s.mine(u0 + q);
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (u0 + q < U) um[u0 + q] = Most<T>(a[q]);
-    } else {
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (u0 + q < U && u0 + q < s.nu) um[u0 + q] = Most<T>(s.mine(u0 + q));
+      for (int q = 0; q < 8; ++q) most.take(Most<T>(a[q]));
     }
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (u0 + q < U) most.take(um[u0 + q]);
+#pragma unroll 4
+    for (; v < s.units; v += NT) most.take(Most<T>(*s.unit(v)));
   }
-  const uint32_t nth = warp_nth(key_of(most.value()), (kk + warps - 1) / warps);
-  if (lane == 0) sh.tau[warp] = nth;
+  const uint32_t most_key = key_of(fmaxf(most.value(), fmaxf(x0, x1)));
+  const uint32_t nth = warp_nth(most_key, (kk + warps - 1) / warps), top_key = __reduce_max_sync(0xffffffffu, most_key);
+  if (lane == 0) {
+    sh.tau[warp] = nth;
+    sh.top[warp] = top_key;
+  }
   __syncthreads();
-  uint32_t tau = 0xFFFFFFFFu;
+  uint32_t tau = 0xFFFFFFFFu, row_key = 0;
 #pragma unroll
   for (int w = 0; w < warps; w += 4) {
-    const uint4 q = *reinterpret_cast<const uint4*>(sh.tau + w);
+    const uint4 q = *reinterpret_cast<const uint4*>(sh.tau + w), r = *reinterpret_cast<const uint4*>(sh.top + w);
     tau = min(tau, min(min(q.x, q.y), min(q.z, q.w)));
+    row_key = max(row_key, max(max(r.x, r.y), max(r.z, r.w)));
   }
-  const float least = value_of(tau);
 
-  // 2. candidates and their places
-  uint32_t reach = 0;
+  // 2. candidates, and the sum of the others relative to the threshold that they are below
+  const bool sums = p.lse || p.tail || p.stats;
+  const float least = value_of(tau);
+  float ref = least > -INFINITY ? least : 0.f, rest = 0.f;
+  const Exponent ex(ref, p.c);
+  {
+    const uint32_t below = (1u << lane) - 1;
+    int* hit = hits + warp * room;
+    int n_hits = 0;
+    F2 acc0 = pack2(0.f, 0.f), acc1 = acc0;
+    const F2 c2 = pack2(p.c, p.c), r2 = pack2(-ex.rc, -ex.rc);
+    const auto take = [&](const uint4& u, int v, F2& acc) {
+      const bool in = Most<T>(u).reaches(least);
+      const uint32_t who = __ballot_sync(0xffffffffu, in);
+      if (who) {
+        const int at = n_hits + __popc(who & below);
+        if (in && at < room) hit[at] = v;
+        n_hits += __popc(who);
+      }
+      if (!sums) return;
+      F2 e[E / 2];
 #pragma unroll
-  for (int u = 0; u < U; ++u) reach |= (uint32_t)um[u].reaches(least) << u;
-  constexpr int room = kHits / warps;
-  uint16_t* hit = hits + warp * room;
-  int n_hits;
-  for (int at = before_lane<5>(__popc(reach), n_hits); reach && at < room; reach &= reach - 1, ++at)
-    hit[at] = (uint16_t)(tid + (__ffs(reach) - 1) * NT);
-  __syncwarp();
-  if (n_hits > room && lane == 0) atomicAdd(&sh.count, kCand + 1);
-  for (int a = lane; a - lane < min(n_hits, room); a += 32) {
-    uint32_t in = 0;
-    int v = 0;
-    if (a < min(n_hits, room) && hit[a] < s.nvec) {
-      v = hit[a];
+      for (int h = 0; h < E / 2; ++h) {
+        float x, y;
+        unpack2(fma2(pair_of<T>(u, h), c2, r2), x, y);
+        e[h] = pack2(ex2(x), ex2(y));
+      }
+#pragma unroll
+      for (int h = E / 4; h > 0; h /= 2)
+#pragma unroll
+        for (int q = 0; q < h; ++q) e[q] = add2(e[q], e[q + h]);
+      if (!in) acc = add2(acc, e[0]);
+    };
+    int r = (s.units + NT - 1) / NT - 1;   // rounds of NT units, the last one first
+    if (r >= 0) {
+      const int v = tid + r * NT;
+      const uint32_t none = sizeof(T) == 4 ? 0xFF800000u : 0xFF80FF80u;
+      take(v < s.units ? *s.unit(v) : make_uint4(none, none, none, none), v, acc0);
+      --r;
+    }
+    for (; r >= 3; r -= 4) {
+      const int v = tid + r * NT;
+      const uint4 a = *s.unit(v), b = *s.unit(v - NT), c = *s.unit(v - 2 * NT), d = *s.unit(v - 3 * NT);
+      take(a, v, acc0);
+      take(b, v - NT, acc1);
+      take(c, v - 2 * NT, acc0);
+      take(d, v - 3 * NT, acc1);
+    }
+    for (; r >= 0; --r) take(*s.unit(tid + r * NT), tid + r * NT, acc0);
+    rest = sum2(add2(acc0, acc1));
+
+    __syncwarp();
+    if (n_hits > room) sh.over = 1;   // (count stays the number of candidates that have a place)
+    n_hits = min(n_hits, room);
+    const auto keep = [&](float x, int i, int at) {
+      if (at < kRoom<NT>) cand[at] = Cand<K>::of(x, i);
+    };
+    for (int a = lane; a - lane < n_hits; a += 32) {
+      const int v = a < n_hits ? hit[a] : s.units;
       float x[E];
-      unit_floats<T>(s.units()[v], x);
+      uint32_t in = 0;
+      if (v < s.units) {
+        unit_floats<T>(*s.unit(v), x);
 #pragma unroll
-      for (int e = 0; e < E; ++e) in |= (uint32_t)(x[e] >= least) << e;
-      if (least == -INFINITY)   // (what fills the units at a slice's ends does not count)
-        for (int e = 0; e < E; ++e)
-          if (v * E + e < s.ph || v * E + e >= s.ph + s.n) in &= ~(1u << e);
+        for (int e = 0; e < E; ++e) {
+          in |= (uint32_t)(x[e] >= least) << e;
+          if (sums && !(x[e] >= least)) rest += ex2(fmaf(x[e], p.c, -ex.rc));
+        }
+      }
+      int n_in, at = 0;
+      const int before = before_lane<4>(__popc(in), n_in);
+      if (lane == 0) at = atomicAdd(&sh.count, n_in);
+      at = __shfl_sync(0xffffffffu, at, 0) + before;
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (in >> e & 1) keep(x[e], s.at(v) + e, at++);
     }
-    int n_in, at = 0;
-    const int before = before_lane<4>(__popc(in), n_in);
-    if (lane == 0) at = atomicAdd(&sh.count, n_in);
-    at = __shfl_sync(0xffffffffu, at, 0) + before;
-    for (; in && at < kCand; in &= in - 1, ++at) {
-      const int i = v * E + __ffs(in) - 1 - s.ph;
-      cand[at] = Cand<K>::of(to_f32(s.at(i)), i);
+    if (e0 >= 0) {
+      if (x0 >= least) keep(x0, e0, atomicAdd(&sh.count, 1));
+      else rest += ex2(fmaf(x0, p.c, -ex.rc));
     }
+    if (e1 >= 0) {
+      if (x1 >= least) keep(x1, e1, atomicAdd(&sh.count, 1));
+      else rest += ex2(fmaf(x1, p.c, -ex.rc));
+    }
+    rest *= ex.scale;
   }
   __syncthreads();
   int count = sh.count;
-  if (count > kCand || count < kk) {
-    search<T>(s, kk, count > kCand ? tau : 0u, cand, sh);
-    count = sh.count;
+  const bool many = count > kRoom<NT> || sh.over;
+  if (many || count < kk || (sums && ex.far)) {
+    Limit limit{tau, s.n};
+    if (many || count < kk) {
+      __syncthreads();
+      limit = search<T>(s, kk, many ? tau : 0u, cand, sh);
+      count = sh.count;
+    }
+    if (sums) {
+      float m = -INFINITY;
+      s.each([&](int i, float x) {
+        if (!limit.takes(key_of(x), i)) m = fmaxf(m, x);
+      });
+      m = block_max<NT>(m, sh.red[6]);
+      ref = m > -INFINITY ? m : 0.f;
+      rest = 0.f;
+      s.each([&](int i, float x) {
+        if (!limit.takes(key_of(x), i)) rest += ex2((x - ref) * p.c);
+      });
+    }
   }
-  const bool sums = p.lse || p.tail || p.stats;
-  const auto place_at = [&](int place, K c) {   // (an element taken leaves the row)
-    const int i = Cand<K>::at(c);
-    own[place] = entry_of(Cand<K>::key(c), s.lo + i);
-    if (sums) s.at(i) = minus_inf<T>();
-  };
+
+  // 3. the candidates' places
   const int runs = (count + 31) / 32, width = runs <= 4 ? 4 : 8;
   for (int r = warp; r < (runs + width - 1) / width * width; r += warps)
     cand[r * 32 + lane] = warp_sort_down(r * 32 + lane < count ? cand[r * 32 + lane] : (K)0);
   __syncthreads();
+  const auto write = [&](int place, float x, int col) {
+    if (p.stats) {
+      p.entries[row * p.k + place] = entry_of(key_of(x), col);
+    } else {
+      p.values[row * p.ldv + place] = x;
+      p.indices[row * p.ldi + place] = col;
+    }
+  };
   for (int a = tid; a < count; a += NT) {
     const K c = cand[a];
     int place = a & 31;
     if (width == 4) place += larger_in_runs<4>(cand, a >> 5, c);
     else
       for (int r = 0; r < runs; r += 8) place += larger_in_runs<8>(cand + r * 32, (a >> 5) - r, c);
-    if (place < kk) place_at(place, c);
+    const float x = value_of(Cand<K>::key(c));
+    const int i = Cand<K>::at(c);
+    sorted[place] = x;
+    if (place < kk) {
+      if (CLUSTER) own[place] = entry_of(Cand<K>::key(c), s.lo + i);
+      else write(place, x, s.lo + i);
+      if (place == kk - 1) {
+        sh.last_key = Cand<K>::key(c);
+        sh.last_at = i;
+      }
+    }
   }
+  if (!CLUSTER && !sums) return;
   __syncthreads();
 
-  // 3. the sum of what is not taken, relative to the smallest that is
-  const uint64_t e = tid < kk ? own[tid] : 0;            // (at least k threads)
-  const auto write = [&](uint64_t c) {
-    if (p.stats) {
-      p.entries[row * p.k + tid] = c;
-    } else {
-      p.values[row * p.ldv + tid] = value_of(entry_key(c));
-      p.indices[row * p.ldi + tid] = entry_col(c);
-    }
-  };
-  if (!CLUSTER && tid < p.k) write(e);
-  float ref = 0.f, rest = 0.f;                           // (with nothing but -infinity and NaN left any reference will do)
+  // what is not taken of them, relative to the smallest that is (by place: the order
+  // in which candidates were found changes no sum)
+  float first = value_of(row_key), first0 = first > -INFINITY ? first : 0.f;
+  float taken = !CLUSTER && tid < kk ? ex2((sorted[tid] - first0) * p.c) : 0.f;   // (at least k threads)
   if (sums && kk > 0) {
-    ref = value_of(entry_key(own[kk - 1]));
-    if (ref == INFINITY) ref = block_max<NT>(max_of(s), sh.red[6]);
-    if (!(ref > -INFINITY)) ref = 0.f;
-    rest = sum_exp(s, Exponent(ref, p.c));
+    const float l = sorted[kk - 1], to = l > -INFINITY ? l : 0.f;
+    if (rest != 0.f && ref != to) rest *= ex2((ref - to) * p.c);
+    ref = to;
+    for (int j = kk + tid; j < count; j += NT) rest += ex2((sorted[j] - ref) * p.c);
   }
-
-  // where the others are so far below that nothing is left of them
+  // where next to nothing is left: relative to the largest that is not taken
   const auto look_closer = [&]() {
     if (!sums || !(rest < 0x1p-60f)) return;
-    const float m = block_max<NT>(max_of(s), sh.red[3]);
+    const Limit limit{sh.last_key, sh.last_at};
+    float m = -INFINITY;
+    s.each([&](int i, float x) {
+      if (!limit.takes(key_of(x), i)) m = fmaxf(m, x);
+    });
+    m = block_max<NT>(m, sh.red[3]);
     if (!(m > -INFINITY)) return;
     ref = m;
-    rest = block_sum<NT>(sum_exp(s, Exponent(ref, p.c)), sh.red[4]);
+    rest = 0.f;
+    s.each([&](int i, float x) {
+      if (!limit.takes(key_of(x), i)) rest += ex2((x - ref) * p.c);
+    });
+    rest = block_sum<NT>(rest, sh.red[4]);
   };
   if (CLUSTER) {
     rest = block_sum<NT>(rest, sh.red[0]);
     look_closer();
     cluster_wait();   // (every block of the cluster runs)
     if (rank != 0) {
-      if (tid < p.k) put64(in_block(smem_addr(own + tid), 0), e);
+      if (tid < p.k) put64(in_block(smem_addr(own + tid), 0), tid < kk ? own[tid] : 0ull);   // (at least k threads)
       if (tid == 0) {
         const uint32_t to = in_block(smem_addr(&sh.part[rank]), 0);
         put32(to, __float_as_uint(ref));
@@ -409,11 +529,12 @@ __global__ void __launch_bounds__(NT, U <= 16 ? (NT <= 256 ? 3 : 2) : 1) topk_ke
     __syncthreads();
   }
 
-  if (CLUSTER && tid < p.k) write(best[tid]);
-  if (!sums) return;
-  const float first = value_of(entry_key(best[0])), first0 = first > -INFINITY ? first : 0.f;
-  float taken = tid < p.k ? ex2((value_of(entry_key(best[tid])) - first0) * p.c) : 0.f;
   if (CLUSTER) {
+    if (tid < p.k) write(tid, value_of(entry_key(best[tid])), entry_col(best[tid]));
+    if (!sums) return;
+    first = value_of(entry_key(best[0]));
+    first0 = first > -INFINITY ? first : 0.f;
+    taken = tid < p.k ? ex2((value_of(entry_key(best[tid])) - first0) * p.c) : 0.f;
     // the rests of the slices and what they took and the row does not, relative to the largest of those
     const uint64_t last = best[p.k - 1];
     ref = -INFINITY;
@@ -439,32 +560,47 @@ __global__ void __launch_bounds__(NT, U <= 16 ? (NT <= 256 ? 3 : 2) : 1) topk_ke
   if (tid == 32 && p.tail) p.tail[row] = ref / p.T + logf(rest);
 }
 
-// Places for the row in shared memory behind the lists.
-unsigned topk_smem(const Cut& cut, int k, int es) {
-  const int64_t entries = (k + 1) / 2 * 2 + (cut.cluster > 1 ? 8 * k : 0);   // (eight lists are looked through)
-  const int64_t word = es == 2 && cut.threads * cut.units * 8 <= 65536 ? 4 : 8;
-  return (unsigned)(entries * 8 + kCand * word + kHits * 2 + 16 + slice_buffer(cut.per, es, cut.threads));
+// Blocks of a row and their threads.  Twice as many threads as entries: their
+// largest elements set the threshold.  More where rows are few; a row
+// is shared only where blocks of 512 for whole rows leave SMs idle and its parts are long, for what
+// the blocks of a cluster tell one another takes microseconds.
+struct TopkCut {
+  int cluster, per, threads;
+};
+TopkCut topk_cut(int64_t rows, int64_t C, int es, int k) {
+  TopkCut c;
+  c.cluster = 1;
+  while (c.cluster < 8 && rows * c.cluster * 2 <= kSMs && ceil_div(C, c.cluster * 2) * es >= 64 * 1024) c.cluster *= 2;
+  c.per = (int)round_up(ceil_div(C, c.cluster), 16 / es);
+  const int64_t blocks = rows * c.cluster, units = c.per * es / 16;
+  c.threads = k <= 64 ? 128 : k <= 128 ? 256 : 512;
+  while (c.threads < 512 && blocks * c.threads * 2 <= kSMs * 1280 && units > c.threads * 4) c.threads *= 2;
+  return c;
 }
 
-template <typename T, bool CLUSTER>
-const void* topk_func(const Cut& cut) {
-  if (cut.threads == 128) return (const void*)topk_kernel<T, CLUSTER, 128, 3>;
-  if (cut.threads == 256) return (const void*)topk_kernel<T, CLUSTER, 256, 16>;
-  return cut.units == 9 ? (const void*)topk_kernel<T, CLUSTER, 512, 9> : (const void*)topk_kernel<T, CLUSTER, 512, 24>;
+template <typename T, bool CLUSTER, typename K>
+const void* topk_func(int threads) {
+  return threads == 128   ? (const void*)topk_kernel<T, CLUSTER, 128, K>
+         : threads == 256 ? (const void*)topk_kernel<T, CLUSTER, 256, K>
+                          : (const void*)topk_kernel<T, CLUSTER, 512, K>;
+}
+template <typename T, typename K>
+const void* topk_func(const TopkCut& cut) {
+  return cut.cluster > 1 ? topk_func<T, true, K>(cut.threads) : topk_func<T, false, K>(cut.threads);
 }
 
 void topk_launch(int dtype, int64_t rows, const TopkParams& q, LaunchRec* rec) {
   const int es = dtype == DT_F32 ? 4 : 2;
-  // twice as many threads as entries: their largest elements set the threshold
-  const Cut cut = cut_rows(q.C, es, 2 * q.k);
+  const TopkCut cut = topk_cut(rows, q.C, es, q.k);
   TopkParams p = q;
   p.per = cut.per;
+  const bool small = es == 2 && cut.per <= 65535;
   rec->grid = dim3((unsigned)rows, 1, (unsigned)cut.cluster);
   rec->block = dim3((unsigned)cut.threads);
   rec->cluster = (unsigned)cut.cluster;
-  rec->smem = topk_smem(cut, p.k, es);
-  if (cut.cluster > 1) rec->func = dtype == DT_F32 ? topk_func<float, true>(cut) : topk_func<__nv_bfloat16, true>(cut);
-  else rec->func = dtype == DT_F32 ? topk_func<float, false>(cut) : topk_func<__nv_bfloat16, false>(cut);
+  rec->smem = (unsigned)((cut.threads < 256 ? 512 : 1024) * ((small ? 4 : 8) + 4) + (cut.cluster > 1 ? 9 * 8 * p.k : 0));
+  rec->func = es == 4 ? topk_func<float, uint64_t>(cut)
+              : small ? topk_func<__nv_bfloat16, uint32_t>(cut) : topk_func<__nv_bfloat16, uint64_t>(cut);
   rec->name = "topk";
   rec->set_args(p);
 }
