@@ -99,6 +99,8 @@ template <> struct Most<float> {
     m = fmaxf(fmaxf(__uint_as_float(a.x), __uint_as_float(a.y)), fmaxf(__uint_as_float(a.z), __uint_as_float(a.w)));
   }
   __device__ __forceinline__ void take(const Most& o) { m = fmaxf(m, o.m); }
+  // Whether it reaches a limit.
+  static __device__ __forceinline__ float limit(float x) { return x; }
   __device__ __forceinline__ bool reaches(float x) const { return m >= x; }
   __device__ __forceinline__ float value() const { return fmaxf(m, -INFINITY); }
 };
@@ -110,9 +112,16 @@ template <> struct Most<__nv_bfloat16> {
     m = __hmax2(__hmax2(two(a.x), two(a.y)), __hmax2(two(a.z), two(a.w)));
   }
   __device__ __forceinline__ void take(const Most& o) { m = __hmax2(m, o.m); }
-  __device__ __forceinline__ bool reaches(float x) const {
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(&m);
-    return __uint_as_float(w << 16) >= x || __uint_as_float(w & 0xFFFF0000u) >= x;
+  static __device__ __forceinline__ uint32_t limit(float x) {   // (a bf16's value)
+    const uint32_t h = __float_as_uint(x) >> 16;
+    return h | h << 16;
+  }
+  __device__ __forceinline__ bool reaches(uint32_t limit) const {
+    uint32_t r;
+    asm("{\n\t.reg .pred p, q;\n\tsetp.ge.bf16x2 p|q, %1, %2;\n\tor.pred p, p, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)
+        : "r"(*reinterpret_cast<const uint32_t*>(&m)), "r"(limit));
+    return r != 0;
   }
   __device__ __forceinline__ float value() const { return fmaxf(fmaxf(__low2float(m), __high2float(m)), -INFINITY); }
 };

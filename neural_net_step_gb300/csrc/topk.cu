@@ -6,12 +6,11 @@
 // Bound by DRAM, and by instruction issue close behind it.  A row is read twice, the
 // second time from L2 and backwards (what was read last is nearest), so that
 // nothing of it is held on the SM and many rows are under way there.
-//   1. Every thread finds the largest of its elements.  The smallest, over the
-//      warps, of each warp's ceil(k / warps)-th largest lane is a threshold that at
-//      least k elements reach, and not many more do where the row is in no
-//      particular order.
-//   2. The second time, 16-byte units that reach it are listed by every warp and the
-//      others' exponentials summed; then the listed units' elements are
+//   1. Every thread finds the largest of its elements.  The k-th largest of those is a
+//      threshold that at least k elements reach, and not many more do where the
+//      row is in no particular order.
+//   2. The second time, 16-byte units that reach it are marked and the
+//      others' exponentials summed; then the marked units' elements are
 //      candidates or join the sum.  Where candidates are too many (equal values, sorted
 //      rows) or too few (NaN), the k-th largest is found by halving the range of
 //      keys, counting each time, and the columns of equals in their order.
@@ -53,13 +52,13 @@ struct TopkParams {
 
 struct __align__(16) TopkShared {
   Red red[7];
-  uint32_t tau[16], top[16];        // of each warp
+  uint32_t top[16];                 // of each warp (read 16 bytes at a time)
+  uint32_t tau;
   int count, over;                  // candidates; units found no place in a warp's list
   int total[16];
   int found;
   uint32_t last_key;                // the smallest taken
   int last_at;
-  uint32_t row_last, row_first;
   float2 part[8];                   // of each block of the cluster: reference and sum of the rest
 };
 
@@ -125,16 +124,6 @@ __device__ __forceinline__ U warp_sort_down(U x) {
   }
   return x;
 }
-// The n-th largest of the warp's values, n from 1.
-__device__ __forceinline__ uint32_t warp_nth(uint32_t x, int n) {
-  if (n > 4) return __shfl_sync(0xffffffffu, warp_sort_down(x), n - 1);
-  while (true) {
-    const uint32_t m = __reduce_max_sync(0xffffffffu, x);
-    if (--n <= 0) return m;
-    if ((threadIdx.x & 31) == __ffs(__ballot_sync(0xffffffffu, x == m)) - 1) x = 0;
-  }
-}
-
 // A candidate of a slice: larger is better, lower element first among equals; 0
 // is none.  bf16 slices of at most 65535 elements need 32 bits.
 template <typename K> struct Cand;
@@ -305,20 +294,30 @@ __global__ void __launch_bounds__(NT, 1280 / NT) topk_kernel(const __grid_consta
 #pragma unroll 4
     for (; v < s.units; v += NT) most.take(Most<T>(*s.unit(v)));
   }
+  // (the threads' largest, made distinct by their numbers, sorted by warps and searched like the candidates below)
   const uint32_t most_key = key_of(fmaxf(most.value(), fmaxf(x0, x1)));
-  const uint32_t nth = warp_nth(most_key, (kk + warps - 1) / warps), top_key = __reduce_max_sync(0xffffffffu, most_key);
-  if (lane == 0) {
-    sh.tau[warp] = nth;
-    sh.top[warp] = top_key;
-  }
+  uint32_t* keys = reinterpret_cast<uint32_t*>(hits);   // [NT]
+  const uint32_t mine = warp_sort_down((most_key & 0xFFFFFE00u) | (uint32_t)tid);
+  keys[tid] = mine;
+  const uint32_t top_key = __reduce_max_sync(0xffffffffu, most_key);
+  if (lane == 0) sh.top[warp] = top_key;
   __syncthreads();
-  uint32_t tau = 0xFFFFFFFFu, row_key = 0;
+  {
+    int place = lane;
+#pragma unroll
+    for (int w = 0; w < warps; w += 4) place += larger_in_runs<4>(keys + w * 32, warp - w, mine);
+    if (place == (kk > 0 ? kk - 1 : 0)) sh.tau = mine & 0xFFFFFE00u;
+  }
+  uint32_t row_key = 0;
 #pragma unroll
   for (int w = 0; w < warps; w += 4) {
-    const uint4 q = *reinterpret_cast<const uint4*>(sh.tau + w), r = *reinterpret_cast<const uint4*>(sh.top + w);
-    tau = min(tau, min(min(q.x, q.y), min(q.z, q.w)));
+    const uint4 r = *reinterpret_cast<const uint4*>(sh.top + w);
     row_key = max(row_key, max(max(r.x, r.y), max(r.z, r.w)));
   }
+  __syncthreads();
+  uint32_t tau = sh.tau;
+  if (sizeof(T) == 2) tau = (tau & 0x80000000u) ? tau & 0xFFFF0000u : tau | 0xFFFFu;   // (a bf16's key again)
+  tau = max(tau, key_of(-INFINITY));
 
   // 2. candidates, and the sum of the others relative to the threshold that they are below
   const bool sums = p.lse || p.tail || p.stats;
@@ -326,19 +325,14 @@ __global__ void __launch_bounds__(NT, 1280 / NT) topk_kernel(const __grid_consta
   float ref = least > -INFINITY ? least : 0.f, rest = 0.f;
   const Exponent ex(ref, p.c);
   {
-    const uint32_t below = (1u << lane) - 1;
     int* hit = hits + warp * room;
-    int n_hits = 0;
+    const auto limit = Most<T>::limit(least);
     F2 acc0 = pack2(0.f, 0.f), acc1 = acc0;
     const F2 c2 = pack2(p.c, p.c), r2 = pack2(-ex.rc, -ex.rc);
-    const auto take = [&](const uint4& u, int v, F2& acc) {
-      const bool in = Most<T>(u).reaches(least);
-      const uint32_t who = __ballot_sync(0xffffffffu, in);
-      if (who) {
-        const int at = n_hits + __popc(who & below);
-        if (in && at < room) hit[at] = v;
-        n_hits += __popc(who);
-      }
+    uint32_t marks = 0;   // this thread's units that reach it, the latest in bit 0
+    const auto take = [&](const uint4& u, F2& acc) {
+      const bool in = Most<T>(u).reaches(limit);
+      marks = marks * 2 + in;
       if (!sums) return;
       F2 e[E / 2];
 #pragma unroll
@@ -353,22 +347,35 @@ __global__ void __launch_bounds__(NT, 1280 / NT) topk_kernel(const __grid_consta
         for (int q = 0; q < h; ++q) e[q] = add2(e[q], e[q + h]);
       if (!in) acc = add2(acc, e[0]);
     };
-    int r = (s.units + NT - 1) / NT - 1;   // rounds of NT units, the last one first
+    int n_hits = 0, r = (s.units + NT - 1) / NT - 1;   // rounds of NT units, the last one first
+    const auto list = [&](int round) {   // the marked units; bit 0: of this round
+      int all;
+      for (int at = n_hits + before_lane<6>(__popc(marks), all); marks && at < room; marks &= marks - 1, ++at)
+        hit[at] = tid + (round + __ffs(marks) - 1) * NT;
+      n_hits += all;
+      marks = 0;
+    };
     if (r >= 0) {
       const int v = tid + r * NT;
       const uint32_t none = sizeof(T) == 4 ? 0xFF800000u : 0xFF80FF80u;
-      take(v < s.units ? *s.unit(v) : make_uint4(none, none, none, none), v, acc0);
+      take(v < s.units ? *s.unit(v) : make_uint4(none, none, none, none), acc0);
       --r;
     }
+    int marked = 1;
     for (; r >= 3; r -= 4) {
-      const int v = tid + r * NT;
-      const uint4 a = *s.unit(v), b = *s.unit(v - NT), c = *s.unit(v - 2 * NT), d = *s.unit(v - 3 * NT);
-      take(a, v, acc0);
-      take(b, v - NT, acc1);
-      take(c, v - 2 * NT, acc0);
-      take(d, v - 3 * NT, acc1);
+      const uint4* u = s.unit(tid + r * NT);
+      const uint4 a = u[0], b = u[-NT], c = u[-2 * NT], d = u[-3 * NT];
+      take(a, acc0);
+      take(b, acc1);
+      take(c, acc0);
+      take(d, acc1);
+      if ((marked += 4) > 28) {
+        list(r - 3);
+        marked = 0;
+      }
     }
-    for (; r >= 0; --r) take(*s.unit(tid + r * NT), tid + r * NT, acc0);
+    for (; r >= 0; --r) take(*s.unit(tid + r * NT), acc0);
+    list(0);
     rest = sum2(add2(acc0, acc1));
 
     __syncwarp();
@@ -379,10 +386,12 @@ __global__ void __launch_bounds__(NT, 1280 / NT) topk_kernel(const __grid_consta
     };
     for (int a = lane; a - lane < n_hits; a += 32) {
       const int v = a < n_hits ? hit[a] : s.units;
-      float x[E];
       uint32_t in = 0;
+      uint4 u = make_uint4(0, 0, 0, 0);
       if (v < s.units) {
-        unit_floats<T>(*s.unit(v), x);
+        u = *s.unit(v);
+        float x[E];
+        unit_floats<T>(u, x);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
           in |= (uint32_t)(x[e] >= least) << e;
@@ -393,9 +402,11 @@ __global__ void __launch_bounds__(NT, 1280 / NT) topk_kernel(const __grid_consta
       const int before = before_lane<4>(__popc(in), n_in);
       if (lane == 0) at = atomicAdd(&sh.count, n_in);
       at = __shfl_sync(0xffffffffu, at, 0) + before;
-#pragma unroll
-      for (int e = 0; e < E; ++e)
-        if (in >> e & 1) keep(x[e], s.at(v) + e, at++);
+      for (; in; in &= in - 1) {
+        const int e = __ffs(in) - 1, w = sizeof(T) == 4 ? e : e >> 1;
+        const uint32_t word = w < 2 ? (w == 0 ? u.x : u.y) : (w == 2 ? u.z : u.w);
+        keep(__uint_as_float(sizeof(T) == 4 ? word : (e & 1) ? word & 0xFFFF0000u : word << 16), s.at(v) + e, at++);
+      }
     }
     if (e0 >= 0) {
       if (x0 >= least) keep(x0, e0, atomicAdd(&sh.count, 1));
