@@ -240,23 +240,8 @@ __device__ __forceinline__ int larger_in_runs(const K* runs, int not_in, K e) {
   return sum;
 }
 
-// Sum of n over the lanes before this one and over all, n < 2^BITS.
-template <int BITS>
-__device__ __forceinline__ int before_lane(int n, int& all) {
-  const uint32_t below = (1u << (threadIdx.x & 31)) - 1;
-  int before = 0;
-  all = 0;
-#pragma unroll
-  for (int b = 0; b < BITS; ++b) {
-    const uint32_t who = __ballot_sync(0xffffffffu, n >> b & 1);
-    before += __popc(who & below) << b;
-    all += __popc(who) << b;
-  }
-  return before;
-}
-
 template <typename T, bool CLUSTER, int NT, typename K>
-__global__ void __launch_bounds__(NT, 1280 / NT) topk_kernel(const __grid_constant__ TopkParams p) {
+__global__ void __launch_bounds__(NT, 1024 / NT) topk_kernel(const __grid_constant__ TopkParams p) {
   pdl_enter();
   constexpr int E = kPer16<T>, warps = NT / 32, room = kRoom<NT> / warps;
   extern __shared__ __align__(16) unsigned char smem[];
@@ -280,19 +265,30 @@ __global__ void __launch_bounds__(NT, 1280 / NT) topk_kernel(const __grid_consta
   const float x0 = e0 >= 0 ? to_f32(s.g[e0]) : -INFINITY, x1 = e1 >= 0 ? to_f32(s.g[e1]) : -INFINITY;
   if (tid == 0) sh.count = sh.over = 0;
 
-  // 1. a threshold that at least kk elements reach
+  // 1. a threshold that at least kk elements reach.  Rounds of NT units; the last eight
+  // stay in registers for the second time.
+  const uint32_t none = sizeof(T) == 4 ? 0xFF800000u : 0xFF80FF80u;   // (-infinity)
+  const int rounds = (s.units + NT - 1) / NT, kept = max(rounds - 8, 0);
   Most<T> most;
+  uint4 held[8];
   {
-    int v = tid;
-    for (; v + 7 * NT < s.units; v += 8 * NT) {
-      uint4 a[8];
+    int r = 0;
+    for (; r + 8 <= kept; r += 8) {
+      const uint4* u = s.unit(tid + r * NT);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) a[q] = *s.unit(v + q * NT);
+      for (int q = 0; q < 8; ++q) held[q] = u[q * NT];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) most.take(Most<T>(a[q]));
+      for (int q = 0; q < 8; ++q) most.take(Most<T>(held[q]));
     }
 #pragma unroll 4
-    for (; v < s.units; v += NT) most.take(Most<T>(*s.unit(v)));
+    for (; r < kept; ++r) most.take(Most<T>(*s.unit(tid + r * NT)));
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const int v = tid + (kept + q) * NT;
+      held[q] = v < s.units ? *s.unit(v) : make_uint4(none, none, none, none);
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) most.take(Most<T>(held[q]));
   }
   // (the threads' largest, made distinct by their numbers, sorted by warps and searched like the candidates below)
   const uint32_t most_key = key_of(fmaxf(most.value(), fmaxf(x0, x1)));
@@ -347,33 +343,33 @@ __global__ void __launch_bounds__(NT, 1280 / NT) topk_kernel(const __grid_consta
         for (int q = 0; q < h; ++q) e[q] = add2(e[q], e[q + h]);
       if (!in) acc = add2(acc, e[0]);
     };
-    int n_hits = 0, r = (s.units + NT - 1) / NT - 1;   // rounds of NT units, the last one first
+    int n_hits = 0;
+    const uint32_t below = (1u << lane) - 1;
     const auto list = [&](int round) {   // the marked units; bit 0: of this round
-      int all;
-      for (int at = n_hits + before_lane<6>(__popc(marks), all); marks && at < room; marks &= marks - 1, ++at)
-        hit[at] = tid + (round + __ffs(marks) - 1) * NT;
-      n_hits += all;
-      marks = 0;
+      while (const uint32_t who = __ballot_sync(0xffffffffu, marks != 0)) {
+        const int at = n_hits + __popc(who & below);
+        if (marks && at < room) hit[at] = tid + (round + __ffs(marks) - 1) * NT;
+        marks &= marks - 1;
+        n_hits += __popc(who);
+      }
     };
-    if (r >= 0) {
-      const int v = tid + r * NT;
-      const uint32_t none = sizeof(T) == 4 ? 0xFF800000u : 0xFF80FF80u;
-      take(v < s.units ? *s.unit(v) : make_uint4(none, none, none, none), acc0);
-      --r;
-    }
-    int marked = 1;
-    for (; r >= 3; r -= 4) {
-      const uint4* u = s.unit(tid + r * NT);
-      const uint4 a = u[0], b = u[-NT], c = u[-2 * NT], d = u[-3 * NT];
-      take(a, acc0);
-      take(b, acc1);
-      take(c, acc0);
-      take(d, acc1);
-      if ((marked += 4) > 28) {
-        list(r - 3);
+#pragma unroll
+    for (int q = 7; q >= 0; --q)
+      if (kept + q < rounds) take(held[q], q & 1 ? acc1 : acc0);
+    int marked = min(rounds, 8), r = kept - 1;
+    for (; r >= 7; r -= 8) {
+      if (marked > 24) {
+        list(r + 1);
         marked = 0;
       }
+      marked += 8;
+      const uint4* u = s.unit(tid + r * NT);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) held[q] = u[-q * NT];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) take(held[q], q & 1 ? acc1 : acc0);
     }
+    if (marked > 25) list(r + 1);   // (at most seven more)
     for (; r >= 0; --r) take(*s.unit(tid + r * NT), acc0);
     list(0);
     rest = sum2(add2(acc0, acc1));
@@ -398,14 +394,19 @@ __global__ void __launch_bounds__(NT, 1280 / NT) topk_kernel(const __grid_consta
           if (sums && !(x[e] >= least)) rest += ex2(fmaf(x[e], p.c, -ex.rc));
         }
       }
-      int n_in, at = 0;
-      const int before = before_lane<4>(__popc(in), n_in);
-      if (lane == 0) at = atomicAdd(&sh.count, n_in);
-      at = __shfl_sync(0xffffffffu, at, 0) + before;
-      for (; in; in &= in - 1) {
-        const int e = __ffs(in) - 1, w = sizeof(T) == 4 ? e : e >> 1;
-        const uint32_t word = w < 2 ? (w == 0 ? u.x : u.y) : (w == 2 ? u.z : u.w);
-        keep(__uint_as_float(sizeof(T) == 4 ? word : (e & 1) ? word & 0xFFFF0000u : word << 16), s.at(v) + e, at++);
+      const int n_in = __reduce_add_sync(0xffffffffu, __popc(in));
+      int base = 0;
+      if (lane == 0) base = atomicAdd(&sh.count, n_in);
+      base = __shfl_sync(0xffffffffu, base, 0);
+      while (const uint32_t who = __ballot_sync(0xffffffffu, in != 0)) {
+        if (in) {
+          const int e = __ffs(in) - 1, w = sizeof(T) == 4 ? e : e >> 1;
+          const uint32_t word = w < 2 ? (w == 0 ? u.x : u.y) : (w == 2 ? u.z : u.w);
+          keep(__uint_as_float(sizeof(T) == 4 ? word : (e & 1) ? word & 0xFFFF0000u : word << 16), s.at(v) + e,
+               base + __popc(who & below));
+          in &= in - 1;
+        }
+        base += __popc(who);
       }
     }
     if (e0 >= 0) {
@@ -585,7 +586,7 @@ TopkCut topk_cut(int64_t rows, int64_t C, int es, int k) {
   c.per = (int)round_up(ceil_div(C, c.cluster), 16 / es);
   const int64_t blocks = rows * c.cluster, units = c.per * es / 16;
   c.threads = k <= 64 ? 128 : k <= 128 ? 256 : 512;
-  while (c.threads < 512 && blocks * c.threads * 2 <= kSMs * 1280 && units > c.threads * 4) c.threads *= 2;
+  while (c.threads < 512 && blocks * c.threads * 2 <= kSMs * 1024 && units > c.threads * 4) c.threads *= 2;
   return c;
 }
 
