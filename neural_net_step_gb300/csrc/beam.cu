@@ -1,12 +1,11 @@
 // Beam search: which (beam, token) pairs go on, and the reordering of the states
 // that belong to the beams.
 //
-// Selection.  total(w, c) = score_w + z_wc - logsumexp(z_w); a finished beam offers
-// its end token at its score.  Only the m best tokens of a beam can be among the m
-// best pairs: the top-k kernel (topk.cu) leaves them per beam with the row's
-// largest logit and sum of exponentials, and one block per batch entry merges the
-// lists.  Totals are formed and compared in 64 bits: scores of -50 leave an fp32
-// sum a step of 4e-6, which would make equals of tokens of different beams.
+// Selection.  Only the m best tokens of a beam can be among the m best pairs: the
+// top-k kernel (topk.cu) finds them, and, where a batch entry's beams are the blocks of
+// a cluster, merges them as well.  Otherwise (more than eight beams, or rows that are shared
+// by blocks) it leaves them in the workspace with the rows' largest logits and sums of
+// exponentials, and one block per batch entry merges the lists here.
 //
 // Reordering.  Bound by DRAM.  A thread owns a column of all beams: it reads the
 // columns of the parents and then writes, so that source and destination may be
@@ -15,7 +14,7 @@
 
 #include <algorithm>
 
-#include "logits.cuh"
+#include "beam.cuh"
 #include "ops.h"
 
 namespace mlpk {
@@ -24,106 +23,28 @@ namespace {
 
 using namespace lg;
 
-constexpr int kMaxBeams = 32;
-constexpr int kMaxOut = 64;
-
 struct BeamMergeParams {
   const uint64_t* entries; const float2* stats;   // [batch * beams][per], [batch * beams]
-  const float* scores; const uint8_t* done;
-  int beams, C, m, per, eos;                      // per = min(m, C) entries of a beam
-  float* scores_out; int32_t* parents; int32_t* tokens; uint8_t* done_out;
+  const float* scores; const uint8_t* in_done;
+  BeamOut out;
 };
 
-// Order of totals as unsigned integers; NaN is 0, below -infinity.
-__device__ __forceinline__ uint64_t total_key(double t) {
-  const uint64_t u = (uint64_t)__double_as_longlong(t + 0.0);
-  const uint64_t k = (u >> 63) ? ~u : (u | 0x8000000000000000ull);
-  return t == t ? k : 0ull;
-}
-__device__ __forceinline__ double total_of(uint64_t k) {
-  const uint64_t u = (k >> 63) ? (k & 0x7FFFFFFFFFFFFFFFull) : ~k;
-  return __longlong_as_double(k ? (long long)u : 0x7FF8000000000000ll);
-}
-
-// Pairs of equal totals go by beam, then by their place in the beam's list.
 __global__ void __launch_bounds__(256) beam_merge_kernel(const __grid_constant__ BeamMergeParams p) {
   pdl_enter();
   extern __shared__ __align__(16) unsigned char smem[];
-  uint64_t* keys = reinterpret_cast<uint64_t*>(smem);                     // [beams][per], descending
-  int* toks = reinterpret_cast<int*>(keys + p.beams * p.per);
-  __shared__ double base[kMaxBeams];   // what a beam's logits are added to
-  __shared__ int kind[kMaxBeams];      // 0: base + logit; 1: every token at base; 2: finished
-  const int tid = threadIdx.x;
-  const int64_t r0 = (int64_t)blockIdx.x * p.beams;
-  if (tid < p.beams) {
-    const float score = p.scores[r0 + tid];
-    double b = (double)score;
-    int k = 0;
-    if (p.done && p.done[r0 + tid]) {
-      k = 2;
-    } else if (!(fabsf(score) < INFINITY)) {
-      k = 1;
-      if (!(score < 0.f)) b = __longlong_as_double(0x7FF8000000000000ll);
-    } else {
-      const float2 st = p.stats[r0 + tid];
-      if (st.x == -INFINITY && !(st.y != 0.f)) {   // nothing but -infinity
-        k = 1;
-        b = -(double)INFINITY;
-      } else {
-        b -= (double)st.x + log((double)st.y);
-        if (!(st.x < INFINITY) || !(b == b)) {
-          k = 1;
-          b = __longlong_as_double(0x7FF8000000000000ll);
-        }
-      }
-    }
-    base[tid] = b;
-    kind[tid] = k;
+  uint64_t* keys = reinterpret_cast<uint64_t*>(smem);
+  int* toks = reinterpret_cast<int*>(keys + p.out.beams * p.out.per);
+  __shared__ BeamBase base[kMaxBeams];
+  const int64_t r0 = (int64_t)blockIdx.x * p.out.beams;
+  if ((int)threadIdx.x < p.out.beams) {
+    const int64_t r = r0 + threadIdx.x;
+    const float score = p.scores[r];
+    const bool done = p.in_done && p.in_done[r];
+    const float2 st = beam_reads_row(score, done) ? p.stats[r] : make_float2(0.f, 0.f);
+    base[threadIdx.x] = beam_base(score, done, st.x, st.y);
   }
   __syncthreads();
-  const int all = p.beams * p.per;
-  for (int a = tid; a < all; a += blockDim.x) {
-    const int w = a / p.per, j = a - w * p.per;
-    uint64_t key;
-    int tok;
-    if (kind[w] == 0) {
-      const uint64_t e = p.entries[(r0 + w) * p.per + j];
-      tok = entry_col(e);
-      key = total_key(base[w] + (double)value_of(entry_key(e)));
-    } else if (kind[w] == 1) {
-      tok = j;
-      key = total_key(base[w]);
-    } else {   // the end token, then the others in order, at -infinity
-      tok = j == 0 ? p.eos : j - 1 + (j - 1 >= p.eos);
-      key = total_key(j == 0 ? base[w] : -(double)INFINITY);
-    }
-    keys[a] = key;
-    toks[a] = tok;
-  }
-  __syncthreads();
-  for (int a = tid; a < all; a += blockDim.x) {
-    const int w = a / p.per;
-    const uint64_t key = keys[a];
-    int place = a - w * p.per;
-    for (int o = 0; o < p.beams; ++o) {
-      if (o == w) continue;
-      const uint64_t* l = keys + o * p.per;   // those before this pair: larger, or equal of a lower beam
-      int lo = 0, hi = p.per;
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (l[mid] > key || (l[mid] == key && o < w)) lo = mid + 1;
-        else hi = mid;
-      }
-      place += lo;
-    }
-    if (place < p.m) {
-      const int64_t at = (int64_t)blockIdx.x * p.m + place;
-      p.scores_out[at] = (float)total_of(key);
-      p.parents[at] = w;
-      p.tokens[at] = toks[a];
-      if (p.done_out) p.done_out[at] = (kind[w] == 2 || toks[a] == p.eos) ? 1 : 0;
-    }
-  }
+  merge_beams(p.out, blockIdx.x, p.entries + r0 * p.out.per, base, keys, toks);
 }
 
 struct ReorderParams {
@@ -196,16 +117,16 @@ int beam_select_plan(const BeamSelectOp& op, LaunchRec* recs, char* err, size_t 
   const int64_t rows = op.batch * op.beams;
   uint64_t* entries = reinterpret_cast<uint64_t*>(op.ws);
   float* stats = reinterpret_cast<float*>(entries + rows * per);
-  beam_rows_plan(op, per, entries, stats, &recs[0]);
+  if (beam_rows_plan(op, per, entries, stats, &recs[0])) return 1;   // (merged there)
   BeamMergeParams p{};
   p.entries = entries; p.stats = reinterpret_cast<const float2*>(stats);
-  p.scores = op.scores; p.done = op.done;
-  p.beams = (int)op.beams; p.C = (int)op.C; p.m = (int)op.m; p.per = per; p.eos = op.eos;
-  p.scores_out = op.scores_out; p.parents = op.parents; p.tokens = op.tokens; p.done_out = op.done_out;
+  p.scores = op.scores; p.in_done = op.done;
+  p.out = BeamOut{(int)op.beams, (int)op.m, per, op.eos, op.scores_out, op.parents, op.tokens, op.done_out};
+  const int all = p.out.beams * per;
   recs[1].func = (const void*)beam_merge_kernel;
   recs[1].grid = dim3((unsigned)op.batch);
-  recs[1].block = dim3(p.beams * per <= 64 ? 64 : p.beams * per <= 128 ? 128 : 256);
-  recs[1].smem = (unsigned)(p.beams * per * 12);
+  recs[1].block = dim3(all <= 64 ? 64 : all <= 128 ? 128 : 256);
+  recs[1].smem = (unsigned)(all * 12);
   recs[1].name = "beam_merge";
   recs[1].set_args(p);
   return 2;

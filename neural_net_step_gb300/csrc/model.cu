@@ -1697,11 +1697,12 @@ mlp_status mlp_op_beam_select(int dtype, int64_t batch, int64_t beams, int64_t C
   op.scores_out = scores_out; op.parents = parents; op.tokens = tokens; op.done_out = done_out; op.ws = workspace;
   LaunchRec r[2];
   char e_[512] = "";
-  if (beam_select_plan(op, r, e_, sizeof(e_)) < 0) return fail(MLP_ERR_SHAPE, "%s", e_);
+  const int n = beam_select_plan(op, r, e_, sizeof(e_));
+  if (n < 0) return fail(MLP_ERR_SHAPE, "%s", e_);
   if (!workspace || ws_bytes < beam_select_workspace(batch, beams, C, m))
     return fail(MLP_ERR_ARG, "beam_select: workspace of %zu bytes is too small", ws_bytes);
   if (!elements_aligned(8, {workspace})) return fail(MLP_ERR_ARG, "misaligned workspace");
-  return run_chain(r, 2, stream);
+  return run_chain(r, n, stream);
 }
 
 mlp_status mlp_op_beam_reorder(int64_t planes, int64_t batch, int64_t beams_in, int64_t beams_out, int64_t row_bytes,

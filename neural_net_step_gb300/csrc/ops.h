@@ -243,8 +243,8 @@ struct DistillOp {
 };
 int distill_plan(const DistillOp& op, LaunchRec* rec, char* err, size_t errlen);
 
-// Beam search (beam.cu): the selection is two records, the rows' best entries
-// (topk.cu) and their merge, joined by the workspace.
+// Beam search (beam.cu): the selection is one record, or two joined by the
+// workspace: the rows' best entries (topk.cu; true: merged already) and their merge.
 struct BeamSelectOp {
   int dtype = 0;
   int64_t batch = 0, beams = 0, C = 0, m = 0;
@@ -258,7 +258,7 @@ struct BeamSelectOp {
 };
 size_t beam_select_workspace(int64_t batch, int64_t beams, int64_t C, int64_t m);   // 0: a shape not taken
 int beam_select_plan(const BeamSelectOp& op, LaunchRec* recs, char* err, size_t errlen);
-int beam_rows_plan(const BeamSelectOp& op, int entries, uint64_t* lists, float* stats, LaunchRec* rec);
+bool beam_rows_plan(const BeamSelectOp& op, int entries, uint64_t* lists, float* stats, LaunchRec* rec);
 struct BeamReorderOp {
   int64_t planes = 0, batch = 0, beams_in = 0, beams_out = 0, row_bytes = 0;
   const void* src = nullptr; int64_t src_pitch = 0, src_plane = 0;   // bytes

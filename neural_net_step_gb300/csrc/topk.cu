@@ -28,6 +28,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "beam.cuh"
 #include "logits.cuh"
 #include "ops.h"
 
@@ -48,7 +49,11 @@ struct TopkParams {
   // {largest logit, sum of exp(z - largest)} of each row
   uint64_t* entries; float2* stats;
   const float* scores; const uint8_t* done;
+  BeamOut out;                      // or the selection itself (BEAMS)
 };
+
+// What the blocks of a cluster are.
+enum TopkMode { ALONE, SLICES, BEAMS };   // (no cluster), slices of a row, the beams of a batch entry
 
 struct __align__(16) TopkShared {
   Red red[7];
@@ -60,6 +65,7 @@ struct __align__(16) TopkShared {
   uint32_t last_key;                // the smallest taken
   int last_at;
   float2 part[8];                   // of each block of the cluster: reference and sum of the rest
+  BeamBase base[8];                 // of each beam of a batch entry
 };
 
 // Candidates of a slice at most, and units listed at most, shared out to the warps.
@@ -240,18 +246,26 @@ __device__ __forceinline__ int larger_in_runs(const K* runs, int not_in, K e) {
   return sum;
 }
 
-template <typename T, bool CLUSTER, int NT, typename K>
+template <typename T, int MODE, int NT, typename K>
 __global__ void __launch_bounds__(NT, 1024 / NT) topk_kernel(const __grid_constant__ TopkParams p) {
   pdl_enter();
   constexpr int E = kPer16<T>, warps = NT / 32, room = kRoom<NT> / warps;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ TopkShared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t row = blockIdx.x;
-  const int rank = CLUSTER ? (int)blockIdx.z : 0, blocks = CLUSTER ? (int)gridDim.z : 1;
-  // beams that offer nothing of their row: the merge knows without it
-  if (p.stats && ((p.done && p.done[row]) || !(fabsf(p.scores[row]) < INFINITY))) return;
-  if (CLUSTER) cluster_arrive();
+  constexpr bool CLUSTER = MODE == SLICES;
+  const int rank = MODE != ALONE ? (int)blockIdx.z : 0, blocks = MODE != ALONE ? (int)gridDim.z : 1;
+  const int64_t row = MODE == BEAMS ? (int64_t)blockIdx.x * p.out.beams + rank : (int64_t)blockIdx.x;
+  if (MODE != ALONE) cluster_arrive();
+  // beams that offer nothing of their row
+  const bool beam = MODE == BEAMS ? rank < p.out.beams : p.stats != nullptr;
+  const float score = beam ? p.scores[row] : 0.f;
+  const bool done = beam && p.done && p.done[row];
+  const bool reads = MODE == BEAMS ? beam && beam_reads_row(score, done) : !beam || beam_reads_row(score, done);
+  if (MODE != BEAMS && !reads) {   // (the merge knows without it)
+    if (MODE == SLICES) cluster_wait();
+    return;
+  }
 
   K* cand = reinterpret_cast<K*>(smem);                            // [kRoom]
   int* hits = reinterpret_cast<int*>(cand + kRoom<NT>);            // [kRoom]: units, warp by warp; then
@@ -259,8 +273,29 @@ __global__ void __launch_bounds__(NT, 1024 / NT) topk_kernel(const __grid_consta
   uint64_t* best = reinterpret_cast<uint64_t*>(hits + kRoom<NT>);  // of a cluster's first block: [k] the row's, descending,
   uint64_t* lists = best + p.k;                                    //   [blocks][k] every block's (0: none)
   uint64_t* own = lists + (int64_t)rank * p.k;
+  // the beams' lists and what their logits are added to go to the first block, which merges them
+  const auto finish_beams = [&](const BeamBase& b) {
+    cluster_wait();   // (every block of the cluster runs)
+    if (beam) {
+      if (rank != 0 && reads && tid < p.k) put64(in_block(smem_addr(own + tid), 0), own[tid]);
+      if (tid == 0) {
+        const uint32_t to = in_block(smem_addr(&sh.base[rank]), 0);
+        put64(to, (uint64_t)__double_as_longlong(b.base));
+        put32(to + 8, (uint32_t)b.kind);
+      }
+    }
+    cluster_arrive();
+    cluster_wait();
+    uint64_t* keys = lists + 8 * p.k;
+    if (rank == 0) merge_beams(p.out, blockIdx.x, lists, sh.base, keys, reinterpret_cast<int*>(keys + 8 * p.k));
+  };
+  if (MODE == BEAMS && !reads) {
+    finish_beams(beam_base(score, done, 0.f, 0.f));
+    return;
+  }
 
-  const Walk<T, NT> s(reinterpret_cast<const T*>(p.z) + row * p.ldz, rank * p.per, min(p.per, p.C - rank * p.per));
+  const int lo = CLUSTER ? rank * p.per : 0;
+  const Walk<T, NT> s(reinterpret_cast<const T*>(p.z) + row * p.ldz, lo, reads ? min(p.per, p.C - lo) : 0);
   const int kk = min(p.k, s.n), e0 = s.first_edge(), e1 = s.last_edge();
   const float x0 = e0 >= 0 ? to_f32(s.g[e0]) : -INFINITY, x1 = e1 >= 0 ? to_f32(s.g[e1]) : -INFINITY;
   if (tid == 0) sh.count = sh.over = 0;
@@ -316,7 +351,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) topk_kernel(const __grid_consta
   tau = max(tau, key_of(-INFINITY));
 
   // 2. candidates, and the sum of the others relative to the threshold that they are below
-  const bool sums = p.lse || p.tail || p.stats;
+  const bool sums = MODE == BEAMS || p.lse || p.tail || p.stats;
   const float least = value_of(tau);
   float ref = least > -INFINITY ? least : 0.f, rest = 0.f;
   const Exponent ex(ref, p.c);
@@ -466,7 +501,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) topk_kernel(const __grid_consta
     const int i = Cand<K>::at(c);
     sorted[place] = x;
     if (place < kk) {
-      if (CLUSTER) own[place] = entry_of(Cand<K>::key(c), s.lo + i);
+      if (MODE != ALONE) own[place] = entry_of(Cand<K>::key(c), s.lo + i);
       else write(place, x, s.lo + i);
       if (place == kk - 1) {
         sh.last_key = Cand<K>::key(c);
@@ -489,7 +524,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) topk_kernel(const __grid_consta
   }
   // where next to nothing is left: relative to the largest that is not taken
   const auto look_closer = [&]() {
-    if (!sums || !(rest < 0x1p-60f)) return;
+    if (!p.tail || !(rest < 0x1p-60f)) return;
     const Limit limit{sh.last_key, sh.last_at};
     float m = -INFINITY;
     s.each([&](int i, float x) {
@@ -565,12 +600,18 @@ __global__ void __launch_bounds__(NT, 1024 / NT) topk_kernel(const __grid_consta
   block_sums<NT>(taken, rest, sh.red[1], sh.red[2]);
   if (!CLUSTER) look_closer();
   const float all = taken + (rest != 0.f ? rest * ex2((ref - first0) * p.c) : 0.f);
+  if (MODE == BEAMS) {
+    finish_beams(beam_base(score, done, first, all));
+    return;
+  }
   if (tid == 0) {
     if (p.stats) p.stats[row] = make_float2(first, all);
     if (p.lse) p.lse[row] = first0 / p.T + logf(all);
   }
   if (tid == 32 && p.tail) p.tail[row] = ref / p.T + logf(rest);
 }
+
+constexpr int64_t kFusedRow = 256 * 1024;
 
 // Blocks of a row and their threads.  Twice as many threads as entries: their
 // largest elements set the threshold.  More where rows are few; a row
@@ -579,10 +620,10 @@ __global__ void __launch_bounds__(NT, 1024 / NT) topk_kernel(const __grid_consta
 struct TopkCut {
   int cluster, per, threads;
 };
-TopkCut topk_cut(int64_t rows, int64_t C, int es, int k) {
+TopkCut topk_cut(int64_t rows, int64_t C, int es, int k, bool whole) {
   TopkCut c;
   c.cluster = 1;
-  while (c.cluster < 8 && rows * c.cluster * 2 <= kSMs && ceil_div(C, c.cluster * 2) * es >= 64 * 1024) c.cluster *= 2;
+  while (!whole && c.cluster < 8 && rows * c.cluster * 2 <= kSMs && ceil_div(C, c.cluster * 2) * es >= 64 * 1024) c.cluster *= 2;
   c.per = (int)round_up(ceil_div(C, c.cluster), 16 / es);
   const int64_t blocks = rows * c.cluster, units = c.per * es / 16;
   c.threads = k <= 64 ? 128 : k <= 128 ? 256 : 512;
@@ -590,30 +631,36 @@ TopkCut topk_cut(int64_t rows, int64_t C, int es, int k) {
   return c;
 }
 
-template <typename T, bool CLUSTER, typename K>
+template <typename T, int MODE, typename K>
 const void* topk_func(int threads) {
-  return threads == 128   ? (const void*)topk_kernel<T, CLUSTER, 128, K>
-         : threads == 256 ? (const void*)topk_kernel<T, CLUSTER, 256, K>
-                          : (const void*)topk_kernel<T, CLUSTER, 512, K>;
+  return threads == 128   ? (const void*)topk_kernel<T, MODE, 128, K>
+         : threads == 256 ? (const void*)topk_kernel<T, MODE, 256, K>
+                          : (const void*)topk_kernel<T, MODE, 512, K>;
 }
 template <typename T, typename K>
-const void* topk_func(const TopkCut& cut) {
-  return cut.cluster > 1 ? topk_func<T, true, K>(cut.threads) : topk_func<T, false, K>(cut.threads);
+const void* topk_func(int mode, int threads) {
+  return mode == ALONE    ? topk_func<T, ALONE, K>(threads)
+         : mode == SLICES ? topk_func<T, SLICES, K>(threads)
+                          : topk_func<T, BEAMS, K>(threads);
 }
 
 void topk_launch(int dtype, int64_t rows, const TopkParams& q, LaunchRec* rec) {
-  const int es = dtype == DT_F32 ? 4 : 2;
-  const TopkCut cut = topk_cut(rows, q.C, es, q.k);
+  const int es = dtype == DT_F32 ? 4 : 2, beams = q.out.beams;   // (0: rows of their own)
+  const TopkCut cut = topk_cut(rows, q.C, es, q.k, beams > 0);
   TopkParams p = q;
   p.per = cut.per;
   const bool small = es == 2 && cut.per <= 65535;
-  rec->grid = dim3((unsigned)rows, 1, (unsigned)cut.cluster);
+  const int blocks = beams > 4 ? 8 : beams > 2 ? 4 : beams > 0 ? 2 : cut.cluster;
+  const int mode = beams > 0 ? BEAMS : blocks > 1 ? SLICES : ALONE;
+  rec->grid = dim3((unsigned)(beams > 0 ? rows / beams : rows), 1, (unsigned)blocks);
   rec->block = dim3((unsigned)cut.threads);
-  rec->cluster = (unsigned)cut.cluster;
-  rec->smem = (unsigned)((cut.threads < 256 ? 512 : 1024) * ((small ? 4 : 8) + 4) + (cut.cluster > 1 ? 9 * 8 * p.k : 0));
-  rec->func = es == 4 ? topk_func<float, uint64_t>(cut)
-              : small ? topk_func<__nv_bfloat16, uint32_t>(cut) : topk_func<__nv_bfloat16, uint64_t>(cut);
-  rec->name = "topk";
+  rec->cluster = (unsigned)blocks;
+  rec->smem = (unsigned)((cut.threads < 256 ? 512 : 1024) * ((small ? 4 : 8) + 4) +
+                         (mode == ALONE ? 0 : mode == SLICES ? 9 * 8 * p.k : (9 * 8 + 8 * 12) * p.k));
+  rec->func = es == 4 ? topk_func<float, uint64_t>(mode, cut.threads)
+              : small ? topk_func<__nv_bfloat16, uint32_t>(mode, cut.threads)
+                      : topk_func<__nv_bfloat16, uint64_t>(mode, cut.threads);
+  rec->name = mode == BEAMS ? "beam_select" : "topk";
   rec->set_args(p);
 }
 
@@ -634,15 +681,22 @@ int topk_plan(const TopkOp& op, LaunchRec* rec, char* err, size_t errlen) {
   return 1;
 }
 
-int beam_rows_plan(const BeamSelectOp& op, int entries, uint64_t* lists, float* stats, LaunchRec* rec) {
+bool beam_rows_plan(const BeamSelectOp& op, int entries, uint64_t* lists, float* stats, LaunchRec* rec) {
   TopkParams p{};
   p.z = op.z; p.ldz = op.ldz; p.C = (int)op.C; p.k = entries;
   p.T = 1.f; p.c = kLog2e;
-  p.entries = lists; p.stats = reinterpret_cast<float2*>(stats);
   p.scores = op.scores; p.done = op.done;
-  topk_launch(op.dtype, op.batch * op.beams, p, rec);
-  rec->name = "beam_rows";
-  return 1;
+  const int64_t rows = op.batch * op.beams;
+  // the beams as a cluster's blocks, where they are few and a block is enough for a row
+  const bool merge = op.beams <= 8 && (rows >= kSMs || op.C * (op.dtype == DT_F32 ? 4 : 2) <= kFusedRow);
+  if (merge) {
+    p.out = BeamOut{(int)op.beams, (int)op.m, entries, op.eos, op.scores_out, op.parents, op.tokens, op.done_out};
+  } else {
+    p.entries = lists; p.stats = reinterpret_cast<float2*>(stats);
+  }
+  topk_launch(op.dtype, rows, p, rec);
+  if (!merge) rec->name = "beam_rows";
+  return merge;
 }
 
 }  // namespace mlpk
