@@ -85,11 +85,16 @@ __device__ __forceinline__ float divergence(float p, float q, float r) {
   return p * (r * r) * h;
 }
 
-// TWO: the hard labels' softmax is at another temperature than the soft ones'.
-template <typename T, bool CLUSTER, bool TWO, int NT>
-__global__ void __launch_bounds__(NT, NT <= 256 ? 3 : 1) distill_kernel(const __grid_constant__ DistillParams p) {
+// The hard labels' softmax next to the soft ones': of the same temperature, at any
+// other (a second exponential an element), or at half of it (T = 2: the square of
+// the first; 8192 x 32000, k = 32: @@ us with a second exponential, @@ so).
+enum Hard { SAME, OTHER, SQUARE };
+
+template <typename T, bool CLUSTER, int HARD, int NT>
+__global__ void __launch_bounds__(NT, NT == 128 ? 5 : NT == 256 ? 3 : 1) distill_kernel(const __grid_constant__ DistillParams p) {
   pdl_enter();
   constexpr int E = kPer16<T>;
+  constexpr bool TWO = HARD != SAME;
   typedef typename BitsOf<T>::type Bits;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ DistillShared sh;
@@ -157,8 +162,10 @@ __global__ void __launch_bounds__(NT, NT <= 256 ? 3 : 1) distill_kernel(const __
   // ---- the sums over the others
   float most = block_max<NT>(max_of(s), sh.red[2]);
   const float ref = most > -INFINITY ? most : 0.f;
-  float sum = block_sum<NT>(sum_exp(s, Exponent(ref, p.c)), sh.red[3]), sum1 = 0.f;
-  if constexpr (TWO) sum1 = block_sum<NT>(sum_exp(s, Exponent(ref, kLog2e)), sh.red[4]);
+  float none, sum1 = 0.f, sum = sum_exp<HARD == SQUARE>(s, Exponent(ref, p.c), sum1);
+  if constexpr (HARD == OTHER) sum1 = sum_exp<false>(s, Exponent(ref, kLog2e), none);
+  if constexpr (TWO) block_sums<NT>(sum, sum1, sh.red[3], sh.red[4]);
+  else sum = block_sum<NT>(sum, sh.red[3]);
 
   // ---- all slices together
   float zy = 0.f;
@@ -223,9 +230,12 @@ __global__ void __launch_bounds__(NT, NT <= 256 ? 3 : 1) distill_kernel(const __
     if constexpr (!TWO) A += p.labels ? A1 : 0.f;
     const Exponent eg(rest, p.c), eg1(rest, kLog2e);
     A *= eg.scale;
-    const float B1 = A1 * eg1.scale;
-    const auto grad = [&](float x) { return TWO ? fmaf(eg1.one(x), B1, eg.one(x) * A) : eg.one(x) * A; };
-    if (eg.far || (TWO && eg1.far)) {
+    const float B1 = A1 * (HARD == SQUARE ? eg.scale * eg.scale : eg1.scale);
+    const auto grad = [&](float x) {
+      const float e = eg.one(x);
+      return HARD == SAME ? e * A : HARD == SQUARE ? e * fmaf(e, B1, A) : fmaf(eg1.one(x), B1, e * A);
+    };
+    if (eg.far || (HARD == OTHER && eg1.far)) {
       for (int i = tid; i < s.nvec * E; i += NT) s.elems()[i] = from_f32<T>(grad(to_f32(s.elems()[i])));
     } else {
       const F2 c2 = pack2(p.c, p.c), r2 = pack2(-eg.rc, -eg.rc), A2 = pack2(A, A);
@@ -237,10 +247,16 @@ __global__ void __launch_bounds__(NT, NT <= 256 ? 3 : 1) distill_kernel(const __
           const F2 x2 = pair_of<T>(in, h);
           float x, y;
           unpack2(fma2(x2, c2, r2), x, y);
-          F2 d = mul2(pack2(ex2(x), ex2(y)), A2);
-          if constexpr (TWO) {
-            unpack2(fma2(x2, c12, r12), x, y);
-            d = fma2(pack2(ex2(x), ex2(y)), B2, d);
+          const F2 e2 = pack2(ex2(x), ex2(y));
+          F2 d;
+          if constexpr (HARD == SQUARE) {
+            d = mul2(e2, fma2(e2, B2, A2));
+          } else {
+            d = mul2(e2, A2);
+            if constexpr (HARD == OTHER) {
+              unpack2(fma2(x2, c12, r12), x, y);
+              d = fma2(pack2(ex2(x), ex2(y)), B2, d);
+            }
           }
           unpack2(d, x, y);
           if constexpr (sizeof(T) == 4) {
@@ -294,22 +310,27 @@ __global__ void __launch_bounds__(NT, NT <= 256 ? 3 : 1) distill_kernel(const __
 
   // ---- the loss, while the gradient leaves
   if (rank == 0) {
-    float kd = 0.f;
-    if (has && p.b != 0.f) {
-      const float ln = logf(St / S), R = sum * f / S;
-      if (mine && col >= 0) kd = divergence(pj, q / S, ((t - ztj) - (tm0 - m0)) / p.T + dl - ln);
-      kd = block_sum<NT>(kd, sh.red[8]);
-      kd += divergence(pr, R, R > 1e-30f ? logf(pr / R) : logf(pr) - ((rest - m0) / p.T + logf(sum) - logf(S)));
-      kd *= p.b;
+    const bool soft = has && p.b != 0.f;
+    const float ln = soft ? logf(St / S) : 0.f;
+    float kd = soft && mine && col >= 0 ? divergence(pj, q / S, ((t - ztj) - (tm0 - m0)) / p.T + dl - ln) : 0.f;
+    if (p.k > 32) kd = block_sum<NT>(kd, sh.red[8]);
+    else if (tid < 32) kd = warp_sum(kd);
+    if (tid == 0) {
+      if (soft) {
+        const float R = sum * f / S;
+        kd += divergence(pr, R, R > 1e-30f ? logf(pr / R) : logf(pr) - ((rest - m0) / p.T + logf(sum) - logf(S)));
+      }
+      p.loss[row] = w * (p.b * kd + (p.labels ? p.a * (logf(S1) + (m0 - zy)) : 0.f));
     }
-    if (tid == 0) p.loss[row] = w * (kd + (p.labels ? p.a * (logf(S1) + (m0 - zy)) : 0.f));
   }
   if (tid == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 
 // How rows are cut: `cluster` blocks of `threads` threads (at least k) share a
 // row, `per` columns each; a slice of at most 64 KB leaves room for three blocks on
-// an SM.
+// an SM.  128 threads for slices of which five and more fit an SM: a block's sums and
+// barriers cost each warp the same, however little of a row it has (16384 x 4000, k = 16: 208 us
+// with 256 threads, 125 with 128); 512 where one fits.
 struct Cut {
   int cluster, per, threads;
 };
@@ -319,21 +340,26 @@ Cut cut_rows(int64_t C, int es, int k) {
   Cut c;
   c.cluster = cs;
   c.per = (int)round_up(ceil_div(C, cs), 16 / es);
-  const int64_t units = c.per * es / 16 + 1;   // (a row's phase adds one)
-  c.threads = units <= 3 * 128 && k <= 128 ? 128 : units <= 16 * 256 ? 256 : 512;
+  const int64_t bytes = (int64_t)c.per * es;
+  c.threads = bytes <= 48 * 1024 && k <= 128 ? 128 : bytes <= 100 * 1024 ? 256 : 512;
   return c;
 }
 
-template <typename T, bool CLUSTER, bool TWO>
+template <typename T, bool CLUSTER, int HARD>
 const void* distill_func(int threads) {
-  return threads == 128   ? (const void*)distill_kernel<T, CLUSTER, TWO, 128>
-         : threads == 256 ? (const void*)distill_kernel<T, CLUSTER, TWO, 256>
-                          : (const void*)distill_kernel<T, CLUSTER, TWO, 512>;
+  return threads == 128   ? (const void*)distill_kernel<T, CLUSTER, HARD, 128>
+         : threads == 256 ? (const void*)distill_kernel<T, CLUSTER, HARD, 256>
+                          : (const void*)distill_kernel<T, CLUSTER, HARD, 512>;
+}
+template <typename T, bool CLUSTER>
+const void* distill_func(int hard, int threads) {
+  return hard == SAME    ? distill_func<T, CLUSTER, SAME>(threads)
+         : hard == OTHER ? distill_func<T, CLUSTER, OTHER>(threads)
+                         : distill_func<T, CLUSTER, SQUARE>(threads);
 }
 template <typename T>
-const void* distill_func(bool cluster, bool two, int threads) {
-  if (cluster) return two ? distill_func<T, true, true>(threads) : distill_func<T, true, false>(threads);
-  return two ? distill_func<T, false, true>(threads) : distill_func<T, false, false>(threads);
+const void* distill_func(bool cluster, int hard, int threads) {
+  return cluster ? distill_func<T, true>(hard, threads) : distill_func<T, false>(hard, threads);
 }
 
 }  // namespace
@@ -355,13 +381,13 @@ int distill_plan(const DistillOp& op, LaunchRec* rec, char* err, size_t errlen) 
   p.T = op.temperature; p.inv_T = 1.f / op.temperature; p.c = kLog2e / op.temperature;
   p.a = op.ce_weight; p.b = op.kd_weight; p.g = op.grad_scale;
   p.err = op.err;
-  const bool two = p.labels && op.temperature != 1.f;
+  const int hard = !p.labels || op.temperature == 1.f ? SAME : op.temperature == 2.f ? SQUARE : OTHER;
   rec->grid = dim3((unsigned)op.B, 1, (unsigned)cut.cluster);
   rec->block = dim3((unsigned)cut.threads);
   rec->cluster = (unsigned)cut.cluster;
   rec->smem = (unsigned)((op.k * 4 + 15) / 16 * 16 + slice_buffer(cut.per, es, cut.threads));
-  rec->func = op.dtype == DT_F32 ? distill_func<float>(cut.cluster > 1, two, cut.threads)
-                                 : distill_func<__nv_bfloat16>(cut.cluster > 1, two, cut.threads);
+  rec->func = op.dtype == DT_F32 ? distill_func<float>(cut.cluster > 1, hard, cut.threads)
+                                 : distill_func<__nv_bfloat16>(cut.cluster > 1, hard, cut.threads);
   rec->name = "distill";
   rec->set_args(p);
   return 1;

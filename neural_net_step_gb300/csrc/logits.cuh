@@ -25,7 +25,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kSMs = 152;
 constexpr int kMaxK = 256;                 // entries kept of a row
 constexpr int64_t kMaxC = 384000;          // columns: eight slices of 192000 bytes of fp32
-constexpr int kAhead = 2 * kSMs;            // rows are asked for so many blocks ahead
+constexpr int kAhead = kSMs;                // rows are asked for so many blocks ahead
 constexpr int64_t kSliceBytes = 64 * 1024; // a slice of at most this leaves room for three blocks on an SM
 
 // 2^t; subnormal results are flushed to zero (PTX ex2.approx).
@@ -279,27 +279,38 @@ struct Exponent {
   // of one x, without the scale
   __device__ __forceinline__ float one(float x) const { return ex2(far ? (x - ref) * c : fmaf(x, c, -rc)); }
 };
-// The sum over this thread's units of exp((x - ref) / T).
-template <typename T, int NT>
-__device__ __forceinline__ float sum_exp(const Slice<T, NT>& s, const Exponent& q) {
+// The sum over this thread's units of exp((x - ref) / T), and with SQUARES the sum
+// of their squares.
+template <bool SQUARES, typename T, int NT>
+__device__ __forceinline__ float sum_exp(const Slice<T, NT>& s, const Exponent& q, float& squares) {
   float sum;
   if (q.far) {
-    sum = 0.f;
-    s.each([&](int, float x) { sum += ex2((x - q.ref) * q.c); });
+    sum = squares = 0.f;
+    s.each([&](int, float x) {
+      const float e = ex2((x - q.ref) * q.c);
+      sum += e;
+      if (SQUARES) squares = fmaf(e, e, squares);
+    });
   } else {
-    F2 a0 = pack2(0.f, 0.f), a1 = a0;
     const F2 c2 = pack2(q.c, q.c), r2 = pack2(-q.rc, -q.rc);
+    F2 a0 = pack2(0.f, 0.f), a1 = a0, b0 = a0, b1 = a0;
     s.each_unit([&](const uint4& u) {
 #pragma unroll
       for (int h = 0; h < kPer16<T> / 2; ++h) {
         float x, y;
         unpack2(fma2(pair_of<T>(u, h), c2, r2), x, y);
         const F2 e = pack2(ex2(x), ex2(y));
-        if (h & 1) a1 = add2(a1, e);
-        else a0 = add2(a0, e);
+        if (h & 1) {
+          a1 = add2(a1, e);
+          if (SQUARES) b1 = fma2(e, e, b1);
+        } else {
+          a0 = add2(a0, e);
+          if (SQUARES) b0 = fma2(e, e, b0);
+        }
       }
     });
     sum = sum2(add2(a0, a1));
+    squares = SQUARES ? sum2(add2(b0, b1)) * (q.scale * q.scale) : 0.f;
   }
   return sum * q.scale;
 }

@@ -57,7 +57,7 @@ enum TopkMode { ALONE, SLICES, BEAMS };   // (no cluster), slices of a row, the 
 
 struct __align__(16) TopkShared {
   Red red[7];
-  uint32_t top[16];                 // of each warp (read 16 bytes at a time)
+  uint32_t top[16], nth[16];        // of each warp (read 16 bytes at a time)
   uint32_t tau;
   int count, over;                  // candidates; units found no place in a warp's list
   int total[16];
@@ -130,6 +130,15 @@ __device__ __forceinline__ U warp_sort_down(U x) {
   }
   return x;
 }
+// The n-th largest of the warp's values, n from 1.
+__device__ __forceinline__ uint32_t warp_nth(uint32_t x, int n) {
+  while (true) {
+    const uint32_t m = __reduce_max_sync(0xffffffffu, x);
+    if (--n <= 0) return m;
+    if ((threadIdx.x & 31) == __ffs(__ballot_sync(0xffffffffu, x == m)) - 1) x = 0;
+  }
+}
+
 // A candidate of a slice: larger is better, lower element first among equals; 0
 // is none.  bf16 slices of at most 65535 elements need 32 bits.
 template <typename K> struct Cand;
@@ -250,6 +259,7 @@ template <typename T, int MODE, int NT, typename K>
 __global__ void __launch_bounds__(NT, 1024 / NT) topk_kernel(const __grid_constant__ TopkParams p) {
   pdl_enter();
   constexpr int E = kPer16<T>, warps = NT / 32, room = kRoom<NT> / warps;
+  constexpr int kCounted = NT > 128 ? NT / 4 : 0;   // candidates whose places are counted: sooner known, more instructions
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ TopkShared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -325,29 +335,38 @@ __global__ void __launch_bounds__(NT, 1024 / NT) topk_kernel(const __grid_consta
 #pragma unroll
     for (int q = 0; q < 8; ++q) most.take(Most<T>(held[q]));
   }
-  // (the threads' largest, made distinct by their numbers, sorted by warps and searched like the candidates below)
   const uint32_t most_key = key_of(fmaxf(most.value(), fmaxf(x0, x1)));
   uint32_t* keys = reinterpret_cast<uint32_t*>(hits);   // [NT]
-  const uint32_t mine = warp_sort_down((most_key & 0xFFFFFE00u) | (uint32_t)tid);
-  keys[tid] = mine;
+  const bool few = NT > 128 && kk * 4 <= NT;
+  uint32_t mine;
+  if (few) {   // the smallest of the warps' ceil(kk / warps)-th largest: a little lower, and sooner known
+    mine = warp_nth(most_key, (kk + warps - 1) / warps);
+    if (lane == 0) sh.nth[warp] = mine;
+  } else {     // distinct by the threads' numbers, sorted by warps and searched like the candidates below
+    mine = warp_sort_down((most_key & 0xFFFFFE00u) | (uint32_t)tid);
+    keys[tid] = mine;
+  }
   const uint32_t top_key = __reduce_max_sync(0xffffffffu, most_key);
   if (lane == 0) sh.top[warp] = top_key;
+  if (tid < kCounted) cand[tid] = 0;
   __syncthreads();
-  {
-    int place = lane;
-#pragma unroll
-    for (int w = 0; w < warps; w += 4) place += larger_in_runs<4>(keys + w * 32, warp - w, mine);
-    if (place == (kk > 0 ? kk - 1 : 0)) sh.tau = mine & 0xFFFFFE00u;
-  }
-  uint32_t row_key = 0;
+  uint32_t tau = 0xFFFFFFFFu, row_key = 0;
 #pragma unroll
   for (int w = 0; w < warps; w += 4) {
-    const uint4 r = *reinterpret_cast<const uint4*>(sh.top + w);
+    const uint4 r = *reinterpret_cast<const uint4*>(sh.top + w), q = *reinterpret_cast<const uint4*>(sh.nth + w);
     row_key = max(row_key, max(max(r.x, r.y), max(r.z, r.w)));
+    tau = min(tau, min(min(q.x, q.y), min(q.z, q.w)));
   }
-  __syncthreads();
-  uint32_t tau = sh.tau;
-  if (sizeof(T) == 2) tau = (tau & 0x80000000u) ? tau & 0xFFFF0000u : tau | 0xFFFFu;   // (a bf16's key again)
+  if (!few) {
+    constexpr int N = warps < 8 ? warps : 8;
+    int place = lane;
+#pragma unroll
+    for (int w = 0; w < warps; w += N) place += larger_in_runs<N>(keys + w * 32, warp - w, mine);
+    if (place == kk - 1) sh.tau = mine & 0xFFFFFE00u;
+    __syncthreads();
+    tau = sh.tau;
+    if (sizeof(T) == 2) tau = (tau & 0x80000000u) ? tau & 0xFFFF0000u : tau | 0xFFFFu;   // (a bf16's key again)
+  }
   tau = max(tau, key_of(-INFINITY));
 
   // 2. candidates, and the sum of the others relative to the threshold that they are below
@@ -463,6 +482,10 @@ __global__ void __launch_bounds__(NT, 1024 / NT) topk_kernel(const __grid_consta
       __syncthreads();
       limit = search<T>(s, kk, many ? tau : 0u, cand, sh);
       count = sh.count;
+      if (count <= kCounted) {   // (zeros behind the last again)
+        if (tid >= count && tid < kCounted) cand[tid] = 0;
+        __syncthreads();
+      }
     }
     if (sums) {
       float m = -INFINITY;
@@ -479,10 +502,6 @@ __global__ void __launch_bounds__(NT, 1024 / NT) topk_kernel(const __grid_consta
   }
 
   // 3. the candidates' places
-  const int runs = (count + 31) / 32, width = runs <= 4 ? 4 : 8;
-  for (int r = warp; r < (runs + width - 1) / width * width; r += warps)
-    cand[r * 32 + lane] = warp_sort_down(r * 32 + lane < count ? cand[r * 32 + lane] : (K)0);
-  __syncthreads();
   const auto write = [&](int place, float x, int col) {
     if (p.stats) {
       p.entries[row * p.k + place] = entry_of(key_of(x), col);
@@ -491,12 +510,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) topk_kernel(const __grid_consta
       p.indices[row * p.ldi + place] = col;
     }
   };
-  for (int a = tid; a < count; a += NT) {
-    const K c = cand[a];
-    int place = a & 31;
-    if (width == 4) place += larger_in_runs<4>(cand, a >> 5, c);
-    else
-      for (int r = 0; r < runs; r += 8) place += larger_in_runs<8>(cand + r * 32, (a >> 5) - r, c);
+  const auto put = [&](int place, K c) {
     const float x = value_of(Cand<K>::key(c));
     const int i = Cand<K>::at(c);
     sorted[place] = x;
@@ -507,6 +521,40 @@ __global__ void __launch_bounds__(NT, 1024 / NT) topk_kernel(const __grid_consta
         sh.last_key = Cand<K>::key(c);
         sh.last_at = i;
       }
+    }
+  };
+  if (count <= kCounted) {   // four neighbouring threads count for one candidate (zeros behind the last)
+    const K c = tid < count * 4 ? cand[tid >> 2] : (K)0;
+    const uint4* all = reinterpret_cast<const uint4*>(cand);
+    constexpr int per16 = 16 / (int)sizeof(K);
+    int n[2] = {0, 0};
+    for (int b = tid & 3; b * 2 * per16 < count; b += 4) {
+      const uint4 o = all[2 * b], q = all[2 * b + 1];
+      if constexpr (sizeof(K) == 4) {
+        n[0] += (o.x > c) + (o.y > c) + (o.z > c) + (o.w > c);
+        n[1] += (q.x > c) + (q.y > c) + (q.z > c) + (q.w > c);
+      } else {
+        const auto two = [](uint32_t l, uint32_t h) { return (uint64_t)h << 32 | l; };
+        n[0] += (two(o.x, o.y) > c) + (two(o.z, o.w) > c);
+        n[1] += (two(q.x, q.y) > c) + (two(q.z, q.w) > c);
+      }
+    }
+    int place = n[0] + n[1];
+    place += __shfl_xor_sync(0xffffffffu, place, 1);
+    place += __shfl_xor_sync(0xffffffffu, place, 2);
+    if (tid < count * 4 && (tid & 3) == 0) put(place, c);
+  } else {
+    const int runs = (count + 31) / 32, width = runs <= 4 ? 4 : 8;
+    for (int r = warp; r < (runs + width - 1) / width * width; r += warps)
+      cand[r * 32 + lane] = warp_sort_down(r * 32 + lane < count ? cand[r * 32 + lane] : (K)0);
+    __syncthreads();
+    for (int a = tid; a < count; a += NT) {
+      const K c = cand[a];
+      int place = a & 31;
+      if (width == 4) place += larger_in_runs<4>(cand, a >> 5, c);
+      else
+        for (int r = 0; r < runs; r += 8) place += larger_in_runs<8>(cand + r * 32, (a >> 5) - r, c);
+      put(place, c);
     }
   }
   if (!CLUSTER && !sums) return;
