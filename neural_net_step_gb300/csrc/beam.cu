@@ -29,11 +29,9 @@ struct BeamMergeParams {
   BeamOut out;
 };
 
-__global__ void __launch_bounds__(256) beam_merge_kernel(const __grid_constant__ BeamMergeParams p) {
+__global__ void __launch_bounds__(512) beam_merge_kernel(const __grid_constant__ BeamMergeParams p) {
   pdl_enter();
   extern __shared__ __align__(16) unsigned char smem[];
-  uint64_t* keys = reinterpret_cast<uint64_t*>(smem);
-  int* toks = reinterpret_cast<int*>(keys + p.out.beams * p.out.per);
   __shared__ BeamBase base[kMaxBeams];
   const int64_t r0 = (int64_t)blockIdx.x * p.out.beams;
   if ((int)threadIdx.x < p.out.beams) {
@@ -44,7 +42,7 @@ __global__ void __launch_bounds__(256) beam_merge_kernel(const __grid_constant__
     base[threadIdx.x] = beam_base(score, done, st.x, st.y);
   }
   __syncthreads();
-  merge_beams(p.out, blockIdx.x, p.entries + r0 * p.out.per, base, keys, toks);
+  merge_beams(p.out, blockIdx.x, p.entries + r0 * p.out.per, base, reinterpret_cast<uint64_t*>(smem));
 }
 
 struct ReorderParams {
@@ -122,11 +120,11 @@ int beam_select_plan(const BeamSelectOp& op, LaunchRec* recs, char* err, size_t 
   p.entries = entries; p.stats = reinterpret_cast<const float2*>(stats);
   p.scores = op.scores; p.in_done = op.done;
   p.out = BeamOut{(int)op.beams, (int)op.m, per, op.eos, op.scores_out, op.parents, op.tokens, op.done_out};
-  const int all = p.out.beams * per;
+  const int all = p.out.beams * merge_stride(per);
   recs[1].func = (const void*)beam_merge_kernel;
   recs[1].grid = dim3((unsigned)op.batch);
-  recs[1].block = dim3(all <= 64 ? 64 : all <= 128 ? 128 : 256);
-  recs[1].smem = (unsigned)(all * 12);
+  recs[1].block = dim3(all <= 128 ? 128 : all <= 256 ? 256 : 512);
+  recs[1].smem = (unsigned)merge_bytes(p.out.beams, per);
   recs[1].name = "beam_merge";
   recs[1].set_args(p);
   return 2;

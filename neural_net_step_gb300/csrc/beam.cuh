@@ -25,15 +25,15 @@ struct __align__(16) BeamBase {
   int kind;
 };
 
-// Order of totals as unsigned integers; NaN is 0, below -infinity.
+// Order of totals as unsigned integers; NaN is 1, below -infinity (0: no pair).
 __device__ __forceinline__ uint64_t total_key(double t) {
   const uint64_t u = (uint64_t)__double_as_longlong(t + 0.0);
   const uint64_t k = (u >> 63) ? ~u : (u | 0x8000000000000000ull);
-  return t == t ? k : 0ull;
+  return t == t ? k : 1ull;
 }
 __device__ __forceinline__ double total_of(uint64_t k) {
   const uint64_t u = (k >> 63) ? (k & 0x7FFFFFFFFFFFFFFFull) : ~k;
-  return __longlong_as_double(k ? (long long)u : 0x7FF8000000000000ll);
+  return __longlong_as_double(k > 1 ? (long long)u : 0x7FF8000000000000ll);
 }
 // log s for a normal s > 0 to 3e-8 (fp64 is slow here: the exponent's part alone is).
 __device__ __forceinline__ double log_of(float s) {
@@ -69,48 +69,63 @@ __device__ __forceinline__ BeamBase beam_base(float score, bool done, float larg
   return b;
 }
 
-// The m best of batch entry b from every beam's `per` best entries, descending; keys
-// and toks: [beams * per] in shared memory.  Pairs of equal totals go by beam, then
-// by their place in the beam's list.
+// Lists are searched eight at a time and without bounds: the merge holds them in
+// places for a power of two of entries, and as many beams as eights go.
+__host__ __device__ inline int merge_stride(int per) {
+  int s = 1;
+  while (s < per) s *= 2;
+  return s;
+}
+__host__ __device__ inline int merge_bytes(int beams, int per) { return (beams + 7) / 8 * 8 * merge_stride(per) * 12; }
+
+// The m best of batch entry b from every beam's `per` best entries, descending; room:
+// merge_bytes in shared memory.  Pairs of equal totals go by beam, then by their place
+// in the beam's list.
 __device__ __forceinline__ void merge_beams(const BeamOut& p, int64_t b, const uint64_t* entries, const BeamBase* base,
-                                            uint64_t* keys, int* toks) {
-  const int all = p.beams * p.per;
-  for (int a = threadIdx.x; a < all; a += blockDim.x) {
-    const int w = a / p.per, j = a - w * p.per;
-    const BeamBase o = base[w];
-    uint64_t key;
-    int tok;
-    if (o.kind == 0) {
-      const uint64_t e = entries[a];
-      tok = entry_col(e);
-      key = total_key(o.base + (double)value_of(entry_key(e)));
-    } else if (o.kind == 1) {
-      tok = j;
-      key = total_key(o.base);
-    } else {   // the end token, then the others in order, at -infinity
-      tok = j == 0 ? p.eos : j - 1 + (j - 1 >= p.eos);
-      key = total_key(j == 0 ? o.base : -(double)INFINITY);
+                                            uint64_t* room) {
+  const int S = merge_stride(p.per), shift = 31 - __clz(S), lists = (p.beams + 7) / 8 * 8;
+  uint64_t* keys = room;                                     // [lists][S]
+  int* toks = reinterpret_cast<int*>(room + lists * S);
+  for (int a = threadIdx.x; a < lists * S; a += blockDim.x) {
+    const int w = a >> shift, j = a & (S - 1);
+    uint64_t key = 0;
+    int tok = 0;
+    if (w < p.beams && j < p.per) {
+      const BeamBase o = base[w];
+      if (o.kind == 0) {
+        const uint64_t e = entries[w * p.per + j];
+        tok = entry_col(e);
+        key = total_key(o.base + (double)value_of(entry_key(e)));
+      } else if (o.kind == 1) {
+        tok = j;
+        key = total_key(o.base);
+      } else {   // the end token, then the others in order, at -infinity
+        tok = j == 0 ? p.eos : j - 1 + (j - 1 >= p.eos);
+        key = total_key(j == 0 ? o.base : -(double)INFINITY);
+      }
     }
     keys[a] = key;
     toks[a] = tok;
   }
   __syncthreads();
-  for (int a = threadIdx.x; a < all; a += blockDim.x) {
-    const int w = a / p.per;
+  for (int a = threadIdx.x; a < p.beams * S; a += blockDim.x) {
+    const int w = a >> shift;
     const uint64_t key = keys[a];
-    int place = a - w * p.per;
-    for (int o0 = 0; o0 < p.beams; o0 += 8) {   // those before this pair: larger, or equal of a lower beam
+    if (key == 0) continue;
+    int place = a & (S - 1);
+    for (int o0 = 0; o0 < lists; o0 += 8) {   // those before this pair: larger, or equal of a lower beam
+      const uint64_t* l = keys + o0 * S;
       int at[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-      for (int step = 1 << (31 - __clz(p.per)); step > 0; step >>= 1) {
+      for (int step = S / 2; step > 0; step >>= 1) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const int o = min(o0 + q, p.beams - 1), to = at[q] + step;
-          const uint64_t v = keys[o * p.per + min(to, p.per) - 1];
-          at[q] = to <= p.per && (v > key || (v == key && o < w)) ? to : at[q];
-        }
+        for (int q = 0; q < 8; ++q)
+          if (l[q * S + at[q] + step - 1] > key - (o0 + q < w)) at[q] += step;
       }
 #pragma unroll
-      for (int q = 0; q < 8; ++q) place += o0 + q < p.beams && o0 + q != w ? at[q] : 0;
+      for (int q = 0; q < 8; ++q) {
+        at[q] += l[q * S + at[q]] > key - (o0 + q < w);
+        place += o0 + q != w ? at[q] : 0;
+      }
     }
     if (place < p.m) {
       const int64_t at = b * p.m + place;

@@ -296,8 +296,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) topk_kernel(const __grid_consta
     }
     cluster_arrive();
     cluster_wait();
-    uint64_t* keys = lists + 8 * p.k;
-    if (rank == 0) merge_beams(p.out, blockIdx.x, lists, sh.base, keys, reinterpret_cast<int*>(keys + 8 * p.k));
+    if (rank == 0) merge_beams(p.out, blockIdx.x, lists, sh.base, lists + 8 * p.k);
   };
   if (MODE == BEAMS && !reads) {
     finish_beams(beam_base(score, done, 0.f, 0.f));
@@ -704,7 +703,7 @@ void topk_launch(int dtype, int64_t rows, const TopkParams& q, LaunchRec* rec) {
   rec->block = dim3((unsigned)cut.threads);
   rec->cluster = (unsigned)blocks;
   rec->smem = (unsigned)((cut.threads < 256 ? 512 : 1024) * ((small ? 4 : 8) + 4) +
-                         (mode == ALONE ? 0 : mode == SLICES ? 9 * 8 * p.k : (9 * 8 + 8 * 12) * p.k));
+                         (mode == ALONE ? 0 : 9 * 8 * p.k + (mode == BEAMS ? merge_bytes(beams, p.k) : 0)));
   rec->func = es == 4 ? topk_func<float, uint64_t>(mode, cut.threads)
               : small ? topk_func<__nv_bfloat16, uint32_t>(mode, cut.threads)
                       : topk_func<__nv_bfloat16, uint64_t>(mode, cut.threads);
