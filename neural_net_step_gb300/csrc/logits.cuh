@@ -267,14 +267,16 @@ __device__ __forceinline__ F2 pair_of(const uint4& a, int h) {
 
 // exp((x - ref) / T) for many x as 2^(x c - ref c), one FMA and one ex2 each.
 // ref c is rounded once for all of them, which scales every term alike by
-// 2^(its rounding): `scale` takes that out of their sum.  Where ref c leaves fp32
-// (masks of the lowest value, small T) the difference is formed first.
+// 2^(its rounding): `scale` takes that out of their sum.  Where ref c is so large that
+// its rounding passes 1 (masks of the lowest value, small T) the difference is
+// formed first.
 struct Exponent {
   float c, ref, rc, scale;
   bool far;
   __device__ __forceinline__ Exponent(float ref_, float c_) : c(c_), ref(ref_), rc(ref_ * c_) {
-    far = !(fabsf(rc) < 1e37f);
-    scale = far ? 1.f : fmaf(-kLn2, fmaf(ref, c, -rc), 1.f);
+    far = !(fabsf(rc) < 0x1p24f);
+    const float off = fmaf(ref, c, -rc);
+    scale = far ? 1.f : fabsf(off) < 0x1p-12f ? fmaf(-kLn2, off, 1.f) : ex2(-off);
   }
   // of one x, without the scale
   __device__ __forceinline__ float one(float x) const { return ex2(far ? (x - ref) * c : fmaf(x, c, -rc)); }

@@ -43,8 +43,19 @@ def check(dtype, z, scores, m, done=None, eos=-1, **kw):
         fin = rows[np.isfinite(rows)]
         tol = 2 * (EX2 + SUM + 4 * U32 * (np.ptp(fin) if fin.size else 0))
         near = np.isfinite(wt[1:]) & np.isfinite(wt[:-1]) & (wt[:-1] - wt[1:] <= tol) & (wp[1:] != wp[:-1])
-        assert not near.any(), "the case leaves the order to rounding: choose another"
-        assert np.array_equal(p[b], wp[:m]) and np.array_equal(t[b], wc[:m]) and np.array_equal(d[b], wd[:m].astype(int))
+        if near.any():   # rounding may order these pairs of different beams either way: the totals are in order, all others are exact
+            all_totals = lo.beam_totals(rows, scores[b], None if done is None else done[b], eos)
+            got = all_totals[p[b], t[b]]
+            assert len(set(zip(p[b], t[b]))) == m and np.abs(got - wt[:m])[np.isfinite(wt[:m])].max() <= tol
+            free = np.zeros(m + 1, bool)
+            free[:-1] |= near[:m]
+            free[1:len(near) + 1] |= near[:m]
+            sure = ~free[:m]
+            assert near.mean() < 0.2
+            assert np.array_equal(p[b][sure], wp[:m][sure]) and np.array_equal(t[b][sure], wc[:m][sure])
+            assert np.array_equal(d[b], (t[b] == eos) | (False if done is None else done[b][p[b]] != 0))
+        else:
+            assert np.array_equal(p[b], wp[:m]) and np.array_equal(t[b], wc[:m]) and np.array_equal(d[b], wd[:m].astype(int))
         fine = np.isfinite(wt[:m])
         assert np.array_equal(s[b][~fine], wt[:m][~fine], equal_nan=True)
         assert_within(s[b][fine], wt[:m][fine], tol + U32 * np.abs(wt[:m][fine]), "scores")
