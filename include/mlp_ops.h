@@ -176,8 +176,8 @@ mlp_status mlp_op_argmax(int dtype, int64_t B, int64_t C, const void* z, int64_t
  *   -infinity where nothing is left), as mlp_op_distill takes it.
  * 1 <= k <= 256, k <= C <= 384000; T = temperature, 1e-6 to 1e6 (it changes the two sums
  * alone).  Entries of -infinity are taken like others, last.  Where a row holds NaN or
- * +infinity its lse is NaN, and its tail too unless only the k entries hold it.  Any
- * base and pitch.  Nothing written may overlap anything read. */
+ * +infinity its lse is NaN, and its tail NaN or +infinity unless only the k entries hold
+ * it.  Any base and pitch.  Nothing written may overlap anything read. */
 enum { MLP_TOPK_MAX = 256, MLP_TOPK_MAX_COLUMNS = 384000 };
 mlp_status mlp_op_topk(int dtype, int64_t B, int64_t C, int64_t k, const void* z, int64_t ldz, float temperature,
                        float* values, int64_t ldv, int32_t* indices, int64_t ldi, float* lse, float* tail,
@@ -229,8 +229,9 @@ mlp_status mlp_op_distill(int dtype, int64_t B, int64_t C, int64_t k, const void
  * scores 0, -infinity, ...), and so has a row of nothing but -infinity; one whose score is
  * NaN or +infinity or whose row holds NaN or +infinity has NaN, below everything.
  * beams <= 32, m <= 64, m <= beams * C, C <= 384000.  With m = beams, scores_out may be scores
- * and done_out may be done.  workspace: 8-byte aligned, at least the bytes below (0: a
- * shape that is refused); workspaces of calls that may overlap must not. */
+ * and done_out may be done; nothing else written may overlap anything read.  workspace:
+ * 8-byte aligned, at least the bytes below (0: a shape that is refused); workspaces of
+ * calls that may overlap must not. */
 size_t mlp_op_beam_select_workspace_bytes(int dtype, int64_t batch, int64_t beams, int64_t C, int64_t m);
 mlp_status mlp_op_beam_select(int dtype, int64_t batch, int64_t beams, int64_t C, int64_t m, const void* z,
                               int64_t ldz, const float* scores, const uint8_t* done, int32_t eos, float* scores_out,

