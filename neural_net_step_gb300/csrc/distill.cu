@@ -91,7 +91,7 @@ __device__ __forceinline__ float divergence(float p, float q, float r) {
 enum Hard { SAME, OTHER, SQUARE };
 
 template <typename T, bool CLUSTER, int HARD, int NT>
-__global__ void __launch_bounds__(NT, NT == 128 ? 5 : NT == 256 ? 3 : 1) distill_kernel(const __grid_constant__ DistillParams p) {
+__global__ void __launch_bounds__(NT, NT == 64 ? 10 : NT == 128 ? 5 : NT == 256 ? 3 : 1) distill_kernel(const __grid_constant__ DistillParams p) {
   pdl_enter();
   constexpr int E = kPer16<T>;
   constexpr bool TWO = HARD != SAME;
@@ -341,13 +341,14 @@ Cut cut_rows(int64_t C, int es, int k) {
   c.cluster = cs;
   c.per = (int)round_up(ceil_div(C, cs), 16 / es);
   const int64_t bytes = (int64_t)c.per * es;
-  c.threads = bytes <= 48 * 1024 && k <= 128 ? 128 : bytes <= 100 * 1024 ? 256 : 512;
+  c.threads = bytes <= 16 * 1024 && k <= 64 ? 64 : bytes <= 48 * 1024 && k <= 128 ? 128 : bytes <= 100 * 1024 ? 256 : 512;
   return c;
 }
 
 template <typename T, bool CLUSTER, int HARD>
 const void* distill_func(int threads) {
-  return threads == 128   ? (const void*)distill_kernel<T, CLUSTER, HARD, 128>
+  return threads == 64    ? (const void*)distill_kernel<T, CLUSTER, HARD, 64>
+         : threads == 128 ? (const void*)distill_kernel<T, CLUSTER, HARD, 128>
          : threads == 256 ? (const void*)distill_kernel<T, CLUSTER, HARD, 256>
                           : (const void*)distill_kernel<T, CLUSTER, HARD, 512>;
 }

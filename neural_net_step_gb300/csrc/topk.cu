@@ -350,18 +350,22 @@ __global__ void __launch_bounds__(NT, 1024 / NT) topk_kernel(const __grid_consta
   if (tid < kCounted) cand[tid] = 0;
   __syncthreads();
   uint32_t tau = 0xFFFFFFFFu, row_key = 0;
+  if constexpr (warps == 2) {
+    row_key = max(sh.top[0], sh.top[1]);
+  } else {
 #pragma unroll
-  for (int w = 0; w < warps; w += 4) {
-    const uint4 r = *reinterpret_cast<const uint4*>(sh.top + w), q = *reinterpret_cast<const uint4*>(sh.nth + w);
-    row_key = max(row_key, max(max(r.x, r.y), max(r.z, r.w)));
-    tau = min(tau, min(min(q.x, q.y), min(q.z, q.w)));
+    for (int w = 0; w < warps; w += 4) {
+      const uint4 r = *reinterpret_cast<const uint4*>(sh.top + w), q = *reinterpret_cast<const uint4*>(sh.nth + w);
+      row_key = max(row_key, max(max(r.x, r.y), max(r.z, r.w)));
+      tau = min(tau, min(min(q.x, q.y), min(q.z, q.w)));
+    }
   }
   if (!few) {
     constexpr int N = warps < 8 ? warps : 8;
     int place = lane;
 #pragma unroll
     for (int w = 0; w < warps; w += N) place += larger_in_runs<N>(keys + w * 32, warp - w, mine);
-    if (place == kk - 1) sh.tau = mine & 0xFFFFFE00u;
+    if (place == max(kk, 1) - 1) sh.tau = mine & 0xFFFFFE00u;
     __syncthreads();
     tau = sh.tau;
     if (sizeof(T) == 2) tau = (tau & 0x80000000u) ? tau & 0xFFFF0000u : tau | 0xFFFFu;   // (a bf16's key again)
@@ -682,7 +686,7 @@ TopkCut topk_cut(int64_t rows, int64_t C, int es, int k, bool whole) {
     c.cluster *= 2;
   c.per = (int)round_up(ceil_div(C, c.cluster), 16 / es);
   const int64_t blocks = rows * c.cluster, units = c.per * es / 16;
-  c.threads = k <= 64 ? 128 : k <= 128 ? 256 : 512;
+  c.threads = k <= 32 ? 64 : k <= 64 ? 128 : k <= 128 ? 256 : 512;
   while (c.threads < 512 && std::min(blocks, kThreads / c.threads) * units * 16 > kKept) c.threads *= 2;
   while (c.threads < 512 && blocks * c.threads * 2 <= kThreads && units > c.threads * 4) c.threads *= 2;
   return c;
@@ -690,7 +694,8 @@ TopkCut topk_cut(int64_t rows, int64_t C, int es, int k, bool whole) {
 
 template <typename T, int MODE, typename K>
 const void* topk_func(int threads) {
-  return threads == 128   ? (const void*)topk_kernel<T, MODE, 128, K>
+  return threads == 64    ? (const void*)topk_kernel<T, MODE, 64, K>
+         : threads == 128 ? (const void*)topk_kernel<T, MODE, 128, K>
          : threads == 256 ? (const void*)topk_kernel<T, MODE, 256, K>
                           : (const void*)topk_kernel<T, MODE, 512, K>;
 }
