@@ -18,7 +18,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmlpstep.so")
 SOURCES = ["simt_gemm.cu", "tc_gemm.cu", "rowops.cu", "model.cu", "noalloc.cu", "head.cu", "norm.cu", "ckpt8.cu", "gated.cu", "gated_tc.cu", "gated_small.cu",
-           "topk.cu", "distill.cu", "beam.cu"]
+           "topk.cu", "topk_f32.cu", "topk_bf16.cu", "topk_bf16_wide.cu", "distill.cu", "distill_f32.cu", "distill_bf16.cu", "beam.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

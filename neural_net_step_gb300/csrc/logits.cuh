@@ -216,6 +216,7 @@ inline int64_t slice_buffer(int64_t per, int es, int threads) { return round_up(
 struct __align__(16) Red { float v[16]; };
 template <int NT>
 __device__ __forceinline__ float red_sum(const Red& red) {
+  if constexpr (NT == 32) return red.v[0];
   if constexpr (NT == 64) return red.v[0] + red.v[1];
   float s = 0.f;
 #pragma unroll
@@ -249,6 +250,7 @@ __device__ __forceinline__ float block_max(float v, Red& red) {
   v = warp_max(v);
   if ((threadIdx.x & 31) == 0) red.v[threadIdx.x >> 5] = v;
   __syncthreads();
+  if constexpr (NT == 32) return red.v[0];
   if constexpr (NT == 64) return fmaxf(red.v[0], red.v[1]);
   float s = -INFINITY;
 #pragma unroll

@@ -1,0 +1,9 @@
+#include "topk.cuh"
+
+namespace mlpk {
+namespace tk {
+
+const void* topk_func_bf16(int mode, int threads) { return topk_func<__nv_bfloat16, uint32_t>(mode, threads); }
+
+}  // namespace tk
+}  // namespace mlpk
