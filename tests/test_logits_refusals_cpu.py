@@ -84,3 +84,20 @@ def test_beam_select_workspace():
     dict(dst=P, dst_pitch=80), dict(dst=P, dst_plane=1024), dict(dst=P, beams_out=3)])
 def test_beam_reorder_refuses(bad):
     _refused(nn.mlp_op_beam_reorder, REO, **bad)
+
+
+def test_every_kernel_in_a_header_takes_one_parameter_block():
+    """Launches pass one argument pointer, so every __global__ function takes exactly one `const __grid_constant__` struct
+    (test_capi_cpu looks at the .cu files)."""
+    import os
+    import re
+    csrc = os.path.join(os.path.dirname(os.path.abspath(nn.__file__)), "csrc")
+    n = 0
+    for f in sorted(os.listdir(csrc)):
+        if f.endswith(".cuh"):
+            txt = re.sub(r"//[^\n]*", "", open(os.path.join(csrc, f)).read())
+            for m in re.finditer(r"__global__", txt):
+                seg = txt[m.end():txt.index("{", m.end())]
+                assert re.fullmatch(r"const __grid_constant__ \w+ \w+", seg[seg.rindex("(") + 1:seg.rindex(")")].strip()), f
+                n += 1
+    assert n >= 2
