@@ -225,9 +225,9 @@ mlp_status mlp_op_distill(int dtype, int64_t B, int64_t C, int64_t k, const void
  *   uint8 [batch, m] (nullable): the parent was finished or the token is eos (eos
  *   may be -1, no end token, where done is null).
  * Totals are formed and compared in 64 bits; equal ones go by beam, then by logit
- * and token.  A beam of score -infinity has every total -infinity (a search starts with
- * scores 0, -infinity, ...), and so has a row of nothing but -infinity; one whose score is
- * NaN or +infinity or whose row holds NaN or +infinity has NaN, below everything.
+ * and token.  A beam of score -infinity, finished or not, has every total -infinity (a search
+ * starts with scores 0, -infinity, ...), and so has a row of nothing but -infinity; one whose
+ * score is NaN or +infinity or whose row holds NaN or +infinity has NaN, below everything.
  * beams <= 32, m <= 64, m <= beams * C, C <= 384000.  With m = beams, scores_out may be scores
  * and done_out may be done; nothing else written may overlap anything read.  workspace:
  * 8-byte aligned, at least the bytes below (0: a shape that is refused); workspaces of

@@ -19,10 +19,10 @@ struct BeamOut {
   float* scores; int32_t* parents; int32_t* tokens; uint8_t* done;   // [batch, m]; done nullable
 };
 // What a beam's logits are added to, and what it offers: 0 base + logit; 1 every
-// token at base; 2 finished.
+// token at base; 2 the end token at base, every other at -infinity.
 struct __align__(16) BeamBase {
   double base;
-  int kind;
+  int kind, done;
 };
 
 // Order of totals as unsigned integers; NaN is 1, below -infinity (0: no pair).
@@ -50,13 +50,13 @@ __device__ __forceinline__ double log_of(float s) {
 __device__ __forceinline__ bool beam_reads_row(float score, bool done) { return !done && fabsf(score) < INFINITY; }
 // largest, sum: of the beam's row, sum of exp(z - largest) (not looked at where it reads none).
 __device__ __forceinline__ BeamBase beam_base(float score, bool done, float largest, float sum) {
-  BeamBase b{(double)score, 0};
+  BeamBase b{(double)score, 0, done};
   const double nan = __longlong_as_double(0x7FF8000000000000ll);
-  if (done) {
-    b.kind = 2;
-  } else if (!(fabsf(score) < INFINITY)) {
+  if (!(fabsf(score) < INFINITY)) {   // (finished or not: a list has to descend)
     b.kind = 1;
     if (!(score < 0.f)) b.base = nan;
+  } else if (done) {
+    b.kind = 2;
   } else if (largest == -INFINITY && !(sum != 0.f)) {   // nothing but -infinity
     b.kind = 1;
     b.base = -(double)INFINITY;
@@ -132,7 +132,7 @@ __device__ __forceinline__ void merge_beams(const BeamOut& p, int64_t b, const u
       p.scores[at] = (float)total_of(key);
       p.parents[at] = w;
       p.tokens[at] = toks[a];
-      if (p.done) p.done[at] = (base[w].kind == 2 || toks[a] == p.eos) ? 1 : 0;
+      if (p.done) p.done[at] = (base[w].done || toks[a] == p.eos) ? 1 : 0;
     }
   }
 }

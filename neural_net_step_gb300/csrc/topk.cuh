@@ -269,6 +269,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 28 : 1024 / NT) topk_kernel(con
         const uint32_t to = in_block(smem_addr(&sh.base[rank]), 0);
         put64(to, (uint64_t)__double_as_longlong(b.base));
         put32(to + 8, (uint32_t)b.kind);
+        put32(to + 12, (uint32_t)b.done);
       }
     }
     cluster_arrive();

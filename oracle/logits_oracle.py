@@ -80,11 +80,11 @@ def beam_totals(z, scores, done=None, eos=-1):
     out = np.full((W, C), np.nan)
     for w in range(W):
         s = float(scores[w])
-        if done is not None and done[w]:
+        if s == -np.inf:
+            out[w] = -np.inf
+        elif np.isfinite(s) and done is not None and done[w]:
             out[w] = -np.inf
             out[w, eos] = s
-        elif s == -np.inf:
-            out[w] = -np.inf
         elif np.isfinite(s) and not np.isnan(z[w]).any() and z[w].max() < np.inf:
             out[w] = -np.inf if z[w].max() == -np.inf else s + (z[w] - lse(z[w]))
     return out

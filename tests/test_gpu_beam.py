@@ -110,6 +110,19 @@ def test_first_step_masks_and_all_finished(dtype):
     check(dtype, z, s, 64)
 
 
+@pytest.mark.parametrize("W,C,m", [(4, 9, 20), (8, 3, 24), (16, 2, 30), (3, 40000, 12), (12, 5000, 24)])
+def test_finished_beams_without_a_score(W, C, m):
+    """A finished beam of score -infinity offers its tokens in order, one of NaN nothing; its flag stays."""
+    rng = np.random.default_rng([9, W])
+    s = scores_of(rng, 3, W)
+    done = np.zeros((3, W), np.uint8)
+    s[:, 1] = -np.inf
+    done[:, :2] = 1
+    s[1, 2], s[2, 0] = np.nan, -np.inf
+    done[1, 2] = 1
+    check(F, logits(rng, 3 * W, C, torch.float32), s, m, done, C - 1)
+
+
 def test_totals_far_below_zero_are_compared_in_64_bits():
     """Scores of -1000: an fp32 total has a step of 6e-5, and beams 1e-5 apart keep their order."""
     rng = np.random.default_rng(4)
