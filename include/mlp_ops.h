@@ -204,8 +204,8 @@ mlp_status mlp_op_topk(int dtype, int64_t B, int64_t C, int64_t k, const void* z
  * hold.  A teacher's row with nothing in it (no entry above -infinity, no tail)
  * has KD 0.  A label or column out of range, or a column given twice, sets bit 1 of
  * err_dev, and that row's loss and gradient are 0.  A teacher that gives weight
- * where the student has none (z = -infinity) has an infinite loss; a row of z that
- * holds NaN or +infinity, or nothing but -infinity, gives NaN.
+ * (p_j that fp32 holds) where the student has none (z = -infinity) has an infinite loss;
+ * a row of z that holds NaN or +infinity, or nothing but -infinity, gives NaN.
  * 1 <= k <= 256, k <= C <= 384000; T from 1e-6 to 1e6.  Any base and pitch; rows of dz with
  * another address modulo 16 than z's are written element by element. */
 mlp_status mlp_op_distill(int dtype, int64_t B, int64_t C, int64_t k, const void* z, int64_t ldz,

@@ -52,10 +52,13 @@ __device__ __forceinline__ void clear(T* dz, int n) {
   for (int i = head + units * E + threadIdx.x; i < n; i += blockDim.x) dz[i] = from_f32<T>(0.f);
 }
 
-// p log(p / q) - p + q for r = log(p / q): p (r - 1 + e^-r), for small r by its
-// series (the terms left out are below 2^-24 of it at 1/2).
-__device__ __forceinline__ float divergence(float p, float q, float r) {
+// p log(p / q) - p + q for log(p / q) = r = d / T + l: p (r - 1 + e^-r), for small r by
+// its series (the terms left out are below 2^-24 of it at 1/2).  A logit masked by
+// the type's lowest value can leave fp32 as d / T, but not as p d / T where p is as small.
+__device__ __forceinline__ float divergence(float p, float q, float d, float T, float l) {
   if (p == 0.f) return q;
+  const float r = d / T + l;
+  if (!(fabsf(r) < INFINITY) && fabsf(d) < INFINITY) return fmaf(p / T, d, fmaf(p, l - 1.f, q));
   if (!(fabsf(r) < 0.5f)) return fmaf(p, r - 1.f, q);
   float h = fmaf(r, 1.f / 40320.f, -1.f / 5040.f);
   h = fmaf(r, h, 1.f / 720.f);
@@ -65,7 +68,6 @@ __device__ __forceinline__ float divergence(float p, float q, float r) {
   h = fmaf(r, h, 0.5f);
   return p * (r * r) * h;
 }
-
 
 template <typename T, bool CLUSTER, int HARD, int NT>
 __global__ void __launch_bounds__(NT, NT == 32 ? 16 : NT == 64 ? 10 : NT == 128 ? 5 : NT == 256 ? 3 : 1) distill_kernel(const __grid_constant__ DistillParams p) {
@@ -289,13 +291,14 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 16 : NT == 64 ? 10 : NT == 128 
   if (rank == 0) {
     const bool soft = has && p.b != 0.f;
     const float ln = soft ? logf(St / S) : 0.f;
-    float kd = soft && mine && col >= 0 ? divergence(pj, q / S, ((t - ztj) - (tm0 - m0)) / p.T + dl - ln) : 0.f;
+    float kd = soft && mine && col >= 0 ? divergence(pj, q / S, (t - ztj) - (tm0 - m0), p.T, dl - ln) : 0.f;
     if (p.k > 32) kd = block_sum<NT>(kd, sh.red[8]);
     else if (tid < 32) kd = warp_sum(kd);
     if (tid == 0) {
       if (soft) {
         const float R = sum * f / S;
-        kd += divergence(pr, R, R > 1e-30f ? logf(pr / R) : logf(pr) - ((rest - m0) / p.T + logf(sum) - logf(S)));
+        kd += R > 1e-30f ? divergence(pr, R, 0.f, p.T, logf(pr / R))
+                         : divergence(pr, R, m0 - rest, p.T, logf(pr) - logf(sum) + logf(S));
       }
       p.loss[row] = w * (p.b * kd + (p.labels ? p.a * (logf(S1) + (m0 - zy)) : 0.f));
     }

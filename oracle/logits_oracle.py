@@ -60,8 +60,9 @@ def distill(z, tv, ti, tail=None, labels=None, weights=None, T=1.0, a=0.0, b=1.0
             if p[-1] > 0:
                 left = lse(x[others])
                 kd += p[-1] * (t[-1] - lse(t) - (left - lse(x)))
-                if left > -np.inf:
-                    d[others] -= p[-1] * np.exp(x[others] - left)
+                if left > -np.inf:   # (shares from differences: log-sums of masks of the lowest value lose the counts)
+                    e = np.exp(x[others] - x[others].max())
+                    d[others] -= p[-1] * e / e.sum()
         loss[i] = b * kd
         d *= b / T
         if y is not None:

@@ -110,6 +110,27 @@ def test_distill_with_a_rest_far_below(dtype, C):
 
 
 @pytest.mark.parametrize("dtype", [F, H])
+@pytest.mark.parametrize("C", [20, 3000])
+def test_distill_of_lowest_values_at_small_temperatures(dtype, C):
+    """A teacher's weight of 1e-40 where the student's mask is the type's lowest value: a loss below one, not infinity."""
+    rng = np.random.default_rng(8)
+    T, k = 0.5, 20
+    z = logits(rng, 3, C, torch.float32)
+    tv, ti, _ = teacher(rng, z.double().numpy(), k, T)
+    for i in range(3):
+        top = tv[i].max()
+        tv[i, 10:] = top - 46.0 - np.arange(10) * 0.1   # e^-92 and less
+        z[i, ti[i, 10:]] = torch.finfo(torch.bfloat16).min
+    z = z.to(TDT[dtype])
+    loss, dz, bits, x = run_distill(dtype, z, tv, ti, T=T)
+    wl, wd, _ = lo.distill(x, tv, ti, T=T)
+    assert np.isfinite(wl).all() and (wl < 3).all()
+    # weights of 1e-40 are multiples of 2^-149: 1e-5 of them, and of their share of the loss
+    assert_within(loss, wl, 1e-4 * (1 + wl), "loss")
+    assert_within(dz, wd, HALF[dtype] * np.abs(wd) + 1e-5, "dz")
+
+
+@pytest.mark.parametrize("dtype", [F, H])
 @pytest.mark.parametrize("T", [1.0, 2.0, 0.5])
 def test_distill_of_every_width(dtype, T):
     rng = np.random.default_rng(7)
