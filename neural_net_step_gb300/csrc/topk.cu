@@ -18,9 +18,11 @@ using namespace tk;
 constexpr int64_t kFusedRow = 256 * 1024;
 
 // Blocks of a row and their threads.
-//   Twice as many threads as entries: their largest elements set the threshold.  One
-// warp for short rows, which a block's barriers would hold up (16384 x 2000 bf16, k = 10:
-// 52 us with 64 threads, 33 with 32; 16384 x 8000, k = 16: 73 and 65).
+//   A third more threads than entries at least: their largest elements set the threshold,
+// which leaves up to 1.9 k candidates so (16384 x 4000 bf16, k = 96: 142 us with 128 threads,
+// 194 with 256; k = 32: 58 with 64, 201 with 32, too few).  One warp for short rows, which
+// a block's barriers would hold up (16384 x 2000, k = 10: 52 us with 64 threads, 33 with
+// 32; 16384 x 8000, k = 16: 73 and 65).
 //   Fewer and larger blocks where the rows under way would not stay in L2 until they are
 // read again (fp32 4096 x 32000, k = 64: 131 us with 1216 rows under way, 107 with 608).
 //   More threads where rows are few (one row of 32000 bf16, k = 50: 5.8 us with 512).
@@ -40,7 +42,7 @@ TopkCut topk_cut(int64_t rows, int64_t C, int es, int k, bool whole) {
     c.cluster *= 2;
   c.per = (int)round_up(ceil_div(C, c.cluster), 16 / es);
   const int64_t blocks = rows * c.cluster, units = c.per * es / 16;
-  c.threads = k <= 16 && units <= kOneWarp ? 32 : k <= 32 ? 64 : k <= 64 ? 128 : k <= 128 ? 256 : 512;
+  c.threads = k <= 24 && units <= kOneWarp ? 32 : k <= 48 ? 64 : k <= 96 ? 128 : k <= 192 ? 256 : 512;
   while (c.threads < 512 && std::min(blocks, kThreads / c.threads) * units * 16 > kKept) c.threads *= 2;
   while (c.threads < 512 && blocks * c.threads * 2 <= kThreads && units > c.threads * 4) c.threads *= 2;
   return c;
