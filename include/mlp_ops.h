@@ -229,7 +229,7 @@ mlp_status mlp_op_distill(int dtype, int64_t B, int64_t C, int64_t k, const void
  * starts with scores 0, -infinity, ...), and so has a row of nothing but -infinity; one whose
  * score is NaN or +infinity or whose row holds NaN or +infinity has NaN, below everything.
  * beams <= 32, m <= 64, m <= beams * C, C <= 384000.  With m = beams, scores_out may be scores
- * and done_out may be done; nothing else written may overlap anything read.  workspace:
+ * and done_out may be done (refused with another m); nothing else written may overlap anything read.  workspace:
  * 8-byte aligned, at least the bytes below (0: a shape that is refused); workspaces of
  * calls that may overlap must not. */
 size_t mlp_op_beam_select_workspace_bytes(int dtype, int64_t batch, int64_t beams, int64_t C, int64_t m);

@@ -1689,6 +1689,9 @@ mlp_status mlp_op_beam_select(int dtype, int64_t batch, int64_t beams, int64_t C
   if (!dtype_ok(dtype)) return fail(MLP_ERR_DTYPE, "bad dtype");
   if (!z || !scores || !scores_out || !parents || !tokens) return fail(MLP_ERR_ARG, "null pointer");
   if (done && (eos < 0 || eos >= C)) return fail(MLP_ERR_ARG, "finished beams need an end token in [0, C)");
+  // (entry b's results lie over entry b's inputs alone only where there are as many)
+  if (m != beams && (scores_out == scores || (done && done_out == done)))
+    return fail(MLP_ERR_ARG, "results over the scores or flags need m = beams");
   if (!elements_aligned(dtype_bytes(dtype), {z}) || !elements_aligned(4, {scores, scores_out, parents, tokens}))
     return fail(MLP_ERR_ARG, "misaligned elements");
   BeamSelectOp op;
