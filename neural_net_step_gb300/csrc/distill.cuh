@@ -115,9 +115,13 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 16 : NT == 64 ? 10 : NT == 128 
   if (col < 0) t = -INFINITY;                   // (unused entries' values are not looked at)
   const float tm = block_max<NT>(t, sh.red[0]);
   const float tm0 = tm > -INFINITY ? tm : 0.f;
-  float tref = fmaxf(tm / p.T, tail);
-  if (!(tref > -INFINITY)) tref = 0.f;
-  const float dl = tm0 / p.T - tref;            // what the largest is below the reference
+  float tref = fmaxf(tm / p.T, tail), dl = tm0 / p.T;   // a reference, and what the largest is below it
+  if (!(fabsf(tref) < INFINITY)) {   // T takes the largest out of fp32 (and no tail counts beside it), or nothing is there
+    dl = 0.f;
+    tref = fmaxf(tref, 0.f);
+  } else {
+    dl -= tref;
+  }
   const float pe = mine ? expf((t - tm0) / p.T + dl) : 0.f;
   const float U = expf(tail - tref);
   const float St = block_sum<NT>(pe, sh.red[1]) + U;
@@ -192,6 +196,10 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 16 : NT == 64 ? 10 : NT == 128 
   const float rest = most > -INFINITY ? most : 0.f;   // the others' exponents are relative to this
   const float m = fmaxf(most, block_max<NT>(mine ? ztj : -INFINITY, sh.red[5]));
   const float m0 = m > -INFINITY ? m : 0.f;
+  // (t - z) - (tm - m): two rows near one another leave t - z few roundings.  One far from the other (32: the usual
+  // distance of an entry from its row's largest) leaves them in tm - m, and what counts is (t - tm) - (z - m).
+  const bool apart = !(fabsf(tm0 - m0) < 32.f);
+  const float from = apart ? tm0 : ztj, to = apart ? ztj : tm0, d = (t - from) - (to - m0);
   const float q = mine ? expf((ztj - m0) / p.T) : 0.f;
   const float f = sum != 0.f ? ex2((rest - m0) * p.c) : 0.f;
   const float S = fmaf(sum, f, block_sum<NT>(q, sh.red[6]));
@@ -293,7 +301,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 16 : NT == 64 ? 10 : NT == 128 
   if (rank == 0) {
     const bool soft = has && p.b != 0.f;
     const float ln = soft ? logf(St / S) : 0.f;
-    float kd = soft && mine && col >= 0 ? divergence(pj, q / S, (t - ztj) - (tm0 - m0), p.T, dl - ln) : 0.f;
+    float kd = soft && mine && col >= 0 ? divergence(pj, q / S, d, p.T, dl - ln) : 0.f;
     if (p.k > 32) kd = block_sum<NT>(kd, sh.red[8]);
     else if (tid < 32) kd = warp_sum(kd);
     if (tid == 0) {
