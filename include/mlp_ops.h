@@ -230,16 +230,17 @@ mlp_status mlp_op_distill(int dtype, int64_t B, int64_t C, int64_t k, const void
  *   scores_out fp32, parents int32 (the beam), tokens int32 [batch, m]; done_out
  *   uint8 [batch, m] (nullable): the parent was finished or the token is eos (eos
  *   may be -1, no end token, where done is null).
- * Totals are formed and compared in 64 bits from each row's logsumexp, whose sum is fp32's (within
- * 3e-7): a beam's own tokens are in the order of their logits, and pairs of different beams whose
- * totals are closer than that may come in either order.  Equal totals go by beam, then by logit
- * and token (by token alone where a beam's logits are not read).  A beam of score -infinity, finished or not, has every total -infinity (a search
- * starts with scores 0, -infinity, ...), and so has a row of nothing but -infinity; one whose
- * score is NaN or +infinity or whose row holds NaN or +infinity has NaN, below everything.
+ * Totals are formed and compared in 64 bits from each row's logsumexp, whose sum is fp32's (off
+ * by about 3e-7): a beam's own tokens are in the order of their logits, and pairs of different
+ * beams whose totals are closer than that may come in either order.  Equal totals go by beam,
+ * then by logit and token (by token alone where a beam's logits are not read).  A beam of score
+ * -infinity, finished or not, has every total -infinity (a search starts with scores
+ * 0, -infinity, ...), and so has a row of nothing but -infinity; one whose score is NaN or
+ * +infinity or whose row holds NaN or +infinity has NaN, below everything.
  * beams <= 32, m <= 64, m <= beams * C, C <= 384000.  With m = beams, scores_out may be scores
- * and done_out may be done (refused with another m); nothing else written may overlap anything read.  workspace:
- * 8-byte aligned, at least the bytes below (0: a shape that is refused); workspaces of
- * calls that may overlap must not. */
+ * and done_out may be done (refused with another m); nothing else written may overlap anything
+ * read.  workspace: 8-byte aligned, at least the bytes below (0: a shape that is refused);
+ * workspaces of calls that may overlap must not. */
 size_t mlp_op_beam_select_workspace_bytes(int dtype, int64_t batch, int64_t beams, int64_t C, int64_t m);
 mlp_status mlp_op_beam_select(int dtype, int64_t batch, int64_t beams, int64_t C, int64_t m, const void* z,
                               int64_t ldz, const float* scores, const uint8_t* done, int32_t eos, float* scores_out,

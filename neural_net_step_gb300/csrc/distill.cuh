@@ -20,8 +20,10 @@
 //   KD = sum over the k columns and the rest of  p log(p / q) - p + q,
 // which is the same (both distributions add up to 1), and of which every term is
 // positive and as exact as its p / q.
-//   16384 x 32000 bf16, k = 64, T = 2: 335 us, 0.94 of the copy rate (each row read twice
-// from DRAM, once to be summed and once for its gradient, it could not be below 470).
+//   16384 x 32000 bf16, k = 64, T = 2: 339 us, 0.93 of the copy rate (each row read twice
+// from DRAM, once to be summed and once for its gradient, it could not be below 470).  The loss
+// alone 241 of 158, the row staged all the same; a gradient whose rows lie at another address
+// modulo 16 516, element by element.
 #pragma once
 #include "distill.h"
 

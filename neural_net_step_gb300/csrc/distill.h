@@ -22,7 +22,8 @@ struct DistillParams {
 
 // The hard labels' softmax next to the soft ones': of the same temperature, at any
 // other (a second exponential an element), or at half of it (T = 2: the square of
-// the first; 8192 x 32000 bf16, k = 32: 219 us with a second exponential, 189 so).
+// the first, at twice its relative error, a few 2^-22; 8192 x 32000 bf16, k = 32: 219 us with a second
+// exponential, 190 so).
 enum Hard { SAME, OTHER, SQUARE };
 
 const void* distill_func_f32(bool cluster, int hard, int threads);

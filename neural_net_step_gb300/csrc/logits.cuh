@@ -1,8 +1,10 @@
-// A row of logits, or a slice of it, in shared memory: what the top-k,
-// distillation and beam kernels share.
+// What the top-k, distillation and beam kernels share: the order of logits, units
+// of 16 bytes, exponentials relative to a reference, sums over a block, the blocks of a
+// cluster; and, for distillation, a row or a slice of it in shared memory (top-k
+// reads its rows from global memory, twice).
 //
 // A row of C elements is cut into slices of `per` elements, one for each block
-// of a cluster.  The slice is copied in 16-byte units whatever the row's
+// of a cluster.  A Slice is copied in 16-byte units whatever the row's
 // alignment: shared memory keeps the row's phase (its address modulo 16), the
 // units that the row only partly covers are copied element by element, and
 // what they and the units behind them hold besides is -infinity, so that

@@ -14,12 +14,15 @@ using namespace lg;
 using namespace tk;
 
 // A beam's row of at most so many bytes is read by one block where rows leave SMs
-// idle (fp32 7 x 5 x 50001: 12.1 us so, 14.1 with two blocks a row and a merge of its own).
+// idle, longer ones by several, with a merge of its own (us, one block a row and several: bf16
+// 1 x 4 x 32000 7.6 and 7.9, x 65536 8.8 and 9.6; fp32 1 x 4 x 50001 9.7 and 10.8, 7 x 5 x 50001 11.9 and 12.2;
+// bf16 8 x 4 x 100003 12.1 and 12.6.  From about 220 KB on it turns: bf16 x 131072 1 x 4 11.0 and 10.3,
+// 8 x 4 13.1 and 11.6).
 constexpr int64_t kFusedRow = 256 * 1024;
 
 // Blocks of a row and their threads.
-//   A third more threads than entries at least: their largest elements set the threshold,
-// which leaves up to 1.9 k candidates so (16384 x 4000 bf16, k = 96: 142 us with 128 threads,
+//   A third more threads than entries at least, whose largest elements set the threshold
+// (where the row has that many units: see topk.cuh), which leaves up to 1.9 k candidates so (16384 x 4000 bf16, k = 96: 142 us with 128 threads,
 // 194 with 256; k = 32: 58 with 64, 201 with 32, too few).  One warp for short rows, which
 // a block's barriers would hold up (16384 x 2000, k = 10: 52 us with 64 threads, 33 with
 // 32; 16384 x 8000, k = 16: 73 and 65).
