@@ -213,7 +213,8 @@ mlp_status mlp_op_topk(int dtype, int64_t B, int64_t C, int64_t k, const void* z
  * by about 2e-7 T of itself and the gradient by 1e-7 T of its largest entry (1e-4 at T = 1000; little
  * is left of either at 1e6).
  * 1 <= k <= 256, k <= C <= 384000; T from 1e-6 to 1e6.  Any base and pitch; rows of dz with
- * another address modulo 16 than z's are written element by element. */
+ * another address modulo 16 than z's are written element by element.  But for dz in z's
+ * place, nothing written may overlap anything read. */
 mlp_status mlp_op_distill(int dtype, int64_t B, int64_t C, int64_t k, const void* z, int64_t ldz,
                           const float* t_values, int64_t ldtv, const int32_t* t_indices, int64_t ldti,
                           const float* t_tail, const int32_t* labels, const float* row_weights, float temperature,
